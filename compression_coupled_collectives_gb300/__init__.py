@@ -394,3 +394,8 @@ def reduce_typed(dtype: int, streams: Sequence[torch.Tensor], n_elems: int, op: 
     nbytes, dev = cccl_get_result(ws, stream)
     _check(dev, "cccl_reduce_typed (device)")
     return out[:nbytes]
+
+
+from .kv import (CCCL_KV_16BIT, CCCL_KV_E4M3, CCCL_KV_INT8, KV_MAX_BATCH, KV_MAX_DIM, KV_MAX_HEADS,  # noqa: E402
+                 KvBatch, KvCache, cccl_kv_attention, cccl_kv_clear_status, cccl_kv_read, cccl_kv_workspace_bytes,
+                 cccl_kv_write, empty_kv_workspace, kv_attention, kv_read, kv_write)

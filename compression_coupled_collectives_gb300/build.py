@@ -12,7 +12,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libcccl.so")
-SOURCES = ["cccl_compress.cu", "cccl_decompress.cu", "cccl_reduce.cu", "cccl_api.cu"]
+SOURCES = ["cccl_compress.cu", "cccl_decompress.cu", "cccl_reduce.cu", "cccl_api.cu",
+           "cccl_kv_api.cu", "cccl_kv_copy.cu", "cccl_kv_attention.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
          "-I", os.path.join(ROOT, "include")]
@@ -27,7 +28,7 @@ def _nvcc() -> str:
 
 def _deps():
     files = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cu", ".cuh", ".h"))]
-    files.append(os.path.join(ROOT, "include", "cccl.h"))
+    files += [os.path.join(ROOT, "include", f) for f in ("cccl.h", "cccl_kv.h")]
     return files
 
 

@@ -108,17 +108,6 @@ AddrRangeFn addr_range_fn() {
     return fn;
 }
 
-// True if [p, p + bytes) lies inside one device (or managed) allocation.
-bool device_range(const void* p, size_t bytes) {
-    const AddrRangeFn range = addr_range_fn();
-    if (p == nullptr || range == nullptr) return false;
-    CUdeviceptr base = 0;
-    size_t size = 0;
-    if (range(&base, &size, reinterpret_cast<CUdeviceptr>(p)) != CUDA_SUCCESS) return false;
-    const uintptr_t a = reinterpret_cast<uintptr_t>(p);
-    return a >= base && bytes <= size && a - base <= size - bytes;
-}
-
 cccl_status clear_ws(void* ws, size_t bytes, cudaStream_t s) {
     return cudaMemsetAsync(ws, 0, bytes, s) == cudaSuccess ? CCCL_OK : CCCL_ERR_CUDA;
 }
@@ -134,7 +123,24 @@ uint64_t elem_bytes(int dtype) {
 
 }  // namespace
 
+namespace cccl {
+
+// True if [p, p + bytes) lies inside one device (or managed) allocation.
+bool device_range(const void* p, size_t bytes) {
+    const AddrRangeFn range = addr_range_fn();
+    if (p == nullptr || range == nullptr) return false;
+    CUdeviceptr base = 0;
+    size_t size = 0;
+    if (range(&base, &size, reinterpret_cast<CUdeviceptr>(p)) != CUDA_SUCCESS) return false;
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+    return a >= base && bytes <= size && a - base <= size - bytes;
+}
+
+}  // namespace cccl
+
 extern "C" {
+
+using cccl::device_range;
 
 size_t cccl_compress_bound(size_t n_elems) {
     if (n_elems == 0 || n_elems > CCCL_MAX_ELEMS) return 0;

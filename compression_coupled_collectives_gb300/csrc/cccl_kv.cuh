@@ -1,0 +1,209 @@
+// cccl_kv.cuh -- what the paged key/value cache kernels share (sm_103a): the
+// launch arguments, the way from a position to its place in the cache, 8-bit
+// codes, and the row-at-a-time form of attention.
+#pragma once
+
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+
+#include "cccl_device.cuh"
+
+namespace cccl {
+
+constexpr int kKv16Bit = 0, kKvInt8 = 1, kKvE4m3 = 2;  // CCCL_KV_*
+
+// Division of 0 <= n < 2^31 by d >= 1 as a multiplication: with
+// 2^(s-1) < d <= 2^s and m = ceil(2^(31+s) / d) the error m d - 2^(31+s) is
+// below d <= 2^s, so floor(n m / 2^(31+s)) = floor(n / d) for n < 2^31.
+struct FastDiv {
+    uint32_t d, m, s;
+};
+inline FastDiv fast_div(uint32_t d) {
+    uint32_t s = 0;
+    while ((1ull << s) < d) ++s;
+    const uint64_t p = 1ull << (31 + s);
+    return FastDiv{d, (uint32_t)((p + d - 1) / d), s};
+}
+__device__ __forceinline__ uint32_t div_by(const FastDiv& f, uint32_t n) {
+    return (uint32_t)(((uint64_t)n * f.m) >> (31 + f.s));
+}
+
+// One call on one cache and batch.  Strides of k and v in bytes, of the
+// scales in floats, of the packed tensors (x, y) in bytes.
+struct KvArgs {
+    uint8_t *k, *v;
+    float *k_scale, *v_scale;
+    int64_t page_stride, token_stride, head_stride;
+    int64_t s_page, s_token, s_head;
+    int64_t pages;
+    const int32_t *table, *cu, *lens;
+    int64_t table_stride, n_tokens;
+    WsHeader* ws;
+    FastDiv page_tokens;
+    int32_t kv_heads, dim, batch, table_pages;
+};
+// The packed K and V of a write or a read.
+struct KvPacked {
+    uint8_t *k, *v;
+    int64_t k_token, k_head, v_token, v_head;
+};
+// What attention adds.
+struct AttnArgs {
+    const uint8_t* q;
+    uint8_t* out;
+    float* lse;
+    int64_t q_token, q_head, o_token, o_head;
+    int64_t window;  // 0: none
+    float scale;
+    int32_t causal, group, q_heads;
+};
+
+// Sequence b's rows and length, with everything that does not fit clamped
+// (and reported): 0 <= row, row + n <= n_tokens, 0 <= len <= table capacity.
+struct Sequence {
+    int64_t row;  // first row of its new tokens
+    int32_t n;    // new tokens
+    int32_t len;  // cached tokens, the new ones included
+};
+__device__ __forceinline__ Sequence load_sequence(const KvArgs& a, int b) {
+    const int64_t lo = a.cu[b], hi = a.cu[b + 1];
+    const int64_t len = a.lens[b];
+    const int64_t cap = min((int64_t)a.table_pages * a.page_tokens.d, (int64_t)0x7FFFFF00);
+    Sequence s;
+    s.row = min(max(lo, (int64_t)0), a.n_tokens);
+    const int64_t end = min(max(hi, s.row), a.n_tokens);
+    s.n = (int32_t)(end - s.row);
+    s.len = (int32_t)min(max(len, (int64_t)0), cap);
+    if (s.row != lo || end != hi || s.len != len) record_error(a.ws, kStatusInvalidArg);
+    return s;
+}
+
+// Page of position p of sequence b (p inside the table), or -1 (reported).
+__device__ __forceinline__ int64_t page_of(const KvArgs& a, int b, uint32_t page_index) {
+    const int64_t e = a.table[(int64_t)b * a.table_stride + page_index];
+    if (e < 0 || e >= a.pages) {
+        record_error(a.ws, kStatusInvalidArg);
+        return -1;
+    }
+    return e;
+}
+// Where position p's vectors lie: byte offset of head 0 in k and v, float
+// offset of its scales.  Returns false for a page outside the cache.
+__device__ __forceinline__ bool slot_of(const KvArgs& a, int b, uint32_t p, int64_t& at, int64_t& scale_at) {
+    const uint32_t pi = div_by(a.page_tokens, p), slot = p - pi * a.page_tokens.d;
+    const int64_t page = page_of(a, b, pi);
+    at = page * a.page_stride + (int64_t)slot * a.token_stride;
+    scale_at = page * a.s_page + (int64_t)slot * a.s_token;
+    return page >= 0;
+}
+
+// The keys that a row at position `pos` of a sequence of `len` tokens sees:
+// first .. last - 1 (empty when last <= first).
+__device__ __forceinline__ void visible_range(const AttnArgs& t, int32_t len, int64_t pos, int32_t& first,
+                                              int32_t& last) {
+    const int64_t hi = t.causal ? min((int64_t)len, pos + 1) : (int64_t)len;
+    const int64_t lo = t.window > 0 ? pos - t.window + 1 : 0;
+    last = (int32_t)max(hi, (int64_t)0);
+    first = (int32_t)min(max(lo, (int64_t)0), (int64_t)last);
+}
+
+// ---------------------------------------------------------------- values
+// The two 16-bit types: bf16 and fp16 as the packed values' type.
+struct BfType {
+    static __device__ __forceinline__ float load(uint16_t b) { return __uint_as_float((uint32_t)b << 16); }
+    static __device__ __forceinline__ uint16_t round(float x) { return __bfloat16_as_ushort(__float2bfloat16_rn(x)); }
+};
+struct HfType {
+    static __device__ __forceinline__ float load(uint16_t b) { return __half2float(__ushort_as_half(b)); }
+    static __device__ __forceinline__ uint16_t round(float x) { return __half_as_ushort(__float2half_rn(x)); }
+};
+template <class T>
+__device__ __forceinline__ uint32_t round_pair(float lo, float hi) {
+    return (uint32_t)T::round(lo) | ((uint32_t)T::round(hi) << 16);
+}
+
+// The binary32 value of an 8-bit code (NaN for E4M3's two NaN codes).
+template <int FMT>
+__device__ __forceinline__ float code_value(uint8_t c) {
+    if (FMT == kKvInt8) return (float)(int8_t)c;
+    __nv_fp8_e4m3 e;
+    e.__x = c;
+    return (float)e;
+}
+// Value i of a stored vector, without its scale.
+template <class T, int FMT>
+__device__ __forceinline__ float stored_value(const uint8_t* vec, int i) {
+    if (FMT == kKv16Bit) return T::load(reinterpret_cast<const uint16_t*>(vec)[i]);
+    return code_value<FMT>(vec[i]);
+}
+
+__device__ __forceinline__ float warp_sum(float x) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, o);
+    return x;
+}
+
+// One row of attention by one warp, straight from the definition: a pass for
+// the maximum, one for the sum of the exponentials, one for the values with
+// their normalised weights (so that no sum passes the values' own size),
+// visible keys only, IEEE arithmetic throughout (a NaN or an infinity among the visible values goes where the
+// formula takes it, one in a hidden place goes nowhere).  The tensor-core
+// kernels compute hidden places as products with zero, which is not the same
+// when such a place holds a NaN or an infinity; they send the rows whose sums
+// come out non-finite through here.
+// Lane l holds values l, l + 32, l + 64, l + 96 of the head.
+template <class T, int FMT>
+__device__ __noinline__ void attend_row(const KvArgs& a, const AttnArgs& t, int b, int32_t len, int64_t row,
+                                        int64_t pos, int head) {
+    const int lane = threadIdx.x & 31;
+    const int kv_head = head / t.group;
+    const uint16_t* q = reinterpret_cast<const uint16_t*>(t.q + row * t.q_token + (int64_t)head * t.q_head);
+    float qv[4], acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) qv[i] = lane + 32 * i < a.dim ? T::load(q[lane + 32 * i]) : 0.f;
+    int32_t first, last;
+    visible_range(t, len, pos, first, last);
+    float m = -INFINITY, sum = 0.f;
+    for (int pass = 0; pass < 3; ++pass) {
+        for (int32_t j = first; j < last; ++j) {
+            int64_t at, scale_at;
+            const bool there = slot_of(a, b, (uint32_t)j, at, scale_at);
+            float s = 0.f, kscale = 1.f, vscale = 1.f;
+            if (there) {
+                const uint8_t* kv = a.k + at + (int64_t)kv_head * a.head_stride;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (lane + 32 * i < a.dim) s += qv[i] * stored_value<T, FMT>(kv, lane + 32 * i);
+                if (FMT != kKv16Bit) {
+                    kscale = a.k_scale[scale_at + (int64_t)kv_head * a.s_head];
+                    vscale = a.v_scale[scale_at + (int64_t)kv_head * a.s_head];
+                }
+            }
+            s = warp_sum(s) * kscale * t.scale;
+            if (pass == 0) {
+                m = (s > m || s != s) ? s : m;  // keeps a NaN: no later s compares above it
+                if (m != m) break;
+            } else if (pass == 1) {
+                sum += expf(s - m);
+            } else {
+                const float p = expf(s - m) / sum;
+                if (there) {
+                    const uint8_t* vv = a.v + at + (int64_t)kv_head * a.head_stride;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (lane + 32 * i < a.dim) acc[i] += p * (stored_value<T, FMT>(vv, lane + 32 * i) * vscale);
+                }
+            }
+        }
+    }
+    uint16_t* out = reinterpret_cast<uint16_t*>(t.out + row * t.o_token + (int64_t)head * t.o_head);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (lane + 32 * i < a.dim) out[lane + 32 * i] = T::round(acc[i]);
+    if (t.lse != nullptr && lane == 0) t.lse[row * t.q_heads + head] = last > first ? m + logf(sum) : -INFINITY;
+}
+
+}  // namespace cccl

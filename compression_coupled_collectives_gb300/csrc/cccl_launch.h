@@ -29,6 +29,9 @@ class PerDeviceOnce {
     std::atomic<uint64_t> done_{0};
 };
 
+// True if [p, p + bytes) lies inside one device (or managed) allocation.
+bool device_range(const void* p, size_t bytes);
+
 constexpr int kMaxRanks = 64;
 
 // Rank r's operand: the compressed stream in[r] of in_bytes[r] bytes, except
