@@ -71,7 +71,7 @@ struct Sequence {
 __device__ __forceinline__ Sequence load_sequence(const KvArgs& a, int b) {
     const int64_t lo = a.cu[b], hi = a.cu[b + 1];
     const int64_t len = a.lens[b];
-    const int64_t cap = min((int64_t)a.table_pages * a.page_tokens.d, (int64_t)0x7FFFFF00);
+    const int64_t cap = min((int64_t)a.table_pages * a.page_tokens.d, (int64_t)0x7FFF0000);
     Sequence s;
     s.row = min(max(lo, (int64_t)0), a.n_tokens);
     const int64_t end = min(max(hi, s.row), a.n_tokens);
@@ -113,10 +113,12 @@ __device__ __forceinline__ void visible_range(const AttnArgs& t, int32_t len, in
 // ---------------------------------------------------------------- values
 // The two 16-bit types: bf16 and fp16 as the packed values' type.
 struct BfType {
+    static constexpr bool kHalf = false;
     static __device__ __forceinline__ float load(uint16_t b) { return __uint_as_float((uint32_t)b << 16); }
     static __device__ __forceinline__ uint16_t round(float x) { return __bfloat16_as_ushort(__float2bfloat16_rn(x)); }
 };
 struct HfType {
+    static constexpr bool kHalf = true;
     static __device__ __forceinline__ float load(uint16_t b) { return __half2float(__ushort_as_half(b)); }
     static __device__ __forceinline__ uint16_t round(float x) { return __half_as_ushort(__float2half_rn(x)); }
 };

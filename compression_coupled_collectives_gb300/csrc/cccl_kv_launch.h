@@ -16,6 +16,10 @@ cudaError_t launch_kv_write(int dtype, int format, const KvArgs& a, const KvPack
 cudaError_t launch_kv_read(int dtype, int format, const KvArgs& a, const KvPacked& x, cudaStream_t stream);
 cudaError_t launch_kv_attention(int dtype, int format, const KvArgs& a, const AttnArgs& t, int max_new, int max_len,
                                 cudaStream_t stream);
+// The kernel for few rows a kv head, and its workspace bytes after the header.
+cudaError_t launch_kv_tokens(int dtype, int format, const KvArgs& a, const AttnArgs& t, int max_len,
+                             cudaStream_t stream);
+size_t kv_tokens_scratch(int dim);
 // Workspace bytes of an attention call after the 16-byte header.
 size_t kv_attention_scratch(int dim, int group, int max_new, int max_len);
 

@@ -1,0 +1,300 @@
+// cccl_kv_schedule.cuh -- how attention's work is divided among thread blocks.
+//
+// Item: one sequence, one kv head and one tile of ROWS rows (a row is a new
+// token and one of the `group` query heads that share the kv head, tokens
+// outermost).  An item walks the cached tokens that any of its rows sees, in
+// tiles of TOKENS aligned to multiples of TOKENS; one that sees none still
+// counts as one tile, so that its zeros get written.  All items' tiles form
+// one line, sequence by sequence, head by head, row tile by row tile, and each
+// of C blocks takes an equal share of the line: sequences of any lengths load
+// the GPU evenly, and one sequence's long context is shared by many blocks.
+// An item that a share's end cuts leaves partial results (an unnormalised
+// accumulator, its maximum and its sum for each row) that a second kernel
+// joins, in the order of the line, so that results do not vary.
+//
+// The lengths are in device memory, so every block works the division out
+// itself (a few loads a sequence).
+#pragma once
+
+#include "cccl_kv.cuh"
+
+namespace cccl {
+
+constexpr int kMaxBatch = 1024;  // CCCL_KV_MAX_BATCH
+
+// Row tile rt of a sequence: its visible tiles.
+struct TileRange {
+    int32_t first, last;  // visible tokens of any row: first .. last - 1
+    int32_t lo, n;        // tiles lo .. lo + n - 1 (n >= 1)
+};
+template <int ROWS, int TOKENS>
+__device__ __forceinline__ TileRange tile_range(const AttnArgs& t, const Sequence& s, int32_t rt) {
+    const int64_t rows = (int64_t)s.n * t.group;
+    const int64_t i0 = ((int64_t)rt * ROWS) / t.group;
+    const int64_t i1 = (min((int64_t)(rt + 1) * ROWS, rows) - 1) / t.group;
+    const int64_t base = (int64_t)s.len - s.n;
+    TileRange r;
+    int32_t ignore;
+    visible_range(t, s.len, base + i0, r.first, ignore);
+    visible_range(t, s.len, base + i1, ignore, r.last);
+    if (r.first >= r.last) {
+        r.first = r.last = r.lo = 0;
+        r.n = 1;
+    } else {
+        r.lo = r.first / TOKENS;
+        r.n = (r.last + TOKENS - 1) / TOKENS - r.lo;
+    }
+    return r;
+}
+template <int ROWS>
+__device__ __forceinline__ int32_t row_tiles(const AttnArgs& t, const Sequence& s) {
+    return (int32_t)(((int64_t)s.n * t.group + ROWS - 1) / ROWS);
+}
+
+// Block-wide: prefix[b] = tiles before sequence b on the line, prefix[batch] =
+// all.  Ends with a barrier.  A sequence's rows must lie below 2^31 times ROWS.
+template <int ROWS, int TOKENS>
+__device__ __forceinline__ void build_prefix(const KvArgs& a, const AttnArgs& t, uint64_t* prefix) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+    for (int b = warp; b < a.batch; b += warps) {
+        const Sequence s = load_sequence(a, b);
+        const int32_t rts = row_tiles<ROWS>(t, s);
+        uint64_t sum = 0;
+        for (int32_t rt = lane; rt < rts; rt += 32) sum += (uint64_t)tile_range<ROWS, TOKENS>(t, s, rt).n;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+        if (lane == 0) prefix[b + 1] = sum * (uint64_t)a.kv_heads;
+    }
+    __syncthreads();
+    if (warp == 0) {
+        uint64_t carry = 0;
+        for (int base = 0; base < a.batch; base += 32) {
+            const int b = base + lane;
+            uint64_t x = b < a.batch ? prefix[b + 1] : 0;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint64_t y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+                if (lane >= o) x += y;
+            }
+            if (b < a.batch) prefix[b + 1] = carry + x;
+            carry += __shfl_sync(0xFFFFFFFFu, x, 31);
+        }
+        if (lane == 0) prefix[0] = 0;
+    }
+    __syncthreads();
+}
+
+// One block's part of one item.
+struct Piece {
+    Sequence seq;
+    TileRange range;
+    int32_t b, kv_head, rt;
+    uint64_t item;        // the item's start on the line
+    int32_t from, count;  // its tiles range.lo + from .. + count - 1
+};
+
+// The item that holds place x of the line.
+template <int ROWS, int TOKENS>
+__device__ __forceinline__ void find_item(const KvArgs& a, const AttnArgs& t, const uint64_t* prefix, uint64_t x,
+                                          Piece& p) {
+    int lo = 0, hi = a.batch;  // prefix[lo] <= x < prefix[hi]
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (prefix[mid] <= x)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    p.b = lo;
+    p.seq = load_sequence(a, lo);
+    const uint64_t per_head = (prefix[lo + 1] - prefix[lo]) / (uint64_t)a.kv_heads;
+    const uint64_t r = x - prefix[lo];
+    p.kv_head = (int32_t)(r / per_head);
+    uint64_t start = prefix[lo] + (uint64_t)p.kv_head * per_head;
+    const int32_t rts = row_tiles<ROWS>(t, p.seq);
+    p.rt = 0;
+    p.range = tile_range<ROWS, TOKENS>(t, p.seq, 0);
+    while (p.rt + 1 < rts && x >= start + (uint64_t)p.range.n) {
+        start += (uint64_t)p.range.n;
+        ++p.rt;
+        p.range = tile_range<ROWS, TOKENS>(t, p.seq, p.rt);
+    }
+    p.item = start;
+}
+
+// Share c of C of a line of T tiles begins here (T < 2^48).
+__device__ __forceinline__ uint64_t share_start(uint64_t T, uint32_t c, uint32_t C) { return T * c / C; }
+
+// What the joining kernel needs to know about the end of share c - 1 (the
+// start of share c): whether an item is cut there for the first time, and
+// which shares hold its parts: the last part of share c - 1, then the first
+// part of shares c .. last.
+struct Cut {
+    int32_t b, kv_head, rt, last;  // last < 0: nothing to join here
+};
+// Written by block c (one thread) for its first piece.
+template <int ROWS, int TOKENS>
+__device__ __forceinline__ Cut cut_of(const Piece& p, uint64_t x0, uint64_t T, uint32_t c, uint32_t C) {
+    Cut u{p.b, p.kv_head, p.rt, -1};
+    if (c > 0 && p.item < x0 && share_start(T, c - 1, C) <= p.item) {
+        const uint64_t end = p.item + (uint64_t)p.range.n;
+        uint32_t last = c;
+        while (last + 1 < C && share_start(T, last + 1, C) < end) ++last;
+        u.last = (int32_t)last;
+    }
+    return u;
+}
+
+// Partial results in the workspace, after the header: C cuts, then two parts
+// for each share, ROWS * (dim + 2) floats each: per row the accumulator, then
+// the maximum (base 2) and the sum of every row.
+struct PartLayout {
+    Cut* cuts;
+    float* parts;
+    int32_t rows, dim;
+    __device__ __forceinline__ float* acc(uint32_t share, int which) const {
+        return parts + ((size_t)share * 2 + which) * (size_t)rows * (dim + 2);
+    }
+    __device__ __forceinline__ float* stats(uint32_t share, int which) const {
+        return acc(share, which) + (size_t)rows * dim;
+    }
+};
+__device__ __forceinline__ PartLayout part_layout(const KvArgs& a, int shares, int rows) {
+    uint8_t* p = reinterpret_cast<uint8_t*>(a.ws) + sizeof(WsHeader);
+    return PartLayout{reinterpret_cast<Cut*>(p), reinterpret_cast<float*>(p + (size_t)shares * sizeof(Cut)), rows,
+                      a.dim};
+}
+inline size_t part_bytes(int shares, int rows, int dim) {
+    return (size_t)shares * (sizeof(Cut) + 2 * (size_t)rows * (size_t)(dim + 2) * sizeof(float));
+}
+
+// Row `row` of an item's tile: its place in the packed tensors.
+struct RowPlace {
+    int64_t token;  // row of the packed tensors
+    int64_t pos;    // position in the sequence
+    int32_t head;   // query head
+};
+__device__ __forceinline__ RowPlace row_place(const AttnArgs& t, const Piece& p, int rows, int row) {
+    const int64_t r = (int64_t)p.rt * rows + row, i = r / t.group;
+    return RowPlace{p.seq.row + i, (int64_t)p.seq.len - p.seq.n + i, (int32_t)(p.kv_head * t.group + (r - i * t.group))};
+}
+// Values d .. d + 7 of a finished row: v / sum, and with d = 0 its log-sum-exp
+// (m in base 2).  True when something is not finite, though the row sees keys:
+// the row is then worked out by fix_row.
+template <class T>
+__device__ __forceinline__ bool store_row_part(const AttnArgs& t, const Piece& p, int rows, int row, int d,
+                                               const float* v, float m, float sum) {
+    const RowPlace at = row_place(t, p, rows, row);
+    int32_t first, last;
+    visible_range(t, p.seq.len, at.pos, first, last);
+    const bool none = last <= first;
+    const float inv = none ? 0.f : 1.f / sum;
+    float y[8];
+    bool odd = false;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        y[i] = none ? 0.f : v[i] * inv;
+        odd |= !(fabsf(y[i]) <= 3.402823466e+38f);
+    }
+    const uint4 w = make_uint4(round_pair<T>(y[0], y[1]), round_pair<T>(y[2], y[3]), round_pair<T>(y[4], y[5]),
+                               round_pair<T>(y[6], y[7]));
+    *reinterpret_cast<uint4*>(t.out + at.token * t.o_token + (int64_t)at.head * t.o_head + 2 * d) = w;
+    if (d == 0 && t.lse != nullptr)
+        t.lse[at.token * t.q_heads + at.head] = none ? -INFINITY : (m + log2f(sum)) * 0.6931471805599453f;
+    return odd;
+}
+// One warp: the row from the definition.
+template <class T, int FMT>
+__device__ __forceinline__ void fix_row(const KvArgs& a, const AttnArgs& t, const Piece& p, int rows, int row) {
+    const RowPlace at = row_place(t, p, rows, row);
+    attend_row<T, FMT>(a, t, p.b, p.seq.len, at.token, at.pos, at.head);
+}
+
+// Joins the parts of the item cut at the start of share blockIdx.x: 4 rows a
+// block, 4 values a thread.  Parts are taken in the order of the line.
+constexpr int kJoinRows = 4, kJoinThreads = 128;
+constexpr int kMaxShares = 304;
+template <class T, int FMT, int ROWS>
+__global__ void __launch_bounds__(kJoinThreads) join_parts_kernel(const __grid_constant__ KvArgs a,
+                                                                  const __grid_constant__ AttnArgs t, int shares) {
+    __shared__ float weight[kJoinRows][kMaxShares + 1];
+    __shared__ float total[kJoinRows], top[kJoinRows];
+    __shared__ uint32_t odd_rows;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const PartLayout parts = part_layout(a, shares, ROWS);
+    const Cut cut = parts.cuts[blockIdx.x];
+    if (cut.last < 0) return;
+    Piece p;
+    p.b = cut.b;
+    p.kv_head = cut.kv_head;
+    p.rt = cut.rt;
+    p.seq = load_sequence(a, cut.b);
+    const int row0 = blockIdx.y * kJoinRows;
+    const int live = (int)min((int64_t)ROWS, (int64_t)p.seq.n * t.group - (int64_t)p.rt * ROWS) - row0;
+    if (live <= 0) return;
+    const int first = (int)blockIdx.x - 1, n = cut.last - first + 1;
+    if (threadIdx.x == 0) odd_rows = 0;
+    for (int i = threadIdx.x; i < n * kJoinRows; i += kJoinThreads) {
+        const int part = i / kJoinRows, r = i % kJoinRows;
+        if (r < live) weight[r][part] = parts.stats(first + part, part == 0 ? 1 : 0)[row0 + r];
+    }
+    __syncthreads();
+    const int r = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (r < live) {
+        float m = -INFINITY;
+        for (int i = lane; i < n; i += 32) m = fmaxf(m, weight[r][i]);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+        const float from = m == -INFINITY ? 0.f : m;
+        float sum = 0.f;
+        for (int i = lane; i < n; i += 32) {
+            const float f = exp2f(weight[r][i] - from);
+            sum += f * parts.stats(first + i, i == 0 ? 1 : 0)[ROWS + row0 + r];
+            weight[r][i] = f;
+        }
+        sum = warp_sum(sum);
+        if (lane == 0) {
+            total[r] = sum;
+            top[r] = m;
+        }
+    }
+    __syncthreads();
+    if (r < live && 4 * lane < a.dim) {
+        float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll 8
+        for (int i = 0; i < n; ++i) {
+            const float4 x = *reinterpret_cast<const float4*>(parts.acc(first + i, i == 0 ? 1 : 0) +
+                                                              (size_t)(row0 + r) * a.dim + 4 * lane);
+            const float f = weight[r][i];
+            v[0] += f * x.x;
+            v[1] += f * x.y;
+            v[2] += f * x.z;
+            v[3] += f * x.w;
+        }
+        // pairs of lanes hold 8 values together: the even one stores them
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[4 + i] = __shfl_down_sync(__activemask(), v[i], 1);
+        if ((lane & 1) == 0 && store_row_part<T>(t, p, ROWS, row0 + r, 4 * lane, v, top[r], total[r]))
+            atomicOr(&odd_rows, 1u << r);
+    }
+    __syncthreads();
+    if (r < live && (odd_rows >> r & 1u)) fix_row<T, FMT>(a, t, p, ROWS, row0 + r);
+}
+
+// Launched so that its blocks may start while the kernel before it still runs;
+// they wait for its end before they read.
+template <class T, int FMT, int ROWS>
+cudaError_t launch_join(const KvArgs& a, const AttnArgs& t, int shares, cudaStream_t s) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)shares, ROWS / kJoinRows);
+    cfg.blockDim = dim3(kJoinThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, join_parts_kernel<T, FMT, ROWS>, a, t, shares);
+}
+
+}  // namespace cccl

@@ -1,0 +1,607 @@
+// cccl_kv_tokens.cu -- attention of few rows a kv head (single tokens, short
+// drafts): the cache is read once and everything else is small, so the kernel
+// is built around the loads.
+//
+// An item is up to 16 rows (new tokens x the query heads that share a kv
+// head).  Each of a block's four warps takes TS consecutive cached tokens of
+// every tile and runs on its own: its ring of stages filled by its own 16-byte
+// asynchronous copies (page lookups one stage ahead of the copies), scores and
+// values by mma.sync with the 16 rows as M, its own running maximum, sum and
+// accumulator in registers.  The four meet once, at the end of an item.
+// tcgen05 is not used here: its M is 128 rows, of which at most 16 would be
+// real, and the tensor work is a few percent of the time anyway.
+//
+// Precision: products of 16-bit values are exact and summed in binary32.  A
+// probability enters the second product as the sum of two 16-bit values (high
+// part and remainder), so nothing is rounded before the result.  8-bit codes
+// are exact in 16 bits; the key's scale multiplies the score and the value's
+// scale the probability, both in binary32 (probabilities then in bf16 pairs,
+// whose exponents hold any scale).
+#include <type_traits>
+
+#include "cccl_kv.cuh"
+#include "cccl_kv_launch.h"
+#include "cccl_kv_schedule.cuh"
+#include "cccl_launch.h"
+
+namespace cccl {
+
+namespace {
+
+constexpr int kRows = 16, kWarps = 4, kThreads = 32 * kWarps;
+constexpr int kBlocksPerSm = 2;
+constexpr int kSms = 152;
+constexpr int kShares = kSms * kBlocksPerSm;
+
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool real) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(real ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t dst, const void* src, bool real) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(real ? 4 : 0) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ldsm4(uint32_t a, uint32_t* r) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(a));
+}
+__device__ __forceinline__ void ldsm4_trans(uint32_t a, uint32_t* r) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(a));
+}
+__device__ __forceinline__ uint4 lds16(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ uint2 lds8(uint32_t a) {
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+    return v;
+}
+template <class T>
+__device__ __forceinline__ void mma16816(float* d, const uint32_t* a, uint32_t b0, uint32_t b1);
+template <>
+__device__ __forceinline__ void mma16816<BfType>(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+template <>
+__device__ __forceinline__ void mma16816<HfType>(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// (hi, lo) with x ~ hi + lo in two 16-bit values each: two probabilities at a time
+template <class T>
+__device__ __forceinline__ void split_pair(float x, float y, uint32_t& hi, uint32_t& lo) {
+    hi = round_pair<T>(x, y);
+    lo = round_pair<T>(x - T::load((uint16_t)(hi & 0xFFFFu)), y - T::load((uint16_t)(hi >> 16)));
+}
+
+// Sizes of the instance for values of T in format FMT and heads of up to DP.
+template <class T_, int FMT_, int DP_>
+struct Shape {
+    using T = T_;
+    using P = typename std::conditional<FMT_ == kKv16Bit, T_, BfType>::type;  // probabilities
+    static constexpr int FMT = FMT_, DP = DP_;
+    static constexpr int kElem = FMT == kKv16Bit ? 2 : 1;
+    static constexpr int kRowBytes = DP * kElem;                      // 64, 128 or 256
+    static constexpr int kTokens = kRowBytes == 256 ? 16 : 32;        // tokens of a warp's stage
+    static constexpr int kTile = kWarps * kTokens;                    // tokens of a block's tile
+    static constexpr int kSide = kTokens * kRowBytes;                 // bytes of K (or V) in a stage
+    static constexpr int kScaleBytes = FMT == kKv16Bit ? 0 : 8 * kTokens;
+    static constexpr int kStage = 2 * kSide + kScaleBytes;
+    static constexpr int kStages = kSide >= 4096 ? 3 : 5;
+    static constexpr int kRing = kStages * kStage;                    // bytes of a warp's ring
+    static constexpr int kMerge = kWarps * kRows * (DP + 4) * 4;      // accumulators at the end of an item
+    static constexpr int kSmem = kWarps * kRing > kMerge ? kWarps * kRing : kMerge;
+};
+
+// Where 16-byte chunk c of row r lies in a stage's K or V.  The swizzles spread
+// what one quarter-warp reads together over all banks: eight rows of one chunk
+// (ldmatrix), or rows r, r + 1 of four chunks (K codes), or rows 0, 2, 4, 6 of
+// two chunks (V codes; two-way conflicts remain at 64-byte rows).
+template <class S, bool V>
+__device__ __forceinline__ uint32_t chunk_at(uint32_t r, uint32_t c) {
+    if (S::FMT == kKv16Bit) return r * S::kRowBytes + ((c ^ (r & 7)) << 4);
+    if (V) return r * S::kRowBytes + ((c ^ (((r >> 1) << 1) & (S::kRowBytes / 16 - 1))) << 4);
+    if (S::kRowBytes == 128) return r * S::kRowBytes + ((c ^ ((r & 1) << 2)) << 4);
+    return r * S::kRowBytes + (c << 4);
+}
+
+// 4 codes -> 16-bit values of type T, exactly, as two pairs: E4M3 in the order
+// (0, 1), (2, 3), INT8 in the order (0, 2), (1, 3) (the cheaper one for each;
+// callers arrange the other operand or the bytes to suit).
+//   INT8 to bf16: with L = the low 7 bits, 0x4300 | L is 128 + L; taking off
+//   0x4300 | (sign bit) = 128 or 256 leaves L or L - 128, the code.
+//   INT8 to fp16: with u = code + 128, 0x6400 | u is 1024 + u; taking off 1152
+//   leaves the code.
+template <class T, int FMT>
+__device__ __forceinline__ void expand4(uint32_t w, uint32_t& a, uint32_t& b) {
+    if (FMT == kKvE4m3) {
+        uint32_t h0, h1;
+        asm("{ .reg .b16 l, h; mov.b32 {l, h}, %2; cvt.rn.f16x2.e4m3x2 %0, l; cvt.rn.f16x2.e4m3x2 %1, h; }"
+            : "=r"(h0), "=r"(h1)
+            : "r"(w));
+        if (T::kHalf) {
+            a = h0;
+            b = h1;
+        } else {
+            const float2 x = __half22float2(*reinterpret_cast<__half2*>(&h0));
+            const float2 y = __half22float2(*reinterpret_cast<__half2*>(&h1));
+            a = round_pair<T>(x.x, x.y);
+            b = round_pair<T>(y.x, y.y);
+        }
+    } else if (T::kHalf) {
+        const uint32_t u = w ^ 0x80808080u;
+        const uint32_t x = (u & 0x00FF00FFu) | 0x64006400u, y = ((u >> 8) & 0x00FF00FFu) | 0x64006400u;
+        const __half2 bias = __half2half2(__ushort_as_half(0x6480));  // 1152
+        const __half2 p = __hsub2(*reinterpret_cast<const __half2*>(&x), bias);
+        const __half2 q = __hsub2(*reinterpret_cast<const __half2*>(&y), bias);
+        a = *reinterpret_cast<const uint32_t*>(&p);
+        b = *reinterpret_cast<const uint32_t*>(&q);
+    } else {
+        const uint32_t v = w >> 8;
+        const uint32_t x = (w & 0x007F007Fu) | 0x43004300u, xs = (w & 0x00800080u) | 0x43004300u;
+        const uint32_t y = (v & 0x007F007Fu) | 0x43004300u, ys = (v & 0x00800080u) | 0x43004300u;
+        const __nv_bfloat162 p = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&x),
+                                         *reinterpret_cast<const __nv_bfloat162*>(&xs));
+        const __nv_bfloat162 q = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&y),
+                                         *reinterpret_cast<const __nv_bfloat162*>(&ys));
+        a = *reinterpret_cast<const uint32_t*>(&p);
+        b = *reinterpret_cast<const uint32_t*>(&q);
+    }
+}
+
+// Where row r of a stage lies in the cache (lane r knows).
+struct RowAt {
+    int64_t at, scale_at;
+    bool real;  // false: outside what the item sees, or in no page of the cache
+};
+template <class S>
+__device__ __forceinline__ RowAt look_up(const KvArgs& a, const Piece& p, int32_t base) {
+    const int32_t pos = base + (int)(threadIdx.x & 31);
+    RowAt r{0, 0, false};
+    if ((int)(threadIdx.x & 31) < S::kTokens && pos >= p.range.first && pos < p.range.last) {
+        r.real = slot_of(a, p.b, (uint32_t)pos, r.at, r.scale_at);
+        if (!r.real) r.at = r.scale_at = 0;
+    }
+    r.at += (int64_t)p.kv_head * a.head_stride;
+    r.scale_at += (int64_t)p.kv_head * a.s_head;
+    return r;
+}
+// This warp's copies of one stage; rows that are not real become zeros.
+template <class S>
+__device__ __forceinline__ void issue_stage(const KvArgs& a, uint32_t stage, const RowAt& r) {
+    const int lane = threadIdx.x & 31;
+    constexpr int kChunks = S::kRowBytes / 16, kPerPass = 32 / kChunks;
+    const int chunk = lane % kChunks;
+    const bool inside = chunk * 16 < a.dim * S::kElem;
+#pragma unroll
+    for (int i = 0; i < S::kTokens / kPerPass; ++i) {
+        const int row = i * kPerPass + lane / kChunks;
+        const int64_t at = __shfl_sync(0xFFFFFFFFu, r.at, row);
+        const bool real = __shfl_sync(0xFFFFFFFFu, (int)r.real, row) != 0 && inside;
+        const int64_t off = real ? at + chunk * 16 : 0;
+        copy16(stage + chunk_at<S, false>(row, chunk), a.k + off, real);
+        copy16(stage + S::kSide + chunk_at<S, true>(row, chunk), a.v + off, real);
+    }
+    if (S::FMT != kKv16Bit && lane < S::kTokens) {
+        copy4(stage + 2 * S::kSide + 4 * lane, a.k_scale + r.scale_at, r.real);
+        copy4(stage + 2 * S::kSide + 4 * S::kTokens + 4 * lane, a.v_scale + r.scale_at, r.real);
+    }
+}
+
+// The query fragments of rows g and g + 8 (zeros where there is no such row).
+template <class S>
+__device__ __forceinline__ void load_queries(const KvArgs& a, const AttnArgs& t, const Piece& p, uint32_t (*q)[4]) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+    const int64_t rows = (int64_t)p.seq.n * t.group;
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+        const int64_t r = (int64_t)p.rt * kRows + g + 8 * half;
+        const bool real = r < rows;
+        const int64_t i = real ? r / t.group : 0, h = real ? r - i * t.group : 0;
+        const uint8_t* src = t.q + (p.seq.row + i) * t.q_token + ((int64_t)p.kv_head * t.group + h) * t.q_head;
+#pragma unroll
+        for (int ks = 0; ks < S::DP / 16; ++ks) {
+            uint32_t lo = 0, hi = 0;
+            if (S::FMT == kKv16Bit) {
+                if (real && 16 * ks < a.dim) {
+                    lo = *reinterpret_cast<const uint32_t*>(src + 2 * (16 * ks + 2 * c));
+                    hi = *reinterpret_cast<const uint32_t*>(src + 2 * (16 * ks + 2 * c + 8));
+                }
+            } else {
+                const int d = 64 * (ks / 4) + 16 * c + 4 * (ks % 4);
+                uint2 w = make_uint2(0, 0);
+                if (real && d < a.dim) w = *reinterpret_cast<const uint2*>(src + 2 * d);
+                lo = S::FMT == kKvE4m3 ? w.x : __byte_perm(w.x, w.y, 0x5410);
+                hi = S::FMT == kKvE4m3 ? w.y : __byte_perm(w.x, w.y, 0x7632);
+            }
+            q[ks][half] = lo;
+            q[ks][2 + half] = hi;
+        }
+    }
+}
+
+// Scores of the stage's tokens, before any scale.
+template <class S>
+__device__ __forceinline__ void scores(uint32_t stage, const uint32_t (*q)[4], float (*s)[4]) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int nt = 0; nt < S::kTokens / 8; ++nt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[nt][i] = 0.f;
+    if (S::FMT == kKv16Bit) {
+#pragma unroll
+        for (int ks = 0; ks < S::DP / 16; ++ks)
+#pragma unroll
+            for (int np = 0; np < S::kTokens / 16; ++np) {
+                uint32_t r[4];
+                ldsm4(stage + chunk_at<S, false>(16 * np + (lane & 7) + ((lane >> 4) << 3), 2 * ks + ((lane >> 3) & 1)),
+                      r);
+                mma16816<typename S::T>(s[2 * np], q[ks], r[0], r[1]);
+                mma16816<typename S::T>(s[2 * np + 1], q[ks], r[2], r[3]);
+            }
+    } else {
+#pragma unroll
+        for (int nt = 0; nt < S::kTokens / 8; ++nt)
+#pragma unroll
+            for (int h = 0; h < S::DP / 64; ++h) {
+                const uint4 v = lds16(stage + chunk_at<S, false>(8 * nt + (lane >> 2), 4 * h + (lane & 3)));
+                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    uint32_t b0, b1;
+                    expand4<typename S::T, S::FMT>(w[j], b0, b1);
+                    mma16816<typename S::T>(s[nt], q[4 * h + j], b0, b1);
+                }
+            }
+    }
+}
+
+// acc += p v over the stage's tokens; p as the fragments of its two parts.
+template <class S>
+__device__ __forceinline__ void values(uint32_t stage, const uint32_t (*hi)[4], const uint32_t (*lo)[4],
+                                       float (*acc)[4]) {
+    const int lane = threadIdx.x & 31;
+    const uint32_t v = stage + S::kSide;
+#pragma unroll
+    for (int kt = 0; kt < S::kTokens / 16; ++kt) {
+        if (S::FMT == kKv16Bit) {
+#pragma unroll
+            for (int j = 0; j < S::DP / 8; j += 2) {
+                uint32_t r[4];
+                ldsm4_trans(v + chunk_at<S, true>(16 * kt + (lane & 15), j + (lane >> 4)), r);
+                mma16816<typename S::T>(acc[j], hi[kt], r[0], r[1]);
+                mma16816<typename S::T>(acc[j + 1], hi[kt], r[2], r[3]);
+                mma16816<typename S::T>(acc[j], lo[kt], r[0], r[1]);
+                mma16816<typename S::T>(acc[j + 1], lo[kt], r[2], r[3]);
+            }
+        } else {
+            // lane (g, c): tokens 2c, 2c + 1, 2c + 8, 2c + 9, DP / 8 values from g DP / 8 on
+            const int g = lane >> 2, c = lane & 3;
+            uint32_t w[4][S::DP / 32];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t row = 16 * kt + 2 * c + (i & 1) + 8 * (i >> 1);
+                if (S::DP == 128) {
+                    const uint4 x = lds16(v + chunk_at<S, true>(row, g));
+                    w[i][0] = x.x;
+                    w[i][1] = x.y;
+                    w[i][S::DP / 32 - 2] = x.z;
+                    w[i][S::DP / 32 - 1] = x.w;
+                } else {
+                    const uint2 x = lds8(v + chunk_at<S, true>(row, g >> 1) + 8 * (g & 1));
+                    w[i][0] = x.x;
+                    w[i][1] = x.y;
+                }
+            }
+            // pairs of tokens at one channel: the byte order that expand4 pairs up
+            constexpr uint32_t kFirst = S::FMT == kKvE4m3 ? 0x5140 : 0x5410;
+            constexpr uint32_t kSecond = S::FMT == kKvE4m3 ? 0x7362 : 0x7632;
+#pragma unroll
+            for (int j = 0; j < S::DP / 32; ++j) {
+                uint32_t b0[4], b1[4];
+                expand4<BfType, S::FMT>(__byte_perm(w[0][j], w[1][j], kFirst), b0[0], b0[1]);
+                expand4<BfType, S::FMT>(__byte_perm(w[0][j], w[1][j], kSecond), b0[2], b0[3]);
+                expand4<BfType, S::FMT>(__byte_perm(w[2][j], w[3][j], kFirst), b1[0], b1[1]);
+                expand4<BfType, S::FMT>(__byte_perm(w[2][j], w[3][j], kSecond), b1[2], b1[3]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    mma16816<BfType>(acc[4 * j + i], hi[kt], b0[i], b1[i]);
+                    mma16816<BfType>(acc[4 * j + i], lo[kt], b0[i], b1[i]);
+                }
+            }
+        }
+    }
+}
+// Channel of column n (0..7) of accumulator tile j.
+template <class S>
+__device__ __forceinline__ int channel(int j, int n) {
+    return S::FMT == kKv16Bit ? 8 * j + n : n * (S::DP / 8) + j;
+}
+
+// The running state of rows g and g + 8 of an item.
+template <class S>
+struct Running {
+    float m[2], l[2];  // maximum (base 2) of the row; this lane's part of the sum
+    float acc[S::DP / 8][4];
+};
+
+// One stage: scores, the softmax's step, values.  base: the stage's first token.
+template <class S>
+__device__ __forceinline__ void step(const AttnArgs& t, const Piece& p, uint32_t stage, int32_t base,
+                                     const uint32_t (*q)[4], const int32_t* first, const int32_t* last, float to_base2,
+                                     Running<S>& st) {
+    const int lane = threadIdx.x & 31, c = lane & 3;
+    constexpr int NT = S::kTokens / 8;
+    float s[NT][4];
+    scores<S>(stage, q, s);
+    float vscale[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        float k0 = to_base2, k1 = to_base2;
+        if (S::FMT != kKv16Bit) {
+            const uint2 ks = lds8(stage + 2 * S::kSide + 4 * (8 * nt + 2 * c));
+            const uint2 vs = lds8(stage + 2 * S::kSide + 4 * S::kTokens + 4 * (8 * nt + 2 * c));
+            k0 *= __uint_as_float(ks.x);
+            k1 *= __uint_as_float(ks.y);
+            vscale[nt][0] = __uint_as_float(vs.x);
+            vscale[nt][1] = __uint_as_float(vs.y);
+        }
+        s[nt][0] *= k0;
+        s[nt][1] *= k1;
+        s[nt][2] *= k0;
+        s[nt][3] *= k1;
+    }
+    // hidden places: only where some row of this lane does not see the whole stage
+    if (base < max(first[0], first[1]) || base + S::kTokens > min(last[0], last[1])) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int32_t j = base + 8 * nt + 2 * c + (i & 1);
+                if (j < first[i >> 1] || j >= last[i >> 1]) s[nt][i] = -INFINITY;
+            }
+    }
+    uint32_t hi[NT / 2][4], lo[NT / 2][4];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        float m = st.m[h];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) m = fmaxf(m, fmaxf(s[nt][2 * h], s[nt][2 * h + 1]));
+        m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+        m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+        const float from = m == -INFINITY ? 0.f : m;  // nothing seen so far: every term is 0
+        const float keep = exp2_fast(st.m[h] - from);
+        st.m[h] = m;
+        float sum = 0.f;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            float x = exp2_fast(s[nt][2 * h] - from), y = exp2_fast(s[nt][2 * h + 1] - from);
+            sum += x + y;
+            if (S::FMT != kKv16Bit) {
+                x *= vscale[nt][0];
+                y *= vscale[nt][1];
+            }
+            using P = typename S::P;
+            split_pair<P>(x, y, hi[nt / 2][2 * (nt % 2) + h], lo[nt / 2][2 * (nt % 2) + h]);
+        }
+        st.l[h] = st.l[h] * keep + sum;
+#pragma unroll
+        for (int j = 0; j < S::DP / 8; ++j) {
+            st.acc[j][2 * h] *= keep;
+            st.acc[j][2 * h + 1] *= keep;
+        }
+    }
+    values<S>(stage, hi, lo, st.acc);
+}
+
+template <class S>
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm)
+    attend_tokens_kernel(const __grid_constant__ KvArgs a, const __grid_constant__ AttnArgs t, uint32_t min_tiles,
+                         int whole_items) {
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ uint64_t prefix[kMaxBatch + 1];
+    __shared__ float stats[2][kWarps][kRows];
+    __shared__ uint32_t odd_rows;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+    build_prefix<kRows, S::kTile>(a, t, prefix);
+    const uint64_t T = prefix[a.batch];
+    // no more shares than give each min_tiles tiles
+    const uint32_t shares = (uint32_t)min((uint64_t)gridDim.x, max((T + min_tiles - 1) / min_tiles, (uint64_t)1));
+    const PartLayout parts = part_layout(a, (int)gridDim.x, kRows);
+    const uint32_t share = blockIdx.x;
+    uint64_t x = share < shares ? share_start(T, share, shares) : T;
+    const uint64_t x0 = x, x1 = share < shares ? share_start(T, share + 1, shares) : T;
+    if (!whole_items && (x >= x1) && threadIdx.x == 0) parts.cuts[share].last = -1;
+    const float to_base2 = t.scale * 1.4426950408889634f;
+    const uint32_t ring = smem_addr(smem) + warp * S::kRing;
+    Piece p;
+    while (x < x1) {
+        find_item<kRows, S::kTile>(a, t, prefix, x, p);
+        const uint64_t end = p.item + (uint64_t)p.range.n;
+        if (whole_items) {
+            if (p.item < x) {  // the share before does all of it
+                x = end;
+                continue;
+            }
+            p.from = 0;
+            p.count = p.range.n;
+        } else {
+            p.from = (int32_t)(x - p.item);
+            p.count = (int32_t)(min(end, x1) - x);
+            if (x == x0 && threadIdx.x == 0) parts.cuts[share] = cut_of<kRows, S::kTile>(p, x0, T, share, shares);
+        }
+        const bool full = p.count == p.range.n;
+        const int which = p.from > 0 ? 0 : 1;
+        x += (uint64_t)p.count;
+
+        const int64_t rows = (int64_t)p.seq.n * t.group;
+        const int32_t live = (int32_t)min((int64_t)kRows, rows - (int64_t)p.rt * kRows);
+        int32_t first[2], last[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int64_t r = (int64_t)p.rt * kRows + g + 8 * h;
+            first[h] = last[h] = 0;
+            if (r < rows)
+                visible_range(t, p.seq.len, (int64_t)p.seq.len - p.seq.n + r / t.group, first[h], last[h]);
+        }
+        uint32_t q[S::DP / 16][4];
+        load_queries<S>(a, t, p, q);
+        Running<S> st;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) st.m[h] = -INFINITY, st.l[h] = 0.f;
+#pragma unroll
+        for (int j = 0; j < S::DP / 8; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) st.acc[j][i] = 0.f;
+
+        const int32_t base0 = (p.range.lo + p.from) * S::kTile + warp * S::kTokens;
+#pragma unroll
+        for (int i = 0; i < S::kStages - 1; ++i) {
+            if (i < p.count) issue_stage<S>(a, ring + i * S::kStage, look_up<S>(a, p, base0 + i * S::kTile));
+            copy_commit();
+        }
+        RowAt ahead = look_up<S>(a, p, base0 + (S::kStages - 1) * S::kTile);
+        int slot = 0, fill = S::kStages - 1;
+        for (int32_t i = 0; i < p.count; ++i) {
+            if (i + S::kStages - 1 < p.count) issue_stage<S>(a, ring + fill * S::kStage, ahead);
+            copy_commit();
+            fill = fill + 1 == S::kStages ? 0 : fill + 1;
+            ahead = look_up<S>(a, p, base0 + (i + S::kStages) * S::kTile);
+            copy_wait<S::kStages - 1>();
+            __syncwarp();
+            const int32_t base = base0 + i * S::kTile;
+            if (base < p.range.last && base + S::kTokens > p.range.first)
+                step<S>(t, p, ring + slot * S::kStage, base, q, first, last, to_base2, st);
+            slot = slot + 1 == S::kStages ? 0 : slot + 1;
+            __syncwarp();
+        }
+        copy_wait<0>();
+        // the four warps' parts meet in shared memory, over the rings
+        __syncthreads();
+        if (threadIdx.x == 0) odd_rows = 0;
+        float* merge = reinterpret_cast<float*>(smem);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            float l = st.l[h];
+            l += __shfl_xor_sync(0xFFFFFFFFu, l, 1);
+            l += __shfl_xor_sync(0xFFFFFFFFu, l, 2);
+            const int row = g + 8 * h;
+            if (row < live) {
+                if (c == 0) {
+                    stats[0][warp][row] = st.m[h];
+                    stats[1][warp][row] = l;
+                }
+#pragma unroll
+                for (int j = 0; j < S::DP / 8; ++j)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        merge[(warp * kRows + row) * (S::DP + 4) + channel<S>(j, 2 * c + i)] = st.acc[j][2 * h + i];
+            }
+        }
+        __syncthreads();
+        const int groups = a.dim / 8;
+        for (int w = threadIdx.x; w < live * groups; w += kThreads) {
+            const int row = w / groups, d = 8 * (w - row * groups);
+            float m = stats[0][0][row];
+#pragma unroll
+            for (int i = 1; i < kWarps; ++i) m = fmaxf(m, stats[0][i][row]);
+            const float from = m == -INFINITY ? 0.f : m;
+            float sum = 0.f, v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll
+            for (int i = 0; i < kWarps; ++i) {
+                const float f = exp2_fast(stats[0][i][row] - from);
+                sum += f * stats[1][i][row];
+                const float4* src = reinterpret_cast<const float4*>(&merge[(i * kRows + row) * (S::DP + 4) + d]);
+                const float4 lo = src[0], hi = src[1];
+                v[0] += f * lo.x;
+                v[1] += f * lo.y;
+                v[2] += f * lo.z;
+                v[3] += f * lo.w;
+                v[4] += f * hi.x;
+                v[5] += f * hi.y;
+                v[6] += f * hi.z;
+                v[7] += f * hi.w;
+            }
+            if (!full) {
+                float4* dst = reinterpret_cast<float4*>(parts.acc(share, which) + row * a.dim + d);
+                dst[0] = make_float4(v[0], v[1], v[2], v[3]);
+                dst[1] = make_float4(v[4], v[5], v[6], v[7]);
+                if (d == 0) {
+                    parts.stats(share, which)[row] = m;
+                    parts.stats(share, which)[kRows + row] = sum;
+                }
+                continue;
+            }
+            if (store_row_part<typename S::T>(t, p, kRows, row, d, v, m, sum)) atomicOr(&odd_rows, 1u << row);
+        }
+        __syncthreads();
+        if (full) {
+            for (uint32_t odd = odd_rows; odd != 0; odd &= odd - 1) {
+                const int row = __ffs(odd) - 1;
+                if (row % kWarps == warp) fix_row<typename S::T, S::FMT>(a, t, p, kRows, row);
+            }
+            __syncthreads();
+        }
+    }
+}
+
+template <class S>
+cudaError_t launch_tokens(const KvArgs& a, const AttnArgs& t, bool whole, uint32_t min_tiles, cudaStream_t s) {
+    static PerDeviceOnce once;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    e = once.run(dev, [] {
+        return cudaFuncSetAttribute(attend_tokens_kernel<S>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+    });
+    if (e != cudaSuccess) return e;
+    attend_tokens_kernel<S><<<kShares, kThreads, S::kSmem, s>>>(a, t, min_tiles, whole ? 1 : 0);
+    e = cudaGetLastError();
+    if (e != cudaSuccess || whole) return e;
+    return launch_join<typename S::T, S::FMT, kRows>(a, t, kShares, s);
+}
+
+template <class T, int FMT>
+cudaError_t launch_dim(const KvArgs& a, const AttnArgs& t, bool whole, uint32_t min_tiles, cudaStream_t s) {
+    return a.dim <= 64 ? launch_tokens<Shape<T, FMT, 64>>(a, t, whole, min_tiles, s)
+                       : launch_tokens<Shape<T, FMT, 128>>(a, t, whole, min_tiles, s);
+}
+
+}  // namespace
+
+size_t kv_tokens_scratch(int dim) { return part_bytes(kShares, kRows, dim); }
+
+cudaError_t launch_kv_tokens(int dtype, int format, const KvArgs& a, const AttnArgs& t, int max_len, cudaStream_t s) {
+    const bool whole = max_len <= 128;
+    const uint32_t min_tiles = 1;
+    if (dtype == (int)Bf16::kCode) {
+        if (format == kKv16Bit) return launch_dim<BfType, kKv16Bit>(a, t, whole, min_tiles, s);
+        return format == kKvInt8 ? launch_dim<BfType, kKvInt8>(a, t, whole, min_tiles, s)
+                                 : launch_dim<BfType, kKvE4m3>(a, t, whole, min_tiles, s);
+    }
+    if (format == kKv16Bit) return launch_dim<HfType, kKv16Bit>(a, t, whole, min_tiles, s);
+    return format == kKvInt8 ? launch_dim<HfType, kKvInt8>(a, t, whole, min_tiles, s)
+                             : launch_dim<HfType, kKvE4m3>(a, t, whole, min_tiles, s);
+}
+
+}  // namespace cccl
