@@ -13,7 +13,8 @@ CSRC = os.path.join(HERE, "csrc")
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libcccl.so")
 SOURCES = ["cccl_compress.cu", "cccl_decompress.cu", "cccl_reduce.cu", "cccl_api.cu",
-           "cccl_kv_api.cu", "cccl_kv_copy.cu", "cccl_kv_attention.cu", "cccl_kv_tokens.cu"]
+           "cccl_kv_api.cu", "cccl_kv_copy.cu", "cccl_kv_attention.cu", "cccl_kv_tokens.cu",
+           "cccl_kv_chunk.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
          "-I", os.path.join(ROOT, "include")]

@@ -30,12 +30,13 @@ cudaError_t rows_one(const KvArgs& a, const AttnArgs& t, cudaStream_t s) {
 }  // namespace
 
 size_t kv_attention_scratch(int dim, int group, int max_new, int) {
-    return (int64_t)group * max_new <= 16 ? kv_tokens_scratch(dim) : 0;
+    return (int64_t)group * max_new <= 16 ? kv_tokens_scratch(dim) : kv_chunk_scratch(dim);
 }
 
 cudaError_t launch_kv_attention(int dtype, int format, const KvArgs& a, const AttnArgs& t, int max_new, int max_len,
                                 cudaStream_t s) {
     if ((int64_t)t.group * max_new <= 16) return launch_kv_tokens(dtype, format, a, t, max_len, s);
+    if (format == kKv16Bit) return launch_kv_chunk(dtype, format, a, t, max_len, s);
     if (dtype == (int)Bf16::kCode) {
         if (format == kKv16Bit) return rows_one<BfType, kKv16Bit>(a, t, s);
         return format == kKvInt8 ? rows_one<BfType, kKvInt8>(a, t, s) : rows_one<BfType, kKvE4m3>(a, t, s);

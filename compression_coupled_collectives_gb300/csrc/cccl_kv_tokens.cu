@@ -33,22 +33,6 @@ constexpr int kBlocksPerSm = 2;
 constexpr int kSms = 152;
 constexpr int kShares = kSms * kBlocksPerSm;
 
-__device__ __forceinline__ float exp2_fast(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool real) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(real ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void copy4(uint32_t dst, const void* src, bool real) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(real ? 4 : 0) : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copy_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 __device__ __forceinline__ void ldsm4(uint32_t a, uint32_t* r) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -122,50 +106,6 @@ __device__ __forceinline__ uint32_t chunk_at(uint32_t r, uint32_t c) {
     if (V) return r * S::kRowBytes + ((c ^ (((r >> 1) << 1) & (S::kRowBytes / 16 - 1))) << 4);
     if (S::kRowBytes == 128) return r * S::kRowBytes + ((c ^ ((r & 1) << 2)) << 4);
     return r * S::kRowBytes + (c << 4);
-}
-
-// 4 codes -> 16-bit values of type T, exactly, as two pairs: E4M3 in the order
-// (0, 1), (2, 3), INT8 in the order (0, 2), (1, 3) (the cheaper one for each;
-// callers arrange the other operand or the bytes to suit).
-//   INT8 to bf16: with L = the low 7 bits, 0x4300 | L is 128 + L; taking off
-//   0x4300 | (sign bit) = 128 or 256 leaves L or L - 128, the code.
-//   INT8 to fp16: with u = code + 128, 0x6400 | u is 1024 + u; taking off 1152
-//   leaves the code.
-template <class T, int FMT>
-__device__ __forceinline__ void expand4(uint32_t w, uint32_t& a, uint32_t& b) {
-    if (FMT == kKvE4m3) {
-        uint32_t h0, h1;
-        asm("{ .reg .b16 l, h; mov.b32 {l, h}, %2; cvt.rn.f16x2.e4m3x2 %0, l; cvt.rn.f16x2.e4m3x2 %1, h; }"
-            : "=r"(h0), "=r"(h1)
-            : "r"(w));
-        if (T::kHalf) {
-            a = h0;
-            b = h1;
-        } else {
-            const float2 x = __half22float2(*reinterpret_cast<__half2*>(&h0));
-            const float2 y = __half22float2(*reinterpret_cast<__half2*>(&h1));
-            a = round_pair<T>(x.x, x.y);
-            b = round_pair<T>(y.x, y.y);
-        }
-    } else if (T::kHalf) {
-        const uint32_t u = w ^ 0x80808080u;
-        const uint32_t x = (u & 0x00FF00FFu) | 0x64006400u, y = ((u >> 8) & 0x00FF00FFu) | 0x64006400u;
-        const __half2 bias = __half2half2(__ushort_as_half(0x6480));  // 1152
-        const __half2 p = __hsub2(*reinterpret_cast<const __half2*>(&x), bias);
-        const __half2 q = __hsub2(*reinterpret_cast<const __half2*>(&y), bias);
-        a = *reinterpret_cast<const uint32_t*>(&p);
-        b = *reinterpret_cast<const uint32_t*>(&q);
-    } else {
-        const uint32_t v = w >> 8;
-        const uint32_t x = (w & 0x007F007Fu) | 0x43004300u, xs = (w & 0x00800080u) | 0x43004300u;
-        const uint32_t y = (v & 0x007F007Fu) | 0x43004300u, ys = (v & 0x00800080u) | 0x43004300u;
-        const __nv_bfloat162 p = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&x),
-                                         *reinterpret_cast<const __nv_bfloat162*>(&xs));
-        const __nv_bfloat162 q = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&y),
-                                         *reinterpret_cast<const __nv_bfloat162*>(&ys));
-        a = *reinterpret_cast<const uint32_t*>(&p);
-        b = *reinterpret_cast<const uint32_t*>(&q);
-    }
 }
 
 // Where row r of a stage lies in the cache (lane r knows).
