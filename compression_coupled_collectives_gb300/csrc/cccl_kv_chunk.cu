@@ -35,6 +35,13 @@ constexpr int kScaleSlots = 4;   // tiles of tokens whose scales are kept
 constexpr int kLoaderWarps = 4;
 constexpr float kSlack = 8.f;    // base 2
 
+// Registers of a thread: the launch's 4 x 128 a warpgroup, divided anew (two
+// softmax warpgroups, the loaders, and 64 for the issuing warp's).
+template <int FMT>
+constexpr int kSoftmaxRegs = FMT == kKv16Bit ? 192 : 176;
+template <int FMT>
+constexpr int kLoaderRegs = FMT == kKv16Bit ? 64 : 96;
+
 // TMEM columns
 constexpr uint32_t kColS = 0, kColO = 256;  // S of row tile i at 128 i (P over it), O at 256 + 128 i
 
@@ -45,7 +52,8 @@ struct Shared {
     uint32_t tmem;
     uint32_t stop;  // a bounded wait ran out: every role leaves
     uint64_t prefix[kMaxBatch + 1];
-    float k_scale[kScaleSlots][kTokens], v_scale[kScaleSlots][kTokens];
+    alignas(16) float k_scale[kScaleSlots][kTokens];
+    alignas(16) float v_scale[kScaleSlots][kTokens];
 };
 
 // ---------------------------------------------------------------- tcgen05
@@ -129,6 +137,13 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
     asm("fma.rn.f32x2 %0, %1, %2, %3;"
         : "=l"(reinterpret_cast<uint64_t&>(d))
         : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)), "l"(reinterpret_cast<uint64_t&>(c)));
+    return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 d;
+    asm("mul.rn.f32x2 %0, %1, %2;"
+        : "=l"(reinterpret_cast<uint64_t&>(d))
+        : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
     return d;
 }
 __device__ __forceinline__ float2 add2(float2 a, float2 b) {
@@ -231,12 +246,88 @@ __device__ __forceinline__ void copy_tile(const KvArgs& a, const uint8_t* data, 
     }
 }
 
+// 8-bit codes pass through registers: a lane takes 16 codes of a row at a time
+// and stores them as 16-bit values.  Lanes of a row's second half store their
+// two chunks the other way round, so that a row's eight lanes meet all banks.
+constexpr int kCodePasses = 8;  // 32 rows, at least 4 a pass
+struct Codes {
+    uint4 w[kCodePasses];
+};
+__device__ __forceinline__ void fetch_codes(const uint8_t* data, const TileRow& r, int lane, int chunks, Codes& c) {
+    const int per_row = chunks > 4 ? 8 : 4, rows_per_pass = 32 / per_row, chunk = lane % per_row;
+#pragma unroll
+    for (int i = 0; i < kCodePasses; ++i) {
+        c.w[i] = make_uint4(0, 0, 0, 0);
+        if (i < per_row) {
+            const int local = i * rows_per_pass + lane / per_row;
+            const int64_t at = __shfl_sync(0xFFFFFFFFu, r.at, local);
+            const bool real = __shfl_sync(0xFFFFFFFFu, (int)r.real, local) != 0;
+            if (real && chunk < chunks) c.w[i] = *reinterpret_cast<const uint4*>(data + at + 16 * chunk);
+        }
+    }
+}
+// power: the row's power of two (fp16 V), or 1.
+template <class T, int FMT, bool POWER>
+__device__ __forceinline__ void store_codes(const Codes& c, uint32_t slot, int warp, int lane, int chunks,
+                                            float power) {
+    const int per_row = chunks > 4 ? 8 : 4, rows_per_pass = 32 / per_row, chunk = lane % per_row;
+#pragma unroll
+    for (int i = 0; i < kCodePasses; ++i) {
+        if (i < per_row) {
+            const int local = i * rows_per_pass + lane / per_row;
+            const uint32_t w[4] = {c.w[i].x, c.w[i].y, c.w[i].z, c.w[i].w};
+            uint32_t v[8];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)  // in the row's order
+                expand4<T, FMT>(FMT == kKvInt8 ? __byte_perm(w[k], 0, 0x3120) : w[k], v[2 * k], v[2 * k + 1]);
+            if (POWER) {
+                const __half2 f = __float2half2_rn(__shfl_sync(0xFFFFFFFFu, power, local));
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const __half2 x = __hmul2(*reinterpret_cast<const __half2*>(&v[k]), f);
+                    v[k] = *reinterpret_cast<const uint32_t*>(&x);
+                }
+            }
+            if (chunk < chunks) {
+                const uint32_t row = 32 * warp + local;
+                const int second = chunk >> 2;  // which of the two goes first
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const int part = k ^ second;
+                    const uint32_t at = slot + swizzled(row, 2 * chunk + part);
+                    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(part ? v[4] : v[0]),
+                                 "r"(part ? v[5] : v[1]), "r"(part ? v[6] : v[2]), "r"(part ? v[7] : v[3])
+                                 : "memory");
+                }
+            }
+        }
+    }
+}
+// The value's scale as power * factor.  bf16: 1 * scale (the factor multiplies
+// the probability, and bf16's exponents hold any scale).  fp16: a power of two
+// that keeps every code exact and finite in fp16 goes to the codes, so that the
+// factor is about 1 and the probability keeps its place in fp16's narrow range:
+// codes are multiples of 1 (INT8) or 2^-9 (E4M3) up to 127 or 448, so powers
+// 2^-24..2^8 or 2^-15..2^6.
+template <class T, int FMT>
+__device__ __forceinline__ void split_scale(float scale, float& power, float& factor) {
+    power = 1.f;
+    factor = scale;
+    if (T::kHalf) {
+        constexpr int kLow = FMT == kKvInt8 ? -24 : -15, kHigh = FMT == kKvInt8 ? 8 : 6;
+        const int e = (int)((__float_as_uint(scale) >> 23) & 0xFF) - 127;
+        const int k = min(max(e, kLow), kHigh);
+        power = __uint_as_float((uint32_t)(127 + k) << 23);
+        factor = scale * __uint_as_float((uint32_t)(127 - k) << 23);
+    }
+}
+
 template <class T, int FMT>
 __device__ __forceinline__ void load_role(const KvArgs& a, const AttnArgs& t, Shared* sh, uint32_t slots,
                                           uint32_t slot_bytes, Walk w) {
     const int warp = (threadIdx.x >> 5) - 8, lane = threadIdx.x & 31;
     const Waiter wait{sh, a.ws};
-    const int chunks = a.dim * 2 / 16;
+    const int chunks = a.dim * (FMT == kKv16Bit ? 2 : 1) / 16;
     uint32_t entry = 0, published = 0;  // K and V tiles, alternating
     Piece p;
     auto publish_to = [&](uint32_t upto) {
@@ -248,27 +339,63 @@ __device__ __forceinline__ void load_role(const KvArgs& a, const AttnArgs& t, Sh
     while (next_piece(a, t, sh->prefix, w, p)) {
         const int32_t base = (p.range.lo + p.from) * kTokens + 32 * warp + lane;
         TileRow r = tile_row(a, p, base);
+        Codes codes;
+        float ks = 0.f, vs = 0.f;
+        if (FMT != kKv16Bit) {
+            fetch_codes(a.k, r, lane, chunks, codes);
+            if (r.real) ks = a.k_scale[r.scale_at], vs = a.v_scale[r.scale_at];
+        }
         for (int32_t j = 0; j < p.count; ++j) {
             const TileRow here = r;
             if (j + 1 < p.count) r = tile_row(a, p, base + (j + 1) * kTokens);
+            float power = 1.f;
 #pragma unroll
             for (int side = 0; side < 2; ++side, ++entry) {
                 const uint32_t s = entry % kSlots, use = entry / kSlots;
+                const uint32_t slot = slots + s * slot_bytes;
                 if (use > 0 && !__all_sync(0xFFFFFFFFu, mbar_test(&sh->kv_free[s], (use - 1) & 1))) {
                     // about to wait: hand over what has been brought so far
-                    copy_wait<0>();
-                    publish_to(entry);
+                    if (FMT == kKv16Bit) {
+                        copy_wait<0>();
+                        publish_to(entry);
+                    }
                     if (!__all_sync(0xFFFFFFFFu, wait(&sh->kv_free[s], (use - 1) & 1))) return;
                 }
-                copy_tile(a, side ? a.v : a.k, slots + s * slot_bytes, here, warp, lane, chunks);
-                copy_commit();
-                copy_wait<2>();
-                if (entry >= 2) publish_to(entry - 1);
+                if (FMT == kKv16Bit) {
+                    copy_tile(a, side ? a.v : a.k, slot, here, warp, lane, chunks);
+                    copy_commit();
+                    copy_wait<2>();
+                    if (entry >= 2) publish_to(entry - 1);
+                    continue;
+                }
+                // this side's codes are here; the next side's are asked for before they are worked on
+                const Codes now = codes;
+                if (side == 0) {
+                    fetch_codes(a.v, here, lane, chunks, codes);
+                    const uint32_t n = (entry / 2) % kScaleSlots;
+                    float factor;
+                    split_scale<T, FMT>(vs, power, factor);
+                    sh->k_scale[n][32 * warp + lane] = ks;
+                    sh->v_scale[n][32 * warp + lane] = factor;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sh->scale_full[n]);
+                    store_codes<T, FMT, false>(now, slot, warp, lane, chunks, 1.f);
+                } else {
+                    ks = vs = 0.f;
+                    if (j + 1 < p.count) {
+                        fetch_codes(a.k, r, lane, chunks, codes);
+                        if (r.real) ks = a.k_scale[r.scale_at], vs = a.v_scale[r.scale_at];
+                    }
+                    store_codes<T, FMT, T::kHalf>(now, slot, warp, lane, chunks, power);
+                }
+                publish_to(entry + 1);
             }
         }
     }
-    copy_wait<0>();
-    publish_to(entry);
+    if (FMT == kKv16Bit) {
+        copy_wait<0>();
+        publish_to(entry);
+    }
 }
 
 // ---------------------------------------------------------------- products
@@ -369,12 +496,13 @@ __device__ __forceinline__ void softmax_role(const KvArgs& a, const AttnArgs& t,
     const bool flip = t.scale < 0.f, zero = t.scale == 0.f;
     const float to_base2 = (zero ? 1.f : fabsf(t.scale)) * 1.4426950408889634f;
     const PartLayout parts = part_layout(a, gridDim.x, kRows);
-    uint32_t s_phase = 0, o_phase = 0;
+    uint32_t s_phase = 0, o_phase = 0, tile = 0;  // tile: this block's tiles of tokens, whoever's
     const uint64_t x0 = w.x;
     bool first_piece = true;
 
     // the next piece that has rows for this warpgroup, with its rows of Q on their way
     Piece p;
+    uint32_t skipped = 0;  // tiles of pieces without
     auto take = [&]() -> bool {
         for (;;) {
             if (!next_piece(a, t, sh->prefix, w, p)) return false;
@@ -383,6 +511,7 @@ __device__ __forceinline__ void softmax_role(const KvArgs& a, const AttnArgs& t,
             }
             first_piece = false;
             if (live_rows(t, p) > i * kTileRows) break;
+            skipped += (uint32_t)p.count;
         }
         bring_row(a, t, p, i, row, q_tile, flip, zero);
         __syncwarp();
@@ -399,7 +528,9 @@ __device__ __forceinline__ void softmax_role(const KvArgs& a, const AttnArgs& t,
         if (is_row) visible_range(t, cur.seq.len, at.pos, first, last);
         float m = -INFINITY, l = 0.f;
         int32_t base = (cur.range.lo + cur.from) * kTokens;
-        for (int32_t j = 0; j < cur.count; ++j, base += kTokens) {
+        tile += skipped;
+        skipped = 0;
+        for (int32_t j = 0; j < cur.count; ++j, ++tile, base += kTokens) {
             if (!__all_sync(0xFFFFFFFFu, wait(&sh->s_full[i], s_phase))) return;
             s_phase ^= 1;
             tc_fence_after();
@@ -407,6 +538,22 @@ __device__ __forceinline__ void softmax_role(const KvArgs& a, const AttnArgs& t,
 #pragma unroll
             for (int c = 0; c < kTokens; c += 32) tc_load32(at_s + c, s + c);
             tc_wait_load();
+            const uint32_t scale_slot = tile % kScaleSlots;
+            if (FMT != kKv16Bit) {
+                if (!__all_sync(0xFFFFFFFFu, wait(&sh->scale_full[scale_slot], (tile / kScaleSlots) & 1))) return;
+#pragma unroll
+                for (int c = 0; c < kTokens; c += 4) {
+                    const float4 f = *reinterpret_cast<const float4*>(&sh->k_scale[scale_slot][c]);
+                    const float2 x = mul2(make_float2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])),
+                                          make_float2(f.x, f.y));
+                    const float2 y = mul2(make_float2(__uint_as_float(s[c + 2]), __uint_as_float(s[c + 3])),
+                                          make_float2(f.z, f.w));
+                    s[c] = __float_as_uint(x.x);
+                    s[c + 1] = __float_as_uint(x.y);
+                    s[c + 2] = __float_as_uint(y.x);
+                    s[c + 3] = __float_as_uint(y.y);
+                }
+            }
             if (base < first || base + kTokens > last) {
                 const int32_t lo = first - base, hi = last - base;  // visible columns lo .. hi - 1
 #pragma unroll
@@ -450,6 +597,11 @@ __device__ __forceinline__ void softmax_role(const KvArgs& a, const AttnArgs& t,
                 y.y = exp2_fast(y.y);
                 sum0 = add2(sum0, x);
                 sum1 = add2(sum1, y);
+                if (FMT != kKv16Bit) {
+                    const float4 f = *reinterpret_cast<const float4*>(&sh->v_scale[scale_slot][c]);
+                    x = mul2(x, make_float2(f.x, f.y));
+                    y = mul2(y, make_float2(f.z, f.w));
+                }
                 pr[c / 2] = pack<T>(x.x, x.y);
                 pr[c / 2 + 1] = pack<T>(y.x, y.y);
                 if (c % 64 == 60) tc_store32(at_s + (c / 64) * 32, pr + (c / 64) * 32);
@@ -564,10 +716,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     w.whole = whole_items;
     const uint32_t slots = base + 2 * tile_bytes;
     if (warp < 8) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs<FMT>));
         softmax_role<T, FMT>(a, t, sh, base + (warp / 4) * tile_bytes, w);
     } else if (warp < 12) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLoaderRegs<FMT>));
         load_role<T, FMT>(a, t, sh, slots, tile_bytes, w);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
@@ -611,8 +763,14 @@ size_t kv_chunk_scratch(int dim) { return part_bytes(kShares, kRows, dim); }
 cudaError_t launch_kv_chunk(int dtype, int format, const KvArgs& a, const AttnArgs& t, int max_len, cudaStream_t s) {
     const bool whole = max_len <= kTokens;
     const uint32_t min_tiles = 1;
-    if (dtype == (int)Bf16::kCode) return launch_one<BfType, kKv16Bit>(a, t, whole, min_tiles, s);
-    return launch_one<HfType, kKv16Bit>(a, t, whole, min_tiles, s);
+    if (dtype == (int)Bf16::kCode) {
+        if (format == kKv16Bit) return launch_one<BfType, kKv16Bit>(a, t, whole, min_tiles, s);
+        return format == kKvInt8 ? launch_one<BfType, kKvInt8>(a, t, whole, min_tiles, s)
+                                 : launch_one<BfType, kKvE4m3>(a, t, whole, min_tiles, s);
+    }
+    if (format == kKv16Bit) return launch_one<HfType, kKv16Bit>(a, t, whole, min_tiles, s);
+    return format == kKvInt8 ? launch_one<HfType, kKvInt8>(a, t, whole, min_tiles, s)
+                             : launch_one<HfType, kKvE4m3>(a, t, whole, min_tiles, s);
 }
 
 }  // namespace cccl
