@@ -148,48 +148,56 @@ __device__ __forceinline__ float warp_sum(float x) {
     return x;
 }
 
-// 4 codes -> 16-bit values of type T, exactly, as two pairs: E4M3 in the order
-// (0, 1), (2, 3), INT8 in the order (0, 2), (1, 3) (the cheaper one for each;
-// callers arrange the other operand or the bytes to suit).
-//   INT8 to bf16: with L = the low 7 bits, 0x4300 | L is 128 + L; taking off
-//   0x4300 | (sign bit) = 128 or 256 leaves L or L - 128, the code.
-//   INT8 to fp16: with u = code + 128, 0x6400 | u is 1024 + u; taking off 1152
-//   leaves the code.
-template <class T, int FMT>
+// 4 codes -> fp16 values, exactly, as two pairs: E4M3 in the order (0, 1),
+// (2, 3), INT8 in the order (0, 2), (1, 3) (the cheaper one for each; callers
+// arrange the other operand or the bytes to suit).  INT8: with u = code + 128
+// (the code's sign bit flipped), 0x6400 | u is 1024 + u; taking off 1152 leaves
+// the code.
+template <int FMT>
 __device__ __forceinline__ void expand4(uint32_t w, uint32_t& a, uint32_t& b) {
     if (FMT == kKvE4m3) {
-        uint32_t h0, h1;
         asm("{ .reg .b16 l, h; mov.b32 {l, h}, %2; cvt.rn.f16x2.e4m3x2 %0, l; cvt.rn.f16x2.e4m3x2 %1, h; }"
-            : "=r"(h0), "=r"(h1)
+            : "=r"(a), "=r"(b)
             : "r"(w));
-        if (T::kHalf) {
-            a = h0;
-            b = h1;
-        } else {
-            const float2 x = __half22float2(*reinterpret_cast<__half2*>(&h0));
-            const float2 y = __half22float2(*reinterpret_cast<__half2*>(&h1));
-            a = round_pair<T>(x.x, x.y);
-            b = round_pair<T>(y.x, y.y);
-        }
-    } else if (T::kHalf) {
-        const uint32_t u = w ^ 0x80808080u;
-        const uint32_t x = (u & 0x00FF00FFu) | 0x64006400u, y = ((u >> 8) & 0x00FF00FFu) | 0x64006400u;
+    } else {
+        const uint32_t x = (w & 0x00FF00FFu) ^ 0x64806480u, y = ((w >> 8) & 0x00FF00FFu) ^ 0x64806480u;
         const __half2 bias = __half2half2(__ushort_as_half(0x6480));  // 1152
         const __half2 p = __hsub2(*reinterpret_cast<const __half2*>(&x), bias);
         const __half2 q = __hsub2(*reinterpret_cast<const __half2*>(&y), bias);
         a = *reinterpret_cast<const uint32_t*>(&p);
         b = *reinterpret_cast<const uint32_t*>(&q);
-    } else {
-        const uint32_t v = w >> 8;
-        const uint32_t x = (w & 0x007F007Fu) | 0x43004300u, xs = (w & 0x00800080u) | 0x43004300u;
-        const uint32_t y = (v & 0x007F007Fu) | 0x43004300u, ys = (v & 0x00800080u) | 0x43004300u;
-        const __nv_bfloat162 p = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&x),
-                                         *reinterpret_cast<const __nv_bfloat162*>(&xs));
-        const __nv_bfloat162 q = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&y),
-                                         *reinterpret_cast<const __nv_bfloat162*>(&ys));
-        a = *reinterpret_cast<const uint32_t*>(&p);
-        b = *reinterpret_cast<const uint32_t*>(&q);
     }
+}
+
+// 8-bit caches are multiplied in fp16, which holds every code exactly.
+//
+// Queries: a bf16 row is first multiplied by a power of two that brings its
+// largest value to 2^14..2^15.  Every value down to 2^-29 of the largest is
+// then exact in fp16, and smaller ones are off by 2^-40 of the largest, far
+// below the binary32 sum's own rounding.  fp16 rows stay as they are.
+// amax: the row's largest pattern without its sign.
+template <class T>
+__device__ __forceinline__ float query_power(uint32_t amax) {
+    if (T::kHalf || amax == 0 || amax >= 0x7F80u) return 1.f;
+    const int e = max((int)(amax >> 7) - 127, -100);
+    return __uint_as_float((uint32_t)(127 + 14 - e) << 23);
+}
+template <class T>
+__device__ __forceinline__ uint32_t scaled_pair(uint32_t w, float power) {
+    if (T::kHalf) return w;
+    const __half2 h = __floats2half2_rn(T::load((uint16_t)(w & 0xFFFFu)) * power, T::load((uint16_t)(w >> 16)) * power);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+// Probabilities times the value's scale: the running maximum of a row's scores
+// is taken with the exponent of the largest value scale of the same tokens, so
+// that exp2(s - reference) * scale stays in fp16's range whatever the scales'
+// size.  The quotient does not depend on the reference.  Limited so that the
+// sum of exp2(s - reference) stays in binary32's range: scales below 2^-100
+// may lose what lies below 2^-124, scales above 2^60 can overflow fp16 (such
+// rows come out non-finite and are worked out by attend_row).
+__device__ __forceinline__ float scale_exponent(uint32_t largest_scale_bits) {
+    const int e = (int)(largest_scale_bits >> 23) - 127;
+    return (float)min(max(e, -100), 60);
 }
 
 __device__ __forceinline__ float exp2_fast(float x) {

@@ -18,6 +18,8 @@
 // 256.  The products of one thread execute in order, so a full S also means
 // that the previous O is done, and S may be written over the P that the
 // product before it reads.
+#include <type_traits>
+
 #include "cccl_kv.cuh"
 #include "cccl_kv_launch.h"
 #include "cccl_kv_schedule.cuh"
@@ -54,6 +56,7 @@ struct Shared {
     uint64_t prefix[kMaxBatch + 1];
     alignas(16) float k_scale[kScaleSlots][kTokens];
     alignas(16) float v_scale[kScaleSlots][kTokens];
+    alignas(16) uint32_t v_top[kScaleSlots][kLoaderWarps];  // the largest value scale of each warp's rows
 };
 
 // ---------------------------------------------------------------- tcgen05
@@ -173,6 +176,10 @@ __device__ __forceinline__ uint32_t pack<HfType>(float lo, float hi) {
     return d;
 }
 
+// The products' operands: 8-bit codes are multiplied in fp16.
+template <class T, int FMT>
+using Operand = typename std::conditional<FMT == kKv16Bit, T, HfType>::type;
+
 // A share's pieces, one after the other (every role walks them by itself).
 struct Walk {
     uint64_t x, x0, x1, T;
@@ -266,59 +273,28 @@ __device__ __forceinline__ void fetch_codes(const uint8_t* data, const TileRow& 
         }
     }
 }
-// power: the row's power of two (fp16 V), or 1.
-template <class T, int FMT, bool POWER>
-__device__ __forceinline__ void store_codes(const Codes& c, uint32_t slot, int warp, int lane, int chunks,
-                                            float power) {
+template <int FMT>
+__device__ __forceinline__ void store_codes(const Codes& c, uint32_t slot, int warp, int lane, int chunks) {
     const int per_row = chunks > 4 ? 8 : 4, rows_per_pass = 32 / per_row, chunk = lane % per_row;
 #pragma unroll
     for (int i = 0; i < kCodePasses; ++i) {
-        if (i < per_row) {
-            const int local = i * rows_per_pass + lane / per_row;
+        if (i < per_row && chunk < chunks) {
+            const uint32_t row = 32 * warp + i * rows_per_pass + lane / per_row;
             const uint32_t w[4] = {c.w[i].x, c.w[i].y, c.w[i].z, c.w[i].w};
             uint32_t v[8];
 #pragma unroll
             for (int k = 0; k < 4; ++k)  // in the row's order
-                expand4<T, FMT>(FMT == kKvInt8 ? __byte_perm(w[k], 0, 0x3120) : w[k], v[2 * k], v[2 * k + 1]);
-            if (POWER) {
-                const __half2 f = __float2half2_rn(__shfl_sync(0xFFFFFFFFu, power, local));
+                expand4<FMT>(FMT == kKvInt8 ? __byte_perm(w[k], 0, 0x3120) : w[k], v[2 * k], v[2 * k + 1]);
+            const int second = chunk >> 2;  // which of the two goes first
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const __half2 x = __hmul2(*reinterpret_cast<const __half2*>(&v[k]), f);
-                    v[k] = *reinterpret_cast<const uint32_t*>(&x);
-                }
-            }
-            if (chunk < chunks) {
-                const uint32_t row = 32 * warp + local;
-                const int second = chunk >> 2;  // which of the two goes first
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const int part = k ^ second;
-                    const uint32_t at = slot + swizzled(row, 2 * chunk + part);
-                    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(part ? v[4] : v[0]),
-                                 "r"(part ? v[5] : v[1]), "r"(part ? v[6] : v[2]), "r"(part ? v[7] : v[3])
-                                 : "memory");
-                }
+            for (int k = 0; k < 2; ++k) {
+                const int part = k ^ second;
+                const uint32_t at = slot + swizzled(row, 2 * chunk + part);
+                asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(part ? v[4] : v[0]),
+                             "r"(part ? v[5] : v[1]), "r"(part ? v[6] : v[2]), "r"(part ? v[7] : v[3])
+                             : "memory");
             }
         }
-    }
-}
-// The value's scale as power * factor.  bf16: 1 * scale (the factor multiplies
-// the probability, and bf16's exponents hold any scale).  fp16: a power of two
-// that keeps every code exact and finite in fp16 goes to the codes, so that the
-// factor is about 1 and the probability keeps its place in fp16's narrow range:
-// codes are multiples of 1 (INT8) or 2^-9 (E4M3) up to 127 or 448, so powers
-// 2^-24..2^8 or 2^-15..2^6.
-template <class T, int FMT>
-__device__ __forceinline__ void split_scale(float scale, float& power, float& factor) {
-    power = 1.f;
-    factor = scale;
-    if (T::kHalf) {
-        constexpr int kLow = FMT == kKvInt8 ? -24 : -15, kHigh = FMT == kKvInt8 ? 8 : 6;
-        const int e = (int)((__float_as_uint(scale) >> 23) & 0xFF) - 127;
-        const int k = min(max(e, kLow), kHigh);
-        power = __uint_as_float((uint32_t)(127 + k) << 23);
-        factor = scale * __uint_as_float((uint32_t)(127 - k) << 23);
     }
 }
 
@@ -348,7 +324,6 @@ __device__ __forceinline__ void load_role(const KvArgs& a, const AttnArgs& t, Sh
         for (int32_t j = 0; j < p.count; ++j) {
             const TileRow here = r;
             if (j + 1 < p.count) r = tile_row(a, p, base + (j + 1) * kTokens);
-            float power = 1.f;
 #pragma unroll
             for (int side = 0; side < 2; ++side, ++entry) {
                 const uint32_t s = entry % kSlots, use = entry / kSlots;
@@ -373,20 +348,20 @@ __device__ __forceinline__ void load_role(const KvArgs& a, const AttnArgs& t, Sh
                 if (side == 0) {
                     fetch_codes(a.v, here, lane, chunks, codes);
                     const uint32_t n = (entry / 2) % kScaleSlots;
-                    float factor;
-                    split_scale<T, FMT>(vs, power, factor);
                     sh->k_scale[n][32 * warp + lane] = ks;
-                    sh->v_scale[n][32 * warp + lane] = factor;
+                    sh->v_scale[n][32 * warp + lane] = vs;
+                    const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(vs));
+                    if (lane == 0) sh->v_top[n][warp] = top;
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&sh->scale_full[n]);
-                    store_codes<T, FMT, false>(now, slot, warp, lane, chunks, 1.f);
+                    store_codes<FMT>(now, slot, warp, lane, chunks);
                 } else {
                     ks = vs = 0.f;
                     if (j + 1 < p.count) {
                         fetch_codes(a.k, r, lane, chunks, codes);
                         if (r.real) ks = a.k_scale[r.scale_at], vs = a.v_scale[r.scale_at];
                     }
-                    store_codes<T, FMT, T::kHalf>(now, slot, warp, lane, chunks, power);
+                    store_codes<FMT>(now, slot, warp, lane, chunks);
                 }
                 publish_to(entry + 1);
             }
@@ -399,12 +374,12 @@ __device__ __forceinline__ void load_role(const KvArgs& a, const AttnArgs& t, Sh
 }
 
 // ---------------------------------------------------------------- products
-template <class T>
+template <class M>
 __device__ __forceinline__ void mma_role(const KvArgs& a, const AttnArgs& t, Shared* sh, uint32_t q_base,
                                          uint32_t slots, uint32_t slot_bytes, Walk w) {
     const Waiter wait{sh, a.ws};
     const uint32_t tmem = sh->tmem;
-    const uint32_t qk = instruction(T::kHalf, kTokens, false), pv = instruction(T::kHalf, a.dim > 64 ? 128 : 64, true);
+    const uint32_t qk = instruction(M::kHalf, kTokens, false), pv = instruction(M::kHalf, a.dim > 64 ? 128 : 64, true);
     const int steps = a.dim / 16;
     const uint32_t q_bytes = slot_bytes;
     uint32_t entry = 0;
@@ -464,12 +439,25 @@ __device__ __forceinline__ void mma_role(const KvArgs& a, const AttnArgs& t, Sha
 // Row `row` (0..127) of row tile i of Q into shared memory; rows that do not
 // exist are zeros.  flip: the sign bit when the scale is negative; zero: the
 // scale is zero (every score is then 0 times the products, so are zeros').
-__device__ __forceinline__ void bring_row(const KvArgs& a, const AttnArgs& t, const Piece& p, int i, int row,
-                                          uint32_t q_tile, bool flip, bool zero) {
+// Returns what undoes the row's power of two (8-bit caches).
+template <class T, int FMT>
+__device__ __forceinline__ float bring_row(const KvArgs& a, const AttnArgs& t, const Piece& p, int i, int row,
+                                           uint32_t q_tile, bool flip, bool zero) {
     const bool real = i * kTileRows + row < live_rows(t, p) && !zero;
     const RowPlace at = row_place(t, p, kRows, i * kTileRows + row);
     const uint4* src = reinterpret_cast<const uint4*>(t.q + at.token * t.q_token + (int64_t)at.head * t.q_head);
     const uint32_t sign = flip ? 0x80008000u : 0u;
+    float power = 1.f;
+    if (FMT != kKv16Bit && real) {
+        uint32_t top = 0;
+#pragma unroll 4
+        for (int c = 0; c < a.dim / 8; ++c) {
+            const uint4 x = src[c];
+            top = vmax_u16x2(vmax_u16x2(top, x.x & 0x7FFF7FFFu), vmax_u16x2(x.y & 0x7FFF7FFFu, x.z & 0x7FFF7FFFu));
+            top = vmax_u16x2(top, x.w & 0x7FFF7FFFu);
+        }
+        power = query_power<T>(max(top & 0xFFFFu, top >> 16));
+    }
 #pragma unroll 4
     for (int c = 0; c < a.dim / 8; ++c) {
         uint4 x = make_uint4(0, 0, 0, 0);
@@ -479,12 +467,16 @@ __device__ __forceinline__ void bring_row(const KvArgs& a, const AttnArgs& t, co
             x.y ^= sign;
             x.z ^= sign;
             x.w ^= sign;
+            if (FMT != kKv16Bit)
+                x = make_uint4(scaled_pair<T>(x.x, power), scaled_pair<T>(x.y, power), scaled_pair<T>(x.z, power),
+                               scaled_pair<T>(x.w, power));
         }
         asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(q_tile + swizzled(row, c)), "r"(x.x), "r"(x.y),
                      "r"(x.z), "r"(x.w)
                      : "memory");
     }
     fence_proxy_async_smem();
+    return 1.f / power;
 }
 
 template <class T, int FMT>
@@ -494,7 +486,8 @@ __device__ __forceinline__ void softmax_role(const KvArgs& a, const AttnArgs& t,
     const uint32_t tmem = sh->tmem + ((uint32_t)(32 * warp) << 16);
     const uint32_t at_s = tmem + kColS + 128 * i, at_o = tmem + kColO + 128 * i;
     const bool flip = t.scale < 0.f, zero = t.scale == 0.f;
-    const float to_base2 = (zero ? 1.f : fabsf(t.scale)) * 1.4426950408889634f;
+    const float scale_base2 = (zero ? 1.f : fabsf(t.scale)) * 1.4426950408889634f;
+    float next_base2 = scale_base2;
     const PartLayout parts = part_layout(a, gridDim.x, kRows);
     uint32_t s_phase = 0, o_phase = 0, tile = 0;  // tile: this block's tiles of tokens, whoever's
     const uint64_t x0 = w.x;
@@ -513,7 +506,7 @@ __device__ __forceinline__ void softmax_role(const KvArgs& a, const AttnArgs& t,
             if (live_rows(t, p) > i * kTileRows) break;
             skipped += (uint32_t)p.count;
         }
-        bring_row(a, t, p, i, row, q_tile, flip, zero);
+        next_base2 = scale_base2 * bring_row<T, FMT>(a, t, p, i, row, q_tile, flip, zero);
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh->q_full[i]);
         return true;
@@ -522,6 +515,7 @@ __device__ __forceinline__ void softmax_role(const KvArgs& a, const AttnArgs& t,
     if (first_piece && !w.whole && threadIdx.x == 0) parts.cuts[w.share].last = -1;
     while (have) {
         const Piece cur = p;
+        const float to_base2 = next_base2;
         const bool is_row = i * kTileRows + row < live_rows(t, cur);
         const RowPlace at = row_place(t, cur, kRows, i * kTileRows + row);
         int32_t first = 0, last = 0;
@@ -566,7 +560,11 @@ __device__ __forceinline__ void softmax_role(const KvArgs& a, const AttnArgs& t,
                 top0 = max3(top0, __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
                 top1 = max3(top1, __uint_as_float(s[c + 2]), __uint_as_float(s[c + 3]));
             }
-            const float top = fmaxf(top0, top1) * to_base2;
+            float top = fmaxf(top0, top1) * to_base2;
+            if (FMT != kKv16Bit) {
+                const uint4 v = *reinterpret_cast<const uint4*>(sh->v_top[scale_slot]);
+                top += scale_exponent(max(max(v.x, v.y), max(v.z, v.w)));
+            }
             if (j == 0) {
                 m = top;
             } else if (__any_sync(0xFFFFFFFFu, top > m + kSlack)) {
@@ -602,8 +600,8 @@ __device__ __forceinline__ void softmax_role(const KvArgs& a, const AttnArgs& t,
                     x = mul2(x, make_float2(f.x, f.y));
                     y = mul2(y, make_float2(f.z, f.w));
                 }
-                pr[c / 2] = pack<T>(x.x, x.y);
-                pr[c / 2 + 1] = pack<T>(y.x, y.y);
+                pr[c / 2] = pack<Operand<T, FMT>>(x.x, x.y);
+                pr[c / 2 + 1] = pack<Operand<T, FMT>>(y.x, y.y);
                 if (c % 64 == 60) tc_store32(at_s + (c / 64) * 32, pr + (c / 64) * 32);
             }
             sum0 = add2(sum0, sum1);
@@ -724,7 +722,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
         if (threadIdx.x == 12 * 32) {
-            mma_role<T>(a, t, sh, base, slots, tile_bytes, w);
+            mma_role<Operand<T, FMT>>(a, t, sh, base, slots, tile_bytes, w);
             tc_commit(&sh->drained);
             if (!mbar_wait(&sh->drained, 0)) record_error(a.ws, kStatusTimeout);
         }

@@ -17,7 +17,7 @@ cudaError_t launch_kv_read(int dtype, int format, const KvArgs& a, const KvPacke
 cudaError_t launch_kv_attention(int dtype, int format, const KvArgs& a, const AttnArgs& t, int max_new, int max_len,
                                 cudaStream_t stream);
 // The kernel for few rows a kv head, and its workspace bytes after the header.
-cudaError_t launch_kv_tokens(int dtype, int format, const KvArgs& a, const AttnArgs& t, int max_len,
+cudaError_t launch_kv_tokens(int dtype, int format, const KvArgs& a, const AttnArgs& t, int max_new, int max_len,
                              cudaStream_t stream);
 size_t kv_tokens_scratch(int dim);
 // The kernel for chunks of rows, and its workspace bytes after the header.

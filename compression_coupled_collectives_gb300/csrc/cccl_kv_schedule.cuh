@@ -213,7 +213,7 @@ __device__ __forceinline__ void fix_row(const KvArgs& a, const AttnArgs& t, cons
 // Joins the parts of the item cut at the start of share blockIdx.x: 4 rows a
 // block, 4 values a thread.  Parts are taken in the order of the line.
 constexpr int kJoinRows = 4, kJoinThreads = 128;
-constexpr int kMaxShares = 304;
+constexpr int kMaxShares = 608;
 template <class T, int FMT, int ROWS>
 __global__ void __launch_bounds__(kJoinThreads) join_parts_kernel(const __grid_constant__ KvArgs a,
                                                                   const __grid_constant__ AttnArgs t, int shares) {

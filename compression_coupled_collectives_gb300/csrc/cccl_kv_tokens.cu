@@ -2,21 +2,25 @@
 // drafts): the cache is read once and everything else is small, so the kernel
 // is built around the loads.
 //
-// An item is up to 16 rows (new tokens x the query heads that share a kv
+// An item is up to 8 or 16 rows (new tokens x the query heads that share a kv
 // head).  Each of a block's four warps takes TS consecutive cached tokens of
 // every tile and runs on its own: its ring of stages filled by its own 16-byte
-// asynchronous copies (page lookups one stage ahead of the copies), scores and
-// values by mma.sync with the 16 rows as M, its own running maximum, sum and
-// accumulator in registers.  The four meet once, at the end of an item.
-// tcgen05 is not used here: its M is 128 rows, of which at most 16 would be
-// real, and the tensor work is a few percent of the time anyway.
+// asynchronous copies (page lookups one stage ahead of the copies), products by
+// mma.sync, its own running maximum, sum and accumulator in registers.  The
+// four meet once, at the end of an item.
+//
+// Both products are taken transposed, S' = K Q' and O' = V' P', so that tokens
+// and channels fill the instruction's 16 and the rows its 8: a tile with the
+// rows as the 16 would be mostly padding, twice the instructions and twice the
+// registers.  tcgen05 is not used here: its M of 128 could be the tokens, but
+// the softmax would then run across threads and every tile would pay the way
+// through TMEM; the tensor work is a small part of the time.
 //
 // Precision: products of 16-bit values are exact and summed in binary32.  A
 // probability enters the second product as the sum of two 16-bit values (high
 // part and remainder), so nothing is rounded before the result.  8-bit codes
-// are exact in 16 bits; the key's scale multiplies the score and the value's
-// scale the probability, both in binary32 (probabilities then in bf16 pairs,
-// whose exponents hold any scale).
+// are exact in fp16; the key's scale multiplies the score and the value's scale
+// the probability, both in binary32.
 #include <type_traits>
 
 #include "cccl_kv.cuh"
@@ -28,10 +32,8 @@ namespace cccl {
 
 namespace {
 
-constexpr int kRows = 16, kWarps = 4, kThreads = 32 * kWarps;
-constexpr int kBlocksPerSm = 2;
+constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr int kSms = 152;
-constexpr int kShares = kSms * kBlocksPerSm;
 
 __device__ __forceinline__ void ldsm4(uint32_t a, uint32_t* r) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -46,6 +48,11 @@ __device__ __forceinline__ void ldsm4_trans(uint32_t a, uint32_t* r) {
 __device__ __forceinline__ uint4 lds16(uint32_t a) {
     uint4 v;
     asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ float lds4(uint32_t a) {
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(a));
     return v;
 }
 __device__ __forceinline__ uint2 lds8(uint32_t a) {
@@ -77,12 +84,21 @@ __device__ __forceinline__ void split_pair(float x, float y, uint32_t& hi, uint3
     lo = round_pair<T>(x - T::load((uint16_t)(hi & 0xFFFFu)), y - T::load((uint16_t)(hi >> 16)));
 }
 
-// Sizes of the instance for values of T in format FMT and heads of up to DP.
-template <class T_, int FMT_, int DP_>
+// [8][8] 16-bit values across the warp, two a lane: transposed.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+// Sizes of the instance for values of T in format FMT, heads of up to DP and
+// items of 8 NR rows.
+template <class T_, int FMT_, int DP_, int NR_>
 struct Shape {
     using T = T_;
-    using P = typename std::conditional<FMT_ == kKv16Bit, T_, BfType>::type;  // probabilities
-    static constexpr int FMT = FMT_, DP = DP_;
+    using M = typename std::conditional<FMT_ == kKv16Bit, T_, HfType>::type;  // the products' operands
+    static constexpr int FMT = FMT_, DP = DP_, NR = NR_;
+    static constexpr int kRows = 8 * NR;
     static constexpr int kElem = FMT == kKv16Bit ? 2 : 1;
     static constexpr int kRowBytes = DP * kElem;                      // 64, 128 or 256
     static constexpr int kTokens = kRowBytes == 256 ? 16 : 32;        // tokens of a warp's stage
@@ -90,9 +106,11 @@ struct Shape {
     static constexpr int kSide = kTokens * kRowBytes;                 // bytes of K (or V) in a stage
     static constexpr int kScaleBytes = FMT == kKv16Bit ? 0 : 8 * kTokens;
     static constexpr int kStage = 2 * kSide + kScaleBytes;
-    static constexpr int kStages = kSide >= 4096 ? 3 : 5;
+    static constexpr int kStages = kStage > 4096 + 512 ? 2 : 4;
     static constexpr int kRing = kStages * kStage;                    // bytes of a warp's ring
     static constexpr int kMerge = kWarps * kRows * (DP + 4) * 4;      // accumulators at the end of an item
+    static constexpr int kBlocksPerSm = 3;
+    static constexpr int kShares = kSms * kBlocksPerSm;
     static constexpr int kSmem = kWarps * kRing > kMerge ? kWarps * kRing : kMerge;
 };
 
@@ -147,14 +165,18 @@ __device__ __forceinline__ void issue_stage(const KvArgs& a, uint32_t stage, con
     }
 }
 
-// The query fragments of rows g and g + 8 (zeros where there is no such row).
+// The query fragments: lane (g, c) holds channels of row 8 nr + g (zeros where
+// there is no such row), 16-bit caches 16 ks + 2 c, + 1 and + 8, + 9; 8-bit
+// caches, whose lanes read 16 codes in a row, 64 (ks / 4) + 16 c + 4 (ks % 4)
+// .. + 3.  inverse[nr]: what undoes the row's power of two.
 template <class S>
-__device__ __forceinline__ void load_queries(const KvArgs& a, const AttnArgs& t, const Piece& p, uint32_t (*q)[4]) {
+__device__ __forceinline__ void load_queries(const KvArgs& a, const AttnArgs& t, const Piece& p,
+                                             uint32_t (*q)[S::DP / 16][2], float* inverse) {
     const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
     const int64_t rows = (int64_t)p.seq.n * t.group;
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-        const int64_t r = (int64_t)p.rt * kRows + g + 8 * half;
+    for (int nr = 0; nr < S::NR; ++nr) {
+        const int64_t r = (int64_t)p.rt * S::kRows + g + 8 * nr;
         const bool real = r < rows;
         const int64_t i = real ? r / t.group : 0, h = real ? r - i * t.group : 0;
         const uint8_t* src = t.q + (p.seq.row + i) * t.q_token + ((int64_t)p.kv_head * t.group + h) * t.q_head;
@@ -170,68 +192,94 @@ __device__ __forceinline__ void load_queries(const KvArgs& a, const AttnArgs& t,
                 const int d = 64 * (ks / 4) + 16 * c + 4 * (ks % 4);
                 uint2 w = make_uint2(0, 0);
                 if (real && d < a.dim) w = *reinterpret_cast<const uint2*>(src + 2 * d);
-                lo = S::FMT == kKvE4m3 ? w.x : __byte_perm(w.x, w.y, 0x5410);
-                hi = S::FMT == kKvE4m3 ? w.y : __byte_perm(w.x, w.y, 0x7632);
+                lo = w.x;
+                hi = w.y;
             }
-            q[ks][half] = lo;
-            q[ks][2 + half] = hi;
+            q[nr][ks][0] = lo;
+            q[nr][ks][1] = hi;
+        }
+        inverse[nr] = 1.f;
+        if (S::FMT != kKv16Bit) {
+            uint32_t top = 0;
+#pragma unroll
+            for (int ks = 0; ks < S::DP / 16; ++ks) {
+                top = vmax_u16x2(top, q[nr][ks][0] & 0x7FFF7FFFu);
+                top = vmax_u16x2(top, q[nr][ks][1] & 0x7FFF7FFFu);
+            }
+            top = max(top & 0xFFFFu, top >> 16);
+            top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+            top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+            const float power = query_power<typename S::T>(top);
+            inverse[nr] = 1.f / power;
+#pragma unroll
+            for (int ks = 0; ks < S::DP / 16; ++ks) {
+                const uint32_t x = scaled_pair<typename S::T>(q[nr][ks][0], power);
+                const uint32_t y = scaled_pair<typename S::T>(q[nr][ks][1], power);
+                q[nr][ks][0] = S::FMT == kKvE4m3 ? x : __byte_perm(x, y, 0x5410);
+                q[nr][ks][1] = S::FMT == kKvE4m3 ? y : __byte_perm(x, y, 0x7632);
+            }
         }
     }
 }
 
-// Scores of the stage's tokens, before any scale.
+// Scores of the stage's tokens before any scale: lane (g, c) holds tokens
+// 16 mt + g and + 8, rows 8 nr + 2 c and + 1.
 template <class S>
-__device__ __forceinline__ void scores(uint32_t stage, const uint32_t (*q)[4], float (*s)[4]) {
+__device__ __forceinline__ void scores(uint32_t stage, const uint32_t (*q)[S::DP / 16][2], float (*s)[S::NR][4]) {
     const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int nt = 0; nt < S::kTokens / 8; ++nt)
+    for (int mt = 0; mt < S::kTokens / 16; ++mt) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) s[nt][i] = 0.f;
-    if (S::FMT == kKv16Bit) {
+        for (int nr = 0; nr < S::NR; ++nr)
 #pragma unroll
-        for (int ks = 0; ks < S::DP / 16; ++ks)
+            for (int i = 0; i < 4; ++i) s[mt][nr][i] = 0.f;
+        if (S::FMT == kKv16Bit) {
 #pragma unroll
-            for (int np = 0; np < S::kTokens / 16; ++np) {
-                uint32_t r[4];
-                ldsm4(stage + chunk_at<S, false>(16 * np + (lane & 7) + ((lane >> 4) << 3), 2 * ks + ((lane >> 3) & 1)),
-                      r);
-                mma16816<typename S::T>(s[2 * np], q[ks], r[0], r[1]);
-                mma16816<typename S::T>(s[2 * np + 1], q[ks], r[2], r[3]);
+            for (int ks = 0; ks < S::DP / 16; ++ks) {
+                uint32_t k[4];
+                ldsm4(stage + chunk_at<S, false>(16 * mt + (lane & 15), 2 * ks + (lane >> 4)), k);
+#pragma unroll
+                for (int nr = 0; nr < S::NR; ++nr) mma16816<typename S::M>(s[mt][nr], k, q[nr][ks][0], q[nr][ks][1]);
             }
-    } else {
-#pragma unroll
-        for (int nt = 0; nt < S::kTokens / 8; ++nt)
+        } else {
 #pragma unroll
             for (int h = 0; h < S::DP / 64; ++h) {
-                const uint4 v = lds16(stage + chunk_at<S, false>(8 * nt + (lane >> 2), 4 * h + (lane & 3)));
-                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                const uint4 x = lds16(stage + chunk_at<S, false>(16 * mt + (lane >> 2), 4 * h + (lane & 3)));
+                const uint4 y = lds16(stage + chunk_at<S, false>(16 * mt + 8 + (lane >> 2), 4 * h + (lane & 3)));
+                const uint32_t w[4] = {x.x, x.y, x.z, x.w}, u[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    uint32_t b0, b1;
-                    expand4<typename S::T, S::FMT>(w[j], b0, b1);
-                    mma16816<typename S::T>(s[nt], q[4 * h + j], b0, b1);
+                    uint32_t k[4];
+                    expand4<S::FMT>(w[j], k[0], k[2]);
+                    expand4<S::FMT>(u[j], k[1], k[3]);
+#pragma unroll
+                    for (int nr = 0; nr < S::NR; ++nr)
+                        mma16816<typename S::M>(s[mt][nr], k, q[nr][4 * h + j][0], q[nr][4 * h + j][1]);
                 }
             }
+        }
     }
 }
 
-// acc += p v over the stage's tokens; p as the fragments of its two parts.
+// acc += V' P' over the stage's tokens; p as the fragments of its two parts.
 template <class S>
-__device__ __forceinline__ void values(uint32_t stage, const uint32_t (*hi)[4], const uint32_t (*lo)[4],
-                                       float (*acc)[4]) {
+__device__ __forceinline__ void values(uint32_t stage, const uint32_t (*hi)[S::NR][2], const uint32_t (*lo)[S::NR][2],
+                                       float (*acc)[S::NR][4]) {
     const int lane = threadIdx.x & 31;
     const uint32_t v = stage + S::kSide;
 #pragma unroll
     for (int kt = 0; kt < S::kTokens / 16; ++kt) {
         if (S::FMT == kKv16Bit) {
 #pragma unroll
-            for (int j = 0; j < S::DP / 8; j += 2) {
-                uint32_t r[4];
-                ldsm4_trans(v + chunk_at<S, true>(16 * kt + (lane & 15), j + (lane >> 4)), r);
-                mma16816<typename S::T>(acc[j], hi[kt], r[0], r[1]);
-                mma16816<typename S::T>(acc[j + 1], hi[kt], r[2], r[3]);
-                mma16816<typename S::T>(acc[j], lo[kt], r[0], r[1]);
-                mma16816<typename S::T>(acc[j + 1], lo[kt], r[2], r[3]);
+            for (int j = 0; j < S::DP / 16; ++j) {
+                uint32_t x[4];
+                ldsm4_trans(v + chunk_at<S, true>(16 * kt + (lane & 7) + ((lane >> 4) << 3), 2 * j + ((lane >> 3) & 1)),
+                            x);
+#pragma unroll
+                for (int nr = 0; nr < S::NR; ++nr) {
+                    mma16816<typename S::M>(acc[j][nr], x, hi[kt][nr][0], hi[kt][nr][1]);
+                    mma16816<typename S::M>(acc[j][nr], x, lo[kt][nr][0], lo[kt][nr][1]);
+                }
             }
         } else {
             // lane (g, c): tokens 2c, 2c + 1, 2c + 8, 2c + 9, DP / 8 values from g DP / 8 on
@@ -257,117 +305,148 @@ __device__ __forceinline__ void values(uint32_t stage, const uint32_t (*hi)[4], 
             constexpr uint32_t kSecond = S::FMT == kKvE4m3 ? 0x7362 : 0x7632;
 #pragma unroll
             for (int j = 0; j < S::DP / 32; ++j) {
-                uint32_t b0[4], b1[4];
-                expand4<BfType, S::FMT>(__byte_perm(w[0][j], w[1][j], kFirst), b0[0], b0[1]);
-                expand4<BfType, S::FMT>(__byte_perm(w[0][j], w[1][j], kSecond), b0[2], b0[3]);
-                expand4<BfType, S::FMT>(__byte_perm(w[2][j], w[3][j], kFirst), b1[0], b1[1]);
-                expand4<BfType, S::FMT>(__byte_perm(w[2][j], w[3][j], kSecond), b1[2], b1[3]);
+                uint32_t x[2][4];
+                expand4<S::FMT>(__byte_perm(w[0][j], w[1][j], kFirst), x[0][0], x[0][1]);
+                expand4<S::FMT>(__byte_perm(w[2][j], w[3][j], kFirst), x[0][2], x[0][3]);
+                expand4<S::FMT>(__byte_perm(w[0][j], w[1][j], kSecond), x[1][0], x[1][1]);
+                expand4<S::FMT>(__byte_perm(w[2][j], w[3][j], kSecond), x[1][2], x[1][3]);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    mma16816<BfType>(acc[4 * j + i], hi[kt], b0[i], b1[i]);
-                    mma16816<BfType>(acc[4 * j + i], lo[kt], b0[i], b1[i]);
-                }
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int nr = 0; nr < S::NR; ++nr) {
+                        mma16816<typename S::M>(acc[2 * j + i][nr], x[i], hi[kt][nr][0], hi[kt][nr][1]);
+                        mma16816<typename S::M>(acc[2 * j + i][nr], x[i], lo[kt][nr][0], lo[kt][nr][1]);
+                    }
             }
         }
     }
 }
-// Channel of column n (0..7) of accumulator tile j.
+// Channel of accumulator tile j, lane group g, half h (element pairs 0, 1 or 2, 3).
 template <class S>
-__device__ __forceinline__ int channel(int j, int n) {
-    return S::FMT == kKv16Bit ? 8 * j + n : n * (S::DP / 8) + j;
+__device__ __forceinline__ int channel(int j, int g, int h) {
+    return S::FMT == kKv16Bit ? 16 * j + g + 8 * h : g * (S::DP / 8) + 2 * j + h;
 }
 
-// The running state of rows g and g + 8 of an item.
+// What a lane carries through an item: rows 8 nr + 2 c + i.
 template <class S>
 struct Running {
-    float m[2], l[2];  // maximum (base 2) of the row; this lane's part of the sum
-    float acc[S::DP / 8][4];
+    float m[S::NR][2], l[S::NR][2];  // reference (base 2) of the row; this lane's part of the sum
+    float acc[S::DP / 16][S::NR][4];
 };
 
-// One stage: scores, the softmax's step, values.  base: the stage's first token.
+// One stage: scores, the softmax's step, values.  base: the stage's first
+// token.  to_base2: the factor of each row's products.
 template <class S>
-__device__ __forceinline__ void step(const AttnArgs& t, const Piece& p, uint32_t stage, int32_t base,
-                                     const uint32_t (*q)[4], const int32_t* first, const int32_t* last, float to_base2,
-                                     Running<S>& st) {
-    const int lane = threadIdx.x & 31, c = lane & 3;
-    constexpr int NT = S::kTokens / 8;
-    float s[NT][4];
+__device__ __forceinline__ void step(uint32_t stage, int32_t base, const uint32_t (*q)[S::DP / 16][2],
+                                     const int32_t (*first)[2], const int32_t (*last)[2], bool whole_stage,
+                                     const float (*to_base2)[2], Running<S>& st) {
+    const int lane = threadIdx.x & 31, g = lane >> 2;
+    constexpr int MT = S::kTokens / 16;
+    float s[MT][S::NR][4];
     scores<S>(stage, q, s);
-    float vscale[NT][2];
+    float vscale[MT][2], extra = 0.f;
+    if (S::FMT != kKv16Bit) {
+        uint32_t top = 0;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-        float k0 = to_base2, k1 = to_base2;
-        if (S::FMT != kKv16Bit) {
-            const uint2 ks = lds8(stage + 2 * S::kSide + 4 * (8 * nt + 2 * c));
-            const uint2 vs = lds8(stage + 2 * S::kSide + 4 * S::kTokens + 4 * (8 * nt + 2 * c));
-            k0 *= __uint_as_float(ks.x);
-            k1 *= __uint_as_float(ks.y);
-            vscale[nt][0] = __uint_as_float(vs.x);
-            vscale[nt][1] = __uint_as_float(vs.y);
-        }
-        s[nt][0] *= k0;
-        s[nt][1] *= k1;
-        s[nt][2] *= k0;
-        s[nt][3] *= k1;
-    }
-    // hidden places: only where some row of this lane does not see the whole stage
-    if (base < max(first[0], first[1]) || base + S::kTokens > min(last[0], last[1])) {
+        for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+            for (int h = 0; h < 2; ++h) {
+                const uint32_t at = stage + 2 * S::kSide + 4 * (16 * mt + 8 * h + g);
+                const float ks = lds4(at);
+                vscale[mt][h] = lds4(at + 4 * S::kTokens);
+                top = max(top, __float_as_uint(vscale[mt][h]));
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int32_t j = base + 8 * nt + 2 * c + (i & 1);
-                if (j < first[i >> 1] || j >= last[i >> 1]) s[nt][i] = -INFINITY;
+                for (int nr = 0; nr < S::NR; ++nr) {
+                    s[mt][nr][2 * h] *= ks;
+                    s[mt][nr][2 * h + 1] *= ks;
+                }
             }
+        extra = scale_exponent(__reduce_max_sync(0xFFFFFFFFu, top));
     }
-    uint32_t hi[NT / 2][4], lo[NT / 2][4];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        float m = st.m[h];
+    for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) m = fmaxf(m, fmaxf(s[nt][2 * h], s[nt][2 * h + 1]));
-        m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-        m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-        const float from = m == -INFINITY ? 0.f : m;  // nothing seen so far: every term is 0
-        const float keep = exp2_fast(st.m[h] - from);
-        st.m[h] = m;
-        float sum = 0.f;
+        for (int nr = 0; nr < S::NR; ++nr)
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            float x = exp2_fast(s[nt][2 * h] - from), y = exp2_fast(s[nt][2 * h + 1] - from);
-            sum += x + y;
-            if (S::FMT != kKv16Bit) {
-                x *= vscale[nt][0];
-                y *= vscale[nt][1];
+            for (int i = 0; i < 4; ++i) s[mt][nr][i] *= to_base2[nr][i & 1];
+    if (!whole_stage) {  // some row of the item does not see all of it
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int nr = 0; nr < S::NR; ++nr)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int32_t j = base + 16 * mt + 8 * (i >> 1) + g;
+                    if (j < first[nr][i & 1] || j >= last[nr][i & 1]) s[mt][nr][i] = -INFINITY;
+                }
+    }
+    uint32_t hi[MT][S::NR][2], lo[MT][S::NR][2];
+    float keep[S::NR][2];
+    bool moved = false;
+#pragma unroll
+    for (int nr = 0; nr < S::NR; ++nr)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            float m = -INFINITY;
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) m = fmaxf(m, fmaxf(s[mt][nr][i], s[mt][nr][2 + i]));
+            m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 4));
+            m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 8));
+            m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 16));
+            m = fmaxf(st.m[nr][i], m + extra);
+            moved |= m != st.m[nr][i];
+            const float from = m == -INFINITY ? 0.f : m;  // nothing seen so far: every term is 0
+            keep[nr][i] = exp2_fast(st.m[nr][i] - from);
+            st.m[nr][i] = m;
+            float sum = 0.f;
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float x = exp2_fast(s[mt][nr][2 * h + i] - from);
+                    sum += x;
+                    if (S::FMT != kKv16Bit) x *= vscale[mt][h];
+                    s[mt][nr][2 * h + i] = x;
+                }
+            st.l[nr][i] = st.l[nr][i] * keep[nr][i] + sum;
+        }
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int nr = 0; nr < S::NR; ++nr)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint32_t x, y;
+                split_pair<typename S::M>(s[mt][nr][2 * h], s[mt][nr][2 * h + 1], x, y);
+                hi[mt][nr][h] = transpose8x8(x);
+                lo[mt][nr][h] = transpose8x8(y);
             }
-            using P = typename S::P;
-            split_pair<P>(x, y, hi[nt / 2][2 * (nt % 2) + h], lo[nt / 2][2 * (nt % 2) + h]);
-        }
-        st.l[h] = st.l[h] * keep + sum;
+    if (__any_sync(0xFFFFFFFFu, moved)) {
 #pragma unroll
-        for (int j = 0; j < S::DP / 8; ++j) {
-            st.acc[j][2 * h] *= keep;
-            st.acc[j][2 * h + 1] *= keep;
-        }
+        for (int j = 0; j < S::DP / 16; ++j)
+#pragma unroll
+            for (int nr = 0; nr < S::NR; ++nr)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) st.acc[j][nr][i] *= keep[nr][i & 1];
     }
     values<S>(stage, hi, lo, st.acc);
 }
 
 template <class S>
-__global__ void __launch_bounds__(kThreads, kBlocksPerSm)
+__global__ void __launch_bounds__(kThreads, S::kBlocksPerSm)
     attend_tokens_kernel(const __grid_constant__ KvArgs a, const __grid_constant__ AttnArgs t, uint32_t min_tiles,
                          int whole_items) {
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ uint64_t prefix[kMaxBatch + 1];
-    __shared__ float stats[2][kWarps][kRows];
+    __shared__ float stats[2][kWarps][S::kRows];
     __shared__ uint32_t odd_rows;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-    build_prefix<kRows, S::kTile>(a, t, prefix);
+    build_prefix<S::kRows, S::kTile>(a, t, prefix);
     const uint64_t T = prefix[a.batch];
     // no more shares than give each min_tiles tiles
     const uint32_t shares = (uint32_t)min((uint64_t)gridDim.x, max((T + min_tiles - 1) / min_tiles, (uint64_t)1));
-    const PartLayout parts = part_layout(a, (int)gridDim.x, kRows);
+    const PartLayout parts = part_layout(a, (int)gridDim.x, S::kRows);
     const uint32_t share = blockIdx.x;
     uint64_t x = share < shares ? share_start(T, share, shares) : T;
     const uint64_t x0 = x, x1 = share < shares ? share_start(T, share + 1, shares) : T;
@@ -376,7 +455,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     const uint32_t ring = smem_addr(smem) + warp * S::kRing;
     Piece p;
     while (x < x1) {
-        find_item<kRows, S::kTile>(a, t, prefix, x, p);
+        find_item<S::kRows, S::kTile>(a, t, prefix, x, p);
         const uint64_t end = p.item + (uint64_t)p.range.n;
         if (whole_items) {
             if (p.item < x) {  // the share before does all of it
@@ -388,31 +467,48 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
         } else {
             p.from = (int32_t)(x - p.item);
             p.count = (int32_t)(min(end, x1) - x);
-            if (x == x0 && threadIdx.x == 0) parts.cuts[share] = cut_of<kRows, S::kTile>(p, x0, T, share, shares);
+            if (x == x0 && threadIdx.x == 0) parts.cuts[share] = cut_of<S::kRows, S::kTile>(p, x0, T, share, shares);
         }
         const bool full = p.count == p.range.n;
         const int which = p.from > 0 ? 0 : 1;
         x += (uint64_t)p.count;
 
         const int64_t rows = (int64_t)p.seq.n * t.group;
-        const int32_t live = (int32_t)min((int64_t)kRows, rows - (int64_t)p.rt * kRows);
-        int32_t first[2], last[2];
+        const int32_t live = (int32_t)min((int64_t)S::kRows, rows - (int64_t)p.rt * S::kRows);
+        int32_t first[S::NR][2], last[S::NR][2], all_from = 0, all_to = 0x7FFFFFFF;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int64_t r = (int64_t)p.rt * kRows + g + 8 * h;
-            first[h] = last[h] = 0;
-            if (r < rows)
-                visible_range(t, p.seq.len, (int64_t)p.seq.len - p.seq.n + r / t.group, first[h], last[h]);
-        }
-        uint32_t q[S::DP / 16][4];
-        load_queries<S>(a, t, p, q);
+        for (int nr = 0; nr < S::NR; ++nr)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int64_t r = (int64_t)p.rt * S::kRows + 8 * nr + 2 * c + i;
+                first[nr][i] = last[nr][i] = 0;
+                if (r < rows) {
+                    visible_range(t, p.seq.len, (int64_t)p.seq.len - p.seq.n + r / t.group, first[nr][i], last[nr][i]);
+                    all_from = max(all_from, first[nr][i]);
+                    all_to = min(all_to, last[nr][i]);
+                }
+            }
+        // tokens that every row sees: all_from .. all_to - 1
+        all_from = __reduce_max_sync(0xFFFFFFFFu, all_from);
+        all_to = __reduce_min_sync(0xFFFFFFFFu, all_to);
+        uint32_t q[S::NR][S::DP / 16][2];
+        float inverse[S::NR], factor[S::NR][2];
+        load_queries<S>(a, t, p, q, inverse);
+#pragma unroll
+        for (int nr = 0; nr < S::NR; ++nr)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                factor[nr][i] = to_base2 * __shfl_sync(0xFFFFFFFFu, inverse[nr], 4 * (2 * c + i));
         Running<S> st;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) st.m[h] = -INFINITY, st.l[h] = 0.f;
+        for (int nr = 0; nr < S::NR; ++nr) {
 #pragma unroll
-        for (int j = 0; j < S::DP / 8; ++j)
+            for (int i = 0; i < 2; ++i) st.m[nr][i] = -INFINITY, st.l[nr][i] = 0.f;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) st.acc[j][i] = 0.f;
+            for (int j = 0; j < S::DP / 16; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) st.acc[j][nr][i] = 0.f;
+        }
 
         const int32_t base0 = (p.range.lo + p.from) * S::kTile + warp * S::kTokens;
 #pragma unroll
@@ -431,7 +527,8 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
             __syncwarp();
             const int32_t base = base0 + i * S::kTile;
             if (base < p.range.last && base + S::kTokens > p.range.first)
-                step<S>(t, p, ring + slot * S::kStage, base, q, first, last, to_base2, st);
+                step<S>(ring + slot * S::kStage, base, q, first, last, base >= all_from && base + S::kTokens <= all_to,
+                        factor, st);
             slot = slot + 1 == S::kStages ? 0 : slot + 1;
             __syncwarp();
         }
@@ -441,23 +538,26 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
         if (threadIdx.x == 0) odd_rows = 0;
         float* merge = reinterpret_cast<float*>(smem);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            float l = st.l[h];
-            l += __shfl_xor_sync(0xFFFFFFFFu, l, 1);
-            l += __shfl_xor_sync(0xFFFFFFFFu, l, 2);
-            const int row = g + 8 * h;
-            if (row < live) {
-                if (c == 0) {
-                    stats[0][warp][row] = st.m[h];
-                    stats[1][warp][row] = l;
+        for (int nr = 0; nr < S::NR; ++nr)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                float l = st.l[nr][i];
+                l += __shfl_xor_sync(0xFFFFFFFFu, l, 4);
+                l += __shfl_xor_sync(0xFFFFFFFFu, l, 8);
+                l += __shfl_xor_sync(0xFFFFFFFFu, l, 16);
+                const int row = 8 * nr + 2 * c + i;
+                if (row < live) {
+                    if (g == 0) {
+                        stats[0][warp][row] = st.m[nr][i];
+                        stats[1][warp][row] = l;
+                    }
+#pragma unroll
+                    for (int j = 0; j < S::DP / 16; ++j)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+                            merge[(warp * S::kRows + row) * (S::DP + 4) + channel<S>(j, g, h)] = st.acc[j][nr][2 * h + i];
                 }
-#pragma unroll
-                for (int j = 0; j < S::DP / 8; ++j)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i)
-                        merge[(warp * kRows + row) * (S::DP + 4) + channel<S>(j, 2 * c + i)] = st.acc[j][2 * h + i];
             }
-        }
         __syncthreads();
         const int groups = a.dim / 8;
         for (int w = threadIdx.x; w < live * groups; w += kThreads) {
@@ -471,7 +571,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
             for (int i = 0; i < kWarps; ++i) {
                 const float f = exp2_fast(stats[0][i][row] - from);
                 sum += f * stats[1][i][row];
-                const float4* src = reinterpret_cast<const float4*>(&merge[(i * kRows + row) * (S::DP + 4) + d]);
+                const float4* src = reinterpret_cast<const float4*>(&merge[(i * S::kRows + row) * (S::DP + 4) + d]);
                 const float4 lo = src[0], hi = src[1];
                 v[0] += f * lo.x;
                 v[1] += f * lo.y;
@@ -488,17 +588,17 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
                 dst[1] = make_float4(v[4], v[5], v[6], v[7]);
                 if (d == 0) {
                     parts.stats(share, which)[row] = m;
-                    parts.stats(share, which)[kRows + row] = sum;
+                    parts.stats(share, which)[S::kRows + row] = sum;
                 }
                 continue;
             }
-            if (store_row_part<typename S::T>(t, p, kRows, row, d, v, m, sum)) atomicOr(&odd_rows, 1u << row);
+            if (store_row_part<typename S::T>(t, p, S::kRows, row, d, v, m, sum)) atomicOr(&odd_rows, 1u << row);
         }
         __syncthreads();
         if (full) {
             for (uint32_t odd = odd_rows; odd != 0; odd &= odd - 1) {
                 const int row = __ffs(odd) - 1;
-                if (row % kWarps == warp) fix_row<typename S::T, S::FMT>(a, t, p, kRows, row);
+                if (row % kWarps == warp) fix_row<typename S::T, S::FMT>(a, t, p, S::kRows, row);
             }
             __syncthreads();
         }
@@ -515,33 +615,40 @@ cudaError_t launch_tokens(const KvArgs& a, const AttnArgs& t, bool whole, uint32
         return cudaFuncSetAttribute(attend_tokens_kernel<S>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
     });
     if (e != cudaSuccess) return e;
-    attend_tokens_kernel<S><<<kShares, kThreads, S::kSmem, s>>>(a, t, min_tiles, whole ? 1 : 0);
+    attend_tokens_kernel<S><<<S::kShares, kThreads, S::kSmem, s>>>(a, t, min_tiles, whole ? 1 : 0);
     e = cudaGetLastError();
     if (e != cudaSuccess || whole) return e;
-    return launch_join<typename S::T, S::FMT, kRows>(a, t, kShares, s);
+    return launch_join<typename S::T, S::FMT, S::kRows>(a, t, S::kShares, s);
 }
 
+template <class T, int FMT, int DP>
+cudaError_t launch_rows(const KvArgs& a, const AttnArgs& t, bool few, bool whole, uint32_t min_tiles, cudaStream_t s) {
+    return few ? launch_tokens<Shape<T, FMT, DP, 1>>(a, t, whole, min_tiles, s)
+               : launch_tokens<Shape<T, FMT, DP, 2>>(a, t, whole, min_tiles, s);
+}
 template <class T, int FMT>
-cudaError_t launch_dim(const KvArgs& a, const AttnArgs& t, bool whole, uint32_t min_tiles, cudaStream_t s) {
-    return a.dim <= 64 ? launch_tokens<Shape<T, FMT, 64>>(a, t, whole, min_tiles, s)
-                       : launch_tokens<Shape<T, FMT, 128>>(a, t, whole, min_tiles, s);
+cudaError_t launch_dim(const KvArgs& a, const AttnArgs& t, bool few, bool whole, uint32_t min_tiles, cudaStream_t s) {
+    return a.dim <= 64 ? launch_rows<T, FMT, 64>(a, t, few, whole, min_tiles, s)
+                       : launch_rows<T, FMT, 128>(a, t, few, whole, min_tiles, s);
 }
 
 }  // namespace
 
-size_t kv_tokens_scratch(int dim) { return part_bytes(kShares, kRows, dim); }
+size_t kv_tokens_scratch(int dim) { return part_bytes(kMaxShares, 16, dim); }
 
-cudaError_t launch_kv_tokens(int dtype, int format, const KvArgs& a, const AttnArgs& t, int max_len, cudaStream_t s) {
+cudaError_t launch_kv_tokens(int dtype, int format, const KvArgs& a, const AttnArgs& t, int max_new, int max_len,
+                             cudaStream_t s) {
     const bool whole = max_len <= 128;
     const uint32_t min_tiles = 1;
+    const bool few = (int64_t)t.group * max_new <= 8;
     if (dtype == (int)Bf16::kCode) {
-        if (format == kKv16Bit) return launch_dim<BfType, kKv16Bit>(a, t, whole, min_tiles, s);
-        return format == kKvInt8 ? launch_dim<BfType, kKvInt8>(a, t, whole, min_tiles, s)
-                                 : launch_dim<BfType, kKvE4m3>(a, t, whole, min_tiles, s);
+        if (format == kKv16Bit) return launch_dim<BfType, kKv16Bit>(a, t, few, whole, min_tiles, s);
+        return format == kKvInt8 ? launch_dim<BfType, kKvInt8>(a, t, few, whole, min_tiles, s)
+                                 : launch_dim<BfType, kKvE4m3>(a, t, few, whole, min_tiles, s);
     }
-    if (format == kKv16Bit) return launch_dim<HfType, kKv16Bit>(a, t, whole, min_tiles, s);
-    return format == kKvInt8 ? launch_dim<HfType, kKvInt8>(a, t, whole, min_tiles, s)
-                             : launch_dim<HfType, kKvE4m3>(a, t, whole, min_tiles, s);
+    if (format == kKv16Bit) return launch_dim<HfType, kKv16Bit>(a, t, few, whole, min_tiles, s);
+    return format == kKvInt8 ? launch_dim<HfType, kKvInt8>(a, t, few, whole, min_tiles, s)
+                             : launch_dim<HfType, kKvE4m3>(a, t, few, whole, min_tiles, s);
 }
 
 }  // namespace cccl
