@@ -56,9 +56,10 @@ struct AttnArgs {
     uint8_t* out;
     float* lse;
     int64_t q_token, q_head, o_token, o_head;
-    int64_t window;  // 0: none
     float scale;
-    int32_t causal, group, q_heads;
+    int32_t window;  // 0: none
+    int32_t causal, q_heads;
+    FastDiv group;  // query heads that share a kv head
 };
 
 // Sequence b's rows and length, with everything that does not fit clamped
@@ -102,12 +103,10 @@ __device__ __forceinline__ bool slot_of(const KvArgs& a, int b, uint32_t p, int6
 
 // The keys that a row at position `pos` of a sequence of `len` tokens sees:
 // first .. last - 1 (empty when last <= first).
-__device__ __forceinline__ void visible_range(const AttnArgs& t, int32_t len, int64_t pos, int32_t& first,
+__device__ __forceinline__ void visible_range(const AttnArgs& t, int32_t len, int32_t pos, int32_t& first,
                                               int32_t& last) {
-    const int64_t hi = t.causal ? min((int64_t)len, pos + 1) : (int64_t)len;
-    const int64_t lo = t.window > 0 ? pos - t.window + 1 : 0;
-    last = (int32_t)max(hi, (int64_t)0);
-    first = (int32_t)min(max(lo, (int64_t)0), (int64_t)last);
+    last = max(t.causal ? min(len, pos + 1) : len, 0);
+    first = t.window > 0 && pos >= t.window ? min(pos - t.window + 1, last) : 0;
 }
 
 // ---------------------------------------------------------------- values
@@ -161,6 +160,22 @@ __device__ __forceinline__ void expand4(uint32_t w, uint32_t& a, uint32_t& b) {
             : "r"(w));
     } else {
         const uint32_t x = (w & 0x00FF00FFu) ^ 0x64806480u, y = ((w >> 8) & 0x00FF00FFu) ^ 0x64806480u;
+        const __half2 bias = __half2half2(__ushort_as_half(0x6480));  // 1152
+        const __half2 p = __hsub2(*reinterpret_cast<const __half2*>(&x), bias);
+        const __half2 q = __hsub2(*reinterpret_cast<const __half2*>(&y), bias);
+        a = *reinterpret_cast<const uint32_t*>(&p);
+        b = *reinterpret_cast<const uint32_t*>(&q);
+    }
+}
+
+// The same, in the order (0, 1), (2, 3) for both.
+template <int FMT>
+__device__ __forceinline__ void expand4_in_order(uint32_t w, uint32_t& a, uint32_t& b) {
+    if (FMT == kKvE4m3) {
+        expand4<FMT>(w, a, b);
+    } else {
+        const uint32_t u = w ^ 0x80808080u;
+        const uint32_t x = __byte_perm(u, 0x64646464u, 0x4140), y = __byte_perm(u, 0x64646464u, 0x4342);
         const __half2 bias = __half2half2(__ushort_as_half(0x6480));  // 1152
         const __half2 p = __hsub2(*reinterpret_cast<const __half2*>(&x), bias);
         const __half2 q = __hsub2(*reinterpret_cast<const __half2*>(&y), bias);
@@ -227,9 +242,9 @@ __device__ __forceinline__ void copy_wait() {
 // Lane l holds values l, l + 32, l + 64, l + 96 of the head.
 template <class T, int FMT>
 __device__ __noinline__ void attend_row(const KvArgs& a, const AttnArgs& t, int b, int32_t len, int64_t row,
-                                        int64_t pos, int head) {
+                                        int32_t pos, int head) {
     const int lane = threadIdx.x & 31;
-    const int kv_head = head / t.group;
+    const int kv_head = (int)div_by(t.group, (uint32_t)head);
     const uint16_t* q = reinterpret_cast<const uint16_t*>(t.q + row * t.q_token + (int64_t)head * t.q_head);
     float qv[4], acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll

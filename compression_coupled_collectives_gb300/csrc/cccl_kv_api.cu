@@ -163,6 +163,7 @@ cccl_status cccl_kv_attention(const cccl_kv_cache* h_cache, const cccl_kv_batch*
         (causal != 0 && causal != 1) || !(scale >= -3.402823466e+38f && scale <= 3.402823466e+38f))
         return CCCL_ERR_INVALID_ARG;
     if (empty(b)) return CCCL_OK;
+    if (b->n_tokens > INT32_MAX / q_heads) return CCCL_ERR_INVALID_ARG;
     cccl::KvArgs a{};
     if (!fill(c, b, d_ws, ws_bytes, cccl_kv_workspace_bytes(c, b, q_heads), &a) ||
         !packed_ok(d_q, b->n_tokens, q_heads, c->head_dim, q_token_stride, q_head_stride) ||
@@ -179,10 +180,10 @@ cccl_status cccl_kv_attention(const cccl_kv_cache* h_cache, const cccl_kv_batch*
     t.q_head = 2 * q_head_stride;
     t.o_token = 2 * o_token_stride;
     t.o_head = 2 * o_head_stride;
-    t.window = window < (int64_t)INT32_MAX ? window : 0;  // one that hides nothing is none
+    t.window = window < INT32_MAX ? (int32_t)window : 0;  // one that hides nothing is none
     t.scale = scale;
     t.causal = causal;
-    t.group = q_heads / c->kv_heads;
+    t.group = cccl::fast_div((uint32_t)(q_heads / c->kv_heads));
     t.q_heads = q_heads;
     const cudaError_t e = cccl::launch_kv_attention(c->dtype, c->format, a, t, b->max_new, b->max_len,
                                                     reinterpret_cast<cudaStream_t>(stream));

@@ -18,6 +18,8 @@
 // 256.  The products of one thread execute in order, so a full S also means
 // that the previous O is done, and S may be written over the P that the
 // product before it reads.
+#include <cuda.h>
+
 #include <type_traits>
 
 #include "cccl_kv.cuh"
@@ -32,28 +34,37 @@ namespace {
 constexpr int kRows = 256, kTileRows = 128, kTokens = 128;
 constexpr int kThreads = 512;
 constexpr int kShares = 152;
-constexpr int kSlots = 4;        // K and V tiles in shared memory
 constexpr int kScaleSlots = 4;   // tiles of tokens whose scales are kept
 constexpr int kLoaderWarps = 4;
+// K and V tiles in shared memory, as 16-bit values; tiles of 8-bit codes on
+// their way there
+constexpr int kMostSlots = 4, kRawSlots = 3;
+template <int FMT>
+constexpr int kSlots = FMT == kKv16Bit ? 4 : 3;
 constexpr float kSlack = 8.f;    // base 2
 
 // Registers of a thread: the launch's 4 x 128 a warpgroup, divided anew (two
-// softmax warpgroups, the loaders, and 64 for the issuing warp's).
+// softmax warpgroups, two of the others).
 template <int FMT>
 constexpr int kSoftmaxRegs = FMT == kKv16Bit ? 192 : 176;
 template <int FMT>
-constexpr int kLoaderRegs = FMT == kKv16Bit ? 64 : 96;
+constexpr int kLoaderRegs = 256 - kSoftmaxRegs<FMT>;
 
 // TMEM columns
 constexpr uint32_t kColS = 0, kColO = 256;  // S of row tile i at 128 i (P over it), O at 256 + 128 i
 
 struct Shared {
     uint64_t q_full[2], s_full[2], p_full[2], o_full[2];
-    uint64_t kv_full[kSlots], kv_free[kSlots], scale_full[kScaleSlots];
+    uint64_t kv_full[kMostSlots], kv_free[kMostSlots], scale_full[kScaleSlots];
+    uint64_t raw_full[kRawSlots], raw_free[kRawSlots];
     uint64_t drained;
     uint32_t tmem;
     uint32_t stop;  // a bounded wait ran out: every role leaves
     uint64_t prefix[kMaxBatch + 1];
+    // each softmax warp's way along the line and its pieces (this one, the next
+    // one): here, so that a thread's registers are free for its row of S
+    Walk walk[8];
+    Piece piece[8][2];
     alignas(16) float k_scale[kScaleSlots][kTokens];
     alignas(16) float v_scale[kScaleSlots][kTokens];
     alignas(16) uint32_t v_top[kScaleSlots][kLoaderWarps];  // the largest value scale of each warp's rows
@@ -180,36 +191,6 @@ __device__ __forceinline__ uint32_t pack<HfType>(float lo, float hi) {
 template <class T, int FMT>
 using Operand = typename std::conditional<FMT == kKv16Bit, T, HfType>::type;
 
-// A share's pieces, one after the other (every role walks them by itself).
-struct Walk {
-    uint64_t x, x0, x1, T;
-    uint32_t share, shares;
-    int32_t whole;
-};
-__device__ __forceinline__ bool next_piece(const KvArgs& a, const AttnArgs& t, const uint64_t* prefix, Walk& w,
-                                           Piece& p) {
-    while (w.x < w.x1) {
-        find_item<kRows, kTokens>(a, t, prefix, w.x, p);
-        const uint64_t end = p.item + (uint64_t)p.range.n;
-        if (w.whole) {
-            const bool before = p.item < w.x;
-            w.x = end;
-            if (before) continue;  // the share before does all of it
-            p.from = 0;
-            p.count = p.range.n;
-        } else {
-            p.from = (int32_t)(w.x - p.item);
-            p.count = (int32_t)(min(end, w.x1) - w.x);
-            w.x += (uint64_t)p.count;
-        }
-        return true;
-    }
-    return false;
-}
-__device__ __forceinline__ int live_rows(const AttnArgs& t, const Piece& p) {
-    return (int)min((int64_t)kRows, (int64_t)p.seq.n * t.group - (int64_t)p.rt * kRows);
-}
-
 // A bounded wait of one role; false: leave (this wait or another's ran out).
 struct Waiter {
     Shared* sh;
@@ -223,158 +204,215 @@ struct Waiter {
 };
 
 // ---------------------------------------------------------------- K and V
-// Loader warp w brings rows 32 w .. 32 w + 31 of every tile.
+// Tiles come through a ring, K and V in turn.  A tile that every row of the
+// item's range covers is brought by TMA, a page (or 128 tokens) a box, each lane
+// of one warp issuing one box; one that the range cuts, or pages that TMA's
+// boxes do not fit (`box` is 0), by 16-byte copies that put zeros where the
+// range ends, so that no product meets what nobody wrote.
+struct Fetch {
+    const CUtensorMap *k, *v;
+    int32_t box;  // tokens of a TMA box; 0: none
+};
 struct TileRow {
-    int64_t at, scale_at;
+    int64_t at;
     bool real;
 };
 __device__ __forceinline__ TileRow tile_row(const KvArgs& a, const Piece& p, int32_t pos) {
-    TileRow r{0, 0, false};
+    TileRow r{0, false};
+    int64_t ignore;
     if (pos >= p.range.first && pos < p.range.last) {
-        r.real = slot_of(a, p.b, (uint32_t)pos, r.at, r.scale_at);
-        if (!r.real) r.at = r.scale_at = 0;
+        r.real = slot_of(a, p.b, (uint32_t)pos, r.at, ignore);
+        if (!r.real) r.at = 0;
     }
     r.at += (int64_t)p.kv_head * a.head_stride;
-    r.scale_at += (int64_t)p.kv_head * a.s_head;
     return r;
 }
-// 16-bit values go straight to shared memory.
-__device__ __forceinline__ void copy_tile(const KvArgs& a, const uint8_t* data, uint32_t slot, const TileRow& r,
-                                          int warp, int lane, int chunks) {
-    // chunks (16 bytes each) of a row: up to 16; lanes beyond them idle
-    const int per_row = chunks > 8 ? 16 : 8, rows_per_pass = 32 / per_row;
-    const int chunk = lane % per_row;
-#pragma unroll 8
-    for (int i = 0; i < 32 / rows_per_pass; ++i) {
-        const int local = i * rows_per_pass + lane / per_row;
-        const int64_t at = __shfl_sync(0xFFFFFFFFu, r.at, local);
-        const bool real = __shfl_sync(0xFFFFFFFFu, (int)r.real, local) != 0;
-        if (chunk < chunks) copy16(slot + swizzled(32 * warp + local, chunk), data + (real ? at + 16 * chunk : 0), real);
-    }
+__device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, int32_t d, int32_t slot, int32_t head,
+                                        int32_t page, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+        "[%6];" ::"r"(dst),
+        "l"(map), "r"(d), "r"(slot), "r"(head), "r"(page), "r"(smem_addr(bar))
+        : "memory");
+}
+__device__ __forceinline__ void arrive_expect(uint64_t* bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_addr(bar)), "r"(bytes) : "memory");
 }
 
-// 8-bit codes pass through registers: a lane takes 16 codes of a row at a time
-// and stores them as 16-bit values.  Lanes of a row's second half store their
-// two chunks the other way round, so that a row's eight lanes meet all banks.
-constexpr int kCodePasses = 8;  // 32 rows, at least 4 a pass
-struct Codes {
-    uint4 w[kCodePasses];
-};
-__device__ __forceinline__ void fetch_codes(const uint8_t* data, const TileRow& r, int lane, int chunks, Codes& c) {
-    const int per_row = chunks > 4 ? 8 : 4, rows_per_pass = 32 / per_row, chunk = lane % per_row;
-#pragma unroll
-    for (int i = 0; i < kCodePasses; ++i) {
-        c.w[i] = make_uint4(0, 0, 0, 0);
-        if (i < per_row) {
-            const int local = i * rows_per_pass + lane / per_row;
-            const int64_t at = __shfl_sync(0xFFFFFFFFu, r.at, local);
-            const bool real = __shfl_sync(0xFFFFFFFFu, (int)r.real, local) != 0;
-            if (real && chunk < chunks) c.w[i] = *reinterpret_cast<const uint4*>(data + at + 16 * chunk);
-        }
-    }
-}
-template <int FMT>
-__device__ __forceinline__ void store_codes(const Codes& c, uint32_t slot, int warp, int lane, int chunks) {
-    const int per_row = chunks > 4 ? 8 : 4, rows_per_pass = 32 / per_row, chunk = lane % per_row;
-#pragma unroll
-    for (int i = 0; i < kCodePasses; ++i) {
-        if (i < per_row && chunk < chunks) {
-            const uint32_t row = 32 * warp + i * rows_per_pass + lane / per_row;
-            const uint32_t w[4] = {c.w[i].x, c.w[i].y, c.w[i].z, c.w[i].w};
-            uint32_t v[8];
-#pragma unroll
-            for (int k = 0; k < 4; ++k)  // in the row's order
-                expand4<FMT>(FMT == kKvInt8 ? __byte_perm(w[k], 0, 0x3120) : w[k], v[2 * k], v[2 * k + 1]);
-            const int second = chunk >> 2;  // which of the two goes first
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const int part = k ^ second;
-                const uint32_t at = slot + swizzled(row, 2 * chunk + part);
-                asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(part ? v[4] : v[0]),
-                             "r"(part ? v[5] : v[1]), "r"(part ? v[6] : v[2]), "r"(part ? v[7] : v[3])
-                             : "memory");
-            }
-        }
-    }
-}
-
-template <class T, int FMT>
-__device__ __forceinline__ void load_role(const KvArgs& a, const AttnArgs& t, Shared* sh, uint32_t slots,
-                                          uint32_t slot_bytes, Walk w) {
-    const int warp = (threadIdx.x >> 5) - 8, lane = threadIdx.x & 31;
+// The role of WARPS warps (this one is `warp`): every tile of the share's
+// pieces to slots of slot_bytes from `slots` on; full[s] is arrived at by each
+// of the warps.
+template <int FMT, int WARPS, int SLOTS>
+__device__ __forceinline__ void fetch_role(const KvArgs& a, const AttnArgs& t, Shared* sh, const Fetch& f, int warp,
+                                           uint32_t slots, uint32_t slot_bytes, uint64_t* full, uint64_t* free_,
+                                           Walk w) {
+    constexpr bool kWide = FMT == kKv16Bit;      // 16-bit values in the swizzled layout; else codes, row after row
+    constexpr int kParts = 4 / WARPS;            // groups of 32 rows of this warp
+    const int lane = threadIdx.x & 31;
     const Waiter wait{sh, a.ws};
-    const int chunks = a.dim * (FMT == kKv16Bit ? 2 : 1) / 16;
-    uint32_t entry = 0, published = 0;  // K and V tiles, alternating
-    Piece p;
-    auto publish_to = [&](uint32_t upto) {
-        fence_proxy_async_smem();
+    const int chunks = a.dim * (kWide ? 2 : 1) / 16, per_row = chunks > 8 ? 16 : 8, chunk = lane % per_row;
+    const int boxes = f.box > 0 ? kTokens / f.box : 1, halves = kWide ? (a.dim > 64 ? 2 : 1) : 1;
+    const int box = lane % boxes, half = lane / boxes;
+    uint32_t entry = 0, handed = 0;
+    auto hand_over = [&](uint32_t upto) {  // this warp's copies of entries below `upto` are done
+        if (handed >= upto) return;
+        if (kWide) fence_proxy_async_smem();
         __syncwarp();
-        for (; published < upto; ++published)
-            if (lane == 0) mbar_arrive(&sh->kv_full[published % kSlots]);
+        for (; handed < upto; ++handed)
+            if (lane == 0) mbar_arrive(&full[handed % SLOTS]);
     };
-    while (next_piece(a, t, sh->prefix, w, p)) {
-        const int32_t base = (p.range.lo + p.from) * kTokens + 32 * warp + lane;
-        TileRow r = tile_row(a, p, base);
-        Codes codes;
-        float ks = 0.f, vs = 0.f;
-        if (FMT != kKv16Bit) {
-            fetch_codes(a.k, r, lane, chunks, codes);
-            if (r.real) ks = a.k_scale[r.scale_at], vs = a.v_scale[r.scale_at];
-        }
+    Piece p;
+    p.item = 0;
+    while (next_piece<kRows, kTokens>(a, t, sh->prefix, w, p)) {
+        const int32_t base = (p.range.lo + p.from) * kTokens;
         for (int32_t j = 0; j < p.count; ++j) {
-            const TileRow here = r;
-            if (j + 1 < p.count) r = tile_row(a, p, base + (j + 1) * kTokens);
-#pragma unroll
-            for (int side = 0; side < 2; ++side, ++entry) {
-                const uint32_t s = entry % kSlots, use = entry / kSlots;
-                const uint32_t slot = slots + s * slot_bytes;
-                if (use > 0 && !__all_sync(0xFFFFFFFFu, mbar_test(&sh->kv_free[s], (use - 1) & 1))) {
-                    // about to wait: hand over what has been brought so far
-                    if (FMT == kKv16Bit) {
-                        copy_wait<0>();
-                        publish_to(entry);
-                    }
-                    if (!__all_sync(0xFFFFFFFFu, wait(&sh->kv_free[s], (use - 1) & 1))) return;
+            const int32_t at = base + j * kTokens;
+            const bool tma = f.box > 0 && at >= p.range.first && at + kTokens <= p.range.last;
+            TileRow rows[kParts];
+            int32_t page = 0, slot0 = 0;
+            if (tma) {
+                if (warp == 0 && half < halves) {
+                    const uint32_t pos = (uint32_t)(at + box * f.box), pi = div_by(a.page_tokens, pos);
+                    slot0 = (int32_t)(pos - pi * a.page_tokens.d);
+                    page = (int32_t)page_of(a, p.b, pi);  // -1: outside the map, zeros
                 }
-                if (FMT == kKv16Bit) {
-                    copy_tile(a, side ? a.v : a.k, slot, here, warp, lane, chunks);
-                    copy_commit();
-                    copy_wait<2>();
-                    if (entry >= 2) publish_to(entry - 1);
+            } else {
+#pragma unroll
+                for (int i = 0; i < kParts; ++i) rows[i] = tile_row(a, p, at + 32 * (warp * kParts + i) + lane);
+            }
+#pragma unroll 1
+            for (int side = 0; side < 2; ++side, ++entry) {
+                const uint32_t s = entry % SLOTS, use = entry / SLOTS;
+                const uint32_t dst = slots + s * slot_bytes;
+                if (use > 0 && !__all_sync(0xFFFFFFFFu, mbar_test(&free_[s], (use - 1) & 1))) {
+                    // about to wait: hand over what has been brought so far
+                    copy_wait<0>();
+                    hand_over(entry);
+                    if (!__all_sync(0xFFFFFFFFu, wait(&free_[s], (use - 1) & 1))) return;
+                }
+                if (tma) {
+                    copy_wait<0>();
+                    hand_over(entry);
+                    ++handed;
+                    if (warp == 0) {
+                        if (lane == 0) arrive_expect(&full[s], slot_bytes);
+                        __syncwarp();
+                        if (half < halves)
+                            tma_box(dst + (kWide ? half * kHalfBytes + box * f.box * 128 : box * f.box * a.dim),
+                                    side ? f.v : f.k, 64 * half, slot0, p.kv_head, page, &full[s]);
+                    } else if (lane == 0) {
+                        mbar_arrive(&full[s]);
+                    }
                     continue;
                 }
-                // this side's codes are here; the next side's are asked for before they are worked on
-                const Codes now = codes;
-                if (side == 0) {
-                    fetch_codes(a.v, here, lane, chunks, codes);
-                    const uint32_t n = (entry / 2) % kScaleSlots;
-                    sh->k_scale[n][32 * warp + lane] = ks;
-                    sh->v_scale[n][32 * warp + lane] = vs;
-                    const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(vs));
-                    if (lane == 0) sh->v_top[n][warp] = top;
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&sh->scale_full[n]);
-                    store_codes<FMT>(now, slot, warp, lane, chunks);
-                } else {
-                    ks = vs = 0.f;
-                    if (j + 1 < p.count) {
-                        fetch_codes(a.k, r, lane, chunks, codes);
-                        if (r.real) ks = a.k_scale[r.scale_at], vs = a.v_scale[r.scale_at];
+                const uint8_t* data = side ? a.v : a.k;
+#pragma unroll
+                for (int part = 0; part < kParts; ++part)
+#pragma unroll 4
+                    for (int i = 0; i < per_row; ++i) {  // 32 / per_row rows a pass
+                        const int local = i * (32 / per_row) + lane / per_row;
+                        const int64_t from = __shfl_sync(0xFFFFFFFFu, rows[part].at, local);
+                        const bool real = __shfl_sync(0xFFFFFFFFu, (int)rows[part].real, local) != 0;
+                        const int row = 32 * (warp * kParts + part) + local;
+                        const uint32_t to = dst + (kWide ? swizzled(row, chunk) : (uint32_t)(row * a.dim + 16 * chunk));
+                        if (chunk < chunks) copy16(to, data + (real ? from + 16 * chunk : 0), real);
                     }
-                    store_codes<FMT>(now, slot, warp, lane, chunks);
-                }
-                publish_to(entry + 1);
+                copy_commit();
+                copy_wait<1>();
+                hand_over(entry);
             }
         }
     }
-    if (FMT == kKv16Bit) {
-        copy_wait<0>();
-        publish_to(entry);
+    copy_wait<0>();
+    hand_over(entry);
+}
+
+// 8-bit caches: codes to fp16, four warps of 32 rows each.  A lane takes 16
+// codes of a row at a time; lanes of a row's second half store their two
+// chunks the other way round, so that a row's eight lanes meet all banks.
+template <int FMT>
+__device__ __forceinline__ void widen_rows(uint32_t from, uint32_t to, int dim, int warp, int lane) {
+    const int chunks = dim / 16, per_row = chunks > 4 ? 8 : 4, chunk = lane % per_row;
+    if (chunk >= chunks) return;
+#pragma unroll 4
+    for (int i = 0; i < per_row; ++i) {  // 32 / per_row rows a pass
+        const uint32_t row = 32 * warp + i * (32 / per_row) + lane / per_row;
+        uint4 x;
+        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
+                     : "r"(from + row * dim + 16 * chunk));
+        const uint32_t c[4] = {x.x, x.y, x.z, x.w};
+        uint32_t v[8];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) expand4_in_order<FMT>(c[k], v[2 * k], v[2 * k + 1]);
+        const int second = chunk >> 2;  // which of the two goes first
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int part = k ^ second;
+            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(to + swizzled(row, 2 * chunk + part)),
+                         "r"(part ? v[4] : v[0]), "r"(part ? v[5] : v[1]), "r"(part ? v[6] : v[2]),
+                         "r"(part ? v[7] : v[3])
+                         : "memory");
+        }
+    }
+}
+// A row's scales (zeros where the range ends: nothing is multiplied there).
+struct RowScales {
+    float k, v;
+};
+__device__ __forceinline__ RowScales row_scales(const KvArgs& a, const Piece& p, int32_t pos) {
+    RowScales r{0.f, 0.f};
+    int64_t ignore, at;
+    if (pos >= p.range.first && pos < p.range.last && slot_of(a, p.b, (uint32_t)pos, ignore, at)) {
+        at += (int64_t)p.kv_head * a.s_head;
+        r.k = a.k_scale[at];
+        r.v = a.v_scale[at];
+    }
+    return r;
+}
+template <int FMT>
+__device__ __forceinline__ void widen_role(const KvArgs& a, const AttnArgs& t, Shared* sh, uint32_t raw,
+                                           uint32_t raw_bytes, uint32_t slots, uint32_t slot_bytes, Walk w) {
+    constexpr int kN = kSlots<FMT>;
+    const int warp = (threadIdx.x >> 5) - 8, lane = threadIdx.x & 31;
+    const Waiter wait{sh, a.ws};
+    uint32_t entry = 0;
+    Piece p;
+    p.item = 0;
+    while (next_piece<kRows, kTokens>(a, t, sh->prefix, w, p)) {
+        const int32_t base = (p.range.lo + p.from) * kTokens + 32 * warp + lane;
+        RowScales scales = row_scales(a, p, base);
+        for (int32_t j = 0; j < p.count; ++j) {
+            {
+                // V of tile j - 1 has a slot, so K of tile j - 2 was freed, so both
+                // row tiles are done with the scales of tile j - 3: four slots do
+                const uint32_t n = (entry / 2) % kScaleSlots;
+                sh->k_scale[n][32 * warp + lane] = scales.k;
+                sh->v_scale[n][32 * warp + lane] = scales.v;
+                const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(scales.v));
+                if (lane == 0) sh->v_top[n][warp] = top;
+            }
+            if (j + 1 < p.count) scales = row_scales(a, p, base + (j + 1) * kTokens);
+#pragma unroll 1
+            for (int side = 0; side < 2; ++side, ++entry) {
+                const uint32_t s = entry % kN, use = entry / kN, q = entry % kRawSlots, turn = entry / kRawSlots;
+                if (!__all_sync(0xFFFFFFFFu, wait(&sh->raw_full[q], turn & 1))) return;
+                if (use > 0 && !__all_sync(0xFFFFFFFFu, wait(&sh->kv_free[s], (use - 1) & 1))) return;
+                widen_rows<FMT>(raw + q * raw_bytes, slots + s * slot_bytes, a.dim, warp, lane);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    if (side == 0) mbar_arrive(&sh->scale_full[(entry / 2) % kScaleSlots]);
+                    mbar_arrive(&sh->kv_full[s]);
+                    mbar_arrive(&sh->raw_free[q]);
+                }
+            }
+        }
     }
 }
 
 // ---------------------------------------------------------------- products
-template <class M>
+template <class M, int SLOTS>
 __device__ __forceinline__ void mma_role(const KvArgs& a, const AttnArgs& t, Shared* sh, uint32_t q_base,
                                          uint32_t slots, uint32_t slot_bytes, Walk w) {
     const Waiter wait{sh, a.ws};
@@ -384,52 +422,67 @@ __device__ __forceinline__ void mma_role(const KvArgs& a, const AttnArgs& t, Sha
     const uint32_t q_bytes = slot_bytes;
     uint32_t entry = 0;
     uint32_t q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
+    // the whole warp walks; one lane issues
+    uint32_t leader;
+    asm volatile("{ .reg .pred p; elect.sync _|p, 0xFFFFFFFF; selp.u32 %0, 1, 0, p; }" : "=r"(leader));
     auto product_qk = [&](int i, uint32_t slot) {
-        const uint64_t qd = operand(q_base + i * q_bytes, 16), kd = operand(slots + slot * slot_bytes, 16);
-#pragma unroll 8
-        for (int ks = 0; ks < steps; ++ks) {
-            const uint32_t off = ((uint32_t)(ks >> 2) * kHalfBytes + (uint32_t)(ks & 3) * 32) >> 4;
-            mma_ss(tmem + kColS + 128 * i, qd + off, kd + off, qk, ks > 0);
+        if (leader) {
+            const uint64_t qd = operand(q_base + i * q_bytes, 16), kd = operand(slots + slot * slot_bytes, 16);
+            const uint32_t d = tmem + kColS + 128 * i;
+#pragma unroll
+            for (int ks = 0; ks < 8; ++ks) {
+                constexpr uint32_t kHalf = kHalfBytes >> 4;
+                if (ks < steps) mma_ss(d, qd + (ks >> 2) * kHalf + (ks & 3) * 2, kd + (ks >> 2) * kHalf + (ks & 3) * 2, qk, ks > 0);
+            }
+            tc_commit(&sh->s_full[i]);
         }
-        tc_commit(&sh->s_full[i]);
+        __syncwarp();
     };
     auto product_pv = [&](int i, uint32_t slot, bool add) {
-        const uint64_t vd = operand(slots + slot * slot_bytes, kHalfBytes);
+        if (leader) {
+            const uint64_t vd = operand(slots + slot * slot_bytes, kHalfBytes);
+            const uint32_t d = tmem + kColO + 128 * i, x = tmem + kColS + 128 * i;
 #pragma unroll
-        for (int kt = 0; kt < kTokens / 16; ++kt)
-            mma_ts(tmem + kColO + 128 * i, tmem + kColS + 128 * i + 8 * kt, vd + (uint32_t)(kt * 2048 >> 4), pv,
-                   add || kt > 0);
+            for (int kt = 0; kt < kTokens / 16; ++kt) mma_ts(d, x + 8 * kt, vd + (kt * 2048 >> 4), pv, add || kt > 0);
+        }
+        __syncwarp();
     };
+    auto commit = [&](uint64_t* bar) {
+        if (leader) tc_commit(bar);
+        __syncwarp();
+    };
+    auto all_wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xFFFFFFFFu, wait(bar, parity)) != 0; };
     Piece p;
-    while (next_piece(a, t, sh->prefix, w, p)) {
-        const int tiles = live_rows(t, p) > kTileRows ? 2 : 1;
+    p.item = 0;
+    while (next_piece<kRows, kTokens>(a, t, sh->prefix, w, p)) {
+        const int tiles = live_rows<kRows>(t, p) > kTileRows ? 2 : 1;
         // K of the first tile
-        if (!wait(&sh->kv_full[entry % kSlots], (entry / kSlots) & 1)) return;
+        if (!all_wait(&sh->kv_full[entry % SLOTS], (entry / SLOTS) & 1)) return;
         for (int i = 0; i < tiles; ++i) {
-            if (!wait(&sh->q_full[i], q_phase[i])) return;
+            if (!all_wait(&sh->q_full[i], q_phase[i])) return;
             q_phase[i] ^= 1;
             tc_fence_after();
-            product_qk(i, entry % kSlots);
+            product_qk(i, entry % SLOTS);
         }
-        tc_commit(&sh->kv_free[entry % kSlots]);
+        commit(&sh->kv_free[entry % SLOTS]);
         ++entry;
         for (int32_t j = 0; j < p.count; ++j) {
             const uint32_t v_entry = entry, k_entry = entry + 1;
             const bool more = j + 1 < p.count;
-            if (!wait(&sh->kv_full[v_entry % kSlots], (v_entry / kSlots) & 1)) return;
-            if (more && !wait(&sh->kv_full[k_entry % kSlots], (k_entry / kSlots) & 1)) return;
+            if (!all_wait(&sh->kv_full[v_entry % SLOTS], (v_entry / SLOTS) & 1)) return;
+            if (more && !all_wait(&sh->kv_full[k_entry % SLOTS], (k_entry / SLOTS) & 1)) return;
             for (int i = 0; i < tiles; ++i) {
-                if (!wait(&sh->p_full[i], p_phase[i])) return;
+                if (!all_wait(&sh->p_full[i], p_phase[i])) return;
                 p_phase[i] ^= 1;
                 tc_fence_after();
-                product_pv(i, v_entry % kSlots, j > 0);
+                product_pv(i, v_entry % SLOTS, j > 0);
                 if (more)
-                    product_qk(i, k_entry % kSlots);
+                    product_qk(i, k_entry % SLOTS);
                 else
-                    tc_commit(&sh->o_full[i]);
+                    commit(&sh->o_full[i]);
             }
-            tc_commit(&sh->kv_free[v_entry % kSlots]);
-            if (more) tc_commit(&sh->kv_free[k_entry % kSlots]);
+            commit(&sh->kv_free[v_entry % SLOTS]);
+            if (more) commit(&sh->kv_free[k_entry % SLOTS]);
             entry += more ? 2 : 1;
         }
     }
@@ -443,7 +496,7 @@ __device__ __forceinline__ void mma_role(const KvArgs& a, const AttnArgs& t, Sha
 template <class T, int FMT>
 __device__ __forceinline__ float bring_row(const KvArgs& a, const AttnArgs& t, const Piece& p, int i, int row,
                                            uint32_t q_tile, bool flip, bool zero) {
-    const bool real = i * kTileRows + row < live_rows(t, p) && !zero;
+    const bool real = i * kTileRows + row < live_rows<kRows>(t, p) && !zero;
     const RowPlace at = row_place(t, p, kRows, i * kTileRows + row);
     const uint4* src = reinterpret_cast<const uint4*>(t.q + at.token * t.q_token + (int64_t)at.head * t.q_head);
     const uint32_t sign = flip ? 0x80008000u : 0u;
@@ -490,41 +543,47 @@ __device__ __forceinline__ void softmax_role(const KvArgs& a, const AttnArgs& t,
     float next_base2 = scale_base2;
     const PartLayout parts = part_layout(a, gridDim.x, kRows);
     uint32_t s_phase = 0, o_phase = 0, tile = 0;  // tile: this block's tiles of tokens, whoever's
-    const uint64_t x0 = w.x;
-    bool first_piece = true;
+    const int me = threadIdx.x >> 5;
+    int at_piece = 1;
+    if (w.x >= w.x1 && !w.whole && threadIdx.x == 0) parts.cuts[w.share].last = -1;
 
     // the next piece that has rows for this warpgroup, with its rows of Q on their way
-    Piece p;
     uint32_t skipped = 0;  // tiles of pieces without
-    auto take = [&]() -> bool {
+    auto take = [&](Walk w, Piece p) -> bool {
         for (;;) {
-            if (!next_piece(a, t, sh->prefix, w, p)) return false;
-            if (first_piece && !w.whole && threadIdx.x == 0) {
-                parts.cuts[w.share] = cut_of<kRows, kTokens>(p, x0, w.T, w.share, w.shares);
-            }
-            first_piece = false;
-            if (live_rows(t, p) > i * kTileRows) break;
+            const bool begin = w.begun == 0;
+            if (!next_piece<kRows, kTokens>(a, t, sh->prefix, w, p)) return false;
+            if (begin && !w.whole && threadIdx.x == 0)
+                parts.cuts[w.share] =
+                    cut_of<kRows, kTokens>(p, share_start(w.T, w.share, w.shares), w.T, w.share, w.shares);
+            if (live_rows<kRows>(t, p) > i * kTileRows) break;
             skipped += (uint32_t)p.count;
         }
+        at_piece ^= 1;
+        if (lane == 0) {
+            sh->walk[me] = w;
+            sh->piece[me][at_piece] = p;
+        }
+        __syncwarp();
         next_base2 = scale_base2 * bring_row<T, FMT>(a, t, p, i, row, q_tile, flip, zero);
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh->q_full[i]);
         return true;
     };
-    bool have = take();
-    if (first_piece && !w.whole && threadIdx.x == 0) parts.cuts[w.share].last = -1;
+    bool have = take(w, Piece{});
     while (have) {
-        const Piece cur = p;
+        const Piece& cur = sh->piece[me][at_piece];
         const float to_base2 = next_base2;
-        const bool is_row = i * kTileRows + row < live_rows(t, cur);
-        const RowPlace at = row_place(t, cur, kRows, i * kTileRows + row);
+        const bool is_row = i * kTileRows + row < live_rows<kRows>(t, cur);
         int32_t first = 0, last = 0;
-        if (is_row) visible_range(t, cur.seq.len, at.pos, first, last);
+        if (is_row)
+            visible_range(t, cur.seq.len, row_place(t, cur, kRows, i * kTileRows + row).pos, first, last);
+        const int32_t count = cur.count;
         float m = -INFINITY, l = 0.f;
         int32_t base = (cur.range.lo + cur.from) * kTokens;
         tile += skipped;
         skipped = 0;
-        for (int32_t j = 0; j < cur.count; ++j, ++tile, base += kTokens) {
+        for (int32_t j = 0; j < count; ++j, ++tile, base += kTokens) {
             if (!__all_sync(0xFFFFFFFFu, wait(&sh->s_full[i], s_phase))) return;
             s_phase ^= 1;
             tc_fence_after();
@@ -612,11 +671,12 @@ __device__ __forceinline__ void softmax_role(const KvArgs& a, const AttnArgs& t,
             if (lane == 0) mbar_arrive(&sh->p_full[i]);
         }
         // the next item's rows of Q may come now: the last S is done, so is every product with these
-        have = take();
+        have = take(sh->walk[me], cur);
         if (!__all_sync(0xFFFFFFFFu, wait(&sh->o_full[i], o_phase))) return;
         o_phase ^= 1;
         tc_fence_after();
         const bool full = cur.count == cur.range.n;
+        const RowPlace at = row_place(t, cur, kRows, i * kTileRows + row);
         const int tile_row = i * kTileRows + row;
         bool odd = false;
         if (full) {
@@ -670,14 +730,17 @@ __device__ __forceinline__ void softmax_role(const KvArgs& a, const AttnArgs& t,
 
 template <class T, int FMT>
 __global__ void __launch_bounds__(kThreads, 1)
-    attend_chunk_kernel(const __grid_constant__ KvArgs a, const __grid_constant__ AttnArgs t, uint32_t min_tiles,
-                        int whole_items) {
+    attend_chunk_kernel(const __grid_constant__ KvArgs a, const __grid_constant__ AttnArgs t,
+                        const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map, int32_t box,
+                        uint32_t min_tiles, int whole_items) {
+    constexpr int kN = kSlots<FMT>;
     extern __shared__ uint8_t raw[];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     // tiles at 1024-byte boundaries (the swizzle's period): Q0, Q1, the K and V slots, then the rest
     const uint32_t base = (smem_addr(raw) + 1023) & ~1023u;
     const uint32_t tile_bytes = (a.dim > 64 ? 2 : 1) * kHalfBytes;
-    Shared* sh = reinterpret_cast<Shared*>(raw + (base - smem_addr(raw)) + (2 + kSlots) * tile_bytes);
+    Shared* sh = reinterpret_cast<Shared*>(raw + (base - smem_addr(raw)) + (2 + kN) * tile_bytes +
+                                           (FMT == kKv16Bit ? 0 : kRawSlots * kTokens * a.dim));
     const int warp = threadIdx.x >> 5;
     if (warp == 0) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&sh->tmem))
@@ -691,9 +754,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&sh->p_full[i], 4);
             mbar_init(&sh->o_full[i], 1);
         }
-        for (int i = 0; i < kSlots; ++i) {
+        for (int i = 0; i < kN; ++i) {
             mbar_init(&sh->kv_full[i], kLoaderWarps);
             mbar_init(&sh->kv_free[i], 1);
+        }
+        for (int i = 0; i < kRawSlots; ++i) {
+            mbar_init(&sh->raw_full[i], 1);
+            mbar_init(&sh->raw_free[i], kLoaderWarps);
         }
         for (int i = 0; i < kScaleSlots; ++i) mbar_init(&sh->scale_full[i], kLoaderWarps);
         mbar_init(&sh->drained, 1);
@@ -704,27 +771,29 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint64_t all = sh->prefix[a.batch];
-    Walk w;
-    w.T = all;
-    w.shares = (uint32_t)min((uint64_t)gridDim.x, max((all + min_tiles - 1) / min_tiles, (uint64_t)1));
-    w.share = blockIdx.x;
-    w.x0 = w.x = w.share < w.shares ? share_start(all, w.share, w.shares) : all;
-    w.x1 = w.share < w.shares ? share_start(all, w.share + 1, w.shares) : all;
-    w.whole = whole_items;
-    const uint32_t slots = base + 2 * tile_bytes;
+    const Walk w = make_walk(sh->prefix[a.batch], blockIdx.x, gridDim.x, min_tiles, whole_items);
+    const uint32_t slots = base + 2 * tile_bytes, raw_codes = slots + kN * tile_bytes;
+    const Fetch fetch{&k_map, &v_map, box};
     if (warp < 8) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs<FMT>));
         softmax_role<T, FMT>(a, t, sh, base + (warp / 4) * tile_bytes, w);
     } else if (warp < 12) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLoaderRegs<FMT>));
-        load_role<T, FMT>(a, t, sh, slots, tile_bytes, w);
+        if constexpr (FMT == kKv16Bit)
+            fetch_role<FMT, 4, kN>(a, t, sh, fetch, warp - 8, slots, tile_bytes, sh->kv_full, sh->kv_free, w);
+        else
+            widen_role<FMT>(a, t, sh, raw_codes, kTokens * a.dim, slots, tile_bytes, w);
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-        if (threadIdx.x == 12 * 32) {
-            mma_role<Operand<T, FMT>>(a, t, sh, base, slots, tile_bytes, w);
-            tc_commit(&sh->drained);
-            if (!mbar_wait(&sh->drained, 0)) record_error(a.ws, kStatusTimeout);
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLoaderRegs<FMT>));
+        if (warp == 12) {
+            mma_role<Operand<T, FMT>, kN>(a, t, sh, base, slots, tile_bytes, w);
+            __syncwarp();
+            if (threadIdx.x == 12 * 32) {  // every product is done before TMEM goes
+                tc_commit(&sh->drained);
+                if (!mbar_wait(&sh->drained, 0)) record_error(a.ws, kStatusTimeout);
+            }
+        } else if (warp == 13 && FMT != kKv16Bit) {
+            fetch_role<FMT, 1, kRawSlots>(a, t, sh, fetch, 0, raw_codes, kTokens * a.dim, sh->raw_full, sh->raw_free, w);
         }
     }
     __syncwarp();
@@ -735,7 +804,54 @@ __global__ void __launch_bounds__(kThreads, 1)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(sh->tmem) : "memory");
 }
 
-size_t shared_bytes(int dim) { return 1024 + (size_t)(2 + kSlots) * (dim > 64 ? 2 : 1) * kHalfBytes + sizeof(Shared); }
+template <int FMT>
+size_t shared_bytes(int dim) {
+    return 1024 + (size_t)(2 + kSlots<FMT>) * (dim > 64 ? 2 : 1) * kHalfBytes +
+           (FMT == kKv16Bit ? 0 : (size_t)kRawSlots * kTokens * dim) + sizeof(Shared);
+}
+
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                              const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeFn encode_fn() {
+    static const EncodeFn fn = []() -> EncodeFn {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess) {
+            cudaGetLastError();
+            return nullptr;
+        }
+        return reinterpret_cast<EncodeFn>(p);
+    }();
+    return fn;
+}
+// K or V as (channel, slot, head, page); a box is up to 64 channels of 16-bit
+// values with the products' swizzle, or all channels of codes, of `box` slots.
+// False where TMA's rules do not hold (the copies then go another way).
+bool make_map(CUtensorMap* map, void* data, bool wide, const KvArgs& a, int32_t box) {
+    const EncodeFn encode = encode_fn();
+    if (encode == nullptr) return false;
+    const cuuint64_t dims[4] = {(cuuint64_t)a.dim, a.page_tokens.d, (cuuint64_t)a.kv_heads, (cuuint64_t)a.pages};
+    const int64_t given[3] = {a.token_stride, a.head_stride, a.page_stride};
+    cuuint64_t strides[3];
+    for (int i = 0; i < 3; ++i) {
+        // an axis of one entry has no step: any legal one will do
+        strides[i] = dims[i + 1] == 1 ? 16 * ((cuuint64_t)a.dim) : (cuuint64_t)given[i];
+        if (strides[i] == 0 || strides[i] >= (1ull << 40)) return false;
+    }
+    const cuuint32_t boxes[4] = {wide ? 64u : (cuuint32_t)a.dim, (cuuint32_t)box, 1, 1}, steps[4] = {1, 1, 1, 1};
+    return encode(map, wide ? CU_TENSOR_MAP_DATA_TYPE_UINT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, data, dims, strides,
+                  boxes, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  wide ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+// Tokens of a TMA box: a page where pages of 8 tokens or more divide a tile,
+// a tile where tiles divide a page, else none.
+int32_t box_tokens(uint32_t page_tokens) {
+    if (page_tokens % kTokens == 0) return kTokens;
+    return page_tokens >= 8 && kTokens % page_tokens == 0 ? (int32_t)page_tokens : 0;
+}
 
 template <class T, int FMT>
 cudaError_t launch_one(const KvArgs& a, const AttnArgs& t, bool whole, uint32_t min_tiles, cudaStream_t s) {
@@ -745,10 +861,15 @@ cudaError_t launch_one(const KvArgs& a, const AttnArgs& t, bool whole, uint32_t 
     if (e != cudaSuccess) return e;
     e = once.run(dev, [] {
         return cudaFuncSetAttribute(attend_chunk_kernel<T, FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    (int)shared_bytes(128));
+                                    (int)shared_bytes<FMT>(128));
     });
     if (e != cudaSuccess) return e;
-    attend_chunk_kernel<T, FMT><<<kShares, kThreads, shared_bytes(a.dim), s>>>(a, t, min_tiles, whole ? 1 : 0);
+    CUtensorMap k_map{}, v_map{};
+    int32_t box = box_tokens(a.page_tokens.d);
+    constexpr bool kWide = FMT == kKv16Bit;
+    if (box > 0 && !(make_map(&k_map, a.k, kWide, a, box) && make_map(&v_map, a.v, kWide, a, box))) box = 0;
+    attend_chunk_kernel<T, FMT>
+        <<<kShares, kThreads, shared_bytes<FMT>(a.dim), s>>>(a, t, k_map, v_map, box, min_tiles, whole ? 1 : 0);
     e = cudaGetLastError();
     if (e != cudaSuccess || whole) return e;
     return launch_join<T, FMT, kRows>(a, t, kShares, s);

@@ -27,16 +27,15 @@ struct TileRange {
     int32_t first, last;  // visible tokens of any row: first .. last - 1
     int32_t lo, n;        // tiles lo .. lo + n - 1 (n >= 1)
 };
+// (A call's rows are below 2^31: n_tokens * q_heads is.)
 template <int ROWS, int TOKENS>
 __device__ __forceinline__ TileRange tile_range(const AttnArgs& t, const Sequence& s, int32_t rt) {
-    const int64_t rows = (int64_t)s.n * t.group;
-    const int64_t i0 = ((int64_t)rt * ROWS) / t.group;
-    const int64_t i1 = (min((int64_t)(rt + 1) * ROWS, rows) - 1) / t.group;
-    const int64_t base = (int64_t)s.len - s.n;
+    const uint32_t rows = (uint32_t)s.n * t.group.d, r0 = (uint32_t)rt * ROWS;
+    const int32_t base = s.len - s.n;
     TileRange r;
     int32_t ignore;
-    visible_range(t, s.len, base + i0, r.first, ignore);
-    visible_range(t, s.len, base + i1, ignore, r.last);
+    visible_range(t, s.len, base + (int32_t)div_by(t.group, r0), r.first, ignore);
+    visible_range(t, s.len, base + (int32_t)div_by(t.group, min(r0 + ROWS, rows) - 1), ignore, r.last);
     if (r.first >= r.last) {
         r.first = r.last = r.lo = 0;
         r.n = 1;
@@ -48,7 +47,7 @@ __device__ __forceinline__ TileRange tile_range(const AttnArgs& t, const Sequenc
 }
 template <int ROWS>
 __device__ __forceinline__ int32_t row_tiles(const AttnArgs& t, const Sequence& s) {
-    return (int32_t)(((int64_t)s.n * t.group + ROWS - 1) / ROWS);
+    return (int32_t)(((uint32_t)s.n * t.group.d + ROWS - 1) / ROWS);
 }
 
 // Block-wide: prefix[b] = tiles before sequence b on the line, prefix[batch] =
@@ -93,10 +92,11 @@ struct Piece {
     int32_t from, count;  // its tiles range.lo + from .. + count - 1
 };
 
-// The item that holds place x of the line.
+// The item that holds place x of the line (a whole warp, all lanes alike).
 template <int ROWS, int TOKENS>
 __device__ __forceinline__ void find_item(const KvArgs& a, const AttnArgs& t, const uint64_t* prefix, uint64_t x,
                                           Piece& p) {
+    const int lane = threadIdx.x & 31;
     int lo = 0, hi = a.batch;  // prefix[lo] <= x < prefix[hi]
     while (hi - lo > 1) {
         const int mid = (lo + hi) / 2;
@@ -107,19 +107,94 @@ __device__ __forceinline__ void find_item(const KvArgs& a, const AttnArgs& t, co
     }
     p.b = lo;
     p.seq = load_sequence(a, lo);
-    const uint64_t per_head = (prefix[lo + 1] - prefix[lo]) / (uint64_t)a.kv_heads;
-    const uint64_t r = x - prefix[lo];
-    p.kv_head = (int32_t)(r / per_head);
-    uint64_t start = prefix[lo] + (uint64_t)p.kv_head * per_head;
-    const int32_t rts = row_tiles<ROWS>(t, p.seq);
+    const uint64_t per_head = (prefix[lo + 1] - prefix[lo]) / (uint32_t)a.kv_heads;
+    p.kv_head = (int32_t)((x - prefix[lo]) / per_head);
+    const uint64_t start = prefix[lo] + (uint64_t)p.kv_head * per_head;
+    // the first row tile whose tiles reach past x: 32 row tiles at a time
+    uint64_t before = 0;
     p.rt = 0;
-    p.range = tile_range<ROWS, TOKENS>(t, p.seq, 0);
-    while (p.rt + 1 < rts && x >= start + (uint64_t)p.range.n) {
-        start += (uint64_t)p.range.n;
-        ++p.rt;
-        p.range = tile_range<ROWS, TOKENS>(t, p.seq, p.rt);
+    const int32_t rts = row_tiles<ROWS>(t, p.seq);
+    for (int32_t base = 0; base < rts; base += 32) {
+        const int32_t rt = base + lane;
+        const uint32_t n = rt < rts ? (uint32_t)tile_range<ROWS, TOKENS>(t, p.seq, rt).n : 0;
+        uint32_t upto = n;  // 32 row tiles of below 2^31 / TOKENS tiles each: below 2^32
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+            if (lane >= o) upto += y;
+        }
+        const uint32_t past = __ballot_sync(0xFFFFFFFFu, start + before + upto > x);
+        if (past != 0) {
+            const int at = __ffs(past) - 1;
+            p.rt = base + at;
+            before += __shfl_sync(0xFFFFFFFFu, upto - n, at);
+            break;
+        }
+        before += __shfl_sync(0xFFFFFFFFu, upto, 31);
     }
-    p.item = start;
+    p.range = tile_range<ROWS, TOKENS>(t, p.seq, p.rt);
+    p.item = start + before;
+}
+// The item after p's on the line (there is one).
+template <int ROWS, int TOKENS>
+__device__ __forceinline__ void next_item(const KvArgs& a, const AttnArgs& t, Piece& p) {
+    p.item += (uint64_t)p.range.n;
+    if (++p.rt >= row_tiles<ROWS>(t, p.seq)) {
+        p.rt = 0;
+        if (++p.kv_head >= a.kv_heads) {
+            p.kv_head = 0;
+            do {
+                p.seq = load_sequence(a, ++p.b);
+            } while (p.seq.n == 0);
+        }
+    }
+    p.range = tile_range<ROWS, TOKENS>(t, p.seq, p.rt);
+}
+
+// One block's share of the line, piece by piece (a whole warp at a time).
+struct Walk {
+    uint64_t x, x1, T;
+    uint32_t share, shares;
+    int32_t whole;  // items are not cut: the block that an item begins in does all of it
+    int32_t begun;  // the caller's piece is the one before
+};
+__device__ __forceinline__ uint64_t share_start(uint64_t T, uint32_t c, uint32_t C);
+__device__ __forceinline__ Walk make_walk(uint64_t T, uint32_t share, uint32_t blocks, uint32_t min_tiles, int whole) {
+    Walk w;
+    w.T = T;
+    w.share = share;
+    // no more shares than give each min_tiles tiles
+    w.shares = (uint32_t)min((uint64_t)blocks, max((T + min_tiles - 1) / min_tiles, (uint64_t)1));
+    w.x = share < w.shares ? share_start(T, share, w.shares) : T;
+    w.x1 = share < w.shares ? share_start(T, share + 1, w.shares) : T;
+    w.whole = whole;
+    w.begun = 0;
+    return w;
+}
+template <int ROWS, int TOKENS>
+__device__ __forceinline__ bool next_piece(const KvArgs& a, const AttnArgs& t, const uint64_t* prefix, Walk& w,
+                                           Piece& p) {
+    while (w.x < w.x1) {
+        if (w.begun == 0)
+            find_item<ROWS, TOKENS>(a, t, prefix, w.x, p);
+        else
+            next_item<ROWS, TOKENS>(a, t, p);
+        w.begun = 1;
+        const uint64_t end = p.item + (uint64_t)p.range.n;
+        if (w.whole) {
+            const bool before = p.item < w.x;
+            w.x = end;
+            if (before) continue;  // the share before does it
+            p.from = 0;
+            p.count = p.range.n;
+        } else {
+            p.from = (int32_t)(w.x - p.item);
+            p.count = (int32_t)(min(end, w.x1) - w.x);
+            w.x += (uint64_t)p.count;
+        }
+        return true;
+    }
+    return false;
 }
 
 // Share c of C of a line of T tiles begins here (T < 2^48).
@@ -168,15 +243,21 @@ inline size_t part_bytes(int shares, int rows, int dim) {
     return (size_t)shares * (sizeof(Cut) + 2 * (size_t)rows * (size_t)(dim + 2) * sizeof(float));
 }
 
+// Rows of the piece's tile that exist.
+template <int ROWS>
+__device__ __forceinline__ int live_rows(const AttnArgs& t, const Piece& p) {
+    return min(ROWS, (int)((uint32_t)p.seq.n * t.group.d) - p.rt * ROWS);
+}
 // Row `row` of an item's tile: its place in the packed tensors.
 struct RowPlace {
     int64_t token;  // row of the packed tensors
-    int64_t pos;    // position in the sequence
+    int32_t pos;    // position in the sequence
     int32_t head;   // query head
 };
 __device__ __forceinline__ RowPlace row_place(const AttnArgs& t, const Piece& p, int rows, int row) {
-    const int64_t r = (int64_t)p.rt * rows + row, i = r / t.group;
-    return RowPlace{p.seq.row + i, (int64_t)p.seq.len - p.seq.n + i, (int32_t)(p.kv_head * t.group + (r - i * t.group))};
+    const uint32_t r = (uint32_t)(p.rt * rows + row), i = div_by(t.group, r);
+    return RowPlace{p.seq.row + i, p.seq.len - p.seq.n + (int32_t)i,
+                    (int32_t)((uint32_t)p.kv_head * t.group.d + (r - i * t.group.d))};
 }
 // Values d .. d + 7 of a finished row: v / sum, and with d = 0 its log-sum-exp
 // (m in base 2).  True when something is not finite, though the row sees keys:
@@ -230,7 +311,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_parts_kernel(const __grid_c
     p.rt = cut.rt;
     p.seq = load_sequence(a, cut.b);
     const int row0 = blockIdx.y * kJoinRows;
-    const int live = (int)min((int64_t)ROWS, (int64_t)p.seq.n * t.group - (int64_t)p.rt * ROWS) - row0;
+    const int live = live_rows<ROWS>(t, p) - row0;
     if (live <= 0) return;
     const int first = (int)blockIdx.x - 1, n = cut.last - first + 1;
     if (threadIdx.x == 0) odd_rows = 0;

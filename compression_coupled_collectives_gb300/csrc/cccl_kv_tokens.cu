@@ -173,13 +173,12 @@ template <class S>
 __device__ __forceinline__ void load_queries(const KvArgs& a, const AttnArgs& t, const Piece& p,
                                              uint32_t (*q)[S::DP / 16][2], float* inverse) {
     const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-    const int64_t rows = (int64_t)p.seq.n * t.group;
+    const int live = live_rows<S::kRows>(t, p);
 #pragma unroll
     for (int nr = 0; nr < S::NR; ++nr) {
-        const int64_t r = (int64_t)p.rt * S::kRows + g + 8 * nr;
-        const bool real = r < rows;
-        const int64_t i = real ? r / t.group : 0, h = real ? r - i * t.group : 0;
-        const uint8_t* src = t.q + (p.seq.row + i) * t.q_token + ((int64_t)p.kv_head * t.group + h) * t.q_head;
+        const bool real = g + 8 * nr < live;
+        const RowPlace at = row_place(t, p, S::kRows, real ? g + 8 * nr : 0);
+        const uint8_t* src = t.q + at.token * t.q_token + (int64_t)at.head * t.q_head;
 #pragma unroll
         for (int ks = 0; ks < S::DP / 16; ++ks) {
             uint32_t lo = 0, hi = 0;
@@ -443,47 +442,28 @@ __global__ void __launch_bounds__(kThreads, S::kBlocksPerSm)
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
     build_prefix<S::kRows, S::kTile>(a, t, prefix);
-    const uint64_t T = prefix[a.batch];
-    // no more shares than give each min_tiles tiles
-    const uint32_t shares = (uint32_t)min((uint64_t)gridDim.x, max((T + min_tiles - 1) / min_tiles, (uint64_t)1));
+    Walk w = make_walk(prefix[a.batch], blockIdx.x, gridDim.x, min_tiles, whole_items);
     const PartLayout parts = part_layout(a, (int)gridDim.x, S::kRows);
-    const uint32_t share = blockIdx.x;
-    uint64_t x = share < shares ? share_start(T, share, shares) : T;
-    const uint64_t x0 = x, x1 = share < shares ? share_start(T, share + 1, shares) : T;
-    if (!whole_items && (x >= x1) && threadIdx.x == 0) parts.cuts[share].last = -1;
+    const uint64_t x0 = w.x;
+    if (!whole_items && w.x >= w.x1 && threadIdx.x == 0) parts.cuts[w.share].last = -1;
     const float to_base2 = t.scale * 1.4426950408889634f;
     const uint32_t ring = smem_addr(smem) + warp * S::kRing;
     Piece p;
-    while (x < x1) {
-        find_item<S::kRows, S::kTile>(a, t, prefix, x, p);
-        const uint64_t end = p.item + (uint64_t)p.range.n;
-        if (whole_items) {
-            if (p.item < x) {  // the share before does all of it
-                x = end;
-                continue;
-            }
-            p.from = 0;
-            p.count = p.range.n;
-        } else {
-            p.from = (int32_t)(x - p.item);
-            p.count = (int32_t)(min(end, x1) - x);
-            if (x == x0 && threadIdx.x == 0) parts.cuts[share] = cut_of<S::kRows, S::kTile>(p, x0, T, share, shares);
-        }
+    for (bool begin = true; next_piece<S::kRows, S::kTile>(a, t, prefix, w, p); begin = false) {
+        if (begin && !whole_items && threadIdx.x == 0)
+            parts.cuts[w.share] = cut_of<S::kRows, S::kTile>(p, x0, w.T, w.share, w.shares);
         const bool full = p.count == p.range.n;
         const int which = p.from > 0 ? 0 : 1;
-        x += (uint64_t)p.count;
-
-        const int64_t rows = (int64_t)p.seq.n * t.group;
-        const int32_t live = (int32_t)min((int64_t)S::kRows, rows - (int64_t)p.rt * S::kRows);
+        const int32_t live = live_rows<S::kRows>(t, p);
         int32_t first[S::NR][2], last[S::NR][2], all_from = 0, all_to = 0x7FFFFFFF;
 #pragma unroll
         for (int nr = 0; nr < S::NR; ++nr)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const int64_t r = (int64_t)p.rt * S::kRows + 8 * nr + 2 * c + i;
                 first[nr][i] = last[nr][i] = 0;
-                if (r < rows) {
-                    visible_range(t, p.seq.len, (int64_t)p.seq.len - p.seq.n + r / t.group, first[nr][i], last[nr][i]);
+                if (8 * nr + 2 * c + i < live) {
+                    visible_range(t, p.seq.len, row_place(t, p, S::kRows, 8 * nr + 2 * c + i).pos, first[nr][i],
+                                  last[nr][i]);
                     all_from = max(all_from, first[nr][i]);
                     all_to = min(all_to, last[nr][i]);
                 }
@@ -560,8 +540,8 @@ __global__ void __launch_bounds__(kThreads, S::kBlocksPerSm)
             }
         __syncthreads();
         const int groups = a.dim / 8;
-        for (int w = threadIdx.x; w < live * groups; w += kThreads) {
-            const int row = w / groups, d = 8 * (w - row * groups);
+        for (int k = threadIdx.x; k < live * groups; k += kThreads) {
+            const int row = k / groups, d = 8 * (k - row * groups);
             float m = stats[0][0][row];
 #pragma unroll
             for (int i = 1; i < kWarps; ++i) m = fmaxf(m, stats[0][i][row]);
@@ -583,12 +563,12 @@ __global__ void __launch_bounds__(kThreads, S::kBlocksPerSm)
                 v[7] += f * hi.w;
             }
             if (!full) {
-                float4* dst = reinterpret_cast<float4*>(parts.acc(share, which) + row * a.dim + d);
+                float4* dst = reinterpret_cast<float4*>(parts.acc(w.share, which) + row * a.dim + d);
                 dst[0] = make_float4(v[0], v[1], v[2], v[3]);
                 dst[1] = make_float4(v[4], v[5], v[6], v[7]);
                 if (d == 0) {
-                    parts.stats(share, which)[row] = m;
-                    parts.stats(share, which)[S::kRows + row] = sum;
+                    parts.stats(w.share, which)[row] = m;
+                    parts.stats(w.share, which)[S::kRows + row] = sum;
                 }
                 continue;
             }
@@ -640,7 +620,7 @@ cudaError_t launch_kv_tokens(int dtype, int format, const KvArgs& a, const AttnA
                              cudaStream_t s) {
     const bool whole = max_len <= 128;
     const uint32_t min_tiles = 1;
-    const bool few = (int64_t)t.group * max_new <= 8;
+    const bool few = (int64_t)t.group.d * max_new <= 8;
     if (dtype == (int)Bf16::kCode) {
         if (format == kKv16Bit) return launch_dim<BfType, kKv16Bit>(a, t, few, whole, min_tiles, s);
         return format == kKvInt8 ? launch_dim<BfType, kKvInt8>(a, t, few, whole, min_tiles, s)

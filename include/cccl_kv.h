@@ -120,7 +120,8 @@ cccl_status cccl_kv_read(const cccl_kv_cache *h_cache, const cccl_kv_batch *h_ba
 /* Attention of the batch's tokens over the cached tokens of their sequences.
  * Row t, query head h of d_q starts at d_q + t * q_token_stride +
  * h * q_head_stride (the cache's dtype; strides multiples of 8); it reads the
- * cache's head h / (q_heads / kv_heads) (q_heads a multiple of kv_heads).
+ * cache's head h / (q_heads / kv_heads) (q_heads a multiple of kv_heads;
+ * n_tokens * q_heads below 2^31).
  * With the row's position p and s_j = scale * q . k_j over the visible keys j
  *     j < kv_lens[b];  j <= p when causal;  j > p - window when window > 0
  * the result is  sum_j exp(s_j - m) v_j / sum_j exp(s_j - m),  m = max s_j,
