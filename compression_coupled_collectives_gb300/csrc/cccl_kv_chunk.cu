@@ -205,8 +205,8 @@ struct Waiter {
 
 // ---------------------------------------------------------------- K and V
 // Tiles come through a ring, K and V in turn.  A tile that every row of the
-// item's range covers is brought by TMA, a page (or 128 tokens) a box, each lane
-// of one warp issuing one box; one that the range cuts, or pages that TMA's
+// item's range covers is brought by TMA, a page (or 128 tokens) a box, each warp
+// issuing the boxes that begin in its rows; one that the range cuts, or pages that TMA's
 // boxes do not fit (`box` is 0), by 16-byte copies that put zeros where the
 // range ends, so that no product meets what nobody wrote.
 struct Fetch {
@@ -251,8 +251,12 @@ __device__ __forceinline__ void fetch_role(const KvArgs& a, const AttnArgs& t, S
     const int lane = threadIdx.x & 31;
     const Waiter wait{sh, a.ws};
     const int chunks = a.dim * (kWide ? 2 : 1) / 16, per_row = chunks > 8 ? 16 : 8, chunk = lane % per_row;
-    const int boxes = f.box > 0 ? kTokens / f.box : 1, halves = kWide ? (a.dim > 64 ? 2 : 1) : 1;
-    const int box = lane % boxes, half = lane / boxes;
+    // this warp's boxes: one for each lane below `issue`
+    const int halves = kWide ? (a.dim > 64 ? 2 : 1) : 1, span = kTokens / WARPS;
+    const int boxes = f.box == 0 || (warp * span) % f.box != 0 ? 0 : (f.box >= span ? 1 : span / f.box);
+    const int issue = boxes * halves, half = boxes > 0 ? lane / boxes : 0;
+    const int first_row = warp * span + (boxes > 0 ? lane % boxes : 0) * f.box;
+    const uint32_t expect = (uint32_t)boxes * (uint32_t)f.box * (slot_bytes / kTokens);
     uint32_t entry = 0, handed = 0;
     auto hand_over = [&](uint32_t upto) {  // this warp's copies of entries below `upto` are done
         if (handed >= upto) return;
@@ -271,8 +275,8 @@ __device__ __forceinline__ void fetch_role(const KvArgs& a, const AttnArgs& t, S
             TileRow rows[kParts];
             int32_t page = 0, slot0 = 0;
             if (tma) {
-                if (warp == 0 && half < halves) {
-                    const uint32_t pos = (uint32_t)(at + box * f.box), pi = div_by(a.page_tokens, pos);
+                if (lane < issue) {
+                    const uint32_t pos = (uint32_t)(at + first_row), pi = div_by(a.page_tokens, pos);
                     slot0 = (int32_t)(pos - pi * a.page_tokens.d);
                     page = (int32_t)page_of(a, p.b, pi);  // -1: outside the map, zeros
                 }
@@ -294,15 +298,11 @@ __device__ __forceinline__ void fetch_role(const KvArgs& a, const AttnArgs& t, S
                     copy_wait<0>();
                     hand_over(entry);
                     ++handed;
-                    if (warp == 0) {
-                        if (lane == 0) arrive_expect(&full[s], slot_bytes);
-                        __syncwarp();
-                        if (half < halves)
-                            tma_box(dst + (kWide ? half * kHalfBytes + box * f.box * 128 : box * f.box * a.dim),
-                                    side ? f.v : f.k, 64 * half, slot0, p.kv_head, page, &full[s]);
-                    } else if (lane == 0) {
-                        mbar_arrive(&full[s]);
-                    }
+                    if (lane == 0) arrive_expect(&full[s], expect);
+                    __syncwarp();
+                    if (lane < issue)
+                        tma_box(dst + (kWide ? half * kHalfBytes + first_row * 128 : first_row * a.dim),
+                                side ? f.v : f.k, 64 * half, slot0, p.kv_head, page, &full[s]);
                     continue;
                 }
                 const uint8_t* data = side ? a.v : a.k;
