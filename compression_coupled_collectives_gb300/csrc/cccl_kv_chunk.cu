@@ -45,10 +45,7 @@ constexpr float kSlack = 8.f;    // base 2
 
 // Registers of a thread: the launch's 4 x 128 a warpgroup, divided anew (two
 // softmax warpgroups, two of the others).
-template <int FMT>
-constexpr int kSoftmaxRegs = FMT == kKv16Bit ? 192 : 176;
-template <int FMT>
-constexpr int kLoaderRegs = 256 - kSoftmaxRegs<FMT>;
+constexpr int kSoftmaxRegs = 192, kLoaderRegs = 64;
 
 // TMEM columns
 constexpr uint32_t kColS = 0, kColO = 256;  // S of row tile i at 128 i (P over it), O at 256 + 128 i
@@ -532,6 +529,15 @@ __device__ __forceinline__ float bring_row(const KvArgs& a, const AttnArgs& t, c
     return 1.f / power;
 }
 
+// 32 scales (every lane the same ones), asked for together.
+__device__ __forceinline__ void load_scales(uint32_t at, float2* f) {
+#pragma unroll
+    for (int k = 0; k < 16; k += 2)
+        asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];"
+                     : "=f"(f[k].x), "=f"(f[k].y), "=f"(f[k + 1].x), "=f"(f[k + 1].y)
+                     : "r"(at + 8 * k));
+}
+
 template <class T, int FMT>
 __device__ __forceinline__ void softmax_role(const KvArgs& a, const AttnArgs& t, Shared* sh, uint32_t q_tile, Walk w) {
     const int i = threadIdx.x / 128, row = threadIdx.x % 128, warp = row >> 5, lane = row & 31;
@@ -594,17 +600,18 @@ __device__ __forceinline__ void softmax_role(const KvArgs& a, const AttnArgs& t,
             const uint32_t scale_slot = tile % kScaleSlots;
             if (FMT != kKv16Bit) {
                 if (!__all_sync(0xFFFFFFFFu, wait(&sh->scale_full[scale_slot], (tile / kScaleSlots) & 1))) return;
+                const uint32_t at = smem_addr(&sh->k_scale[scale_slot][0]);
 #pragma unroll
-                for (int c = 0; c < kTokens; c += 4) {
-                    const float4 f = *reinterpret_cast<const float4*>(&sh->k_scale[scale_slot][c]);
-                    const float2 x = mul2(make_float2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])),
-                                          make_float2(f.x, f.y));
-                    const float2 y = mul2(make_float2(__uint_as_float(s[c + 2]), __uint_as_float(s[c + 3])),
-                                          make_float2(f.z, f.w));
-                    s[c] = __float_as_uint(x.x);
-                    s[c + 1] = __float_as_uint(x.y);
-                    s[c + 2] = __float_as_uint(y.x);
-                    s[c + 3] = __float_as_uint(y.y);
+                for (int c = 0; c < kTokens; c += 32) {
+                    float2 f[16];
+                    load_scales(at + 4 * c, f);
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) {
+                        const float2 x = mul2(make_float2(__uint_as_float(s[c + 2 * k]), __uint_as_float(s[c + 2 * k + 1])),
+                                              f[k]);
+                        s[c + 2 * k] = __float_as_uint(x.x);
+                        s[c + 2 * k + 1] = __float_as_uint(x.y);
+                    }
                 }
             }
             if (base < first || base + kTokens > last) {
@@ -645,23 +652,28 @@ __device__ __forceinline__ void softmax_role(const KvArgs& a, const AttnArgs& t,
             float2 sum0 = make_float2(0.f, 0.f), sum1 = make_float2(0.f, 0.f);
             uint32_t pr[kTokens / 2];
 #pragma unroll
-            for (int c = 0; c < kTokens; c += 4) {
-                float2 x = fma2(make_float2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), scale2, from2);
-                float2 y = fma2(make_float2(__uint_as_float(s[c + 2]), __uint_as_float(s[c + 3])), scale2, from2);
-                x.x = exp2_fast(x.x);
-                x.y = exp2_fast(x.y);
-                y.x = exp2_fast(y.x);
-                y.y = exp2_fast(y.y);
-                sum0 = add2(sum0, x);
-                sum1 = add2(sum1, y);
-                if (FMT != kKv16Bit) {
-                    const float4 f = *reinterpret_cast<const float4*>(&sh->v_scale[scale_slot][c]);
-                    x = mul2(x, make_float2(f.x, f.y));
-                    y = mul2(y, make_float2(f.z, f.w));
+            for (int c = 0; c < kTokens; c += 32) {
+                float2 f[16];
+                if (FMT != kKv16Bit) load_scales(smem_addr(&sh->v_scale[scale_slot][0]) + 4 * c, f);
+#pragma unroll
+                for (int k = 0; k < 16; k += 2) {
+                    const int i0 = c + 2 * k;
+                    float2 x = fma2(make_float2(__uint_as_float(s[i0]), __uint_as_float(s[i0 + 1])), scale2, from2);
+                    float2 y = fma2(make_float2(__uint_as_float(s[i0 + 2]), __uint_as_float(s[i0 + 3])), scale2, from2);
+                    x.x = exp2_fast(x.x);
+                    x.y = exp2_fast(x.y);
+                    y.x = exp2_fast(y.x);
+                    y.y = exp2_fast(y.y);
+                    sum0 = add2(sum0, x);
+                    sum1 = add2(sum1, y);
+                    if (FMT != kKv16Bit) {
+                        x = mul2(x, f[k]);
+                        y = mul2(y, f[k + 1]);
+                    }
+                    pr[i0 / 2] = pack<Operand<T, FMT>>(x.x, x.y);
+                    pr[i0 / 2 + 1] = pack<Operand<T, FMT>>(y.x, y.y);
                 }
-                pr[c / 2] = pack<Operand<T, FMT>>(x.x, x.y);
-                pr[c / 2 + 1] = pack<Operand<T, FMT>>(y.x, y.y);
-                if (c % 64 == 60) tc_store32(at_s + (c / 64) * 32, pr + (c / 64) * 32);
+                if (c % 64 == 32) tc_store32(at_s + (c / 64) * 32, pr + (c / 64) * 32);
             }
             sum0 = add2(sum0, sum1);
             l += sum0.x + sum0.y;
@@ -775,16 +787,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t slots = base + 2 * tile_bytes, raw_codes = slots + kN * tile_bytes;
     const Fetch fetch{&k_map, &v_map, box};
     if (warp < 8) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs<FMT>));
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
         softmax_role<T, FMT>(a, t, sh, base + (warp / 4) * tile_bytes, w);
     } else if (warp < 12) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLoaderRegs<FMT>));
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLoaderRegs));
         if constexpr (FMT == kKv16Bit)
             fetch_role<FMT, 4, kN>(a, t, sh, fetch, warp - 8, slots, tile_bytes, sh->kv_full, sh->kv_free, w);
         else
             widen_role<FMT>(a, t, sh, raw_codes, kTokens * a.dim, slots, tile_bytes, w);
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLoaderRegs<FMT>));
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLoaderRegs));
         if (warp == 12) {
             mma_role<Operand<T, FMT>, kN>(a, t, sh, base, slots, tile_bytes, w);
             __syncwarp();
