@@ -34,6 +34,7 @@ namespace {
 constexpr int kRows = 256, kTileRows = 128, kTokens = 128;
 constexpr int kThreads = 512;
 constexpr int kShares = 152;
+constexpr int kMaxDim = 128;     // CCCL_KV_MAX_DIM
 constexpr int kScaleSlots = 4;   // tiles of tokens whose scales are kept
 constexpr int kLoaderWarps = 4;
 // K and V tiles in shared memory, as 16-bit values; tiles of 8-bit codes on
@@ -57,7 +58,7 @@ struct Shared {
     uint64_t drained;
     uint32_t tmem;
     uint32_t stop;  // a bounded wait ran out: every role leaves
-    uint64_t prefix[kMaxBatch + 1];
+    uint32_t prefix[kMaxBatch + 1];
     // each softmax warp's way along the line and its pieces (this one, the next
     // one): here, so that a thread's registers are free for its row of S
     Walk walk[8];
@@ -497,32 +498,32 @@ __device__ __forceinline__ float bring_row(const KvArgs& a, const AttnArgs& t, c
     const RowPlace at = row_place(t, p, kRows, i * kTileRows + row);
     const uint4* src = reinterpret_cast<const uint4*>(t.q + at.token * t.q_token + (int64_t)at.head * t.q_head);
     const uint32_t sign = flip ? 0x80008000u : 0u;
+    uint4 x[kMaxDim / 8];
+#pragma unroll
+    for (int c = 0; c < kMaxDim / 8; ++c) {
+        x[c] = make_uint4(0, 0, 0, 0);
+        if (real && 8 * c < a.dim) x[c] = src[c];
+    }
     float power = 1.f;
-    if (FMT != kKv16Bit && real) {
+    if (FMT != kKv16Bit) {
         uint32_t top = 0;
-#pragma unroll 4
-        for (int c = 0; c < a.dim / 8; ++c) {
-            const uint4 x = src[c];
-            top = vmax_u16x2(vmax_u16x2(top, x.x & 0x7FFF7FFFu), vmax_u16x2(x.y & 0x7FFF7FFFu, x.z & 0x7FFF7FFFu));
-            top = vmax_u16x2(top, x.w & 0x7FFF7FFFu);
+#pragma unroll
+        for (int c = 0; c < kMaxDim / 8; ++c) {
+            top = vmax_u16x2(vmax_u16x2(top, x[c].x & 0x7FFF7FFFu),
+                             vmax_u16x2(x[c].y & 0x7FFF7FFFu, x[c].z & 0x7FFF7FFFu));
+            top = vmax_u16x2(top, x[c].w & 0x7FFF7FFFu);
         }
         power = query_power<T>(max(top & 0xFFFFu, top >> 16));
     }
-#pragma unroll 4
-    for (int c = 0; c < a.dim / 8; ++c) {
-        uint4 x = make_uint4(0, 0, 0, 0);
-        if (real) {
-            x = src[c];
-            x.x ^= sign;
-            x.y ^= sign;
-            x.z ^= sign;
-            x.w ^= sign;
-            if (FMT != kKv16Bit)
-                x = make_uint4(scaled_pair<T>(x.x, power), scaled_pair<T>(x.y, power), scaled_pair<T>(x.z, power),
-                               scaled_pair<T>(x.w, power));
-        }
-        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(q_tile + swizzled(row, c)), "r"(x.x), "r"(x.y),
-                     "r"(x.z), "r"(x.w)
+#pragma unroll
+    for (int c = 0; c < kMaxDim / 8; ++c) {
+        if (8 * c >= a.dim) break;
+        uint4 y = make_uint4(x[c].x ^ sign, x[c].y ^ sign, x[c].z ^ sign, x[c].w ^ sign);
+        if (FMT != kKv16Bit)
+            y = make_uint4(scaled_pair<T>(y.x, power), scaled_pair<T>(y.y, power), scaled_pair<T>(y.z, power),
+                           scaled_pair<T>(y.w, power));
+        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(q_tile + swizzled(row, c)), "r"(y.x), "r"(y.y),
+                     "r"(y.z), "r"(y.w)
                      : "memory");
     }
     fence_proxy_async_smem();
@@ -556,12 +557,13 @@ __device__ __forceinline__ void softmax_role(const KvArgs& a, const AttnArgs& t,
     // the next piece that has rows for this warpgroup, with its rows of Q on their way
     uint32_t skipped = 0;  // tiles of pieces without
     auto take = [&](Walk w, Piece p) -> bool {
+        __syncwarp();  // every lane has its copies
         for (;;) {
             const bool begin = w.begun == 0;
             if (!next_piece<kRows, kTokens>(a, t, sh->prefix, w, p)) return false;
             if (begin && !w.whole && threadIdx.x == 0)
                 parts.cuts[w.share] =
-                    cut_of<kRows, kTokens>(p, share_start(w.T, w.share, w.shares), w.T, w.share, w.shares);
+                    cut_of<kRows, kTokens>(p, w.line, w.share);
             if (live_rows<kRows>(t, p) > i * kTileRows) break;
             skipped += (uint32_t)p.count;
         }
@@ -817,10 +819,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <int FMT>
-size_t shared_bytes(int dim) {
+constexpr size_t shared_bytes(int dim) {
     return 1024 + (size_t)(2 + kSlots<FMT>) * (dim > 64 ? 2 : 1) * kHalfBytes +
            (FMT == kKv16Bit ? 0 : (size_t)kRawSlots * kTokens * dim) + sizeof(Shared);
 }
+
+static_assert(shared_bytes<kKv16Bit>(128) <= 232448 && shared_bytes<kKvInt8>(128) <= 232448, "227 KB a block");
 
 using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
                               const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,

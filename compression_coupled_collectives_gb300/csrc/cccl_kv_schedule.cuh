@@ -51,9 +51,10 @@ __device__ __forceinline__ int32_t row_tiles(const AttnArgs& t, const Sequence& 
 }
 
 // Block-wide: prefix[b] = tiles before sequence b on the line, prefix[batch] =
-// all.  Ends with a barrier.  A sequence's rows must lie below 2^31 times ROWS.
+// all.  Ends with a barrier.  2^32 tiles would take hours: such lengths are
+// reported as invalid and the line is empty.
 template <int ROWS, int TOKENS>
-__device__ __forceinline__ void build_prefix(const KvArgs& a, const AttnArgs& t, uint64_t* prefix) {
+__device__ __forceinline__ void build_prefix(const KvArgs& a, const AttnArgs& t, uint32_t* prefix) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
     for (int b = warp; b < a.batch; b += warps) {
         const Sequence s = load_sequence(a, b);
@@ -62,7 +63,7 @@ __device__ __forceinline__ void build_prefix(const KvArgs& a, const AttnArgs& t,
         for (int32_t rt = lane; rt < rts; rt += 32) sum += (uint64_t)tile_range<ROWS, TOKENS>(t, s, rt).n;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-        if (lane == 0) prefix[b + 1] = sum * (uint64_t)a.kv_heads;
+        if (lane == 0) prefix[b + 1] = (uint32_t)min(sum * (uint32_t)a.kv_heads, (uint64_t)0xFFFFFFFFu);
     }
     __syncthreads();
     if (warp == 0) {
@@ -75,10 +76,14 @@ __device__ __forceinline__ void build_prefix(const KvArgs& a, const AttnArgs& t,
                 const uint64_t y = __shfl_up_sync(0xFFFFFFFFu, x, o);
                 if (lane >= o) x += y;
             }
-            if (b < a.batch) prefix[b + 1] = carry + x;
+            if (b < a.batch) prefix[b + 1] = (uint32_t)min(carry + x, (uint64_t)0xFFFFFFFFu);
             carry += __shfl_sync(0xFFFFFFFFu, x, 31);
         }
         if (lane == 0) prefix[0] = 0;
+        if (carry >= 0xFFFFFFFFu) {
+            if (lane == 0) record_error(a.ws, kStatusInvalidArg);
+            for (int b = lane; b < a.batch; b += 32) prefix[b + 1] = 0;
+        }
     }
     __syncthreads();
 }
@@ -88,13 +93,13 @@ struct Piece {
     Sequence seq;
     TileRange range;
     int32_t b, kv_head, rt;
-    uint64_t item;        // the item's start on the line
+    uint32_t item;        // the item's start on the line
     int32_t from, count;  // its tiles range.lo + from .. + count - 1
 };
 
 // The item that holds place x of the line (a whole warp, all lanes alike).
 template <int ROWS, int TOKENS>
-__device__ __forceinline__ void find_item(const KvArgs& a, const AttnArgs& t, const uint64_t* prefix, uint64_t x,
+__device__ __forceinline__ void find_item(const KvArgs& a, const AttnArgs& t, const uint32_t* prefix, uint32_t x,
                                           Piece& p) {
     const int lane = threadIdx.x & 31;
     int lo = 0, hi = a.batch;  // prefix[lo] <= x < prefix[hi]
@@ -107,17 +112,17 @@ __device__ __forceinline__ void find_item(const KvArgs& a, const AttnArgs& t, co
     }
     p.b = lo;
     p.seq = load_sequence(a, lo);
-    const uint64_t per_head = (prefix[lo + 1] - prefix[lo]) / (uint32_t)a.kv_heads;
+    const uint32_t per_head = (prefix[lo + 1] - prefix[lo]) / (uint32_t)a.kv_heads;
     p.kv_head = (int32_t)((x - prefix[lo]) / per_head);
-    const uint64_t start = prefix[lo] + (uint64_t)p.kv_head * per_head;
+    const uint32_t start = prefix[lo] + (uint32_t)p.kv_head * per_head;
     // the first row tile whose tiles reach past x: 32 row tiles at a time
-    uint64_t before = 0;
+    uint32_t before = 0;
     p.rt = 0;
     const int32_t rts = row_tiles<ROWS>(t, p.seq);
     for (int32_t base = 0; base < rts; base += 32) {
         const int32_t rt = base + lane;
         const uint32_t n = rt < rts ? (uint32_t)tile_range<ROWS, TOKENS>(t, p.seq, rt).n : 0;
-        uint32_t upto = n;  // 32 row tiles of below 2^31 / TOKENS tiles each: below 2^32
+        uint32_t upto = n;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, upto, o);
@@ -138,7 +143,7 @@ __device__ __forceinline__ void find_item(const KvArgs& a, const AttnArgs& t, co
 // The item after p's on the line (there is one).
 template <int ROWS, int TOKENS>
 __device__ __forceinline__ void next_item(const KvArgs& a, const AttnArgs& t, Piece& p) {
-    p.item += (uint64_t)p.range.n;
+    p.item += (uint32_t)p.range.n;
     if (++p.rt >= row_tiles<ROWS>(t, p.seq)) {
         p.rt = 0;
         if (++p.kv_head >= a.kv_heads) {
@@ -151,28 +156,38 @@ __device__ __forceinline__ void next_item(const KvArgs& a, const AttnArgs& t, Pi
     p.range = tile_range<ROWS, TOKENS>(t, p.seq, p.rt);
 }
 
+// Share c of a line of T = each * shares + rest tiles begins at
+// floor(T c / shares).
+struct Line {
+    uint32_t each, rest, shares;
+};
+__device__ __forceinline__ uint32_t share_start(const Line& l, uint32_t c) {
+    return l.each * c + l.rest * c / l.shares;  // rest, c < 2^9
+}
+
 // One block's share of the line, piece by piece (a whole warp at a time).
 struct Walk {
-    uint64_t x, x1, T;
-    uint32_t share, shares;
+    Line line;
+    uint32_t x, x1, share;
     int32_t whole;  // items are not cut: the block that an item begins in does all of it
     int32_t begun;  // the caller's piece is the one before
 };
-__device__ __forceinline__ uint64_t share_start(uint64_t T, uint32_t c, uint32_t C);
-__device__ __forceinline__ Walk make_walk(uint64_t T, uint32_t share, uint32_t blocks, uint32_t min_tiles, int whole) {
+__device__ __forceinline__ Walk make_walk(uint32_t T, uint32_t share, uint32_t blocks, uint32_t min_tiles, int whole) {
     Walk w;
-    w.T = T;
     w.share = share;
     // no more shares than give each min_tiles tiles
-    w.shares = (uint32_t)min((uint64_t)blocks, max((T + min_tiles - 1) / min_tiles, (uint64_t)1));
-    w.x = share < w.shares ? share_start(T, share, w.shares) : T;
-    w.x1 = share < w.shares ? share_start(T, share + 1, w.shares) : T;
+    w.line.shares = min(blocks, max((T - 1) / min_tiles + 1, 1u));
+    if (T == 0) w.line.shares = 1;
+    w.line.each = T / w.line.shares;
+    w.line.rest = T - w.line.each * w.line.shares;
+    w.x = share < w.line.shares ? share_start(w.line, share) : T;
+    w.x1 = share < w.line.shares ? share_start(w.line, share + 1) : T;
     w.whole = whole;
     w.begun = 0;
     return w;
 }
 template <int ROWS, int TOKENS>
-__device__ __forceinline__ bool next_piece(const KvArgs& a, const AttnArgs& t, const uint64_t* prefix, Walk& w,
+__device__ __forceinline__ bool next_piece(const KvArgs& a, const AttnArgs& t, const uint32_t* prefix, Walk& w,
                                            Piece& p) {
     while (w.x < w.x1) {
         if (w.begun == 0)
@@ -180,7 +195,7 @@ __device__ __forceinline__ bool next_piece(const KvArgs& a, const AttnArgs& t, c
         else
             next_item<ROWS, TOKENS>(a, t, p);
         w.begun = 1;
-        const uint64_t end = p.item + (uint64_t)p.range.n;
+        const uint32_t end = p.item + (uint32_t)p.range.n;
         if (w.whole) {
             const bool before = p.item < w.x;
             w.x = end;
@@ -190,15 +205,12 @@ __device__ __forceinline__ bool next_piece(const KvArgs& a, const AttnArgs& t, c
         } else {
             p.from = (int32_t)(w.x - p.item);
             p.count = (int32_t)(min(end, w.x1) - w.x);
-            w.x += (uint64_t)p.count;
+            w.x += (uint32_t)p.count;
         }
         return true;
     }
     return false;
 }
-
-// Share c of C of a line of T tiles begins here (T < 2^48).
-__device__ __forceinline__ uint64_t share_start(uint64_t T, uint32_t c, uint32_t C) { return T * c / C; }
 
 // What the joining kernel needs to know about the end of share c - 1 (the
 // start of share c): whether an item is cut there for the first time, and
@@ -209,12 +221,12 @@ struct Cut {
 };
 // Written by block c (one thread) for its first piece.
 template <int ROWS, int TOKENS>
-__device__ __forceinline__ Cut cut_of(const Piece& p, uint64_t x0, uint64_t T, uint32_t c, uint32_t C) {
+__device__ __forceinline__ Cut cut_of(const Piece& p, const Line& l, uint32_t c) {
     Cut u{p.b, p.kv_head, p.rt, -1};
-    if (c > 0 && p.item < x0 && share_start(T, c - 1, C) <= p.item) {
-        const uint64_t end = p.item + (uint64_t)p.range.n;
+    if (c > 0 && p.item < share_start(l, c) && share_start(l, c - 1) <= p.item) {
+        const uint32_t end = p.item + (uint32_t)p.range.n;
         uint32_t last = c;
-        while (last + 1 < C && share_start(T, last + 1, C) < end) ++last;
+        while (last + 1 < l.shares && share_start(l, last + 1) < end) ++last;
         u.last = (int32_t)last;
     }
     return u;

@@ -436,7 +436,7 @@ __global__ void __launch_bounds__(kThreads, S::kBlocksPerSm)
     attend_tokens_kernel(const __grid_constant__ KvArgs a, const __grid_constant__ AttnArgs t, uint32_t min_tiles,
                          int whole_items) {
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ uint64_t prefix[kMaxBatch + 1];
+    __shared__ uint32_t prefix[kMaxBatch + 1];
     __shared__ float stats[2][kWarps][S::kRows];
     __shared__ uint32_t odd_rows;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -444,14 +444,13 @@ __global__ void __launch_bounds__(kThreads, S::kBlocksPerSm)
     build_prefix<S::kRows, S::kTile>(a, t, prefix);
     Walk w = make_walk(prefix[a.batch], blockIdx.x, gridDim.x, min_tiles, whole_items);
     const PartLayout parts = part_layout(a, (int)gridDim.x, S::kRows);
-    const uint64_t x0 = w.x;
     if (!whole_items && w.x >= w.x1 && threadIdx.x == 0) parts.cuts[w.share].last = -1;
     const float to_base2 = t.scale * 1.4426950408889634f;
     const uint32_t ring = smem_addr(smem) + warp * S::kRing;
     Piece p;
     for (bool begin = true; next_piece<S::kRows, S::kTile>(a, t, prefix, w, p); begin = false) {
         if (begin && !whole_items && threadIdx.x == 0)
-            parts.cuts[w.share] = cut_of<S::kRows, S::kTile>(p, x0, w.T, w.share, w.shares);
+            parts.cuts[w.share] = cut_of<S::kRows, S::kTile>(p, w.line, w.share);
         const bool full = p.count == p.range.n;
         const int which = p.from > 0 ? 0 : 1;
         const int32_t live = live_rows<S::kRows>(t, p);
