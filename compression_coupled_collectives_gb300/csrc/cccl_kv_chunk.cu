@@ -9,8 +9,9 @@
 // of rows is in its softmax the tensor core works on the other.
 //
 // Warps: 0-3 and 4-7 softmax of row tiles 0 and 1 (they also bring in their
-// rows of Q and write the result), 8-11 bring K and V in, 12 issues the
-// products.  One block an SM: 512 columns of TMEM (S0, S1, O0, O1).
+// rows of Q and write the result); 8-11 bring K and V in, or widen 8-bit codes
+// that 13 brings in; 12 issues the products; 14 walks along the block's share
+// of the line and hands the pieces to the others.  One block an SM: 512 columns of TMEM (S0, S1, O0, O1).
 //
 // The running maximum is only moved when a score exceeds it by more than 2^8
 // (the accumulator is then rescaled in TMEM); any fixed reference gives the
@@ -34,15 +35,15 @@ namespace {
 constexpr int kRows = 256, kTileRows = 128, kTokens = 128;
 constexpr int kThreads = 512;
 constexpr int kShares = 152;
-constexpr int kMaxDim = 128;     // CCCL_KV_MAX_DIM
-constexpr int kScaleSlots = 4;   // tiles of tokens whose scales are kept
+constexpr int kScaleSlots = 3;   // tiles of tokens whose scales are kept
 constexpr int kLoaderWarps = 4;
 // K and V tiles in shared memory, as 16-bit values; tiles of 8-bit codes on
 // their way there
 constexpr int kMostSlots = 4, kRawSlots = 3;
 template <int FMT>
 constexpr int kSlots = FMT == kKv16Bit ? 4 : 3;
-constexpr float kSlack = 8.f;    // base 2
+constexpr int kStageBytes = 8 * 32 * 32;  // the softmax warps' rows on their way out
+constexpr float kSlack = 8.f;             // base 2
 
 // Registers of a thread: the launch's 4 x 128 a warpgroup, divided anew (two
 // softmax warpgroups, two of the others).
@@ -50,6 +51,8 @@ constexpr int kSoftmaxRegs = 192, kLoaderRegs = 64;
 
 // TMEM columns
 constexpr uint32_t kColS = 0, kColO = 256;  // S of row tile i at 128 i (P over it), O at 256 + 128 i
+
+constexpr int kRing = 4;  // pieces handed on and not yet taken by all
 
 struct Shared {
     uint64_t q_full[2], s_full[2], p_full[2], o_full[2];
@@ -59,10 +62,11 @@ struct Shared {
     uint32_t tmem;
     uint32_t stop;  // a bounded wait ran out: every role leaves
     uint32_t prefix[kMaxBatch + 1];
-    // each softmax warp's way along the line and its pieces (this one, the next
-    // one): here, so that a thread's registers are free for its row of S
-    Walk walk[8];
-    Piece piece[8][2];
+    // One warp walks along the line and hands the pieces on; every other warp
+    // takes a copy (softmax warps keep two, this piece and the next, here rather
+    // than in registers, which hold a row of S).
+    Piece ring[kRing], piece[8][2];
+    uint64_t piece_full[kRing], piece_free[kRing];
     alignas(16) float k_scale[kScaleSlots][kTokens];
     alignas(16) float v_scale[kScaleSlots][kTokens];
     alignas(16) uint32_t v_top[kScaleSlots][kLoaderWarps];  // the largest value scale of each warp's rows
@@ -190,16 +194,54 @@ template <class T, int FMT>
 using Operand = typename std::conditional<FMT == kKv16Bit, T, HfType>::type;
 
 // A bounded wait of one role; false: leave (this wait or another's ran out).
+// Most waits are over at the first look; the others' code is kept in one place.
+__device__ __forceinline__ bool wait_long(Shared* sh, WsHeader* ws, uint64_t* bar, uint32_t parity) {
+    if (mbar_wait(bar, parity)) return true;
+    record_error(ws, kStatusTimeout);
+    *reinterpret_cast<volatile uint32_t*>(&sh->stop) = 1;
+    return false;
+}
+// A whole warp waits.
 struct Waiter {
     Shared* sh;
     WsHeader* ws;
     __device__ __forceinline__ bool operator()(uint64_t* bar, uint32_t parity) const {
-        if (mbar_wait(bar, parity)) return true;
-        record_error(ws, kStatusTimeout);
-        *reinterpret_cast<volatile uint32_t*>(&sh->stop) = 1;
-        return false;
+        if (__all_sync(0xFFFFFFFFu, mbar_test(bar, parity))) return true;
+        return __all_sync(0xFFFFFFFFu, wait_long(sh, ws, bar, parity)) != 0;
     }
 };
+
+// The walking warp: pieces to the ring, one without tiles at the end; then, for
+// the joining kernel, whether an item is cut at this share's start.
+__device__ __forceinline__ void walk_role(const KvArgs& a, const AttnArgs& t, Shared* sh, Walk w) {
+    const Waiter wait{sh, a.ws};
+    const int lane = threadIdx.x & 31;
+    Cut cut{0, 0, 0, -1, {}};
+    Piece p{};
+    for (uint32_t n = 0;; ++n) {
+        const uint32_t s = n % kRing, use = n / kRing;
+        const bool more = next_piece<kRows, kTokens>(a, t, sh->prefix, w, p);
+        if (n == 0 && more && !w.whole) cut = cut_of<kRows, kTokens>(p, w.line, w.share);
+        if (use > 0 && !wait(&sh->piece_free[s], (use - 1) & 1)) return;
+        if (lane == 0) {
+            sh->ring[s] = p;
+            if (!more) sh->ring[s].count = 0;
+            mbar_arrive(&sh->piece_full[s]);
+        }
+        if (!more) break;
+    }
+    if (!w.whole && lane == 0) part_layout(a, gridDim.x, kRows).cuts[w.share] = cut;
+}
+// The other warps: piece n.  Its count is 0 after the last one; false: leave.
+__device__ __forceinline__ bool take_piece(const Waiter& wait, uint32_t n, Piece* to) {
+    Shared* sh = wait.sh;
+    const uint32_t s = n % kRing;
+    if (!wait(&sh->piece_full[s], (n / kRing) & 1)) return false;
+    *to = sh->ring[s];
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(&sh->piece_free[s]);
+    return true;
+}
 
 // ---------------------------------------------------------------- K and V
 // Tiles come through a ring, K and V in turn.  A tile that every row of the
@@ -242,8 +284,7 @@ __device__ __forceinline__ void arrive_expect(uint64_t* bar, uint32_t bytes) {
 // of the warps.
 template <int FMT, int WARPS, int SLOTS>
 __device__ __forceinline__ void fetch_role(const KvArgs& a, const AttnArgs& t, Shared* sh, const Fetch& f, int warp,
-                                           uint32_t slots, uint32_t slot_bytes, uint64_t* full, uint64_t* free_,
-                                           Walk w) {
+                                           uint32_t slots, uint32_t slot_bytes, uint64_t* full, uint64_t* free_) {
     constexpr bool kWide = FMT == kKv16Bit;      // 16-bit values in the swizzled layout; else codes, row after row
     constexpr int kParts = 4 / WARPS;            // groups of 32 rows of this warp
     const int lane = threadIdx.x & 31;
@@ -264,8 +305,7 @@ __device__ __forceinline__ void fetch_role(const KvArgs& a, const AttnArgs& t, S
             if (lane == 0) mbar_arrive(&full[handed % SLOTS]);
     };
     Piece p;
-    p.item = 0;
-    while (next_piece<kRows, kTokens>(a, t, sh->prefix, w, p)) {
+    for (uint32_t n = 0; take_piece(wait, n, &p) && p.count > 0; ++n) {
         const int32_t base = (p.range.lo + p.from) * kTokens;
         for (int32_t j = 0; j < p.count; ++j) {
             const int32_t at = base + j * kTokens;
@@ -290,7 +330,7 @@ __device__ __forceinline__ void fetch_role(const KvArgs& a, const AttnArgs& t, S
                     // about to wait: hand over what has been brought so far
                     copy_wait<0>();
                     hand_over(entry);
-                    if (!__all_sync(0xFFFFFFFFu, wait(&free_[s], (use - 1) & 1))) return;
+                    if (!wait(&free_[s], (use - 1) & 1)) return;
                 }
                 if (tma) {
                     copy_wait<0>();
@@ -370,20 +410,19 @@ __device__ __forceinline__ RowScales row_scales(const KvArgs& a, const Piece& p,
 }
 template <int FMT>
 __device__ __forceinline__ void widen_role(const KvArgs& a, const AttnArgs& t, Shared* sh, uint32_t raw,
-                                           uint32_t raw_bytes, uint32_t slots, uint32_t slot_bytes, Walk w) {
+                                           uint32_t raw_bytes, uint32_t slots, uint32_t slot_bytes) {
     constexpr int kN = kSlots<FMT>;
     const int warp = (threadIdx.x >> 5) - 8, lane = threadIdx.x & 31;
     const Waiter wait{sh, a.ws};
     uint32_t entry = 0;
     Piece p;
-    p.item = 0;
-    while (next_piece<kRows, kTokens>(a, t, sh->prefix, w, p)) {
+    for (uint32_t n = 0; take_piece(wait, n, &p) && p.count > 0; ++n) {
         const int32_t base = (p.range.lo + p.from) * kTokens + 32 * warp + lane;
         RowScales scales = row_scales(a, p, base);
         for (int32_t j = 0; j < p.count; ++j) {
             {
                 // V of tile j - 1 has a slot, so K of tile j - 2 was freed, so both
-                // row tiles are done with the scales of tile j - 3: four slots do
+                // row tiles are done with the scales of tile j - 3: three slots do
                 const uint32_t n = (entry / 2) % kScaleSlots;
                 sh->k_scale[n][32 * warp + lane] = scales.k;
                 sh->v_scale[n][32 * warp + lane] = scales.v;
@@ -394,7 +433,7 @@ __device__ __forceinline__ void widen_role(const KvArgs& a, const AttnArgs& t, S
 #pragma unroll 1
             for (int side = 0; side < 2; ++side, ++entry) {
                 const uint32_t s = entry % kN, use = entry / kN, q = entry % kRawSlots, turn = entry / kRawSlots;
-                if (!__all_sync(0xFFFFFFFFu, wait(&sh->raw_full[q], turn & 1))) return;
+                if (!wait(&sh->raw_full[q], turn & 1)) return;
                 if (use > 0 && !__all_sync(0xFFFFFFFFu, wait(&sh->kv_free[s], (use - 1) & 1))) return;
                 widen_rows<FMT>(raw + q * raw_bytes, slots + s * slot_bytes, a.dim, warp, lane);
                 fence_proxy_async_smem();
@@ -412,7 +451,7 @@ __device__ __forceinline__ void widen_role(const KvArgs& a, const AttnArgs& t, S
 // ---------------------------------------------------------------- products
 template <class M, int SLOTS>
 __device__ __forceinline__ void mma_role(const KvArgs& a, const AttnArgs& t, Shared* sh, uint32_t q_base,
-                                         uint32_t slots, uint32_t slot_bytes, Walk w) {
+                                         uint32_t slots, uint32_t slot_bytes) {
     const Waiter wait{sh, a.ws};
     const uint32_t tmem = sh->tmem;
     const uint32_t qk = instruction(M::kHalf, kTokens, false), pv = instruction(M::kHalf, a.dim > 64 ? 128 : 64, true);
@@ -449,28 +488,27 @@ __device__ __forceinline__ void mma_role(const KvArgs& a, const AttnArgs& t, Sha
         if (leader) tc_commit(bar);
         __syncwarp();
     };
-    auto all_wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xFFFFFFFFu, wait(bar, parity)) != 0; };
     Piece p;
-    p.item = 0;
-    while (next_piece<kRows, kTokens>(a, t, sh->prefix, w, p)) {
+    for (uint32_t n = 0; take_piece(wait, n, &p) && p.count > 0; ++n) {
         const int tiles = live_rows<kRows>(t, p) > kTileRows ? 2 : 1;
+        const int32_t count = p.count;
         // K of the first tile
-        if (!all_wait(&sh->kv_full[entry % SLOTS], (entry / SLOTS) & 1)) return;
+        if (!wait(&sh->kv_full[entry % SLOTS], (entry / SLOTS) & 1)) return;
         for (int i = 0; i < tiles; ++i) {
-            if (!all_wait(&sh->q_full[i], q_phase[i])) return;
+            if (!wait(&sh->q_full[i], q_phase[i])) return;
             q_phase[i] ^= 1;
             tc_fence_after();
             product_qk(i, entry % SLOTS);
         }
         commit(&sh->kv_free[entry % SLOTS]);
         ++entry;
-        for (int32_t j = 0; j < p.count; ++j) {
+        for (int32_t j = 0; j < count; ++j) {
             const uint32_t v_entry = entry, k_entry = entry + 1;
-            const bool more = j + 1 < p.count;
-            if (!all_wait(&sh->kv_full[v_entry % SLOTS], (v_entry / SLOTS) & 1)) return;
-            if (more && !all_wait(&sh->kv_full[k_entry % SLOTS], (k_entry / SLOTS) & 1)) return;
+            const bool more = j + 1 < count;
+            if (!wait(&sh->kv_full[v_entry % SLOTS], (v_entry / SLOTS) & 1)) return;
+            if (more && !wait(&sh->kv_full[k_entry % SLOTS], (k_entry / SLOTS) & 1)) return;
             for (int i = 0; i < tiles; ++i) {
-                if (!all_wait(&sh->p_full[i], p_phase[i])) return;
+                if (!wait(&sh->p_full[i], p_phase[i])) return;
                 p_phase[i] ^= 1;
                 tc_fence_after();
                 product_pv(i, v_entry % SLOTS, j > 0);
@@ -487,47 +525,82 @@ __device__ __forceinline__ void mma_role(const KvArgs& a, const AttnArgs& t, Sha
 }
 
 // ---------------------------------------------------------------- softmax
-// Row `row` (0..127) of row tile i of Q into shared memory; rows that do not
-// exist are zeros.  flip: the sign bit when the scale is negative; zero: the
-// scale is zero (every score is then 0 times the products, so are zeros').
-// Returns what undoes the row's power of two (8-bit caches).
+// Rows 32 warp .. + 31 of row tile i of Q into shared memory, 16 lanes a row;
+// rows that do not exist are zeros.  flip: the sign bit when the scale is
+// negative; zero: the scale is zero (every score is then 0 times the products,
+// so are zeros').  Returns what undoes the power of two of row 32 warp + lane
+// (8-bit caches).  (Loops are kept small here and at an item's end: code that
+// runs once an item is fetched anew each time, at its length's cost.)
 template <class T, int FMT>
-__device__ __forceinline__ float bring_row(const KvArgs& a, const AttnArgs& t, const Piece& p, int i, int row,
-                                           uint32_t q_tile, bool flip, bool zero) {
-    const bool real = i * kTileRows + row < live_rows<kRows>(t, p) && !zero;
-    const RowPlace at = row_place(t, p, kRows, i * kTileRows + row);
-    const uint4* src = reinterpret_cast<const uint4*>(t.q + at.token * t.q_token + (int64_t)at.head * t.q_head);
+__device__ __forceinline__ float bring_rows(const KvArgs& a, const AttnArgs& t, const Piece& p, int i, int warp,
+                                            uint32_t q_tile, bool flip, bool zero) {
+    const int lane = threadIdx.x & 31, chunk = lane & 15;
+    const int row0 = i * kTileRows + 32 * warp, live = zero ? 0 : live_rows<kRows>(t, p) - row0;
+    const RowPlace mine = row_place(t, p, kRows, row0 + lane);
+    const int64_t from = mine.token * t.q_token + (int64_t)mine.head * t.q_head;
+    const bool inside = 8 * chunk < a.dim;
     const uint32_t sign = flip ? 0x80008000u : 0u;
-    uint4 x[kMaxDim / 8];
+    float inverse = 1.f;
+    constexpr int kEach = 4;  // loads in flight
+#pragma unroll 1
+    for (int part = 0; part < 32; part += 2 * kEach) {
+        uint4 x[kEach];
 #pragma unroll
-    for (int c = 0; c < kMaxDim / 8; ++c) {
-        x[c] = make_uint4(0, 0, 0, 0);
-        if (real && 8 * c < a.dim) x[c] = src[c];
-    }
-    float power = 1.f;
-    if (FMT != kKv16Bit) {
-        uint32_t top = 0;
-#pragma unroll
-        for (int c = 0; c < kMaxDim / 8; ++c) {
-            top = vmax_u16x2(vmax_u16x2(top, x[c].x & 0x7FFF7FFFu),
-                             vmax_u16x2(x[c].y & 0x7FFF7FFFu, x[c].z & 0x7FFF7FFFu));
-            top = vmax_u16x2(top, x[c].w & 0x7FFF7FFFu);
+        for (int k = 0; k < kEach; ++k) {
+            const int row = part + 2 * k + (lane >> 4);
+            const int64_t at = __shfl_sync(0xFFFFFFFFu, from, row);
+            x[k] = make_uint4(0, 0, 0, 0);
+            if (row < live && inside) x[k] = *reinterpret_cast<const uint4*>(t.q + at + 16 * chunk);
         }
-        power = query_power<T>(max(top & 0xFFFFu, top >> 16));
-    }
 #pragma unroll
-    for (int c = 0; c < kMaxDim / 8; ++c) {
-        if (8 * c >= a.dim) break;
-        uint4 y = make_uint4(x[c].x ^ sign, x[c].y ^ sign, x[c].z ^ sign, x[c].w ^ sign);
-        if (FMT != kKv16Bit)
-            y = make_uint4(scaled_pair<T>(y.x, power), scaled_pair<T>(y.y, power), scaled_pair<T>(y.z, power),
-                           scaled_pair<T>(y.w, power));
-        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(q_tile + swizzled(row, c)), "r"(y.x), "r"(y.y),
-                     "r"(y.z), "r"(y.w)
-                     : "memory");
+        for (int k = 0; k < kEach; ++k) {
+            uint4 y = make_uint4(x[k].x ^ sign, x[k].y ^ sign, x[k].z ^ sign, x[k].w ^ sign);
+            if (FMT != kKv16Bit && !T::kHalf) {
+                uint32_t top = vmax_u16x2(vmax_u16x2(y.x & 0x7FFF7FFFu, y.y & 0x7FFF7FFFu),
+                                          vmax_u16x2(y.z & 0x7FFF7FFFu, y.w & 0x7FFF7FFFu));
+#pragma unroll
+                for (int o = 1; o < 16; o <<= 1) top = vmax_u16x2(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+                const float power = query_power<T>(max(top & 0xFFFFu, top >> 16));
+                y = make_uint4(scaled_pair<T>(y.x, power), scaled_pair<T>(y.y, power), scaled_pair<T>(y.z, power),
+                               scaled_pair<T>(y.w, power));
+                const float to_owner = __shfl_sync(0xFFFFFFFFu, power, (lane & 1) * 16);
+                if ((lane >> 1) == part / 2 + k) inverse = 1.f / to_owner;
+            }
+            if (inside)
+                asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(
+                                 q_tile + swizzled(32 * warp + part + 2 * k + (lane >> 4), chunk)),
+                             "r"(y.x), "r"(y.y), "r"(y.z), "r"(y.w)
+                             : "memory");
+        }
     }
     fence_proxy_async_smem();
-    return 1.f / power;
+    return inverse;
+}
+
+// A warp's 32 rows of 32 bytes each, a row a lane, to global memory: through
+// shared memory, so that a store instruction writes whole sectors.  to: where
+// this lane's row goes (null: nowhere).
+__device__ __forceinline__ void store_rows(uint32_t stage, const uint32_t* words, uint8_t* to) {
+    const int lane = threadIdx.x & 31;
+    // the 16-byte halves of rows 4..7 of 8 are swapped: a quarter-warp meets all banks
+    auto at = [&](int r, int c) { return stage + r * 32 + ((c ^ ((r >> 2) & 1)) << 4); };
+    __syncwarp();
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at(lane, c)), "r"(words[4 * c]),
+                     "r"(words[4 * c + 1]), "r"(words[4 * c + 2]), "r"(words[4 * c + 3])
+                     : "memory");
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const int row = 16 * k + (lane >> 1);
+        const uint64_t dst = __shfl_sync(0xFFFFFFFFu, reinterpret_cast<uint64_t>(to), row);
+        uint4 x;
+        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
+                     : "r"(at(row, lane & 1)));
+        if (dst != 0) *reinterpret_cast<uint4*>(dst + 16 * (lane & 1)) = x;
+    }
 }
 
 // 32 scales (every lane the same ones), asked for together.
@@ -539,69 +612,124 @@ __device__ __forceinline__ void load_scales(uint32_t at, float2* f) {
                      : "r"(at + 8 * k));
 }
 
+// n low bits set (0 for n <= 0, all for n >= 32)
+__device__ __forceinline__ uint32_t bits_below(int32_t n) {
+    return n <= 0 ? 0u : (n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u);
+}
+
 template <class T, int FMT>
-__device__ __forceinline__ void softmax_role(const KvArgs& a, const AttnArgs& t, Shared* sh, uint32_t q_tile, Walk w) {
+__device__ __forceinline__ void softmax_role(const KvArgs& a, const AttnArgs& t, Shared* sh, uint32_t q_tile,
+                                             uint32_t stages) {
     const int i = threadIdx.x / 128, row = threadIdx.x % 128, warp = row >> 5, lane = row & 31;
+    const int me = threadIdx.x >> 5;
     const Waiter wait{sh, a.ws};
-    const uint32_t tmem = sh->tmem + ((uint32_t)(32 * warp) << 16);
+    const uint32_t tmem = sh->tmem + ((uint32_t)(32 * warp) << 16), stage = stages + me * (32 * 32);
     const uint32_t at_s = tmem + kColS + 128 * i, at_o = tmem + kColO + 128 * i;
     const bool flip = t.scale < 0.f, zero = t.scale == 0.f;
     const float scale_base2 = (zero ? 1.f : fabsf(t.scale)) * 1.4426950408889634f;
-    float next_base2 = scale_base2;
-    const PartLayout parts = part_layout(a, gridDim.x, kRows);
-    uint32_t s_phase = 0, o_phase = 0, tile = 0;  // tile: this block's tiles of tokens, whoever's
-    const int me = threadIdx.x >> 5;
-    int at_piece = 1;
-    if (w.x >= w.x1 && !w.whole && threadIdx.x == 0) parts.cuts[w.share].last = -1;
-
-    // the next piece that has rows for this warpgroup, with its rows of Q on their way
-    uint32_t skipped = 0;  // tiles of pieces without
-    auto take = [&](Walk w, Piece p) -> bool {
-        __syncwarp();  // every lane has its copies
-        for (;;) {
-            const bool begin = w.begun == 0;
-            if (!next_piece<kRows, kTokens>(a, t, sh->prefix, w, p)) return false;
-            if (begin && !w.whole && threadIdx.x == 0)
-                parts.cuts[w.share] =
-                    cut_of<kRows, kTokens>(p, w.line, w.share);
-            if (live_rows<kRows>(t, p) > i * kTileRows) break;
-            skipped += (uint32_t)p.count;
+    uint32_t s_phase = 0, o_phase = 0, taken = 0, tile = 0;  // tile: this block's tiles of tokens, whoever's
+    int slot = 1;                                 // of the piece at hand
+    int32_t first = 0, last = 0;                  // what this row sees
+    float m = -INFINITY, l = 0.f;
+    for (bool begin = true;; begin = false) {
+        // the next piece that has rows for this warpgroup.  Its rows of Q may
+        // come now: the last S is done, so is every product with these.
+        uint32_t skipped = 0;  // tiles of pieces without
+        float to_base2 = scale_base2;
+        Piece* const next = &sh->piece[me][slot ^ 1];
+        for (;; ++taken) {
+            Piece p;
+            if (!take_piece(wait, taken, &p)) return;
+            if (p.count > 0 && live_rows<kRows>(t, p) <= i * kTileRows) {
+                skipped += (uint32_t)p.count;
+                continue;
+            }
+            if (lane == 0) *next = p;
+            __syncwarp();
+            break;
         }
-        at_piece ^= 1;
-        if (lane == 0) {
-            sh->walk[me] = w;
-            sh->piece[me][at_piece] = p;
+        ++taken;
+        const bool more = next->count > 0;
+        if (more) {
+            to_base2 *= bring_rows<T, FMT>(a, t, *next, i, warp, q_tile, flip, zero);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh->q_full[i]);
         }
-        __syncwarp();
-        next_base2 = scale_base2 * bring_row<T, FMT>(a, t, p, i, row, q_tile, flip, zero);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh->q_full[i]);
-        return true;
-    };
-    bool have = take(w, Piece{});
-    while (have) {
-        const Piece& cur = sh->piece[me][at_piece];
-        const float to_base2 = next_base2;
-        const bool is_row = i * kTileRows + row < live_rows<kRows>(t, cur);
-        int32_t first = 0, last = 0;
-        if (is_row)
+        if (!begin) {  // the end of the piece at hand
+            const Piece& cur = sh->piece[me][slot];
+            if (!wait(&sh->o_full[i], o_phase)) return;
+            o_phase ^= 1;
+            tc_fence_after();
+            const bool full = cur.count == cur.range.n;
+            const int tile_row = i * kTileRows + row;
+            const bool is_row = tile_row < live_rows<kRows>(t, cur);
+            const RowPlace at = row_place(t, cur, kRows, tile_row);
+            const PartLayout parts = part_layout(a, gridDim.x, kRows);
+            const int which = cur.from > 0 ? 0 : 1;
+            const bool none = last <= first;
+            const float inv = none ? 0.f : 1.f / l;
+            uint8_t* dst = !is_row ? nullptr
+                           : full  ? t.out + at.token * t.o_token + (int64_t)at.head * t.o_head
+                                   : reinterpret_cast<uint8_t*>(parts.acc(blockIdx.x, which) + (size_t)tile_row * a.dim);
+            bool odd = false;
+#pragma unroll 1
+            for (int c = 0; c < a.dim; c += 16) {
+                uint32_t o[16];
+                tc_load16(at_o + c, o);
+                tc_wait_load();
+                if (full) {
+#pragma unroll
+                    for (int k = 0; k < 16; k += 2) {
+                        const float u = none ? 0.f : __uint_as_float(o[k]) * inv;
+                        const float v = none ? 0.f : __uint_as_float(o[k + 1]) * inv;
+                        odd |= !(fabsf(u) <= 3.402823466e+38f) || !(fabsf(v) <= 3.402823466e+38f);
+                        o[k / 2] = pack<T>(u, v);
+                    }
+                }
+                // 32 bytes of a row at a time: 16 results, or 8 values of a part
+#pragma unroll 1
+                for (int h = 0; h < (full ? 1 : 2); ++h) {
+                    uint32_t y[8];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) y[k] = h == 0 ? o[k] : o[8 + k];
+                    store_rows(stage, y, dst == nullptr ? nullptr : dst + c * (full ? 2 : 4) + 32 * h);
+                }
+            }
+            if (full) {
+                if (is_row && t.lse != nullptr)
+                    t.lse[at.token * t.q_heads + at.head] = none ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+                for (uint32_t todo = __ballot_sync(0xFFFFFFFFu, odd && is_row); todo != 0; todo &= todo - 1) {
+                    __syncwarp();
+                    fix_row<T, FMT>(a, t, cur, kRows, i * kTileRows + 32 * warp + __ffs(todo) - 1);
+                }
+            } else if (is_row) {
+                parts.stats(blockIdx.x, which)[tile_row] = m;
+                parts.stats(blockIdx.x, which)[kRows + tile_row] = l;
+            }
+            tc_fence_before();
+        }
+        if (!more) return;
+        slot ^= 1;
+        tile += skipped;
+        const Piece& cur = sh->piece[me][slot];
+        first = last = 0;
+        if (i * kTileRows + row < live_rows<kRows>(t, cur))
             visible_range(t, cur.seq.len, row_place(t, cur, kRows, i * kTileRows + row).pos, first, last);
         const int32_t count = cur.count;
-        float m = -INFINITY, l = 0.f;
+        m = -INFINITY;
+        l = 0.f;
         int32_t base = (cur.range.lo + cur.from) * kTokens;
-        tile += skipped;
-        skipped = 0;
         for (int32_t j = 0; j < count; ++j, ++tile, base += kTokens) {
-            if (!__all_sync(0xFFFFFFFFu, wait(&sh->s_full[i], s_phase))) return;
+            if (!wait(&sh->s_full[i], s_phase)) return;
             s_phase ^= 1;
             tc_fence_after();
+            const uint32_t scale_slot = tile % kScaleSlots;
+            if (FMT != kKv16Bit && !wait(&sh->scale_full[scale_slot], (tile / kScaleSlots) & 1)) return;
             uint32_t s[kTokens];
 #pragma unroll
             for (int c = 0; c < kTokens; c += 32) tc_load32(at_s + c, s + c);
             tc_wait_load();
-            const uint32_t scale_slot = tile % kScaleSlots;
             if (FMT != kKv16Bit) {
-                if (!__all_sync(0xFFFFFFFFu, wait(&sh->scale_full[scale_slot], (tile / kScaleSlots) & 1))) return;
                 const uint32_t at = smem_addr(&sh->k_scale[scale_slot][0]);
 #pragma unroll
                 for (int c = 0; c < kTokens; c += 32) {
@@ -617,10 +745,12 @@ __device__ __forceinline__ void softmax_role(const KvArgs& a, const AttnArgs& t,
                 }
             }
             if (base < first || base + kTokens > last) {
-                const int32_t lo = first - base, hi = last - base;  // visible columns lo .. hi - 1
 #pragma unroll
-                for (int c = 0; c < kTokens; ++c)
-                    if (c < lo || c >= hi) s[c] = 0xFF800000u;
+                for (int c = 0; c < kTokens; c += 32) {
+                    const uint32_t seen = bits_below(last - base - c) & ~bits_below(first - base - c);
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) s[c + k] = (seen >> k & 1u) != 0 ? s[c + k] : 0xFF800000u;
+                }
             }
             float top0 = -INFINITY, top1 = -INFINITY;
 #pragma unroll
@@ -684,61 +814,6 @@ __device__ __forceinline__ void softmax_role(const KvArgs& a, const AttnArgs& t,
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh->p_full[i]);
         }
-        // the next item's rows of Q may come now: the last S is done, so is every product with these
-        have = take(sh->walk[me], cur);
-        if (!__all_sync(0xFFFFFFFFu, wait(&sh->o_full[i], o_phase))) return;
-        o_phase ^= 1;
-        tc_fence_after();
-        const bool full = cur.count == cur.range.n;
-        const RowPlace at = row_place(t, cur, kRows, i * kTileRows + row);
-        const int tile_row = i * kTileRows + row;
-        bool odd = false;
-        if (full) {
-            const bool none = last <= first;
-            const float inv = none ? 0.f : 1.f / l;
-            uint8_t* dst = t.out + at.token * t.o_token + (int64_t)at.head * t.o_head;
-            for (int c = 0; c < a.dim; c += 16) {
-                uint32_t o[16];
-                tc_load16(at_o + c, o);
-                tc_wait_load();
-                uint32_t y[8];
-#pragma unroll
-                for (int k = 0; k < 16; k += 2) {
-                    const float u = none ? 0.f : __uint_as_float(o[k]) * inv;
-                    const float v = none ? 0.f : __uint_as_float(o[k + 1]) * inv;
-                    odd |= !(fabsf(u) <= 3.402823466e+38f) || !(fabsf(v) <= 3.402823466e+38f);
-                    y[k / 2] = pack<T>(u, v);
-                }
-                if (is_row) {
-                    *reinterpret_cast<uint4*>(dst + 2 * c) = make_uint4(y[0], y[1], y[2], y[3]);
-                    *reinterpret_cast<uint4*>(dst + 2 * c + 16) = make_uint4(y[4], y[5], y[6], y[7]);
-                }
-            }
-            if (is_row && t.lse != nullptr)
-                t.lse[at.token * t.q_heads + at.head] = none ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
-            for (uint32_t todo = __ballot_sync(0xFFFFFFFFu, odd && is_row); todo != 0; todo &= todo - 1) {
-                __syncwarp();
-                fix_row<T, FMT>(a, t, cur, kRows, i * kTileRows + 32 * warp + __ffs(todo) - 1);
-            }
-        } else {
-            const int which = cur.from > 0 ? 0 : 1;
-            float* dst = parts.acc(w.share, which) + (size_t)tile_row * a.dim;
-            for (int c = 0; c < a.dim; c += 16) {
-                uint32_t o[16];
-                tc_load16(at_o + c, o);
-                tc_wait_load();
-                if (is_row) {
-#pragma unroll
-                    for (int k = 0; k < 16; k += 4)
-                        *reinterpret_cast<uint4*>(dst + c + k) = make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]);
-                }
-            }
-            if (is_row) {
-                parts.stats(w.share, which)[tile_row] = m;
-                parts.stats(w.share, which)[kRows + tile_row] = l;
-            }
-        }
-        tc_fence_before();
     }
 }
 
@@ -753,8 +828,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     // tiles at 1024-byte boundaries (the swizzle's period): Q0, Q1, the K and V slots, then the rest
     const uint32_t base = (smem_addr(raw) + 1023) & ~1023u;
     const uint32_t tile_bytes = (a.dim > 64 ? 2 : 1) * kHalfBytes;
-    Shared* sh = reinterpret_cast<Shared*>(raw + (base - smem_addr(raw)) + (2 + kN) * tile_bytes +
-                                           (FMT == kKv16Bit ? 0 : kRawSlots * kTokens * a.dim));
+    const uint32_t raw_bytes = FMT == kKv16Bit ? 0 : kRawSlots * kTokens * a.dim;
+    Shared* sh = reinterpret_cast<Shared*>(raw + (base - smem_addr(raw)) + (2 + kN) * tile_bytes + raw_bytes +
+                                           kStageBytes);
     const int warp = threadIdx.x >> 5;
     if (warp == 0) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&sh->tmem))
@@ -777,6 +853,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&sh->raw_free[i], kLoaderWarps);
         }
         for (int i = 0; i < kScaleSlots; ++i) mbar_init(&sh->scale_full[i], kLoaderWarps);
+        for (int i = 0; i < kRing; ++i) {
+            mbar_init(&sh->piece_full[i], 1);
+            mbar_init(&sh->piece_free[i], FMT == kKv16Bit ? 13 : 14);  // the warps that take pieces
+        }
         mbar_init(&sh->drained, 1);
         sh->stop = 0;
         fence_mbar_init();
@@ -785,29 +865,30 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const Walk w = make_walk(sh->prefix[a.batch], blockIdx.x, gridDim.x, min_tiles, whole_items);
     const uint32_t slots = base + 2 * tile_bytes, raw_codes = slots + kN * tile_bytes;
     const Fetch fetch{&k_map, &v_map, box};
     if (warp < 8) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
-        softmax_role<T, FMT>(a, t, sh, base + (warp / 4) * tile_bytes, w);
+        softmax_role<T, FMT>(a, t, sh, base + (warp / 4) * tile_bytes, raw_codes + raw_bytes);
     } else if (warp < 12) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLoaderRegs));
         if constexpr (FMT == kKv16Bit)
-            fetch_role<FMT, 4, kN>(a, t, sh, fetch, warp - 8, slots, tile_bytes, sh->kv_full, sh->kv_free, w);
+            fetch_role<FMT, 4, kN>(a, t, sh, fetch, warp - 8, slots, tile_bytes, sh->kv_full, sh->kv_free);
         else
-            widen_role<FMT>(a, t, sh, raw_codes, kTokens * a.dim, slots, tile_bytes, w);
+            widen_role<FMT>(a, t, sh, raw_codes, kTokens * a.dim, slots, tile_bytes);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLoaderRegs));
         if (warp == 12) {
-            mma_role<Operand<T, FMT>, kN>(a, t, sh, base, slots, tile_bytes, w);
+            mma_role<Operand<T, FMT>, kN>(a, t, sh, base, slots, tile_bytes);
             __syncwarp();
             if (threadIdx.x == 12 * 32) {  // every product is done before TMEM goes
                 tc_commit(&sh->drained);
-                if (!mbar_wait(&sh->drained, 0)) record_error(a.ws, kStatusTimeout);
+                wait_long(sh, a.ws, &sh->drained, 0);
             }
         } else if (warp == 13 && FMT != kKv16Bit) {
-            fetch_role<FMT, 1, kRawSlots>(a, t, sh, fetch, 0, raw_codes, kTokens * a.dim, sh->raw_full, sh->raw_free, w);
+            fetch_role<FMT, 1, kRawSlots>(a, t, sh, fetch, 0, raw_codes, kTokens * a.dim, sh->raw_full, sh->raw_free);
+        } else if (warp == 14) {
+            walk_role(a, t, sh, make_walk(sh->prefix[a.batch], blockIdx.x, gridDim.x, min_tiles, whole_items));
         }
     }
     __syncwarp();
@@ -821,7 +902,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <int FMT>
 constexpr size_t shared_bytes(int dim) {
     return 1024 + (size_t)(2 + kSlots<FMT>) * (dim > 64 ? 2 : 1) * kHalfBytes +
-           (FMT == kKv16Bit ? 0 : (size_t)kRawSlots * kTokens * dim) + sizeof(Shared);
+           (FMT == kKv16Bit ? 0 : (size_t)kRawSlots * kTokens * dim) + kStageBytes + sizeof(Shared);
 }
 
 static_assert(shared_bytes<kKv16Bit>(128) <= 232448 && shared_bytes<kKvInt8>(128) <= 232448, "227 KB a block");
@@ -888,7 +969,7 @@ cudaError_t launch_one(const KvArgs& a, const AttnArgs& t, bool whole, uint32_t 
         <<<kShares, kThreads, shared_bytes<FMT>(a.dim), s>>>(a, t, k_map, v_map, box, min_tiles, whole ? 1 : 0);
     e = cudaGetLastError();
     if (e != cudaSuccess || whole) return e;
-    return launch_join<T, FMT, kRows>(a, t, kShares, s);
+    return launch_join<T, FMT, kRows, JoinShape<8, 1, 4, kShares>>(a, t, kShares, s);
 }
 
 }  // namespace

@@ -218,11 +218,12 @@ __device__ __forceinline__ bool next_piece(const KvArgs& a, const AttnArgs& t, c
 // part of shares c .. last.
 struct Cut {
     int32_t b, kv_head, rt, last;  // last < 0: nothing to join here
+    Sequence seq;
 };
 // Written by block c (one thread) for its first piece.
 template <int ROWS, int TOKENS>
 __device__ __forceinline__ Cut cut_of(const Piece& p, const Line& l, uint32_t c) {
-    Cut u{p.b, p.kv_head, p.rt, -1};
+    Cut u{p.b, p.kv_head, p.rt, -1, p.seq};
     if (c > 0 && p.item < share_start(l, c) && share_start(l, c - 1) <= p.item) {
         const uint32_t end = p.item + (uint32_t)p.range.n;
         uint32_t last = c;
@@ -303,15 +304,22 @@ __device__ __forceinline__ void fix_row(const KvArgs& a, const AttnArgs& t, cons
     attend_row<T, FMT>(a, t, p.b, p.seq.len, at.token, at.pos, at.head);
 }
 
-// Joins the parts of the item cut at the start of share blockIdx.x: 4 rows a
-// block, 4 values a thread.  Parts are taken in the order of the line.
-constexpr int kJoinRows = 4, kJoinThreads = 128;
-constexpr int kMaxShares = 608;
-template <class T, int FMT, int ROWS>
-__global__ void __launch_bounds__(kJoinThreads) join_parts_kernel(const __grid_constant__ KvArgs a,
-                                                                  const __grid_constant__ AttnArgs t, int shares) {
-    __shared__ float weight[kJoinRows][kMaxShares + 1];
-    __shared__ float total[kJoinRows], top[kJoinRows];
+// Joins the parts of the item cut at the start of share blockIdx.x.  A block has
+// GROUPS groups of STRIDES warps; a group joins EACH rows at a time, its warps
+// taking every STRIDES-th part (items of few rows can have hundreds of parts,
+// items of many have few), and adds its warps' sums in their order.
+constexpr int kMaxShares = 456;
+template <int GROUPS_, int STRIDES_, int EACH_, int PARTS_>
+struct JoinShape {
+    static constexpr int GROUPS = GROUPS_, STRIDES = STRIDES_, EACH = EACH_, PARTS = PARTS_;
+    static constexpr int kRows = GROUPS * EACH, kThreads = 32 * GROUPS * STRIDES;
+};
+template <class T, int FMT, int ROWS, class J>
+__global__ void __launch_bounds__(J::kThreads) join_parts_kernel(const __grid_constant__ KvArgs a,
+                                                                 const __grid_constant__ AttnArgs t, int shares) {
+    __shared__ float weight[J::kRows][J::PARTS + 1], sums[J::kRows][J::PARTS + 1];
+    __shared__ float total[J::kRows], top[J::kRows];
+    __shared__ float4 meet[J::STRIDES > 1 ? J::STRIDES : 1][J::STRIDES > 1 ? J::kRows : 1][32];
     __shared__ uint32_t odd_rows;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const PartLayout parts = part_layout(a, shares, ROWS);
@@ -321,19 +329,22 @@ __global__ void __launch_bounds__(kJoinThreads) join_parts_kernel(const __grid_c
     p.b = cut.b;
     p.kv_head = cut.kv_head;
     p.rt = cut.rt;
-    p.seq = load_sequence(a, cut.b);
-    const int row0 = blockIdx.y * kJoinRows;
-    const int live = live_rows<ROWS>(t, p) - row0;
+    p.seq = cut.seq;
+    const int row0 = blockIdx.y * J::kRows, live = live_rows<ROWS>(t, p) - row0;
     if (live <= 0) return;
     const int first = (int)blockIdx.x - 1, n = cut.last - first + 1;
     if (threadIdx.x == 0) odd_rows = 0;
-    for (int i = threadIdx.x; i < n * kJoinRows; i += kJoinThreads) {
-        const int part = i / kJoinRows, r = i % kJoinRows;
-        if (r < live) weight[r][part] = parts.stats(first + part, part == 0 ? 1 : 0)[row0 + r];
+    for (int i = threadIdx.x; i < n * J::kRows; i += J::kThreads) {
+        const int part = i / J::kRows, r = i % J::kRows;
+        if (r < live) {
+            const float* st = parts.stats(first + part, part == 0);
+            weight[r][part] = st[row0 + r];
+            sums[r][part] = st[ROWS + row0 + r];
+        }
     }
     __syncthreads();
-    const int r = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (r < live) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    for (int r = warp; r < min(J::kRows, live); r += J::kThreads / 32) {
         float m = -INFINITY;
         for (int i = lane; i < n; i += 32) m = fmaxf(m, weight[r][i]);
 #pragma unroll
@@ -342,7 +353,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_parts_kernel(const __grid_c
         float sum = 0.f;
         for (int i = lane; i < n; i += 32) {
             const float f = exp2f(weight[r][i] - from);
-            sum += f * parts.stats(first + i, i == 0 ? 1 : 0)[ROWS + row0 + r];
+            sum += f * sums[r][i];
             weight[r][i] = f;
         }
         sum = warp_sum(sum);
@@ -352,42 +363,78 @@ __global__ void __launch_bounds__(kJoinThreads) join_parts_kernel(const __grid_c
         }
     }
     __syncthreads();
-    if (r < live && 4 * lane < a.dim) {
-        float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-#pragma unroll 8
-        for (int i = 0; i < n; ++i) {
-            const float4 x = *reinterpret_cast<const float4*>(parts.acc(first + i, i == 0 ? 1 : 0) +
-                                                              (size_t)(row0 + r) * a.dim + 4 * lane);
-            const float f = weight[r][i];
-            v[0] += f * x.x;
-            v[1] += f * x.y;
-            v[2] += f * x.z;
-            v[3] += f * x.w;
-        }
-        // pairs of lanes hold 8 values together: the even one stores them
+    const int group = warp / J::STRIDES, stride = warp % J::STRIDES;
+    const int r0 = group * J::EACH;
+    float4 v[J::EACH];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[4 + i] = __shfl_down_sync(__activemask(), v[i], 1);
-        if ((lane & 1) == 0 && store_row_part<T>(t, p, ROWS, row0 + r, 4 * lane, v, top[r], total[r]))
-            atomicOr(&odd_rows, 1u << r);
+    for (int k = 0; k < J::EACH; ++k) v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    const bool inside = 4 * lane < a.dim;
+#pragma unroll 4
+    for (int i = stride; i < n; i += J::STRIDES) {
+        const float* src = parts.acc(first + i, i == 0) + (size_t)(row0 + r0) * a.dim + 4 * lane;
+#pragma unroll
+        for (int k = 0; k < J::EACH; ++k) {
+            if (r0 + k < live && inside) {
+                const float4 x = *reinterpret_cast<const float4*>(src + (size_t)k * a.dim);
+                const float f = weight[r0 + k][i];
+                v[k].x += f * x.x;
+                v[k].y += f * x.y;
+                v[k].z += f * x.z;
+                v[k].w += f * x.w;
+            }
+        }
+    }
+    if (J::STRIDES > 1) {
+#pragma unroll
+        for (int k = 0; k < J::EACH; ++k) meet[stride][r0 + k][lane] = v[k];
+        __syncthreads();
+        if (stride == 0) {
+#pragma unroll
+            for (int k = 0; k < J::EACH; ++k)
+#pragma unroll
+                for (int i = 1; i < J::STRIDES; ++i) {
+                    const float4 x = meet[i][r0 + k][lane];
+                    v[k].x += x.x;
+                    v[k].y += x.y;
+                    v[k].z += x.z;
+                    v[k].w += x.w;
+                }
+        }
+    }
+    if (stride == 0) {
+#pragma unroll
+        for (int k = 0; k < J::EACH; ++k) {
+            // pairs of lanes hold 8 values together: the even one stores them
+            const float y[8] = {v[k].x, v[k].y, v[k].z, v[k].w, __shfl_down_sync(0xFFFFFFFFu, v[k].x, 1),
+                                __shfl_down_sync(0xFFFFFFFFu, v[k].y, 1), __shfl_down_sync(0xFFFFFFFFu, v[k].z, 1),
+                                __shfl_down_sync(0xFFFFFFFFu, v[k].w, 1)};
+            const int r = r0 + k;
+            if (r < live && inside && (lane & 1) == 0 &&
+                store_row_part<T>(t, p, ROWS, row0 + r, 4 * lane, y, top[r], total[r]))
+                atomicOr(&odd_rows, 1u << r);
+        }
     }
     __syncthreads();
-    if (r < live && (odd_rows >> r & 1u)) fix_row<T, FMT>(a, t, p, ROWS, row0 + r);
+    for (uint32_t odd = odd_rows; odd != 0; odd &= odd - 1) {
+        const int r = __ffs(odd) - 1;
+        if (r % (J::kThreads / 32) == warp) fix_row<T, FMT>(a, t, p, ROWS, row0 + r);
+    }
 }
 
 // Launched so that its blocks may start while the kernel before it still runs;
 // they wait for its end before they read.
-template <class T, int FMT, int ROWS>
+template <class T, int FMT, int ROWS, class J>
 cudaError_t launch_join(const KvArgs& a, const AttnArgs& t, int shares, cudaStream_t s) {
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)shares, ROWS / kJoinRows);
-    cfg.blockDim = dim3(kJoinThreads);
+    cfg.gridDim = dim3((unsigned)shares, ROWS / J::kRows);
+    cfg.blockDim = dim3(J::kThreads);
     cfg.stream = s;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, join_parts_kernel<T, FMT, ROWS>, a, t, shares);
+    return cudaLaunchKernelEx(&cfg, join_parts_kernel<T, FMT, ROWS, J>, a, t, shares);
 }
 
 }  // namespace cccl

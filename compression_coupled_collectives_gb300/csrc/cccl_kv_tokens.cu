@@ -597,7 +597,7 @@ cudaError_t launch_tokens(const KvArgs& a, const AttnArgs& t, bool whole, uint32
     attend_tokens_kernel<S><<<S::kShares, kThreads, S::kSmem, s>>>(a, t, min_tiles, whole ? 1 : 0);
     e = cudaGetLastError();
     if (e != cudaSuccess || whole) return e;
-    return launch_join<typename S::T, S::FMT, S::kRows>(a, t, S::kShares, s);
+    return launch_join<typename S::T, S::FMT, S::kRows, JoinShape<4, 4, 1, kMaxShares>>(a, t, S::kShares, s);
 }
 
 template <class T, int FMT, int DP>
