@@ -137,7 +137,8 @@ __device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t leading) {
     return (uint64_t)((addr & 0x3FFFF) >> 4) | ((uint64_t)(leading >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
            (1ull << 46) | (2ull << 61);
 }
-// kind::f16: binary32 accumulator, M = 128, both operands of one type.
+// kind::f16: binary32 accumulator, M = 128, both operands of one type (bit 13
+// would change A's sign).
 __device__ __forceinline__ uint32_t instruction(bool half, int n, bool b_mn_major) {
     const uint32_t type = half ? 0u : 1u;
     return (1u << 4) | (type << 7) | (type << 10) | ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) |
@@ -454,7 +455,8 @@ __device__ __forceinline__ void mma_role(const KvArgs& a, const AttnArgs& t, Sha
                                          uint32_t slots, uint32_t slot_bytes) {
     const Waiter wait{sh, a.ws};
     const uint32_t tmem = sh->tmem;
-    const uint32_t qk = instruction(M::kHalf, kTokens, false), pv = instruction(M::kHalf, a.dim > 64 ? 128 : 64, true);
+    // a negative scale: Q enters with its sign changed, the softmax takes the scale's size
+    const uint32_t qk = instruction(M::kHalf, kTokens, false) | (t.scale < 0.f ? 1u << 13 : 0u), pv = instruction(M::kHalf, a.dim > 64 ? 128 : 64, true);
     const int steps = a.dim / 16;
     const uint32_t q_bytes = slot_bytes;
     uint32_t entry = 0;
@@ -526,22 +528,34 @@ __device__ __forceinline__ void mma_role(const KvArgs& a, const AttnArgs& t, Sha
 
 // ---------------------------------------------------------------- softmax
 // Rows 32 warp .. + 31 of row tile i of Q into shared memory, 16 lanes a row;
-// rows that do not exist are zeros.  flip: the sign bit when the scale is
-// negative; zero: the scale is zero (every score is then 0 times the products,
-// so are zeros').  Returns what undoes the power of two of row 32 warp + lane
-// (8-bit caches).  (Loops are kept small here and at an item's end: code that
-// runs once an item is fetched anew each time, at its length's cost.)
+// rows that do not exist are zeros, and all are when the scale is zero (every
+// score is then 0 times the products, so are zeros').  A row that goes as it is
+// comes by asynchronous copies, which the caller waits for; bf16 rows for 8-bit
+// caches pass through registers for their power of two, and what undoes that
+// of row 32 warp + lane is returned.  (Code that runs once an item is fetched
+// anew each time and waits behind the K and V copies in flight: it is kept
+// short, with few rounds to memory.)
 template <class T, int FMT>
 __device__ __forceinline__ float bring_rows(const KvArgs& a, const AttnArgs& t, const Piece& p, int i, int warp,
-                                            uint32_t q_tile, bool flip, bool zero) {
+                                            uint32_t q_tile, bool zero) {
     const int lane = threadIdx.x & 31, chunk = lane & 15;
     const int row0 = i * kTileRows + 32 * warp, live = zero ? 0 : live_rows<kRows>(t, p) - row0;
     const RowPlace mine = row_place(t, p, kRows, row0 + lane);
     const int64_t from = mine.token * t.q_token + (int64_t)mine.head * t.q_head;
     const bool inside = 8 * chunk < a.dim;
-    const uint32_t sign = flip ? 0x80008000u : 0u;
     float inverse = 1.f;
-    constexpr int kEach = 4;  // loads in flight
+    if (FMT == kKv16Bit || T::kHalf) {
+#pragma unroll 4
+        for (int k = 0; k < 32; k += 2) {
+            const int row = k + (lane >> 4);
+            const int64_t at = __shfl_sync(0xFFFFFFFFu, from, row);
+            const bool real = row < live;
+            if (inside) copy16(q_tile + swizzled(32 * warp + row, chunk), t.q + (real ? at + 16 * chunk : 0), real);
+        }
+        copy_commit();
+        return inverse;
+    }
+    constexpr int kEach = 8;  // loads in flight
 #pragma unroll 1
     for (int part = 0; part < 32; part += 2 * kEach) {
         uint4 x[kEach];
@@ -554,18 +568,16 @@ __device__ __forceinline__ float bring_rows(const KvArgs& a, const AttnArgs& t, 
         }
 #pragma unroll
         for (int k = 0; k < kEach; ++k) {
-            uint4 y = make_uint4(x[k].x ^ sign, x[k].y ^ sign, x[k].z ^ sign, x[k].w ^ sign);
-            if (FMT != kKv16Bit && !T::kHalf) {
-                uint32_t top = vmax_u16x2(vmax_u16x2(y.x & 0x7FFF7FFFu, y.y & 0x7FFF7FFFu),
-                                          vmax_u16x2(y.z & 0x7FFF7FFFu, y.w & 0x7FFF7FFFu));
+            uint4 y = x[k];
+            uint32_t top = vmax_u16x2(vmax_u16x2(y.x & 0x7FFF7FFFu, y.y & 0x7FFF7FFFu),
+                                      vmax_u16x2(y.z & 0x7FFF7FFFu, y.w & 0x7FFF7FFFu));
 #pragma unroll
-                for (int o = 1; o < 16; o <<= 1) top = vmax_u16x2(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-                const float power = query_power<T>(max(top & 0xFFFFu, top >> 16));
-                y = make_uint4(scaled_pair<T>(y.x, power), scaled_pair<T>(y.y, power), scaled_pair<T>(y.z, power),
-                               scaled_pair<T>(y.w, power));
-                const float to_owner = __shfl_sync(0xFFFFFFFFu, power, (lane & 1) * 16);
-                if ((lane >> 1) == part / 2 + k) inverse = 1.f / to_owner;
-            }
+            for (int o = 1; o < 16; o <<= 1) top = vmax_u16x2(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+            const float power = query_power<T>(max(top & 0xFFFFu, top >> 16));
+            y = make_uint4(scaled_pair<T>(y.x, power), scaled_pair<T>(y.y, power), scaled_pair<T>(y.z, power),
+                           scaled_pair<T>(y.w, power));
+            const float to_owner = __shfl_sync(0xFFFFFFFFu, power, (lane & 1) * 16);
+            if ((lane >> 1) == part / 2 + k) inverse = 1.f / to_owner;
             if (inside)
                 asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(
                                  q_tile + swizzled(32 * warp + part + 2 * k + (lane >> 4), chunk)),
@@ -573,14 +585,13 @@ __device__ __forceinline__ float bring_rows(const KvArgs& a, const AttnArgs& t, 
                              : "memory");
         }
     }
-    fence_proxy_async_smem();
     return inverse;
 }
 
 // A warp's 32 rows of 32 bytes each, a row a lane, to global memory: through
 // shared memory, so that a store instruction writes whole sectors.  to: where
-// this lane's row goes (null: nowhere).
-__device__ __forceinline__ void store_rows(uint32_t stage, const uint32_t* words, uint8_t* to) {
+// this lane's halves (16 bytes) of rows lane / 2 and 16 + lane / 2 go, or null.
+__device__ __forceinline__ void store_rows(uint32_t stage, const uint32_t* words, uint8_t* const* to, int64_t offset) {
     const int lane = threadIdx.x & 31;
     // the 16-byte halves of rows 4..7 of 8 are swapped: a quarter-warp meets all banks
     auto at = [&](int r, int c) { return stage + r * 32 + ((c ^ ((r >> 2) & 1)) << 4); };
@@ -593,13 +604,11 @@ __device__ __forceinline__ void store_rows(uint32_t stage, const uint32_t* words
     __syncwarp();
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-        const int row = 16 * k + (lane >> 1);
-        const uint64_t dst = __shfl_sync(0xFFFFFFFFu, reinterpret_cast<uint64_t>(to), row);
         uint4 x;
         asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
                      : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
-                     : "r"(at(row, lane & 1)));
-        if (dst != 0) *reinterpret_cast<uint4*>(dst + 16 * (lane & 1)) = x;
+                     : "r"(at(16 * k + (lane >> 1), lane & 1)));
+        if (to[k] != nullptr) *reinterpret_cast<uint4*>(to[k] + offset) = x;
     }
 }
 
@@ -625,7 +634,7 @@ __device__ __forceinline__ void softmax_role(const KvArgs& a, const AttnArgs& t,
     const Waiter wait{sh, a.ws};
     const uint32_t tmem = sh->tmem + ((uint32_t)(32 * warp) << 16), stage = stages + me * (32 * 32);
     const uint32_t at_s = tmem + kColS + 128 * i, at_o = tmem + kColO + 128 * i;
-    const bool flip = t.scale < 0.f, zero = t.scale == 0.f;
+    const bool zero = t.scale == 0.f;
     const float scale_base2 = (zero ? 1.f : fabsf(t.scale)) * 1.4426950408889634f;
     uint32_t s_phase = 0, o_phase = 0, taken = 0, tile = 0;  // tile: this block's tiles of tokens, whoever's
     int slot = 1;                                 // of the piece at hand
@@ -650,11 +659,7 @@ __device__ __forceinline__ void softmax_role(const KvArgs& a, const AttnArgs& t,
         }
         ++taken;
         const bool more = next->count > 0;
-        if (more) {
-            to_base2 *= bring_rows<T, FMT>(a, t, *next, i, warp, q_tile, flip, zero);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sh->q_full[i]);
-        }
+        if (more) to_base2 *= bring_rows<T, FMT>(a, t, *next, i, warp, q_tile, zero);
         if (!begin) {  // the end of the piece at hand
             const Piece& cur = sh->piece[me][slot];
             if (!wait(&sh->o_full[i], o_phase)) return;
@@ -668,31 +673,44 @@ __device__ __forceinline__ void softmax_role(const KvArgs& a, const AttnArgs& t,
             const int which = cur.from > 0 ? 0 : 1;
             const bool none = last <= first;
             const float inv = none ? 0.f : 1.f / l;
-            uint8_t* dst = !is_row ? nullptr
-                           : full  ? t.out + at.token * t.o_token + (int64_t)at.head * t.o_head
-                                   : reinterpret_cast<uint8_t*>(parts.acc(blockIdx.x, which) + (size_t)tile_row * a.dim);
+            uint8_t* const dst =
+                !is_row ? nullptr
+                : full  ? t.out + at.token * t.o_token + (int64_t)at.head * t.o_head
+                        : reinterpret_cast<uint8_t*>(parts.acc(blockIdx.x, which) + (size_t)tile_row * a.dim);
+            uint8_t* to[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const uint64_t x = __shfl_sync(0xFFFFFFFFu, reinterpret_cast<uint64_t>(dst), 16 * k + (lane >> 1));
+                to[k] = x != 0 ? reinterpret_cast<uint8_t*>(x) + 16 * (lane & 1) : nullptr;
+            }
             bool odd = false;
+            uint32_t ahead[32];
+            tc_load32(at_o, ahead);
 #pragma unroll 1
-            for (int c = 0; c < a.dim; c += 16) {
-                uint32_t o[16];
-                tc_load16(at_o + c, o);
+            for (int c = 0; c < a.dim; c += 32) {
+                uint32_t o[32];
                 tc_wait_load();
+#pragma unroll
+                for (int k = 0; k < 32; ++k) o[k] = ahead[k];
+                if (c + 32 < a.dim) tc_load32(at_o + c + 32, ahead);
                 if (full) {
 #pragma unroll
-                    for (int k = 0; k < 16; k += 2) {
-                        const float u = none ? 0.f : __uint_as_float(o[k]) * inv;
-                        const float v = none ? 0.f : __uint_as_float(o[k + 1]) * inv;
-                        odd |= !(fabsf(u) <= 3.402823466e+38f) || !(fabsf(v) <= 3.402823466e+38f);
-                        o[k / 2] = pack<T>(u, v);
-                    }
-                }
-                // 32 bytes of a row at a time: 16 results, or 8 values of a part
-#pragma unroll 1
-                for (int h = 0; h < (full ? 1 : 2); ++h) {
-                    uint32_t y[8];
+                    for (int h = 0; h < 32; h += 16) {
+                        if (c + h >= a.dim) break;
+                        uint32_t y[8];
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) y[k] = h == 0 ? o[k] : o[8 + k];
-                    store_rows(stage, y, dst == nullptr ? nullptr : dst + c * (full ? 2 : 4) + 32 * h);
+                        for (int k = 0; k < 16; k += 2) {
+                            const float u = none ? 0.f : __uint_as_float(o[h + k]) * inv;
+                            const float v = none ? 0.f : __uint_as_float(o[h + k + 1]) * inv;
+                            odd |= !(fabsf(u) <= 3.402823466e+38f) || !(fabsf(v) <= 3.402823466e+38f);
+                            y[k / 2] = pack<T>(u, v);
+                        }
+                        store_rows(stage, y, to, 2 * (c + h));
+                    }
+                } else {
+#pragma unroll
+                    for (int h = 0; h < 32; h += 8)
+                        if (c + h < a.dim) store_rows(stage, o + h, to, 4 * (c + h));
                 }
             }
             if (full) {
@@ -709,6 +727,10 @@ __device__ __forceinline__ void softmax_role(const KvArgs& a, const AttnArgs& t,
             tc_fence_before();
         }
         if (!more) return;
+        copy_wait<0>();
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh->q_full[i]);
         slot ^= 1;
         tile += skipped;
         const Piece& cur = sh->piece[me][slot];
