@@ -35,6 +35,7 @@ namespace {
 constexpr int kRows = 256, kTileRows = 128, kTokens = 128;
 constexpr int kThreads = 512;
 constexpr int kShares = 152;
+static_assert(kShares <= kManyShares, "the joining kernel has room for every share's part");
 constexpr int kScaleSlots = 3;   // tiles of tokens whose scales are kept
 constexpr int kLoaderWarps = 4;
 // K and V tiles in shared memory, as 16-bit values; tiles of 8-bit codes on
@@ -42,8 +43,13 @@ constexpr int kLoaderWarps = 4;
 constexpr int kMostSlots = 4, kRawSlots = 3;
 template <int FMT>
 constexpr int kSlots = FMT == kKv16Bit ? 4 : 3;
-constexpr int kStageBytes = 8 * 32 * 32;  // the softmax warps' rows on their way out
-constexpr float kSlack = 8.f;             // base 2
+constexpr float kSlack = 8.f;    // base 2
+// Halves of result rows (128 bytes) that a softmax warp has on their way out at
+// a time
+template <int FMT>
+constexpr int kStageRows = FMT == kKv16Bit ? 16 : 8;
+template <int FMT>
+constexpr int kStageBytes = 8 * 128 * kStageRows<FMT>;
 
 // Registers of a thread: the launch's 4 x 128 a warpgroup, divided anew (two
 // softmax warpgroups, two of the others).
@@ -555,9 +561,9 @@ __device__ __forceinline__ float bring_rows(const KvArgs& a, const AttnArgs& t, 
         copy_commit();
         return inverse;
     }
-    constexpr int kEach = 8;  // loads in flight
-#pragma unroll 1
-    for (int part = 0; part < 32; part += 2 * kEach) {
+    constexpr int kEach = 16;  // loads in flight: all of them
+    constexpr int part = 0;
+    {
         uint4 x[kEach];
 #pragma unroll
         for (int k = 0; k < kEach; ++k) {
@@ -588,27 +594,36 @@ __device__ __forceinline__ float bring_rows(const KvArgs& a, const AttnArgs& t, 
     return inverse;
 }
 
-// A warp's 32 rows of 32 bytes each, a row a lane, to global memory: through
-// shared memory, so that a store instruction writes whole sectors.  to: where
-// this lane's halves (16 bytes) of rows lane / 2 and 16 + lane / 2 go, or null.
-__device__ __forceinline__ void store_rows(uint32_t stage, const uint32_t* words, uint8_t* const* to, int64_t offset) {
-    const int lane = threadIdx.x & 31;
-    // the 16-byte halves of rows 4..7 of 8 are swapped: a quarter-warp meets all banks
-    auto at = [&](int r, int c) { return stage + r * 32 + ((c ^ ((r >> 2) & 1)) << 4); };
-    __syncwarp();
+// 64 columns of a warp's 32 result rows (16-bit, a row a lane) to global
+// memory, STEP rows at a time through shared memory, so that a store
+// instruction writes 128-byte runs.  to: where this lane's row goes (null:
+// nowhere); the first `bytes` of the 128 exist.  Chunk c of row r lies at chunk
+// c ^ r: the writing lanes (rows) and the reading ones (chunks) meet all banks.
+template <int STEP>
+__device__ __forceinline__ void store_rows(uint32_t stage, const uint32_t* words, uint8_t* to, int bytes) {
+    const int lane = threadIdx.x & 31, chunk = lane & 7;
+#pragma unroll 1
+    for (int pass = 0; pass < 32; pass += STEP) {
+        __syncwarp();
+        const int r = lane - pass;
+        if (r >= 0 && r < STEP) {
 #pragma unroll
-    for (int c = 0; c < 2; ++c)
-        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at(lane, c)), "r"(words[4 * c]),
-                     "r"(words[4 * c + 1]), "r"(words[4 * c + 2]), "r"(words[4 * c + 3])
-                     : "memory");
-    __syncwarp();
+            for (int c = 0; c < 8; ++c)
+                asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(stage + r * 128 + ((c ^ (r & 7)) << 4)),
+                             "r"(words[4 * c]), "r"(words[4 * c + 1]), "r"(words[4 * c + 2]), "r"(words[4 * c + 3])
+                             : "memory");
+        }
+        __syncwarp();
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        uint4 x;
-        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-                     : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
-                     : "r"(at(16 * k + (lane >> 1), lane & 1)));
-        if (to[k] != nullptr) *reinterpret_cast<uint4*>(to[k] + offset) = x;
+        for (int k = 0; k < STEP; k += 4) {
+            const int row = k + (lane >> 3);
+            const uint64_t dst = __shfl_sync(0xFFFFFFFFu, reinterpret_cast<uint64_t>(to), pass + row);
+            uint4 x;
+            asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                         : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
+                         : "r"(stage + row * 128 + ((chunk ^ (row & 7)) << 4)));
+            if (dst != 0 && 16 * chunk < bytes) *reinterpret_cast<uint4*>(dst + 16 * chunk) = x;
+        }
     }
 }
 
@@ -632,7 +647,7 @@ __device__ __forceinline__ void softmax_role(const KvArgs& a, const AttnArgs& t,
     const int i = threadIdx.x / 128, row = threadIdx.x % 128, warp = row >> 5, lane = row & 31;
     const int me = threadIdx.x >> 5;
     const Waiter wait{sh, a.ws};
-    const uint32_t tmem = sh->tmem + ((uint32_t)(32 * warp) << 16), stage = stages + me * (32 * 32);
+    const uint32_t tmem = sh->tmem + ((uint32_t)(32 * warp) << 16), stage = stages + me * (128 * kStageRows<FMT>);
     const uint32_t at_s = tmem + kColS + 128 * i, at_o = tmem + kColO + 128 * i;
     const bool zero = t.scale == 0.f;
     const float scale_base2 = (zero ? 1.f : fabsf(t.scale)) * 1.4426950408889634f;
@@ -673,44 +688,35 @@ __device__ __forceinline__ void softmax_role(const KvArgs& a, const AttnArgs& t,
             const int which = cur.from > 0 ? 0 : 1;
             const bool none = last <= first;
             const float inv = none ? 0.f : 1.f / l;
-            uint8_t* const dst =
-                !is_row ? nullptr
-                : full  ? t.out + at.token * t.o_token + (int64_t)at.head * t.o_head
-                        : reinterpret_cast<uint8_t*>(parts.acc(blockIdx.x, which) + (size_t)tile_row * a.dim);
-            uint8_t* to[2];
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const uint64_t x = __shfl_sync(0xFFFFFFFFu, reinterpret_cast<uint64_t>(dst), 16 * k + (lane >> 1));
-                to[k] = x != 0 ? reinterpret_cast<uint8_t*>(x) + 16 * (lane & 1) : nullptr;
-            }
             bool odd = false;
-            uint32_t ahead[32];
-            tc_load32(at_o, ahead);
+            if (full) {
+                uint8_t* const to = t.out + at.token * t.o_token + (int64_t)at.head * t.o_head;
 #pragma unroll 1
-            for (int c = 0; c < a.dim; c += 32) {
-                uint32_t o[32];
-                tc_wait_load();
+                for (int c = 0; c < a.dim; c += 64) {
+                    uint32_t o[64], y[32];
+                    tc_load32(at_o + c, o);
+                    tc_load32(at_o + c + 32, o + 32);
+                    tc_wait_load();
 #pragma unroll
-                for (int k = 0; k < 32; ++k) o[k] = ahead[k];
-                if (c + 32 < a.dim) tc_load32(at_o + c + 32, ahead);
-                if (full) {
-#pragma unroll
-                    for (int h = 0; h < 32; h += 16) {
-                        if (c + h >= a.dim) break;
-                        uint32_t y[8];
-#pragma unroll
-                        for (int k = 0; k < 16; k += 2) {
-                            const float u = none ? 0.f : __uint_as_float(o[h + k]) * inv;
-                            const float v = none ? 0.f : __uint_as_float(o[h + k + 1]) * inv;
-                            odd |= !(fabsf(u) <= 3.402823466e+38f) || !(fabsf(v) <= 3.402823466e+38f);
-                            y[k / 2] = pack<T>(u, v);
-                        }
-                        store_rows(stage, y, to, 2 * (c + h));
+                    for (int k = 0; k < 64; k += 2) {
+                        const float u = none ? 0.f : __uint_as_float(o[k]) * inv;
+                        const float v = none ? 0.f : __uint_as_float(o[k + 1]) * inv;
+                        odd |= c + k < a.dim && !(fabsf(u) <= 3.402823466e+38f && fabsf(v) <= 3.402823466e+38f);
+                        y[k / 2] = pack<T>(u, v);
                     }
-                } else {
+                    store_rows<kStageRows<FMT>>(stage, y, is_row ? to + 2 * c : nullptr, 2 * (a.dim - c));
+                }
+            } else {
+                float* dst = parts.acc(blockIdx.x, which) + tile_row;
+#pragma unroll 1
+                for (int c = 0; c < a.dim; c += 16) {
+                    uint32_t o[16];
+                    tc_load16(at_o + c, o);
+                    tc_wait_load();
+                    if (is_row) {
 #pragma unroll
-                    for (int h = 0; h < 32; h += 8)
-                        if (c + h < a.dim) store_rows(stage, o + h, to, 4 * (c + h));
+                        for (int k = 0; k < 16; ++k) dst[(size_t)(c + k) * kRows] = __uint_as_float(o[k]);
+                    }
                 }
             }
             if (full) {
@@ -852,7 +858,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tile_bytes = (a.dim > 64 ? 2 : 1) * kHalfBytes;
     const uint32_t raw_bytes = FMT == kKv16Bit ? 0 : kRawSlots * kTokens * a.dim;
     Shared* sh = reinterpret_cast<Shared*>(raw + (base - smem_addr(raw)) + (2 + kN) * tile_bytes + raw_bytes +
-                                           kStageBytes);
+                                           kStageBytes<FMT>);
     const int warp = threadIdx.x >> 5;
     if (warp == 0) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&sh->tmem))
@@ -924,7 +930,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <int FMT>
 constexpr size_t shared_bytes(int dim) {
     return 1024 + (size_t)(2 + kSlots<FMT>) * (dim > 64 ? 2 : 1) * kHalfBytes +
-           (FMT == kKv16Bit ? 0 : (size_t)kRawSlots * kTokens * dim) + kStageBytes + sizeof(Shared);
+           (FMT == kKv16Bit ? 0 : (size_t)kRawSlots * kTokens * dim) + kStageBytes<FMT> + sizeof(Shared);
 }
 
 static_assert(shared_bytes<kKv16Bit>(128) <= 232448 && shared_bytes<kKvInt8>(128) <= 232448, "227 KB a block");
@@ -972,6 +978,8 @@ int32_t box_tokens(uint32_t page_tokens) {
     return page_tokens >= 8 && kTokens % page_tokens == 0 ? (int32_t)page_tokens : 0;
 }
 
+constexpr int join_bytes(int dim) { return (int)sizeof(float) * kJoinMany * (dim + 1); }
+
 template <class T, int FMT>
 cudaError_t launch_one(const KvArgs& a, const AttnArgs& t, bool whole, uint32_t min_tiles, cudaStream_t s) {
     static PerDeviceOnce once;
@@ -979,6 +987,9 @@ cudaError_t launch_one(const KvArgs& a, const AttnArgs& t, bool whole, uint32_t 
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     e = once.run(dev, [] {
+        const cudaError_t set = cudaFuncSetAttribute(join_columns_kernel<T, FMT, kRows>,
+                                                     cudaFuncAttributeMaxDynamicSharedMemorySize, join_bytes(128));
+        if (set != cudaSuccess) return set;
         return cudaFuncSetAttribute(attend_chunk_kernel<T, FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     (int)shared_bytes<FMT>(128));
     });
@@ -991,7 +1002,8 @@ cudaError_t launch_one(const KvArgs& a, const AttnArgs& t, bool whole, uint32_t 
         <<<kShares, kThreads, shared_bytes<FMT>(a.dim), s>>>(a, t, k_map, v_map, box, min_tiles, whole ? 1 : 0);
     e = cudaGetLastError();
     if (e != cudaSuccess || whole) return e;
-    return launch_join<T, FMT, kRows, JoinShape<8, 1, 4, kShares>>(a, t, kShares, s);
+    return launch_join(join_columns_kernel<T, FMT, kRows>, a, t, kShares, kRows / kJoinMany, kJoinManyThreads,
+                       (size_t)join_bytes(a.dim), s);
 }
 
 }  // namespace

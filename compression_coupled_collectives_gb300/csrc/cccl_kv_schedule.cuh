@@ -97,65 +97,6 @@ struct Piece {
     int32_t from, count;  // its tiles range.lo + from .. + count - 1
 };
 
-// The item that holds place x of the line (a whole warp, all lanes alike).
-template <int ROWS, int TOKENS>
-__device__ __forceinline__ void find_item(const KvArgs& a, const AttnArgs& t, const uint32_t* prefix, uint32_t x,
-                                          Piece& p) {
-    const int lane = threadIdx.x & 31;
-    int lo = 0, hi = a.batch;  // prefix[lo] <= x < prefix[hi]
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) / 2;
-        if (prefix[mid] <= x)
-            lo = mid;
-        else
-            hi = mid;
-    }
-    p.b = lo;
-    p.seq = load_sequence(a, lo);
-    const uint32_t per_head = (prefix[lo + 1] - prefix[lo]) / (uint32_t)a.kv_heads;
-    p.kv_head = (int32_t)((x - prefix[lo]) / per_head);
-    const uint32_t start = prefix[lo] + (uint32_t)p.kv_head * per_head;
-    // the first row tile whose tiles reach past x: 32 row tiles at a time
-    uint32_t before = 0;
-    p.rt = 0;
-    const int32_t rts = row_tiles<ROWS>(t, p.seq);
-    for (int32_t base = 0; base < rts; base += 32) {
-        const int32_t rt = base + lane;
-        const uint32_t n = rt < rts ? (uint32_t)tile_range<ROWS, TOKENS>(t, p.seq, rt).n : 0;
-        uint32_t upto = n;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, upto, o);
-            if (lane >= o) upto += y;
-        }
-        const uint32_t past = __ballot_sync(0xFFFFFFFFu, start + before + upto > x);
-        if (past != 0) {
-            const int at = __ffs(past) - 1;
-            p.rt = base + at;
-            before += __shfl_sync(0xFFFFFFFFu, upto - n, at);
-            break;
-        }
-        before += __shfl_sync(0xFFFFFFFFu, upto, 31);
-    }
-    p.range = tile_range<ROWS, TOKENS>(t, p.seq, p.rt);
-    p.item = start + before;
-}
-// The item after p's on the line (there is one).
-template <int ROWS, int TOKENS>
-__device__ __forceinline__ void next_item(const KvArgs& a, const AttnArgs& t, Piece& p) {
-    p.item += (uint32_t)p.range.n;
-    if (++p.rt >= row_tiles<ROWS>(t, p.seq)) {
-        p.rt = 0;
-        if (++p.kv_head >= a.kv_heads) {
-            p.kv_head = 0;
-            do {
-                p.seq = load_sequence(a, ++p.b);
-            } while (p.seq.n == 0);
-        }
-    }
-    p.range = tile_range<ROWS, TOKENS>(t, p.seq, p.rt);
-}
-
 // Share c of a line of T = each * shares + rest tiles begins at
 // floor(T c / shares).
 struct Line {
@@ -186,14 +127,62 @@ __device__ __forceinline__ Walk make_walk(uint32_t T, uint32_t share, uint32_t b
     w.begun = 0;
     return w;
 }
+// The next piece; false at the share's end.  p is the piece before, once there
+// was one.  (Items after the first are reached by stepping on; what finds the
+// first shares its code with that, since all of it runs cold.)
 template <int ROWS, int TOKENS>
 __device__ __forceinline__ bool next_piece(const KvArgs& a, const AttnArgs& t, const uint32_t* prefix, Walk& w,
                                            Piece& p) {
+    const int lane = threadIdx.x & 31;
     while (w.x < w.x1) {
-        if (w.begun == 0)
-            find_item<ROWS, TOKENS>(a, t, prefix, w.x, p);
-        else
-            next_item<ROWS, TOKENS>(a, t, p);
+        bool enter = w.begun == 0;  // another sequence
+        if (w.begun == 0) {
+            int lo = 0, hi = a.batch;  // prefix[lo] <= x < prefix[hi]
+#pragma unroll 1
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) / 2;
+                if (prefix[mid] <= w.x)
+                    lo = mid;
+                else
+                    hi = mid;
+            }
+            p.b = lo;
+        } else {
+            p.item += (uint32_t)p.range.n;
+            if (++p.rt >= row_tiles<ROWS>(t, p.seq)) {
+                p.rt = 0;
+                if (++p.kv_head >= a.kv_heads) {
+                    p.kv_head = 0;
+                    enter = true;
+                    do ++p.b;
+                    while (prefix[p.b + 1] == prefix[p.b]);  // no new tokens
+                }
+            }
+        }
+        if (enter) p.seq = load_sequence(a, p.b);
+        if (w.begun == 0) {
+            const uint32_t per_head = (prefix[p.b + 1] - prefix[p.b]) / (uint32_t)a.kv_heads;
+            p.kv_head = (int32_t)((w.x - prefix[p.b]) / per_head);
+            p.item = prefix[p.b] + (uint32_t)p.kv_head * per_head;
+            // the first row tile whose tiles reach past x: 32 row tiles at a time
+            const int32_t rts = row_tiles<ROWS>(t, p.seq);
+#pragma unroll 1
+            for (int32_t base = 0;; base += 32) {
+                const uint32_t n = base + lane < rts ? (uint32_t)tile_range<ROWS, TOKENS>(t, p.seq, base + lane).n : 0;
+                uint32_t upto = n;
+#pragma unroll 1
+                for (int o = 1; o < 32; o <<= 1) {
+                    const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+                    if (lane >= o) upto += y;
+                }
+                const uint32_t past = __ballot_sync(0xFFFFFFFFu, p.item + upto > w.x);
+                const int at = past != 0 ? __ffs(past) - 1 : 31;
+                p.item += __shfl_sync(0xFFFFFFFFu, past != 0 ? upto - n : upto, at);
+                p.rt = base + at;
+                if (past != 0 || base + 32 >= rts) break;
+            }
+        }
+        p.range = tile_range<ROWS, TOKENS>(t, p.seq, p.rt);
         w.begun = 1;
         const uint32_t end = p.item + (uint32_t)p.range.n;
         if (w.whole) {
@@ -234,8 +223,10 @@ __device__ __forceinline__ Cut cut_of(const Piece& p, const Line& l, uint32_t c)
 }
 
 // Partial results in the workspace, after the header: C cuts, then two parts
-// for each share, ROWS * (dim + 2) floats each: per row the accumulator, then
-// the maximum (base 2) and the sum of every row.
+// for each share, ROWS * (dim + 2) floats each: the accumulators, row by row
+// (items of few rows) or column by column (256 rows, whose threads hold a row
+// each and so write whole lines), then every row's reference (base 2), then
+// every row's sum.
 struct PartLayout {
     Cut* cuts;
     float* parts;
@@ -304,137 +295,178 @@ __device__ __forceinline__ void fix_row(const KvArgs& a, const AttnArgs& t, cons
     attend_row<T, FMT>(a, t, p.b, p.seq.len, at.token, at.pos, at.head);
 }
 
-// Joins the parts of the item cut at the start of share blockIdx.x.  A block has
-// GROUPS groups of STRIDES warps; a group joins EACH rows at a time, its warps
-// taking every STRIDES-th part (items of few rows can have hundreds of parts,
-// items of many have few), and adds its warps' sums in their order.
-constexpr int kMaxShares = 456;
-template <int GROUPS_, int STRIDES_, int EACH_, int PARTS_>
-struct JoinShape {
-    static constexpr int GROUPS = GROUPS_, STRIDES = STRIDES_, EACH = EACH_, PARTS = PARTS_;
-    static constexpr int kRows = GROUPS * EACH, kThreads = 32 * GROUPS * STRIDES;
+// What the joining kernels of share blockIdx.x begin with: the cut, and for the
+// block's rows row0 .. row0 + JOIN - 1 the parts' weights and what they add up to.
+template <int JOIN, int PARTS>
+struct JoinShared {
+    float weight[JOIN][PARTS + 1], sums[JOIN][PARTS + 1];
+    float total[JOIN], top[JOIN];
+    uint32_t odd_rows;
 };
-template <class T, int FMT, int ROWS, class J>
-__global__ void __launch_bounds__(J::kThreads) join_parts_kernel(const __grid_constant__ KvArgs a,
-                                                                 const __grid_constant__ AttnArgs t, int shares) {
-    __shared__ float weight[J::kRows][J::PARTS + 1], sums[J::kRows][J::PARTS + 1];
-    __shared__ float total[J::kRows], top[J::kRows];
-    __shared__ float4 meet[J::STRIDES > 1 ? J::STRIDES : 1][J::STRIDES > 1 ? J::kRows : 1][32];
-    __shared__ uint32_t odd_rows;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const PartLayout parts = part_layout(a, shares, ROWS);
+template <int ROWS, int JOIN, int PARTS>
+__device__ __forceinline__ bool join_begin(const KvArgs& a, const AttnArgs& t, const PartLayout& parts,
+                                           JoinShared<JOIN, PARTS>& sh, Piece& p, int& live, int& first, int& n) {
     const Cut cut = parts.cuts[blockIdx.x];
-    if (cut.last < 0) return;
-    Piece p;
+    if (cut.last < 0) return false;
     p.b = cut.b;
     p.kv_head = cut.kv_head;
     p.rt = cut.rt;
     p.seq = cut.seq;
-    const int row0 = blockIdx.y * J::kRows, live = live_rows<ROWS>(t, p) - row0;
-    if (live <= 0) return;
-    const int first = (int)blockIdx.x - 1, n = cut.last - first + 1;
-    if (threadIdx.x == 0) odd_rows = 0;
-    for (int i = threadIdx.x; i < n * J::kRows; i += J::kThreads) {
-        const int part = i / J::kRows, r = i % J::kRows;
-        if (r < live) {
-            const float* st = parts.stats(first + part, part == 0);
-            weight[r][part] = st[row0 + r];
-            sums[r][part] = st[ROWS + row0 + r];
-        }
+    const int row0 = blockIdx.y * JOIN;
+    live = live_rows<ROWS>(t, p) - row0;
+    if (live <= 0) return false;
+    first = (int)blockIdx.x - 1;
+    n = cut.last - first + 1;
+    if (threadIdx.x == 0) sh.odd_rows = 0;
+    for (int i = threadIdx.x; i < n * JOIN; i += blockDim.x) {
+        const int part = i / JOIN, r = i % JOIN;
+        const float* st = parts.stats(first + part, part == 0);
+        sh.weight[r][part] = r < live ? st[row0 + r] : -INFINITY;
+        sh.sums[r][part] = r < live ? st[ROWS + row0 + r] : 0.f;
     }
     __syncthreads();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    for (int r = warp; r < min(J::kRows, live); r += J::kThreads / 32) {
+    for (int r = warp; r < JOIN; r += blockDim.x >> 5) {
         float m = -INFINITY;
-        for (int i = lane; i < n; i += 32) m = fmaxf(m, weight[r][i]);
+        for (int i = lane; i < n; i += 32) m = fmaxf(m, sh.weight[r][i]);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
         const float from = m == -INFINITY ? 0.f : m;
         float sum = 0.f;
         for (int i = lane; i < n; i += 32) {
-            const float f = exp2f(weight[r][i] - from);
-            sum += f * sums[r][i];
-            weight[r][i] = f;
+            const float f = exp2f(sh.weight[r][i] - from);
+            sum += f * sh.sums[r][i];
+            sh.weight[r][i] = f;
         }
         sum = warp_sum(sum);
         if (lane == 0) {
-            total[r] = sum;
-            top[r] = m;
+            sh.total[r] = sum;
+            sh.top[r] = m;
         }
     }
     __syncthreads();
-    const int group = warp / J::STRIDES, stride = warp % J::STRIDES;
-    const int r0 = group * J::EACH;
-    float4 v[J::EACH];
-#pragma unroll
-    for (int k = 0; k < J::EACH; ++k) v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-    const bool inside = 4 * lane < a.dim;
+    return true;
+}
+template <class T, int FMT, int ROWS, int JOIN, int PARTS>
+__device__ __forceinline__ void join_end(const KvArgs& a, const AttnArgs& t, JoinShared<JOIN, PARTS>& sh,
+                                         const Piece& p) {
+    __syncthreads();
+    for (uint32_t odd = sh.odd_rows; odd != 0; odd &= odd - 1) {
+        const int r = __ffs(odd) - 1;
+        if (r % (int)(blockDim.x >> 5) == (int)(threadIdx.x >> 5))
+            fix_row<T, FMT>(a, t, p, ROWS, (int)blockIdx.y * JOIN + r);
+    }
+}
+
+// Items of few rows, up to hundreds of parts: 4 rows a block, 4 warps a row,
+// each taking every 4th part; a row's warps are added in their order.
+constexpr int kMaxShares = 456;
+constexpr int kJoinFew = 4, kJoinFewThreads = 512;
+template <class T, int FMT, int ROWS>
+__global__ void __launch_bounds__(kJoinFewThreads) join_rows_kernel(const __grid_constant__ KvArgs a,
+                                                                    const __grid_constant__ AttnArgs t, int shares) {
+    __shared__ JoinShared<kJoinFew, kMaxShares> sh;
+    __shared__ float4 meet[4][kJoinFew][32];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const PartLayout parts = part_layout(a, shares, ROWS);
+    Piece p;
+    int live, first, n;
+    if (!join_begin<ROWS>(a, t, parts, sh, p, live, first, n)) return;
+    const int lane = threadIdx.x & 31, r = threadIdx.x >> 7, stride = (threadIdx.x >> 5) & 3;
+    const int row = blockIdx.y * kJoinFew + r;
+    const bool mine = r < live && 4 * lane < a.dim;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-    for (int i = stride; i < n; i += J::STRIDES) {
-        const float* src = parts.acc(first + i, i == 0) + (size_t)(row0 + r0) * a.dim + 4 * lane;
-#pragma unroll
-        for (int k = 0; k < J::EACH; ++k) {
-            if (r0 + k < live && inside) {
-                const float4 x = *reinterpret_cast<const float4*>(src + (size_t)k * a.dim);
-                const float f = weight[r0 + k][i];
-                v[k].x += f * x.x;
-                v[k].y += f * x.y;
-                v[k].z += f * x.z;
-                v[k].w += f * x.w;
-            }
+    for (int i = stride; i < n; i += 4) {
+        if (mine) {
+            const float4 x = *reinterpret_cast<const float4*>(parts.acc(first + i, i == 0) + (size_t)row * a.dim + 4 * lane);
+            const float f = sh.weight[r][i];
+            v.x += f * x.x;
+            v.y += f * x.y;
+            v.z += f * x.z;
+            v.w += f * x.w;
         }
     }
-    if (J::STRIDES > 1) {
-#pragma unroll
-        for (int k = 0; k < J::EACH; ++k) meet[stride][r0 + k][lane] = v[k];
-        __syncthreads();
-        if (stride == 0) {
-#pragma unroll
-            for (int k = 0; k < J::EACH; ++k)
-#pragma unroll
-                for (int i = 1; i < J::STRIDES; ++i) {
-                    const float4 x = meet[i][r0 + k][lane];
-                    v[k].x += x.x;
-                    v[k].y += x.y;
-                    v[k].z += x.z;
-                    v[k].w += x.w;
-                }
-        }
-    }
+    meet[stride][r][lane] = v;
+    __syncthreads();
     if (stride == 0) {
 #pragma unroll
-        for (int k = 0; k < J::EACH; ++k) {
-            // pairs of lanes hold 8 values together: the even one stores them
-            const float y[8] = {v[k].x, v[k].y, v[k].z, v[k].w, __shfl_down_sync(0xFFFFFFFFu, v[k].x, 1),
-                                __shfl_down_sync(0xFFFFFFFFu, v[k].y, 1), __shfl_down_sync(0xFFFFFFFFu, v[k].z, 1),
-                                __shfl_down_sync(0xFFFFFFFFu, v[k].w, 1)};
-            const int r = r0 + k;
-            if (r < live && inside && (lane & 1) == 0 &&
-                store_row_part<T>(t, p, ROWS, row0 + r, 4 * lane, y, top[r], total[r]))
-                atomicOr(&odd_rows, 1u << r);
+        for (int i = 1; i < 4; ++i) {
+            const float4 x = meet[i][r][lane];
+            v.x += x.x;
+            v.y += x.y;
+            v.z += x.z;
+            v.w += x.w;
         }
+        // pairs of lanes hold 8 values together: the even one stores them
+        const float y[8] = {v.x, v.y, v.z, v.w, __shfl_down_sync(0xFFFFFFFFu, v.x, 1),
+                            __shfl_down_sync(0xFFFFFFFFu, v.y, 1), __shfl_down_sync(0xFFFFFFFFu, v.z, 1),
+                            __shfl_down_sync(0xFFFFFFFFu, v.w, 1)};
+        if (mine && (lane & 1) == 0 && store_row_part<T>(t, p, ROWS, row, 4 * lane, y, sh.top[r], sh.total[r]))
+            atomicOr(&sh.odd_rows, 1u << r);
+    }
+    join_end<T, FMT, ROWS>(a, t, sh, p);
+}
+
+// Items of 256 rows, few parts: 32 rows a block, a row a lane, 16 columns a
+// warp; the rows go out through shared memory.
+constexpr int kJoinMany = 32, kJoinManyThreads = 256, kManyShares = 152;
+template <class T, int FMT, int ROWS>
+__global__ void __launch_bounds__(kJoinManyThreads) join_columns_kernel(const __grid_constant__ KvArgs a,
+                                                                        const __grid_constant__ AttnArgs t,
+                                                                        int shares) {
+    __shared__ JoinShared<kJoinMany, kManyShares> sh;
+    extern __shared__ float tile[];  // [32][dim + 1]
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const PartLayout parts = part_layout(a, shares, ROWS);
+    Piece p;
+    int live, first, n;
+    if (!join_begin<ROWS>(a, t, parts, sh, p, live, first, n)) return;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int row0 = blockIdx.y * kJoinMany;
+    if (16 * warp < a.dim) {
+        float v[16];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) v[k] = 0.f;
+        for (int i = 0; i < n; ++i) {
+            const float f = sh.weight[lane][i];
+            const float* src = parts.acc(first + i, i == 0) + (size_t)(16 * warp) * ROWS + row0 + lane;
+            float x[16];
+#pragma unroll
+            for (int k = 0; k < 16; ++k) x[k] = lane < live ? src[k * ROWS] : 0.f;
+#pragma unroll
+            for (int k = 0; k < 16; ++k) v[k] += f * x[k];
+        }
+#pragma unroll
+        for (int k = 0; k < 16; ++k) tile[lane * (a.dim + 1) + 16 * warp + k] = v[k];
     }
     __syncthreads();
-    for (uint32_t odd = odd_rows; odd != 0; odd &= odd - 1) {
-        const int r = __ffs(odd) - 1;
-        if (r % (J::kThreads / 32) == warp) fix_row<T, FMT>(a, t, p, ROWS, row0 + r);
+    const int groups = a.dim / 8;
+    for (int k = threadIdx.x; k < min(live, kJoinMany) * groups; k += kJoinManyThreads) {
+        const int r = k / groups, d = 8 * (k - r * groups);
+        float y[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] = tile[r * (a.dim + 1) + d + e];
+        if (store_row_part<T>(t, p, ROWS, row0 + r, d, y, sh.top[r], sh.total[r])) atomicOr(&sh.odd_rows, 1u << r);
     }
+    join_end<T, FMT, ROWS>(a, t, sh, p);
 }
 
 // Launched so that its blocks may start while the kernel before it still runs;
 // they wait for its end before they read.
-template <class T, int FMT, int ROWS, class J>
-cudaError_t launch_join(const KvArgs& a, const AttnArgs& t, int shares, cudaStream_t s) {
+inline cudaError_t launch_join(void (*kernel)(KvArgs, AttnArgs, int), const KvArgs& a, const AttnArgs& t, int shares,
+                               int blocks_y, int threads, size_t shared, cudaStream_t s) {
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)shares, ROWS / J::kRows);
-    cfg.blockDim = dim3(J::kThreads);
+    cfg.gridDim = dim3((unsigned)shares, (unsigned)blocks_y);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = shared;
     cfg.stream = s;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, join_parts_kernel<T, FMT, ROWS, J>, a, t, shares);
+    return cudaLaunchKernelEx(&cfg, kernel, a, t, shares);
 }
 
 }  // namespace cccl

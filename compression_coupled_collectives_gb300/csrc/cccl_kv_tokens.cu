@@ -597,7 +597,8 @@ cudaError_t launch_tokens(const KvArgs& a, const AttnArgs& t, bool whole, uint32
     attend_tokens_kernel<S><<<S::kShares, kThreads, S::kSmem, s>>>(a, t, min_tiles, whole ? 1 : 0);
     e = cudaGetLastError();
     if (e != cudaSuccess || whole) return e;
-    return launch_join<typename S::T, S::FMT, S::kRows, JoinShape<4, 4, 1, kMaxShares>>(a, t, S::kShares, s);
+    return launch_join(join_rows_kernel<typename S::T, S::FMT, S::kRows>, a, t, S::kShares, S::kRows / kJoinFew,
+                       kJoinFewThreads, 0, s);
 }
 
 template <class T, int FMT, int DP>
