@@ -514,16 +514,17 @@ __device__ __forceinline__ void mma_role(const KvArgs& a, const AttnArgs& t, Sha
             const uint32_t v_entry = entry, k_entry = entry + 1;
             const bool more = j + 1 < count;
             if (!wait(&sh->kv_full[v_entry % SLOTS], (v_entry / SLOTS) & 1)) return;
-            if (more && !wait(&sh->kv_full[k_entry % SLOTS], (k_entry / SLOTS) & 1)) return;
             for (int i = 0; i < tiles; ++i) {
                 if (!wait(&sh->p_full[i], p_phase[i])) return;
                 p_phase[i] ^= 1;
                 tc_fence_after();
                 product_pv(i, v_entry % SLOTS, j > 0);
-                if (more)
+                if (more) {
+                    if (i == 0 && !wait(&sh->kv_full[k_entry % SLOTS], (k_entry / SLOTS) & 1)) return;
                     product_qk(i, k_entry % SLOTS);
-                else
+                } else {
                     commit(&sh->o_full[i]);
+                }
             }
             commit(&sh->kv_free[v_entry % SLOTS]);
             if (more) commit(&sh->kv_free[k_entry % SLOTS]);
@@ -561,9 +562,9 @@ __device__ __forceinline__ float bring_rows(const KvArgs& a, const AttnArgs& t, 
         copy_commit();
         return inverse;
     }
-    constexpr int kEach = 16;  // loads in flight: all of them
-    constexpr int part = 0;
-    {
+    constexpr int kEach = 8;  // loads in flight
+#pragma unroll 1
+    for (int part = 0; part < 32; part += 2 * kEach) {
         uint4 x[kEach];
 #pragma unroll
         for (int k = 0; k < kEach; ++k) {
