@@ -10,7 +10,7 @@
 //
 // Warps: 0-3 and 4-7 softmax of row tiles 0 and 1 (they also bring in their
 // rows of Q and write the result); 8-11 bring K and V in, or widen 8-bit codes
-// that 13 brings in; 12 issues the products; 14 walks along the block's share
+// that 13 and 15 bring in; 12 issues the products; 14 walks along the block's share
 // of the line and hands the pieces to the others.  One block an SM: 512 columns of TMEM (S0, S1, O0, O1).
 //
 // The running maximum is only moved when a score exceeds it by more than 2^8
@@ -264,15 +264,30 @@ struct TileRow {
     int64_t at;
     bool real;
 };
-__device__ __forceinline__ TileRow tile_row(const KvArgs& a, const Piece& p, int32_t pos) {
-    TileRow r{0, false};
-    int64_t ignore;
-    if (pos >= p.range.first && pos < p.range.last) {
-        r.real = slot_of(a, p.b, (uint32_t)pos, r.at, ignore);
-        if (!r.real) r.at = 0;
+// Positions pos + 32 i of a lane: the page entries are asked for together.
+template <int N>
+__device__ __forceinline__ void tile_rows(const KvArgs& a, const Piece& p, int32_t pos, TileRow* r) {
+    int32_t page[N];
+    uint32_t slot[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        // inside the visible range, so inside the table
+        const int32_t at = pos + 32 * i;
+        r[i].real = at >= p.range.first && at < p.range.last;
+        const uint32_t pi = div_by(a.page_tokens, r[i].real ? (uint32_t)at : 0u);
+        slot[i] = (uint32_t)at - pi * a.page_tokens.d;
+        page[i] = a.table[(int64_t)p.b * a.table_stride + pi];
     }
-    r.at += (int64_t)p.kv_head * a.head_stride;
-    return r;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        if (r[i].real && (page[i] < 0 || page[i] >= a.pages)) {
+            record_error(a.ws, kStatusInvalidArg);
+            r[i].real = false;
+        }
+        r[i].at = r[i].real ? page[i] * a.page_stride + (int64_t)slot[i] * a.token_stride +
+                                  (int64_t)p.kv_head * a.head_stride
+                            : 0;
+    }
 }
 __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, int32_t d, int32_t slot, int32_t head,
                                         int32_t page, uint64_t* bar) {
@@ -326,8 +341,7 @@ __device__ __forceinline__ void fetch_role(const KvArgs& a, const AttnArgs& t, S
                     page = (int32_t)page_of(a, p.b, pi);  // -1: outside the map, zeros
                 }
             } else {
-#pragma unroll
-                for (int i = 0; i < kParts; ++i) rows[i] = tile_row(a, p, at + 32 * (warp * kParts + i) + lane);
+                tile_rows<kParts>(a, p, at + 32 * warp * kParts + lane, rows);
             }
 #pragma unroll 1
             for (int side = 0; side < 2; ++side, ++entry) {
@@ -441,7 +455,7 @@ __device__ __forceinline__ void widen_role(const KvArgs& a, const AttnArgs& t, S
             for (int side = 0; side < 2; ++side, ++entry) {
                 const uint32_t s = entry % kN, use = entry / kN, q = entry % kRawSlots, turn = entry / kRawSlots;
                 if (!wait(&sh->raw_full[q], turn & 1)) return;
-                if (use > 0 && !__all_sync(0xFFFFFFFFu, wait(&sh->kv_free[s], (use - 1) & 1))) return;
+                if (use > 0 && !wait(&sh->kv_free[s], (use - 1) & 1)) return;
                 widen_rows<FMT>(raw + q * raw_bytes, slots + s * slot_bytes, a.dim, warp, lane);
                 fence_proxy_async_smem();
                 __syncwarp();
@@ -878,13 +892,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&sh->kv_free[i], 1);
         }
         for (int i = 0; i < kRawSlots; ++i) {
-            mbar_init(&sh->raw_full[i], 1);
+            mbar_init(&sh->raw_full[i], 2);
             mbar_init(&sh->raw_free[i], kLoaderWarps);
         }
         for (int i = 0; i < kScaleSlots; ++i) mbar_init(&sh->scale_full[i], kLoaderWarps);
         for (int i = 0; i < kRing; ++i) {
             mbar_init(&sh->piece_full[i], 1);
-            mbar_init(&sh->piece_free[i], FMT == kKv16Bit ? 13 : 14);  // the warps that take pieces
+            mbar_init(&sh->piece_free[i], FMT == kKv16Bit ? 13 : 15);  // the warps that take pieces
         }
         mbar_init(&sh->drained, 1);
         sh->stop = 0;
@@ -914,8 +928,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_commit(&sh->drained);
                 wait_long(sh, a.ws, &sh->drained, 0);
             }
-        } else if (warp == 13 && FMT != kKv16Bit) {
-            fetch_role<FMT, 1, kRawSlots>(a, t, sh, fetch, 0, raw_codes, kTokens * a.dim, sh->raw_full, sh->raw_free);
+        } else if (warp != 14 && FMT != kKv16Bit) {  // 13 and 15
+            fetch_role<FMT, 2, kRawSlots>(a, t, sh, fetch, (warp - 13) / 2, raw_codes, kTokens * a.dim, sh->raw_full,
+                                          sh->raw_free);
         } else if (warp == 14) {
             walk_role(a, t, sh, make_walk(sh->prefix[a.batch], blockIdx.x, gridDim.x, min_tiles, whole_items));
         }
