@@ -34,6 +34,8 @@ class _Batch(ctypes.Structure):
                 ("batch", _i32), ("table_pages", _i32), ("max_new", _i32), ("max_len", _i32)]
 
 
+# the current stream's handle without a Stream object (a decoding step makes many calls)
+_current_stream = torch._C._cuda_getCurrentRawStream
 _lib.cccl_kv_clear_status.argtypes = [_vp, _sz, _vp]
 _lib.cccl_kv_clear_status.restype = ctypes.c_int
 _lib.cccl_kv_workspace_bytes.argtypes = [_vp, _vp, ctypes.c_int]
@@ -45,6 +47,7 @@ _lib.cccl_kv_attention.argtypes = [_vp, _vp, _vp, ctypes.c_int, _i64, _i64, ctyp
                                    _i64, _i64, _vp, _vp, _sz, _vp]
 _lib.cccl_kv_attention.restype = ctypes.c_int
 
+_write, _read, _attention = _lib.cccl_kv_write, _lib.cccl_kv_read, _lib.cccl_kv_attention
 _DTYPE = {torch.bfloat16: CCCL_DTYPE_BF16, torch.float16: CCCL_DTYPE_FP16}
 _CODES = (torch.int8, torch.uint8, torch.float8_e4m3fn)
 
@@ -86,6 +89,7 @@ class KvCache:
                          None if v_scale is None else v_scale.data_ptr(), _DTYPE[dtype], fmt, heads, dim, page_tokens,
                          0, pages, k.stride(0), k.stride(1), k.stride(2), *ss)
         self._ref = ctypes.addressof(self._c)
+        self._device, self._scale = k.get_device(), 1.0 / math.sqrt(dim)
 
     @classmethod
     def empty(cls, pages: int, page_tokens: int, kv_heads: int, head_dim: int, *, dtype: torch.dtype = torch.bfloat16,
@@ -135,35 +139,41 @@ def cccl_kv_clear_status(ws: torch.Tensor, stream=None) -> None:
     _check(_lib.cccl_kv_clear_status(ws.data_ptr(), ws.nbytes, _stream(stream)), "cccl_kv_clear_status")
 
 
-def _packed(x: torch.Tensor, cache: KvCache, batch: KvBatch, what: str, heads: int | None = None) -> torch.Tensor:
+def _raw_stream(cache: KvCache, stream) -> int:
+    return _current_stream(cache._device) if stream is None else stream.cuda_stream
+
+
+def _packed(x: torch.Tensor, cache: KvCache, n_tokens: int, heads: int, what: str) -> tuple[int, int]:
+    """Token and head stride of a packed [n_tokens, heads, head_dim] tensor."""
     if x.dtype is not cache.dtype:
         raise TypeError("%s: expected %s, got %s" % (what, cache.dtype, x.dtype))
-    if x.dim() != 3 or x.shape[0] != batch.n_tokens or x.shape[2] != cache.head_dim or x.stride(2) != 1 or \
-            (heads is not None and x.shape[1] != heads):
-        raise ValueError("%s: expected [n_tokens, heads, head_dim], contiguous in its last axis" % what)
-    return x
+    if tuple(x.shape) == (n_tokens, heads, cache.head_dim):
+        token, head, inner = x.stride()
+        if inner == 1:
+            return token, head
+    raise ValueError("%s: expected [n_tokens, heads, head_dim], contiguous in its last axis" % what)
 
 
 def cccl_kv_write(cache: KvCache, batch: KvBatch, k: torch.Tensor, v: torch.Tensor, ws: torch.Tensor,
                   stream=None) -> None:
     """Enqueue storing of ``k`` and ``v`` [n_tokens, kv_heads, head_dim] in the cache."""
-    _packed(k, cache, batch, "k", cache.kv_heads)
-    _packed(v, cache, batch, "v", cache.kv_heads)
-    kt, kh, _ = k.stride()
-    vt, vh, _ = v.stride()
-    _check(_lib.cccl_kv_write(cache._ref, batch._ref, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, ws.data_ptr(),
-                              ws.nbytes, _stream(stream)), "cccl_kv_write")
+    kt, kh = _packed(k, cache, batch.n_tokens, cache.kv_heads, "k")
+    vt, vh = _packed(v, cache, batch.n_tokens, cache.kv_heads, "v")
+    status = _write(cache._ref, batch._ref, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, ws.data_ptr(), ws.nbytes,
+                    _raw_stream(cache, stream))
+    if status:
+        _check(status, "cccl_kv_write")
 
 
 def cccl_kv_read(cache: KvCache, batch: KvBatch, k: torch.Tensor, v: torch.Tensor, ws: torch.Tensor,
                  stream=None) -> None:
     """Enqueue reading of the batch's tokens into ``k`` and ``v`` [n_tokens, kv_heads, head_dim]."""
-    _packed(k, cache, batch, "k", cache.kv_heads)
-    _packed(v, cache, batch, "v", cache.kv_heads)
-    kt, kh, _ = k.stride()
-    vt, vh, _ = v.stride()
-    _check(_lib.cccl_kv_read(cache._ref, batch._ref, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, ws.data_ptr(),
-                             ws.nbytes, _stream(stream)), "cccl_kv_read")
+    kt, kh = _packed(k, cache, batch.n_tokens, cache.kv_heads, "k")
+    vt, vh = _packed(v, cache, batch.n_tokens, cache.kv_heads, "v")
+    status = _read(cache._ref, batch._ref, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, ws.data_ptr(), ws.nbytes,
+                   _raw_stream(cache, stream))
+    if status:
+        _check(status, "cccl_kv_read")
 
 
 def cccl_kv_attention(cache: KvCache, batch: KvBatch, q: torch.Tensor, out: torch.Tensor, ws: torch.Tensor, *,
@@ -172,17 +182,16 @@ def cccl_kv_attention(cache: KvCache, batch: KvBatch, q: torch.Tensor, out: torc
     """Enqueue attention of ``q`` [n_tokens, q_heads, head_dim] over the cache
     into ``out`` (same shape); ``lse`` (float32 [n_tokens, q_heads], contiguous)
     receives the log of each row's sum.  ``scale`` defaults to head_dim ** -0.5."""
-    _packed(q, cache, batch, "q")
     heads = q.shape[1]
-    _packed(out, cache, batch, "out", heads)
+    qt, qh = _packed(q, cache, batch.n_tokens, heads, "q")
+    ot, oh = _packed(out, cache, batch.n_tokens, heads, "out")
     if lse is not None and (lse.dtype != torch.float32 or lse.shape != q.shape[:2] or not lse.is_contiguous()):
         raise ValueError("lse: expected a contiguous float32 [n_tokens, q_heads]")
-    qt, qh, _ = q.stride()
-    ot, oh, _ = out.stride()
-    _check(_lib.cccl_kv_attention(cache._ref, batch._ref, q.data_ptr(), heads, qt, qh,
-                                  1.0 / math.sqrt(cache.head_dim) if scale is None else scale, 1 if causal else 0,
-                                  window, out.data_ptr(), ot, oh, None if lse is None else lse.data_ptr(),
-                                  ws.data_ptr(), ws.nbytes, _stream(stream)), "cccl_kv_attention")
+    status = _attention(cache._ref, batch._ref, q.data_ptr(), heads, qt, qh, cache._scale if scale is None else scale,
+                        1 if causal else 0, window, out.data_ptr(), ot, oh, None if lse is None else lse.data_ptr(),
+                        ws.data_ptr(), ws.nbytes, _raw_stream(cache, stream))
+    if status:
+        _check(status, "cccl_kv_attention")
 
 
 # ---------------------------------------------------------------- conveniences
