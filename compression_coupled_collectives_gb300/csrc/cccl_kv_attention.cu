@@ -15,7 +15,7 @@ size_t kv_attention_scratch(int dim, int group, int max_new, int) {
 cudaError_t launch_kv_attention(int dtype, int format, const KvArgs& a, const AttnArgs& t, int max_new, int max_len,
                                 cudaStream_t s) {
     return few_rows((int)t.group.d, max_new) ? launch_kv_tokens(dtype, format, a, t, max_new, max_len, s)
-                                      : launch_kv_chunk(dtype, format, a, t, max_len, s);
+                                      : launch_kv_chunk(dtype, format, a, t, max_new, max_len, s);
 }
 
 }  // namespace cccl

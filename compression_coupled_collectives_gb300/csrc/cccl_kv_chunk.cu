@@ -864,7 +864,7 @@ template <class T, int FMT>
 __global__ void __launch_bounds__(kThreads, 1)
     attend_chunk_kernel(const __grid_constant__ KvArgs a, const __grid_constant__ AttnArgs t,
                         const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map, int32_t box,
-                        uint32_t min_tiles, int whole_items) {
+                        int whole_items) {
     constexpr int kN = kSlots<FMT>;
     extern __shared__ uint8_t raw[];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -932,7 +932,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             fetch_role<FMT, 2, kRawSlots>(a, t, sh, fetch, (warp - 13) / 2, raw_codes, kTokens * a.dim, sh->raw_full,
                                           sh->raw_free);
         } else if (warp == 14) {
-            walk_role(a, t, sh, make_walk(sh->prefix[a.batch], blockIdx.x, gridDim.x, min_tiles, whole_items));
+            walk_role(a, t, sh, make_walk(sh->prefix[a.batch], blockIdx.x, gridDim.x, whole_items));
         }
     }
     __syncwarp();
@@ -997,7 +997,7 @@ int32_t box_tokens(uint32_t page_tokens) {
 constexpr int join_bytes(int dim) { return (int)sizeof(float) * kJoinMany * (dim + 1); }
 
 template <class T, int FMT>
-cudaError_t launch_one(const KvArgs& a, const AttnArgs& t, bool whole, uint32_t min_tiles, cudaStream_t s) {
+cudaError_t launch_one(const KvArgs& a, const AttnArgs& t, int max_new, int max_len, cudaStream_t s) {
     static PerDeviceOnce once;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -1014,11 +1014,14 @@ cudaError_t launch_one(const KvArgs& a, const AttnArgs& t, bool whole, uint32_t 
     int32_t box = box_tokens(a.page_tokens.d);
     constexpr bool kWide = FMT == kKv16Bit;
     if (box > 0 && !(make_map(&k_map, a.k, kWide, a, box) && make_map(&v_map, a.v, kWide, a, box))) box = 0;
+    // one tile at most: nothing to cut
+    const bool whole = max_len <= kTokens;
+    const int shares = shares_for(a, t, max_new, max_len, kRows, kTokens, kShares);
     attend_chunk_kernel<T, FMT>
-        <<<kShares, kThreads, shared_bytes<FMT>(a.dim), s>>>(a, t, k_map, v_map, box, min_tiles, whole ? 1 : 0);
+        <<<shares, kThreads, shared_bytes<FMT>(a.dim), s>>>(a, t, k_map, v_map, box, whole ? 1 : 0);
     e = cudaGetLastError();
     if (e != cudaSuccess || whole) return e;
-    return launch_join(join_columns_kernel<T, FMT, kRows>, a, t, kShares, kRows / kJoinMany, kJoinManyThreads,
+    return launch_join(join_columns_kernel<T, FMT, kRows>, a, t, shares, kRows / kJoinMany, kJoinManyThreads,
                        (size_t)join_bytes(a.dim), s);
 }
 
@@ -1026,17 +1029,16 @@ cudaError_t launch_one(const KvArgs& a, const AttnArgs& t, bool whole, uint32_t 
 
 size_t kv_chunk_scratch(int dim) { return part_bytes(kShares, kRows, dim); }
 
-cudaError_t launch_kv_chunk(int dtype, int format, const KvArgs& a, const AttnArgs& t, int max_len, cudaStream_t s) {
-    const bool whole = max_len <= kTokens;
-    const uint32_t min_tiles = 1;
+cudaError_t launch_kv_chunk(int dtype, int format, const KvArgs& a, const AttnArgs& t, int max_new, int max_len,
+                            cudaStream_t s) {
     if (dtype == (int)Bf16::kCode) {
-        if (format == kKv16Bit) return launch_one<BfType, kKv16Bit>(a, t, whole, min_tiles, s);
-        return format == kKvInt8 ? launch_one<BfType, kKvInt8>(a, t, whole, min_tiles, s)
-                                 : launch_one<BfType, kKvE4m3>(a, t, whole, min_tiles, s);
+        if (format == kKv16Bit) return launch_one<BfType, kKv16Bit>(a, t, max_new, max_len, s);
+        return format == kKvInt8 ? launch_one<BfType, kKvInt8>(a, t, max_new, max_len, s)
+                                 : launch_one<BfType, kKvE4m3>(a, t, max_new, max_len, s);
     }
-    if (format == kKv16Bit) return launch_one<HfType, kKv16Bit>(a, t, whole, min_tiles, s);
-    return format == kKvInt8 ? launch_one<HfType, kKvInt8>(a, t, whole, min_tiles, s)
-                             : launch_one<HfType, kKvE4m3>(a, t, whole, min_tiles, s);
+    if (format == kKv16Bit) return launch_one<HfType, kKv16Bit>(a, t, max_new, max_len, s);
+    return format == kKvInt8 ? launch_one<HfType, kKvInt8>(a, t, max_new, max_len, s)
+                             : launch_one<HfType, kKvE4m3>(a, t, max_new, max_len, s);
 }
 
 }  // namespace cccl

@@ -3,12 +3,13 @@
 // moves 2 D bytes on the packed side and D or 2 D (and a 4-byte scale) on the
 // cache's.
 //
-// A vector (token, head, K or V) belongs to a group of G lanes, 8 values a
-// lane on a write and on a 16-bit read (16-byte accesses on the packed side).
+// A vector (token, head, K or V) belongs to a group of G lanes, 16 values a lane
+// (32 bytes of values, 16 of codes), several vectors in flight a lane.
 // The maximum is taken over the patterns of |x| as integers, two values per
 // instruction: for non-negative 16-bit floats the order of the patterns is the
 // order of the values, and a NaN's pattern lies above infinity's, so a NaN
-// stays the maximum.
+// stays the maximum.  A vector whose maximum is not finite gets a NaN as its
+// scale, whatever its codes.
 #include "cccl_kv.cuh"
 #include "cccl_kv_launch.h"
 
@@ -17,8 +18,8 @@ namespace cccl {
 namespace {
 
 constexpr int kCopyThreads = 256;
-constexpr int kMaxTokensPerBlock = 16;
-constexpr int kUnroll = 4;  // vectors a lane group keeps in flight
+constexpr int kMaxTokensPerBlock = 32;
+constexpr int kUnroll = 2;  // vectors a lane group keeps in flight
 
 // Tokens t0 .. t0 + count - 1 of a block: where each lies in the cache, and
 // whether it lies there at all.
@@ -26,33 +27,33 @@ struct TokenSlots {
     int64_t at[kMaxTokensPerBlock], scale_at[kMaxTokensPerBlock];
     int8_t state[kMaxTokensPerBlock];  // 0 no sequence's row, 1 in the cache, 2 not in the cache
 };
+// Warp 0, a token a lane.
 __device__ __forceinline__ void find_slots(const KvArgs& a, int64_t t0, int count, TokenSlots& s) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    for (int i = warp; i < count; i += kCopyThreads / 32) {
-        const int64_t t = t0 + i;
-        // the last sequence that starts at or before t: 32 candidates a step
-        int lo = 0, hi = a.batch;  // starts at lo, or no sequence does
-        while (hi - lo > 1) {
-            const int step = (hi - lo + 31) / 32;
-            const int c = lo + lane * step;
-            const uint32_t le = __ballot_sync(0xFFFFFFFFu, c < hi && (lane == 0 || a.cu[c] <= t));
-            const int at = 31 - __clz(le);
-            lo += at * step;
-            hi = min(hi, lo + step);
-        }
-        if (lane == 0) {
-            const Sequence q = load_sequence(a, lo);
-            int state = 0;
-            int64_t at = 0, sat = 0;
-            if (t >= q.row && t < q.row + q.n) {
-                const int64_t pos = (int64_t)q.len - q.n + (t - q.row);
-                state = pos >= 0 && slot_of(a, lo, (uint32_t)pos, at, sat) ? 1 : 2;
-            }
-            s.at[i] = at;
-            s.scale_at[i] = sat;
-            s.state[i] = (int8_t)state;
-        }
+    const int lane = threadIdx.x & 31;
+    if (threadIdx.x >= 32) return;
+    // the last sequence that starts at or before t0: 32 candidates a step
+    int lo = 0, hi = a.batch;  // starts at lo, or no sequence does
+    while (hi - lo > 1) {
+        const int step = (hi - lo + 31) / 32;
+        const int c = lo + lane * step;
+        const uint32_t le = __ballot_sync(0xFFFFFFFFu, c < hi && (lane == 0 || a.cu[c] <= t0));
+        const int at = 31 - __clz(le);
+        lo += at * step;
+        hi = min(hi, lo + step);
     }
+    if (lane >= count) return;
+    const int64_t t = t0 + lane;
+    while (lo + 1 < a.batch && a.cu[lo + 1] <= t) ++lo;
+    const Sequence q = load_sequence(a, lo);
+    int state = 0;
+    int64_t at = 0, sat = 0;
+    if (t >= q.row && t < q.row + q.n) {
+        const int64_t pos = (int64_t)q.len - q.n + (t - q.row);
+        state = pos >= 0 && slot_of(a, lo, (uint32_t)pos, at, sat) ? 1 : 2;
+    }
+    s.at[lane] = at;
+    s.scale_at[lane] = sat;
+    s.state[lane] = (int8_t)state;
 }
 
 __device__ __forceinline__ uint4 load_stream(const void* p) {
@@ -60,12 +61,14 @@ __device__ __forceinline__ uint4 load_stream(const void* p) {
 }
 __device__ __forceinline__ uint32_t pair_abs_max(uint32_t x, uint32_t y) { return vmax_u16x2(x & 0x7FFF7FFFu, y); }
 
+// 16 values as codes.  INT8: adding 1.5 * 2^23 rounds a value below 2^22 to an
+// integer, ties to even, and leaves it in the sum's low bits.
 template <class T, int FMT>
-__device__ __forceinline__ uint2 encode8(const uint4& x, float inv) {
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-    uint32_t c[2];
+__device__ __forceinline__ uint4 encode16(const uint4* x, float inv) {
+    const uint32_t w[8] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w};
+    uint32_t c[4];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    for (int h = 0; h < 4; ++h) {
         float y[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -73,67 +76,77 @@ __device__ __forceinline__ uint2 encode8(const uint4& x, float inv) {
             y[i] = T::load((uint16_t)((i & 1) ? word >> 16 : word & 0xFFFFu)) * inv;
         }
         if (FMT == kKvInt8) {
-            uint32_t r = 0;
+            uint32_t r[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int v = __float2int_rn(y[i]);  // 0 for a NaN
-                r |= ((uint32_t)min(max(v, -127), 127) & 0xFFu) << (8 * i);
-            }
-            c[h] = r;
+            for (int i = 0; i < 4; ++i) r[i] = __float_as_uint(__fadd_rn(y[i], 12582912.f));
+            c[h] = __byte_perm(__byte_perm(r[0], r[1], 0x0040), __byte_perm(r[2], r[3], 0x0040), 0x5410);
         } else {
             const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(y[0], y[1]), __NV_SATFINITE, __NV_E4M3);
             const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(y[2], y[3]), __NV_SATFINITE, __NV_E4M3);
             c[h] = lo | (hi << 16);
         }
     }
-    return make_uint2(c[0], c[1]);
+    return make_uint4(c[0], c[1], c[2], c[3]);
 }
 
-// G lanes hold one vector, 8 values each.
+// Vector `vec` of a block's tokens: K of every head, then V of every head, token by token.
+struct VecPlace {
+    int tok, head;
+    bool is_v;
+};
+__device__ __forceinline__ VecPlace vec_place(const FastDiv& per_token, int kv_heads, int vec) {
+    const int tok = (int)div_by(per_token, (uint32_t)vec), r = vec - tok * (int)per_token.d;
+    return VecPlace{tok, r >= kv_heads ? r - kv_heads : r, r >= kv_heads};
+}
+
 template <class T, int FMT, int G>
 __global__ void __launch_bounds__(kCopyThreads) kv_write_kernel(const __grid_constant__ KvArgs a,
-                                                                const __grid_constant__ KvPacked x, int tokens) {
+                                                                const __grid_constant__ KvPacked x, FastDiv per_token,
+                                                                int tokens) {
     __shared__ TokenSlots slots;
     const int64_t t0 = (int64_t)blockIdx.x * tokens;
     const int count = (int)min((int64_t)tokens, a.n_tokens - t0);
     find_slots(a, t0, count, slots);
-    __syncthreads();
     const int part = threadIdx.x % G;
-    const bool inside = 8 * part < a.dim;
-    const int per_token = 2 * a.kv_heads;  // K of every head, then V of every head
-    const int total = count * per_token;
+    const bool inside = 16 * part < a.dim;
+    const int total = count * (int)per_token.d;
     constexpr int kGroups = kCopyThreads / G;
+    __syncthreads();
     for (int base = threadIdx.x / G; base - (int)(threadIdx.x / G) < total; base += kGroups * kUnroll) {
-        uint4 val[kUnroll];
-        int tok[kUnroll], head[kUnroll];
-        bool live[kUnroll], is_v[kUnroll];
+        uint4 val[kUnroll][2];
+        VecPlace p[kUnroll];
+        bool live[kUnroll];
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
             const int vec = base + u * kGroups;
-            tok[u] = vec / per_token;
-            const int r = vec - tok[u] * per_token;
-            is_v[u] = r >= a.kv_heads;
-            head[u] = is_v[u] ? r - a.kv_heads : r;
-            live[u] = vec < total && slots.state[tok[u]] == 1;
-            val[u] = make_uint4(0, 0, 0, 0);
+            p[u] = vec_place(per_token, a.kv_heads, vec);
+            live[u] = vec < total && slots.state[p[u].tok] == 1;
+            val[u][0] = val[u][1] = make_uint4(0, 0, 0, 0);
             if (live[u] && inside) {
-                const uint8_t* src = is_v[u] ? x.v + (t0 + tok[u]) * x.v_token + head[u] * x.v_head
-                                             : x.k + (t0 + tok[u]) * x.k_token + head[u] * x.k_head;
-                val[u] = load_stream(src + 16 * part);
+                const uint8_t* src = p[u].is_v ? x.v + (t0 + p[u].tok) * x.v_token + p[u].head * x.v_head
+                                               : x.k + (t0 + p[u].tok) * x.k_token + p[u].head * x.k_head;
+                val[u][0] = load_stream(src + 32 * part);
+                val[u][1] = load_stream(src + 32 * part + 16);
             }
         }
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
+            uint8_t* const row = (p[u].is_v ? a.v : a.k) + slots.at[live[u] ? p[u].tok : 0] + p[u].head * a.head_stride;
             if (FMT == kKv16Bit) {
-                if (live[u] && inside)
-                    *reinterpret_cast<uint4*>((is_v[u] ? a.v : a.k) + slots.at[tok[u]] + head[u] * a.head_stride +
-                                              16 * part) = val[u];
+                if (live[u] && inside) {
+                    *reinterpret_cast<uint4*>(row + 32 * part) = val[u][0];
+                    *reinterpret_cast<uint4*>(row + 32 * part + 16) = val[u][1];
+                }
                 continue;
             }
-            uint32_t m = pair_abs_max(val[u].x, 0);
-            m = pair_abs_max(val[u].y, m);
-            m = pair_abs_max(val[u].z, m);
-            m = pair_abs_max(val[u].w, m);
+            uint32_t m = 0;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                m = pair_abs_max(val[u][i].x, m);
+                m = pair_abs_max(val[u][i].y, m);
+                m = pair_abs_max(val[u][i].z, m);
+                m = pair_abs_max(val[u][i].w, m);
+            }
 #pragma unroll
             for (int o = G / 2; o > 0; o >>= 1) m = vmax_u16x2(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
             const float amax = T::load((uint16_t)max(m & 0xFFFFu, m >> 16));
@@ -142,80 +155,80 @@ __global__ void __launch_bounds__(kCopyThreads) kv_write_kernel(const __grid_con
             // subnormal maximum does not turn zeros into NaN
             const float inv = amax == 0.f ? 0.f : fminf(kLimit / amax, 3.402823466e+38f);
             if (live[u]) {
-                if (inside)
-                    *reinterpret_cast<uint2*>((is_v[u] ? a.v : a.k) + slots.at[tok[u]] + head[u] * a.head_stride +
-                                              8 * part) = encode8<T, FMT>(val[u], inv);
+                if (inside) *reinterpret_cast<uint4*>(row + 16 * part) = encode16<T, FMT>(val[u], inv);
                 if (part == 0)
-                    (is_v[u] ? a.v_scale : a.k_scale)[slots.scale_at[tok[u]] + head[u] * a.s_head] = amax / kLimit;
+                    (p[u].is_v ? a.v_scale : a.k_scale)[slots.scale_at[p[u].tok] + p[u].head * a.s_head] =
+                        amax <= 3.402823466e+38f ? amax / kLimit : __uint_as_float(0x7FC00000u);
             }
         }
     }
 }
 
-// 8 codes -> 8 values of 16 bits
+// 16 codes -> 16 values of 16 bits: to fp16 exactly, then code * scale rounded once.
 template <class T, int FMT>
-__device__ __forceinline__ uint4 decode8(uint32_t lo, uint32_t hi, float scale) {
-    uint32_t w[4];
+__device__ __forceinline__ void decode16(const uint4& c, float scale, uint4* y) {
+    const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+    uint32_t v[8];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const uint32_t c = h ? hi : lo;
-        float y[4];
+    for (int h = 0; h < 4; ++h) {
+        uint32_t p[2];
+        expand4_in_order<FMT>(w[h], p[0], p[1]);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) y[i] = code_value<FMT>((uint8_t)(c >> (8 * i))) * scale;
-        w[2 * h] = round_pair<T>(y[0], y[1]);
-        w[2 * h + 1] = round_pair<T>(y[2], y[3]);
+        for (int i = 0; i < 2; ++i) {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&p[i]));
+            v[2 * h + i] = round_pair<T>(f.x * scale, f.y * scale);
+        }
     }
-    return make_uint4(w[0], w[1], w[2], w[3]);
+    y[0] = make_uint4(v[0], v[1], v[2], v[3]);
+    y[1] = make_uint4(v[4], v[5], v[6], v[7]);
 }
 
 template <class T, int FMT, int G>
 __global__ void __launch_bounds__(kCopyThreads) kv_read_kernel(const __grid_constant__ KvArgs a,
-                                                               const __grid_constant__ KvPacked x, int tokens) {
+                                                               const __grid_constant__ KvPacked x, FastDiv per_token,
+                                                               int tokens) {
     __shared__ TokenSlots slots;
     const int64_t t0 = (int64_t)blockIdx.x * tokens;
     const int count = (int)min((int64_t)tokens, a.n_tokens - t0);
     find_slots(a, t0, count, slots);
-    __syncthreads();
     const int part = threadIdx.x % G;
-    const bool inside = 8 * part < a.dim;
-    const int per_token = 2 * a.kv_heads;
-    const int total = count * per_token;
+    const bool inside = 16 * part < a.dim;
+    const int total = count * (int)per_token.d;
     constexpr int kGroups = kCopyThreads / G;
+    __syncthreads();
     for (int base = threadIdx.x / G; base - (int)(threadIdx.x / G) < total; base += kGroups * kUnroll) {
-        uint4 val[kUnroll];
+        uint4 val[kUnroll][2];
         float scale[kUnroll];
-        int tok[kUnroll], head[kUnroll];
-        bool live[kUnroll], is_v[kUnroll];
+        VecPlace p[kUnroll];
+        bool live[kUnroll];
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
             const int vec = base + u * kGroups;
-            tok[u] = vec / per_token;
-            const int r = vec - tok[u] * per_token;
-            is_v[u] = r >= a.kv_heads;
-            head[u] = is_v[u] ? r - a.kv_heads : r;
-            const int state = vec < total ? slots.state[tok[u]] : 0;
+            p[u] = vec_place(per_token, a.kv_heads, vec);
+            const int state = vec < total ? slots.state[p[u].tok] : 0;
             live[u] = state != 0 && inside;
-            val[u] = make_uint4(0, 0, 0, 0);
+            val[u][0] = val[u][1] = make_uint4(0, 0, 0, 0);
             scale[u] = 1.f;
             if (state == 1 && inside) {
-                const uint8_t* src = (is_v[u] ? a.v : a.k) + slots.at[tok[u]] + head[u] * a.head_stride;
+                const uint8_t* src = (p[u].is_v ? a.v : a.k) + slots.at[p[u].tok] + p[u].head * a.head_stride;
                 if (FMT == kKv16Bit) {
-                    val[u] = load_stream(src + 16 * part);
+                    val[u][0] = load_stream(src + 32 * part);
+                    val[u][1] = load_stream(src + 32 * part + 16);
                 } else {
-                    const uint2 c = __ldcs(reinterpret_cast<const uint2*>(src + 8 * part));
-                    val[u].x = c.x;
-                    val[u].y = c.y;
-                    scale[u] = (is_v[u] ? a.v_scale : a.k_scale)[slots.scale_at[tok[u]] + head[u] * a.s_head];
+                    val[u][0] = load_stream(src + 16 * part);
+                    scale[u] = (p[u].is_v ? a.v_scale : a.k_scale)[slots.scale_at[p[u].tok] + p[u].head * a.s_head];
                 }
             }
         }
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
             if (!live[u]) continue;
-            uint8_t* dst = is_v[u] ? x.v + (t0 + tok[u]) * x.v_token + head[u] * x.v_head
-                                   : x.k + (t0 + tok[u]) * x.k_token + head[u] * x.k_head;
-            const uint4 y = FMT == kKv16Bit ? val[u] : decode8<T, FMT>(val[u].x, val[u].y, scale[u]);
-            __stcs(reinterpret_cast<uint4*>(dst + 16 * part), y);
+            uint8_t* dst = p[u].is_v ? x.v + (t0 + p[u].tok) * x.v_token + p[u].head * x.v_head
+                                     : x.k + (t0 + p[u].tok) * x.k_token + p[u].head * x.k_head;
+            uint4 y[2] = {val[u][0], val[u][1]};
+            if (FMT != kKv16Bit) decode16<T, FMT>(val[u][0], scale[u], y);
+            __stcs(reinterpret_cast<uint4*>(dst + 32 * part), y[0]);
+            __stcs(reinterpret_cast<uint4*>(dst + 32 * part + 16), y[1]);
         }
     }
 }
@@ -230,21 +243,23 @@ int tokens_per_block(int64_t n) {
 template <class T, int FMT>
 cudaError_t write_one(const KvArgs& a, const KvPacked& x, cudaStream_t s) {
     const int tpb = tokens_per_block(a.n_tokens);
+    const FastDiv per_token = fast_div((uint32_t)(2 * a.kv_heads));
     const dim3 grid((unsigned)((a.n_tokens + tpb - 1) / tpb));
     if (a.dim <= 64)
-        kv_write_kernel<T, FMT, 8><<<grid, kCopyThreads, 0, s>>>(a, x, tpb);
+        kv_write_kernel<T, FMT, 4><<<grid, kCopyThreads, 0, s>>>(a, x, per_token, tpb);
     else
-        kv_write_kernel<T, FMT, 16><<<grid, kCopyThreads, 0, s>>>(a, x, tpb);
+        kv_write_kernel<T, FMT, 8><<<grid, kCopyThreads, 0, s>>>(a, x, per_token, tpb);
     return cudaGetLastError();
 }
 template <class T, int FMT>
 cudaError_t read_one(const KvArgs& a, const KvPacked& x, cudaStream_t s) {
     const int tpb = tokens_per_block(a.n_tokens);
+    const FastDiv per_token = fast_div((uint32_t)(2 * a.kv_heads));
     const dim3 grid((unsigned)((a.n_tokens + tpb - 1) / tpb));
     if (a.dim <= 64)
-        kv_read_kernel<T, FMT, 8><<<grid, kCopyThreads, 0, s>>>(a, x, tpb);
+        kv_read_kernel<T, FMT, 4><<<grid, kCopyThreads, 0, s>>>(a, x, per_token, tpb);
     else
-        kv_read_kernel<T, FMT, 16><<<grid, kCopyThreads, 0, s>>>(a, x, tpb);
+        kv_read_kernel<T, FMT, 8><<<grid, kCopyThreads, 0, s>>>(a, x, per_token, tpb);
     return cudaGetLastError();
 }
 

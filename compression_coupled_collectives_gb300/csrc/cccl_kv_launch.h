@@ -21,7 +21,8 @@ cudaError_t launch_kv_tokens(int dtype, int format, const KvArgs& a, const AttnA
                              cudaStream_t stream);
 size_t kv_tokens_scratch(int dim);
 // The kernel for chunks of rows, and its workspace bytes after the header.
-cudaError_t launch_kv_chunk(int dtype, int format, const KvArgs& a, const AttnArgs& t, int max_len, cudaStream_t stream);
+cudaError_t launch_kv_chunk(int dtype, int format, const KvArgs& a, const AttnArgs& t, int max_new, int max_len,
+                            cudaStream_t stream);
 size_t kv_chunk_scratch(int dim);
 // Workspace bytes of an attention call after the 16-byte header.
 size_t kv_attention_scratch(int dim, int group, int max_new, int max_len);

@@ -56,14 +56,26 @@ __device__ __forceinline__ int32_t row_tiles(const AttnArgs& t, const Sequence& 
 template <int ROWS, int TOKENS>
 __device__ __forceinline__ void build_prefix(const KvArgs& a, const AttnArgs& t, uint32_t* prefix) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+    // a thread a sequence; those of many row tiles are left to a warp each
+    constexpr int32_t kFew = 4;
+    constexpr uint32_t kLeft = 0xFFFFFFFFu;
+    for (int b = threadIdx.x; b < a.batch; b += blockDim.x) {
+        const Sequence s = load_sequence(a, b);
+        const int32_t rts = row_tiles<ROWS>(t, s);
+        uint64_t sum = 0;
+        for (int32_t rt = 0; rt < min(rts, kFew); ++rt) sum += (uint64_t)tile_range<ROWS, TOKENS>(t, s, rt).n;
+        prefix[b + 1] = rts > kFew ? kLeft : (uint32_t)min(sum * (uint32_t)a.kv_heads, (uint64_t)(kLeft - 1));
+    }
+    __syncthreads();
     for (int b = warp; b < a.batch; b += warps) {
+        if (prefix[b + 1] != kLeft) continue;
         const Sequence s = load_sequence(a, b);
         const int32_t rts = row_tiles<ROWS>(t, s);
         uint64_t sum = 0;
         for (int32_t rt = lane; rt < rts; rt += 32) sum += (uint64_t)tile_range<ROWS, TOKENS>(t, s, rt).n;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-        if (lane == 0) prefix[b + 1] = (uint32_t)min(sum * (uint32_t)a.kv_heads, (uint64_t)0xFFFFFFFFu);
+        if (lane == 0) prefix[b + 1] = (uint32_t)min(sum * (uint32_t)a.kv_heads, (uint64_t)(kLeft - 1));
     }
     __syncthreads();
     if (warp == 0) {
@@ -80,7 +92,7 @@ __device__ __forceinline__ void build_prefix(const KvArgs& a, const AttnArgs& t,
             carry += __shfl_sync(0xFFFFFFFFu, x, 31);
         }
         if (lane == 0) prefix[0] = 0;
-        if (carry >= 0xFFFFFFFFu) {
+        if (carry >= kLeft - 1) {
             if (lane == 0) record_error(a.ws, kStatusInvalidArg);
             for (int b = lane; b < a.batch; b += 32) prefix[b + 1] = 0;
         }
@@ -113,12 +125,10 @@ struct Walk {
     int32_t whole;  // items are not cut: the block that an item begins in does all of it
     int32_t begun;  // the caller's piece is the one before
 };
-__device__ __forceinline__ Walk make_walk(uint32_t T, uint32_t share, uint32_t blocks, uint32_t min_tiles, int whole) {
+__device__ __forceinline__ Walk make_walk(uint32_t T, uint32_t share, uint32_t blocks, int whole) {
     Walk w;
     w.share = share;
-    // no more shares than give each min_tiles tiles
-    w.line.shares = min(blocks, max((T - 1) / min_tiles + 1, 1u));
-    if (T == 0) w.line.shares = 1;
+    w.line.shares = max(min(blocks, T), 1u);  // a tile each at least
     w.line.each = T / w.line.shares;
     w.line.rest = T - w.line.each * w.line.shares;
     w.x = share < w.line.shares ? share_start(w.line, share) : T;
@@ -450,6 +460,14 @@ __global__ void __launch_bounds__(kJoinManyThreads) join_columns_kernel(const __
         if (store_row_part<T>(t, p, ROWS, row0 + r, d, y, sh.top[r], sh.total[r])) atomicOr(&sh.odd_rows, 1u << r);
     }
     join_end<T, FMT, ROWS>(a, t, sh, p);
+}
+
+// Shares that a call can need, at most `most`: the tiles of a batch whose
+// sequences keep to the program's expectations.
+inline int shares_for(const KvArgs& a, const AttnArgs& t, int max_new, int max_len, int rows, int tokens, int most) {
+    const double row_tiles = ((double)max_new * t.group.d + rows - 1) / rows, tiles = ((double)max_len + 2 * tokens - 1) / tokens;
+    const double all = (double)a.batch * a.kv_heads * row_tiles * tiles;
+    return all < most ? (int)all : most;
 }
 
 // Launched so that its blocks may start while the kernel before it still runs;

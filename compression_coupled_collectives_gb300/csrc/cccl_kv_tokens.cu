@@ -433,8 +433,7 @@ __device__ __forceinline__ void step(uint32_t stage, int32_t base, const uint32_
 
 template <class S>
 __global__ void __launch_bounds__(kThreads, S::kBlocksPerSm)
-    attend_tokens_kernel(const __grid_constant__ KvArgs a, const __grid_constant__ AttnArgs t, uint32_t min_tiles,
-                         int whole_items) {
+    attend_tokens_kernel(const __grid_constant__ KvArgs a, const __grid_constant__ AttnArgs t, int whole_items) {
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ uint32_t prefix[kMaxBatch + 1];
     __shared__ float stats[2][kWarps][S::kRows];
@@ -442,7 +441,7 @@ __global__ void __launch_bounds__(kThreads, S::kBlocksPerSm)
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
     build_prefix<S::kRows, S::kTile>(a, t, prefix);
-    Walk w = make_walk(prefix[a.batch], blockIdx.x, gridDim.x, min_tiles, whole_items);
+    Walk w = make_walk(prefix[a.batch], blockIdx.x, gridDim.x, whole_items);
     const PartLayout parts = part_layout(a, (int)gridDim.x, S::kRows);
     if (!whole_items && w.x >= w.x1 && threadIdx.x == 0) parts.cuts[w.share].last = -1;
     const float to_base2 = t.scale * 1.4426950408889634f;
@@ -585,7 +584,7 @@ __global__ void __launch_bounds__(kThreads, S::kBlocksPerSm)
 }
 
 template <class S>
-cudaError_t launch_tokens(const KvArgs& a, const AttnArgs& t, bool whole, uint32_t min_tiles, cudaStream_t s) {
+cudaError_t launch_tokens(const KvArgs& a, const AttnArgs& t, int max_new, int max_len, cudaStream_t s) {
     static PerDeviceOnce once;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -594,22 +593,25 @@ cudaError_t launch_tokens(const KvArgs& a, const AttnArgs& t, bool whole, uint32
         return cudaFuncSetAttribute(attend_tokens_kernel<S>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
     });
     if (e != cudaSuccess) return e;
-    attend_tokens_kernel<S><<<S::kShares, kThreads, S::kSmem, s>>>(a, t, min_tiles, whole ? 1 : 0);
+    // one tile at most: nothing to cut
+    const bool whole = max_len <= S::kTile;
+    const int shares = shares_for(a, t, max_new, max_len, S::kRows, S::kTile, S::kShares);
+    attend_tokens_kernel<S><<<shares, kThreads, S::kSmem, s>>>(a, t, whole ? 1 : 0);
     e = cudaGetLastError();
     if (e != cudaSuccess || whole) return e;
-    return launch_join(join_rows_kernel<typename S::T, S::FMT, S::kRows>, a, t, S::kShares, S::kRows / kJoinFew,
+    return launch_join(join_rows_kernel<typename S::T, S::FMT, S::kRows>, a, t, shares, S::kRows / kJoinFew,
                        kJoinFewThreads, 0, s);
 }
 
 template <class T, int FMT, int DP>
-cudaError_t launch_rows(const KvArgs& a, const AttnArgs& t, bool few, bool whole, uint32_t min_tiles, cudaStream_t s) {
-    return few ? launch_tokens<Shape<T, FMT, DP, 1>>(a, t, whole, min_tiles, s)
-               : launch_tokens<Shape<T, FMT, DP, 2>>(a, t, whole, min_tiles, s);
+cudaError_t launch_rows(const KvArgs& a, const AttnArgs& t, int max_new, int max_len, cudaStream_t s) {
+    return (int64_t)t.group.d * max_new <= 8 ? launch_tokens<Shape<T, FMT, DP, 1>>(a, t, max_new, max_len, s)
+                                             : launch_tokens<Shape<T, FMT, DP, 2>>(a, t, max_new, max_len, s);
 }
 template <class T, int FMT>
-cudaError_t launch_dim(const KvArgs& a, const AttnArgs& t, bool few, bool whole, uint32_t min_tiles, cudaStream_t s) {
-    return a.dim <= 64 ? launch_rows<T, FMT, 64>(a, t, few, whole, min_tiles, s)
-                       : launch_rows<T, FMT, 128>(a, t, few, whole, min_tiles, s);
+cudaError_t launch_dim(const KvArgs& a, const AttnArgs& t, int max_new, int max_len, cudaStream_t s) {
+    return a.dim <= 64 ? launch_rows<T, FMT, 64>(a, t, max_new, max_len, s)
+                       : launch_rows<T, FMT, 128>(a, t, max_new, max_len, s);
 }
 
 }  // namespace
@@ -618,17 +620,14 @@ size_t kv_tokens_scratch(int dim) { return part_bytes(kMaxShares, 16, dim); }
 
 cudaError_t launch_kv_tokens(int dtype, int format, const KvArgs& a, const AttnArgs& t, int max_new, int max_len,
                              cudaStream_t s) {
-    const bool whole = max_len <= 128;
-    const uint32_t min_tiles = 1;
-    const bool few = (int64_t)t.group.d * max_new <= 8;
     if (dtype == (int)Bf16::kCode) {
-        if (format == kKv16Bit) return launch_dim<BfType, kKv16Bit>(a, t, few, whole, min_tiles, s);
-        return format == kKvInt8 ? launch_dim<BfType, kKvInt8>(a, t, few, whole, min_tiles, s)
-                                 : launch_dim<BfType, kKvE4m3>(a, t, few, whole, min_tiles, s);
+        if (format == kKv16Bit) return launch_dim<BfType, kKv16Bit>(a, t, max_new, max_len, s);
+        return format == kKvInt8 ? launch_dim<BfType, kKvInt8>(a, t, max_new, max_len, s)
+                                 : launch_dim<BfType, kKvE4m3>(a, t, max_new, max_len, s);
     }
-    if (format == kKv16Bit) return launch_dim<HfType, kKv16Bit>(a, t, few, whole, min_tiles, s);
-    return format == kKvInt8 ? launch_dim<HfType, kKvInt8>(a, t, few, whole, min_tiles, s)
-                             : launch_dim<HfType, kKvE4m3>(a, t, few, whole, min_tiles, s);
+    if (format == kKv16Bit) return launch_dim<HfType, kKv16Bit>(a, t, max_new, max_len, s);
+    return format == kKvInt8 ? launch_dim<HfType, kKvInt8>(a, t, max_new, max_len, s)
+                             : launch_dim<HfType, kKvE4m3>(a, t, max_new, max_len, s);
 }
 
 }  // namespace cccl

@@ -104,7 +104,7 @@ size_t cccl_kv_workspace_bytes(const cccl_kv_cache *h_cache, const cccl_kv_batch
  * 448, scale = a / L, inv = min(L / a, largest finite) (0 when a = 0); the
  * code is x * inv rounded to the nearest integer, ties to even, or to the
  * nearest E4M3 value, limited to +-L.  A vector with a NaN or an infinity gets
- * a scale that is not finite, and reads back as NaN throughout.
+ * a NaN as its scale, and reads back as NaN throughout.
  * Two rows of one call that name the same page and slot: one of them stays.
  * Returns INVALID_ARG, CUDA or OK. */
 cccl_status cccl_kv_write(const cccl_kv_cache *h_cache, const cccl_kv_batch *h_batch, const void *d_k,
