@@ -117,8 +117,8 @@ size_t cccl_kv_workspace_bytes(const cccl_kv_cache* h_cache, const cccl_kv_batch
     if (!shapes_ok(h_cache, h_batch) || q_heads < 0 || q_heads > CCCL_KV_MAX_HEADS) return 0;
     if (q_heads == 0) return sizeof(cccl::WsHeader);
     if (q_heads % h_cache->kv_heads != 0) return 0;
-    return sizeof(cccl::WsHeader) + cccl::kv_attention_scratch(h_cache->head_dim, q_heads / h_cache->kv_heads,
-                                                               h_batch->max_new, h_batch->max_len);
+    return sizeof(cccl::WsHeader) + cccl::kv_attention_scratch(h_cache->format, h_cache->head_dim,
+                                                               q_heads / h_cache->kv_heads, h_batch->max_new);
 }
 
 static cccl_status copy_call(bool write, const cccl_kv_cache* c, const cccl_kv_batch* b, const void* d_k, int64_t kt,

@@ -1014,8 +1014,11 @@ cudaError_t launch_one(const KvArgs& a, const AttnArgs& t, int max_new, int max_
     int32_t box = box_tokens(a.page_tokens.d);
     constexpr bool kWide = FMT == kKv16Bit;
     if (box > 0 && !(make_map(&k_map, a.k, kWide, a, box) && make_map(&v_map, a.v, kWide, a, box))) box = 0;
-    // one tile at most: nothing to cut
-    const bool whole = max_len <= kTokens;
+    // Cutting items costs a second kernel and the parts' way through memory, 8 to
+    // 12 us; not cutting them costs up to one item's time at the end.  Six chunks
+    // of up to 97 tokens over 1500: 32.6 us whole, 37.3 cut; three of 700 over
+    // 2500: 49.9, 63.9; two of 256 over 4096: 63.9, 45.4.
+    const bool whole = max_len <= 20 * kTokens;
     const int shares = shares_for(a, t, max_new, max_len, kRows, kTokens, kShares);
     attend_chunk_kernel<T, FMT>
         <<<shares, kThreads, shared_bytes<FMT>(a.dim), s>>>(a, t, k_map, v_map, box, whole ? 1 : 0);

@@ -25,6 +25,6 @@ cudaError_t launch_kv_chunk(int dtype, int format, const KvArgs& a, const AttnAr
                             cudaStream_t stream);
 size_t kv_chunk_scratch(int dim);
 // Workspace bytes of an attention call after the 16-byte header.
-size_t kv_attention_scratch(int dim, int group, int max_new, int max_len);
+size_t kv_attention_scratch(int format, int dim, int group, int max_new);
 
 }  // namespace cccl

@@ -593,8 +593,12 @@ cudaError_t launch_tokens(const KvArgs& a, const AttnArgs& t, int max_new, int m
         return cudaFuncSetAttribute(attend_tokens_kernel<S>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
     });
     if (e != cudaSuccess) return e;
-    // one tile at most: nothing to cut
-    const bool whole = max_len <= S::kTile;
+    // Cutting items costs a second kernel, about 3.5 us; not cutting them costs up
+    // to one item's time at the end.  64 tokens over 512 (8 tiles, 512 items): 28.0
+    // us whole, 31.4 cut; over 1024: 47.6, 44.4; one over 517 (8 items): 12.2, 9.8;
+    // 8 over 256 (4 tiles): 9.1, 9.7.
+    const int64_t items = (int64_t)a.batch * a.kv_heads;
+    const bool whole = max_len <= (items >= S::kShares ? 8 : 4) * S::kTile;
     const int shares = shares_for(a, t, max_new, max_len, S::kRows, S::kTile, S::kShares);
     attend_tokens_kernel<S><<<shares, kThreads, S::kSmem, s>>>(a, t, whole ? 1 : 0);
     e = cudaGetLastError();
