@@ -145,6 +145,10 @@ ATTEND = [
 ]
 
 
+# what makes a call cut items among blocks and join their parts: an expectation of long sequences
+CUT = dict(max_len=1 << 20)
+
+
 @pytest.mark.parametrize("fmt", ["16bit", "int8", "e4m3"])
 @pytest.mark.parametrize("dtype", [BF, HF])
 @pytest.mark.parametrize("shape", range(len(ATTEND)))
@@ -152,9 +156,72 @@ def test_attention(cc, shape, dtype, fmt):
     lens, new, heads, group, dim, page = ATTEND[shape]
     c = Case(lens, new, heads=heads, group=group, dim=dim, page=page, dtype=dtype, fmt=fmt, seed=shape,
              layout=["thd", "htd", "kv"][shape % 3], fill=float("nan"))
-    cache, batch = c.objects(cc)
-    out, lse = cc.kv_attention(cache, batch, c.q)
-    check(c, out, lse)
+    for over in ({}, CUT):
+        cache, batch = c.objects(cc, **over)
+        out, lse = cc.kv_attention(cache, batch, c.q)
+        check(c, out, lse)
+
+
+LONGER = [
+    # lens, new, heads, group, dim, page: tiles that whole pages cover, at every page size that divides or is
+    # divided by a tile, and at others; rows below, at and above one tile of rows
+    ([3000, 1025], [70, 64], 2, 4, 128, 8),
+    ([2700], [129], 1, 2, 64, 64),
+    ([1500, 4000], [33, 300], 2, 1, 128, 128),
+    ([2900, 128], [40, 128], 1, 8, 96, 256),
+    ([2600, 513, 1024], [20, 100, 3], 2, 6, 16, 48),
+    ([1300], [90], 2, 3, 48, 16),
+    ([5000], [12], 2, 4, 128, 16),
+    ([5000, 700], [1, 1], 2, 8, 128, 128),
+    ([2048], [2], 1, 16, 64, 12),
+]
+
+
+@pytest.mark.parametrize("window", [0, 700])
+@pytest.mark.parametrize("dtype,fmt", [(BF, "16bit"), (HF, "16bit"), (BF, "int8"), (HF, "int8"), (BF, "e4m3")])
+@pytest.mark.parametrize("shape", range(len(LONGER)))
+def test_attention_over_many_tiles(cc, shape, dtype, fmt, window):
+    lens, new, heads, group, dim, page = LONGER[shape]
+    c = Case(lens, new, heads=heads, group=group, dim=dim, page=page, dtype=dtype, fmt=fmt, seed=20 + shape,
+             layout=["htd", "kv", "thd"][shape % 3], fill=float("nan"))
+    for over in ({}, CUT):
+        cache, batch = c.objects(cc, **over)
+        out, lse = cc.kv_attention(cache, batch, c.q, window=window)
+        check(c, out, lse, window=window)
+
+
+def test_many_sequences(cc):
+    """As many as a call takes, some of them without tokens."""
+    lens = [(7 * b) % 41 for b in range(1024)]
+    new = [min(n, 1 + b % 3) if b % 5 else 0 for b, n in enumerate(lens)]
+    c = Case(lens, new, heads=1, group=2, dim=64, page=16, fmt="int8", seed=40)
+    for over in ({}, CUT):
+        cache, batch = c.objects(cc, **over)
+        out, lse = cc.kv_attention(cache, batch, c.q)
+        check(c, out, lse)
+        cache, batch = c.objects(cc, max_new=500, **over)  # the other kernel
+        out, lse = cc.kv_attention(cache, batch, c.q)
+        check(c, out, lse)
+
+
+def test_queries_of_very_different_sizes(cc):
+    """One row's size has no effect on another's, and a row of infinities none on its neighbours."""
+    for fmt in ("int8", "e4m3", "16bit"):
+        for new in (1, 40):
+            c = Case([400], [new], heads=1, group=8, dim=64, page=16, fmt=fmt, seed=41)
+            c.q[:, 1] *= 1e30
+            c.q[:, 2] *= 1e-30
+            c.q[:, 3] = float("inf")
+            c.q[:, 4] = 0
+            cache, batch = c.objects(cc)
+            out, lse = cc.kv_attention(cache, batch, c.q)
+            ref, ref_lse, tol, ltol = c.attention()
+            rows = [0, 2, 4, 5, 6, 7]
+            assert ((out.double() - ref).abs() <= tol)[:, rows].all()
+            assert ((lse.double() - ref_lse).abs() <= ltol)[:, rows].all()
+            # one key holds all of the weight
+            assert ((out.double() - ref).abs() <= tol)[:, 1].all()
+            assert out[:, 3].isnan().all()
 
 
 @pytest.mark.parametrize("new", [1, 70])
@@ -163,9 +230,10 @@ def test_attention(cc, shape, dtype, fmt):
 def test_attention_masks(cc, causal, window, fmt, new):
     c = Case([300, 129, 1, 40], [new, new, new, new], heads=2, group=3, dim=64, page=16, fmt=fmt, seed=window % 1000,
              fill=float("inf"))
-    cache, batch = c.objects(cc)
-    out, lse = cc.kv_attention(cache, batch, c.q, causal=causal, window=window)
-    check(c, out, lse, causal=causal, window=window if window < 1 << 31 else 0)
+    for over in ({}, CUT):
+        cache, batch = c.objects(cc, **over)
+        out, lse = cc.kv_attention(cache, batch, c.q, causal=causal, window=window)
+        check(c, out, lse, causal=causal, window=window if window < 1 << 31 else 0)
 
 
 @pytest.mark.parametrize("new", [1, 40])
@@ -188,9 +256,10 @@ def test_hints_do_not_change_what_is_computed(cc, fmt, new):
         check(c, out, lse)
 
 
+@pytest.mark.parametrize("over", [{}, CUT])
 @pytest.mark.parametrize("new", [1, 64])
 @pytest.mark.parametrize("value", [float("nan"), float("inf"), float("-inf")])
-def test_hidden_values_have_no_effect(cc, value, new):
+def test_hidden_values_have_no_effect(cc, value, new, over):
     """K and V of hidden positions inside the cache hold what must not be read."""
     c = Case([260], [new], heads=2, group=2, dim=128, page=16, seed=5)
     window = 100
@@ -202,7 +271,7 @@ def test_hidden_values_have_no_effect(cc, value, new):
         p = c.lens[0] - 1
         c.v[int(c.table[0, p // 16]), p % 16] = value
         c.k[int(c.table[0, p // 16]), p % 16] = value
-    cache, batch = c.objects(cc)
+    cache, batch = c.objects(cc, **over)
     out, lse = cc.kv_attention(cache, batch, c.q, window=window)
     rows = slice(0, c.T - 1) if new > 1 else slice(0, c.T)
     ref, ref_lse, tol, ltol = c.attention(window=window)
@@ -213,12 +282,13 @@ def test_hidden_values_have_no_effect(cc, value, new):
         assert not torch.isfinite(out[-1]).all()  # where it is visible, it shows
 
 
+@pytest.mark.parametrize("over", [{}, CUT])
 @pytest.mark.parametrize("new", [1, 64])
-def test_visible_values_go_where_the_formula_takes_them(cc, new):
+def test_visible_values_go_where_the_formula_takes_them(cc, new, over):
     c = Case([200], [new], heads=2, group=2, dim=64, page=16, seed=6)
     at = (int(c.table[0, 3]), 2)
     c.v[at][0, 7] = float("inf")  # head 0, one channel
-    cache, batch = c.objects(cc)
+    cache, batch = c.objects(cc, **over)
     out, _ = cc.kv_attention(cache, batch, c.q)
     assert (out[:, :2, 7] == math.inf).all()
     keep = torch.ones(64, dtype=torch.bool, device="cuda")
@@ -228,14 +298,15 @@ def test_visible_values_go_where_the_formula_takes_them(cc, new):
     assert ((out.double() - ref).abs() <= tol)[:, :2][..., keep].all()
 
 
+@pytest.mark.parametrize("over", [{}, CUT])
 @pytest.mark.parametrize("new", [1, 64])
-def test_large_values_do_not_overflow_on_the_way(cc, new):
+def test_large_values_do_not_overflow_on_the_way(cc, new, over):
     """Values near binary32's limit: the mean of equal values is that value."""
     c = Case([500], [new], heads=1, group=2, dim=64, seed=7)
     big = torch.tensor(3e38, device="cuda").to(BF)
     c.v[:] = big
     c.q[:] = 0
-    cache, batch = c.objects(cc)
+    cache, batch = c.objects(cc, **over)
     out, _ = cc.kv_attention(cache, batch, c.q)
     assert (out.float() / big.float() - 1).abs().max() <= 2.0 ** -8
 
@@ -318,6 +389,34 @@ def test_device_errors_are_reported_and_clamped(cc):
                 if spoil not in ("page", "negative page") or new == 40 and spoil == "page":
                     assert cc.cccl_get_result(ws)[1] == (0 if spoil == "page" and 90 - 40 > 47 else
                                                         cc.CCCL_ERR_INVALID_ARG), spoil
+
+
+def test_refusals_on_the_gpu(cc):
+    """Buffers that are too small, not aligned, or not in one allocation: refused, and nothing runs."""
+    c = Case([100], [4], heads=2, group=2, dim=64, seed=16)
+    cache, batch = c.objects(cc)
+    ws = cc.empty_kv_workspace(cache, batch, 4)
+    out = torch.full_like(c.q, 2.0)
+
+    def refused(f, *a, **kw):
+        with pytest.raises(cc.CcclError) as e:
+            f(*a, **kw)
+        assert e.value.status == cc.CCCL_ERR_INVALID_ARG
+
+    refused(cc.cccl_kv_attention, cache, batch, c.q, out, ws[:-16])
+    refused(cc.cccl_kv_attention, cache, batch, c.q, out, ws[4:])
+    refused(cc.cccl_kv_attention, cache, batch, c.q, out, ws, window=-1)
+    refused(cc.cccl_kv_attention, cache, batch, c.q, out, ws, scale=float("nan"))
+    odd = torch.zeros(c.q.numel() + 8, dtype=BF, device="cuda")[1:1 + c.q.numel()].view(c.q.shape)  # 2-byte aligned
+    refused(cc.cccl_kv_attention, cache, batch, odd, out, ws)
+    refused(cc.cccl_kv_attention, cache, batch, c.q, odd, ws)
+    refused(cc.cccl_kv_attention, cache, batch, torch.zeros(c.T, 3, 64, dtype=BF, device="cuda"),
+            torch.zeros(c.T, 3, 64, dtype=BF, device="cuda"), ws)  # 3 query heads for 2 kv heads
+    host = torch.zeros(c.T, 2, 64, dtype=BF)
+    refused(cc.cccl_kv_write, cache, batch, host, host, ws)
+    refused(cc.cccl_kv_write, cache, batch, c.k_new, c.v_new, ws[:8])
+    assert (out == 2.0).all()
+    assert cc.cccl_get_result(ws)[1] == 0
 
 
 def test_empty_calls_do_nothing(cc):
