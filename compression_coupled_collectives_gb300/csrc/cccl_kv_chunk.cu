@@ -319,6 +319,12 @@ __device__ __forceinline__ void fetch_role(const KvArgs& a, const AttnArgs& t, S
     const int first_row = warp * span + (boxes > 0 ? lane % boxes : 0) * f.box;
     const uint32_t expect = (uint32_t)boxes * (uint32_t)f.box * (slot_bytes / kTokens);
     uint32_t entry = 0, handed = 0;
+    // leaving early: no copy of this warp may still be in flight when the block ends
+    auto leave = [&]() {
+        copy_wait<0>();
+        if (f.box > 0)
+            for (uint32_t k = entry > SLOTS ? entry - SLOTS : 0; k < entry; ++k) mbar_wait(&full[k % SLOTS], (k / SLOTS) & 1);
+    };
     auto hand_over = [&](uint32_t upto) {  // this warp's copies of entries below `upto` are done
         if (handed >= upto) return;
         if (kWide) fence_proxy_async_smem();
@@ -351,7 +357,7 @@ __device__ __forceinline__ void fetch_role(const KvArgs& a, const AttnArgs& t, S
                     // about to wait: hand over what has been brought so far
                     copy_wait<0>();
                     hand_over(entry);
-                    if (!wait(&free_[s], (use - 1) & 1)) return;
+                    if (!wait(&free_[s], (use - 1) & 1)) return leave();
                 }
                 if (tma) {
                     copy_wait<0>();
@@ -384,6 +390,7 @@ __device__ __forceinline__ void fetch_role(const KvArgs& a, const AttnArgs& t, S
     }
     copy_wait<0>();
     hand_over(entry);
+    if (*reinterpret_cast<volatile uint32_t*>(&sh->stop) != 0) leave();
 }
 
 // 8-bit caches: codes to fp16, four warps of 32 rows each.  A lane takes 16

@@ -111,7 +111,8 @@ class KvBatch:
     ``cu_tokens`` [batch + 1] and ``kv_lens`` [batch], all int32 on the device.
     ``n_tokens`` rows are in the packed tensors; ``max_new`` and ``max_len`` are
     the most new tokens and the longest length the program expects of a
-    sequence (they choose between kernels; results do not depend on them)."""
+    sequence (they choose kernels and how work is divided: results may differ
+    in their rounding and no more)."""
 
     def __init__(self, page_table: torch.Tensor, cu_tokens: torch.Tensor, kv_lens: torch.Tensor, *, n_tokens: int,
                  max_new: int, max_len: int):
@@ -205,9 +206,16 @@ def empty_kv_workspace(cache: KvCache, batch: KvBatch, q_heads: int = 0) -> torc
     return ws
 
 
-def _finish(ws: torch.Tensor, stream, what: str) -> None:
-    _, dev = cccl_get_result(ws, stream)
+def _finish(ws: torch.Tensor, what: str) -> None:
+    _, dev = cccl_get_result(ws, None)
     _check(dev, what + " (device)")
+
+
+def _hand_over(stream, *outs: torch.Tensor) -> None:
+    """Results that `stream`'s memory holds are used on the current stream from here on."""
+    if stream is not None:
+        for t in outs:
+            t.record_stream(torch.cuda.current_stream(t.device))
 
 
 def kv_write(cache: KvCache, batch: KvBatch, k: torch.Tensor, v: torch.Tensor, stream=None) -> None:
@@ -215,7 +223,7 @@ def kv_write(cache: KvCache, batch: KvBatch, k: torch.Tensor, v: torch.Tensor, s
     with torch.cuda.stream(stream):
         ws = empty_kv_workspace(cache, batch)
         cccl_kv_write(cache, batch, k, v, ws)
-        _finish(ws, None, "cccl_kv_write")
+        _finish(ws, "cccl_kv_write")
 
 
 def kv_read(cache: KvCache, batch: KvBatch, stream=None) -> tuple[torch.Tensor, torch.Tensor]:
@@ -225,7 +233,8 @@ def kv_read(cache: KvCache, batch: KvBatch, stream=None) -> tuple[torch.Tensor, 
         shape = (batch.n_tokens, cache.kv_heads, cache.head_dim)
         k, v = (torch.empty(shape, dtype=cache.dtype, device=cache.k.device) for _ in range(2))
         cccl_kv_read(cache, batch, k, v, ws)
-        _finish(ws, None, "cccl_kv_read")
+        _finish(ws, "cccl_kv_read")
+    _hand_over(stream, k, v)
     return k, v
 
 
@@ -237,5 +246,6 @@ def kv_attention(cache: KvCache, batch: KvBatch, q: torch.Tensor, *, scale: floa
         out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
         lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
         cccl_kv_attention(cache, batch, q, out, ws, scale=scale, causal=causal, window=window, lse=lse)
-        _finish(ws, None, "cccl_kv_attention")
+        _finish(ws, "cccl_kv_attention")
+    _hand_over(stream, out, lse)
     return out, lse

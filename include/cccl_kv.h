@@ -84,7 +84,8 @@ typedef struct {
     int32_t batch;             /* 0..CCCL_KV_MAX_BATCH; 0 makes every call a no-op */
     int32_t table_pages;       /* usable entries of a table row, >= 1 */
     int32_t max_new, max_len;  /* what the program expects as the most new tokens and the longest length of a
-                                * sequence, both >= 1: they choose between kernels; results do not depend on them */
+                                * sequence, both >= 1: they choose kernels and how work is divided, so that results
+                                * may differ in their rounding and no more */
 } cccl_kv_batch;
 
 /* Zero the status header of a workspace, on `stream`. */
@@ -132,7 +133,10 @@ cccl_status cccl_kv_read(const cccl_kv_cache *h_cache, const cccl_kv_batch *h_ba
  * or unwritten place has no effect, NaN and infinities included.
  * Scores, maxima, sums and accumulators are binary32; 16-bit operands enter
  * the tensor cores as they are, 8-bit codes exactly (their scales are applied
- * in binary32).  Results do not change from call to call.
+ * in binary32), queries for 8-bit caches exactly down to 2^-29 of a row's
+ * largest value.  Calls with few rows a kv head round nothing else before the
+ * result; others round each probability once to 16 bits.  The same call gives
+ * the same bits.  d_out may not overlap d_q or the cache.
  * Returns INVALID_ARG, CUDA or OK. */
 cccl_status cccl_kv_attention(const cccl_kv_cache *h_cache, const cccl_kv_batch *h_batch, const void *d_q, int q_heads,
                               int64_t q_token_stride, int64_t q_head_stride, float scale, int causal, int64_t window,

@@ -174,6 +174,7 @@ LONGER = [
     ([5000], [12], 2, 4, 128, 16),
     ([5000, 700], [1, 1], 2, 8, 128, 128),
     ([2048], [2], 1, 16, 64, 12),
+    ([900], [60], 1, 2, 64, 200),
 ]
 
 
