@@ -7,7 +7,18 @@
 // every tile and runs on its own: its ring of stages filled by its own 16-byte
 // asynchronous copies (page lookups one stage ahead of the copies), products by
 // mma.sync, its own running maximum, sum and accumulator in registers.  The
-// four meet once, at the end of an item.
+// four meet once, at the end of an item: with m the largest of their maxima,
+//   out = sum_i 2^(m_i - m) acc_i / sum_i 2^(m_i - m) sum_i .
+// The same joins the parts of an item that several blocks share, by a cluster's
+// shared memory (few, short items) or by a second kernel (any).
+//
+// What bounds it: the loads.  32 tokens over 32 x 4096 cached (8 kv heads of
+// 128, groups of 4, 16-bit): 88 us, 6.1 TB/s, DRAM 77 % busy under the profiler;
+// INT8, 16 x 16384: 106 us, 5.4 TB/s, DRAM 68 % and half of the issue slots
+// taken, by the codes' way to fp16.  Three blocks an SM with 70 KB of copies in
+// flight each did better than two with longer rings or four with spills.  Short
+// calls are bound by the launch, the first page lookups and the joining: one
+// token over 517: 7.3 us.
 //
 // Both products are taken transposed, S' = K Q' and O' = V' P', so that tokens
 // and channels fill the instruction's 16 and the rows its 8: a tile with the
@@ -21,6 +32,7 @@
 // part and remainder), so nothing is rounded before the result.  8-bit codes
 // are exact in fp16; the key's scale multiplies the score and the value's scale
 // the probability, both in binary32.
+#include <algorithm>
 #include <type_traits>
 
 #include "cccl_kv.cuh"
@@ -111,7 +123,8 @@ struct Shape {
     static constexpr int kMerge = kWarps * kRows * (DP + 4) * 4;      // accumulators at the end of an item
     static constexpr int kBlocksPerSm = 3;
     static constexpr int kShares = kSms * kBlocksPerSm;
-    static constexpr int kSmem = kWarps * kRing > kMerge ? kWarps * kRing : kMerge;
+    static constexpr int kGather = kRows * (DP + 4) * 4;              // a block's own, for its cluster
+    static constexpr int kSmem = kWarps * kRing > kMerge + kGather ? kWarps * kRing : kMerge + kGather;
 };
 
 // Where 16-byte chunk c of row r lies in a stage's K or V.  The swizzles spread
@@ -431,17 +444,52 @@ __device__ __forceinline__ void step(uint32_t stage, int32_t base, const uint32_
     values<S>(stage, hi, lo, st.acc);
 }
 
+// Blocks of a cluster.
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t in_block(uint32_t addr, uint32_t rank) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ float4 load_cluster4(uint32_t a) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(a)
+                 : "memory");
+    return v;
+}
+__device__ __forceinline__ float load_cluster(uint32_t a) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+    return v;
+}
+constexpr int kCluster = 8;  // at most
+
+// cluster: 1, or how many blocks share every item of their cluster's share
+// (then whole_items): each takes that part of the item's tiles, and they put
+// the parts together through each other's shared memory, in the blocks' order.
 template <class S>
 __global__ void __launch_bounds__(kThreads, S::kBlocksPerSm)
-    attend_tokens_kernel(const __grid_constant__ KvArgs a, const __grid_constant__ AttnArgs t, int whole_items) {
+    attend_tokens_kernel(const __grid_constant__ KvArgs a, const __grid_constant__ AttnArgs t, int whole_items,
+                         int cluster) {
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ uint32_t prefix[kMaxBatch + 1];
     __shared__ float stats[2][kWarps][S::kRows];
+    __shared__ float gathered[2][S::kRows];
     __shared__ uint32_t odd_rows;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
     build_prefix<S::kRows, S::kTile>(a, t, prefix);
-    Walk w = make_walk(prefix[a.batch], blockIdx.x, gridDim.x, whole_items);
+    const uint32_t rank = cluster > 1 ? cluster_rank() : 0;
+    Walk w = make_walk(prefix[a.batch], blockIdx.x / cluster, gridDim.x / cluster, whole_items);
     const PartLayout parts = part_layout(a, (int)gridDim.x, S::kRows);
     if (!whole_items && w.x >= w.x1 && threadIdx.x == 0) parts.cuts[w.share].last = -1;
     const float to_base2 = t.scale * 1.4426950408889634f;
@@ -452,6 +500,8 @@ __global__ void __launch_bounds__(kThreads, S::kBlocksPerSm)
             parts.cuts[w.share] = cut_of<S::kRows, S::kTile>(p, w.line, w.share);
         const bool full = p.count == p.range.n;
         const int which = p.from > 0 ? 0 : 1;
+        const int32_t from = p.from + (int32_t)rank * p.count / cluster;
+        const int32_t count = p.from + (int32_t)(rank + 1) * p.count / cluster - from;
         const int32_t live = live_rows<S::kRows>(t, p);
         int32_t first[S::NR][2], last[S::NR][2], all_from = 0, all_to = 0x7FFFFFFF;
 #pragma unroll
@@ -488,16 +538,16 @@ __global__ void __launch_bounds__(kThreads, S::kBlocksPerSm)
                 for (int i = 0; i < 4; ++i) st.acc[j][nr][i] = 0.f;
         }
 
-        const int32_t base0 = (p.range.lo + p.from) * S::kTile + warp * S::kTokens;
+        const int32_t base0 = (p.range.lo + from) * S::kTile + warp * S::kTokens;
 #pragma unroll
         for (int i = 0; i < S::kStages - 1; ++i) {
-            if (i < p.count) issue_stage<S>(a, ring + i * S::kStage, look_up<S>(a, p, base0 + i * S::kTile));
+            if (i < count) issue_stage<S>(a, ring + i * S::kStage, look_up<S>(a, p, base0 + i * S::kTile));
             copy_commit();
         }
         RowAt ahead = look_up<S>(a, p, base0 + (S::kStages - 1) * S::kTile);
         int slot = 0, fill = S::kStages - 1;
-        for (int32_t i = 0; i < p.count; ++i) {
-            if (i + S::kStages - 1 < p.count) issue_stage<S>(a, ring + fill * S::kStage, ahead);
+        for (int32_t i = 0; i < count; ++i) {
+            if (i + S::kStages - 1 < count) issue_stage<S>(a, ring + fill * S::kStage, ahead);
             copy_commit();
             fill = fill + 1 == S::kStages ? 0 : fill + 1;
             ahead = look_up<S>(a, p, base0 + (i + S::kStages) * S::kTile);
@@ -560,6 +610,16 @@ __global__ void __launch_bounds__(kThreads, S::kBlocksPerSm)
                 v[6] += f * hi.z;
                 v[7] += f * hi.w;
             }
+            if (cluster > 1) {
+                float4* dst = reinterpret_cast<float4*>(smem + S::kMerge) + (row * (S::DP + 4) + d) / 4;
+                dst[0] = make_float4(v[0], v[1], v[2], v[3]);
+                dst[1] = make_float4(v[4], v[5], v[6], v[7]);
+                if (d == 0) {
+                    gathered[0][row] = m;
+                    gathered[1][row] = sum;
+                }
+                continue;
+            }
             if (!full) {
                 float4* dst = reinterpret_cast<float4*>(parts.acc(w.share, which) + row * a.dim + d);
                 dst[0] = make_float4(v[0], v[1], v[2], v[3]);
@@ -571,6 +631,48 @@ __global__ void __launch_bounds__(kThreads, S::kBlocksPerSm)
                 continue;
             }
             if (store_row_part<typename S::T>(t, p, S::kRows, row, d, v, m, sum)) atomicOr(&odd_rows, 1u << row);
+        }
+        if (cluster > 1) {
+            __syncwarp();
+            cluster_sync();
+            // this block finishes rows rank, rank + cluster, ...: a warp each
+            const int row = (int)rank + cluster * warp;
+            if (row < live) {
+                // loads of kCluster parts at once: of fewer, the last again, with no weight
+                float m = -INFINITY, part_m[kCluster], part_sum[kCluster];
+                float4 x[kCluster];
+                const uint32_t at = smem_addr(smem) + S::kMerge + 4 * (row * (S::DP + 4) + min(4 * lane, S::DP));
+#pragma unroll
+                for (int k = 0; k < kCluster; ++k) {
+                    const int from_block = min(k, cluster - 1);
+                    part_m[k] = load_cluster(in_block(smem_addr(&gathered[0][row]), from_block));
+                    part_sum[k] = load_cluster(in_block(smem_addr(&gathered[1][row]), from_block));
+                    x[k] = load_cluster4(in_block(at, from_block));
+                }
+#pragma unroll
+                for (int k = 0; k < kCluster; ++k) m = fmaxf(m, part_m[k]);
+                const float base = m == -INFINITY ? 0.f : m;
+                float sum = 0.f, v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll
+                for (int k = 0; k < kCluster; ++k) {
+                    const float f = k < cluster ? exp2_fast(part_m[k] - base) : 0.f;
+                    sum += f * part_sum[k];
+                    v[0] += f * x[k].x;
+                    v[1] += f * x[k].y;
+                    v[2] += f * x[k].z;
+                    v[3] += f * x[k].w;
+                }
+                // pairs of lanes hold 8 values together: the even one stores them
+#pragma unroll
+                for (int k = 0; k < 4; ++k) v[4 + k] = __shfl_down_sync(0xFFFFFFFFu, v[k], 1);
+                bool odd = false;
+                if ((lane & 1) == 0 && 4 * lane < a.dim)
+                    odd = store_row_part<typename S::T>(t, p, S::kRows, row, 4 * lane, v, m, sum);
+                if (__any_sync(0xFFFFFFFFu, odd)) fix_row<typename S::T, S::FMT>(a, t, p, S::kRows, row);
+            }
+            __syncwarp();
+            cluster_sync();  // nobody's shared memory is written again, or given up, before all have read it
+            continue;
         }
         __syncthreads();
         if (full) {
@@ -595,12 +697,39 @@ cudaError_t launch_tokens(const KvArgs& a, const AttnArgs& t, int max_new, int m
     if (e != cudaSuccess) return e;
     // Cutting items costs a second kernel, about 3.5 us; not cutting them costs up
     // to one item's time at the end.  64 tokens over 512 (8 tiles, 512 items): 28.0
-    // us whole, 31.4 cut; over 1024: 47.6, 44.4; one over 517 (8 items): 12.2, 9.8;
-    // 8 over 256 (4 tiles): 9.1, 9.7.
+    // us whole, 31.4 cut; over 1024: 47.6, 44.4; 8 over 256 (4 tiles): 9.1, 9.7.
     const int64_t items = (int64_t)a.batch * a.kv_heads;
     const bool whole = max_len <= (items >= S::kShares ? 8 : 4) * S::kTile;
+    // Few items: each is shared by a cluster of 4 or 8 blocks, which join their
+    // parts through shared memory.  Without, with (us; 8 kv heads of 128, 16-bit,
+    // tiles of 64 tokens): one token over 120: 6.4, 6.7 (not taken); 250: 8.0, 6.9;
+    // 517: 9.8, 7.3; 2048: 12.0, 9.5; 4096: 15.9, 12.8.  Two: 250: 8.4, 7.6; 1024:
+    // 10.5, 9.5; 2048: 12.5, 10.7; 4096: 15.2, 15.8 (not taken).  Four: 1024: 11.3,
+    // 11.8 (not taken).  Blocks a cluster, 4 and 8: one over 250: 7.0, 7.5; two
+    // over 517: 9.0, 9.8; one over 2048: 12.8, 10.1.  A share does the items that
+    // begin in it, and lengths differ: with one share an item some do two (two
+    // tokens over 2048: 14.1 against 10.7), with up to four few do.
+    const int64_t tiled = items * (((int64_t)t.group.d * max_new + S::kRows - 1) / S::kRows);
+    const bool alone = tiled * kCluster * 2 <= kSms;
+    if (tiled * kCluster * 2 <= S::kShares && max_len > 2 * S::kTile && max_len <= (alone ? 64 : 32) * S::kTile) {
+        const int cluster = max_len <= 8 * S::kTile ? kCluster / 2 : kCluster;
+        const bool equal = a.batch == 1 && tiled == items;
+        const int64_t clusters = equal ? items : std::min<int64_t>(4 * tiled, S::kShares / cluster);
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3((unsigned)(clusters * cluster));
+        cfg.blockDim = dim3(kThreads);
+        cfg.dynamicSmemBytes = S::kSmem;
+        cfg.stream = s;
+        cudaLaunchAttribute at[1];
+        at[0].id = cudaLaunchAttributeClusterDimension;
+        at[0].val.clusterDim.x = cluster;
+        at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+        cfg.attrs = at;
+        cfg.numAttrs = 1;
+        return cudaLaunchKernelEx(&cfg, attend_tokens_kernel<S>, a, t, 1, cluster);
+    }
     const int shares = shares_for(a, t, max_new, max_len, S::kRows, S::kTile, S::kShares);
-    attend_tokens_kernel<S><<<shares, kThreads, S::kSmem, s>>>(a, t, whole ? 1 : 0);
+    attend_tokens_kernel<S><<<shares, kThreads, S::kSmem, s>>>(a, t, whole ? 1 : 0, 1);
     e = cudaGetLastError();
     if (e != cudaSuccess || whole) return e;
     return launch_join(join_rows_kernel<typename S::T, S::FMT, S::kRows>, a, t, shares, S::kRows / kJoinFew,
