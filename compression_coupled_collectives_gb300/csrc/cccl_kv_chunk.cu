@@ -10,15 +10,32 @@
 //
 // Warps: 0-3 and 4-7 softmax of row tiles 0 and 1 (they also bring in their
 // rows of Q and write the result); 8-11 bring K and V in, or widen 8-bit codes
-// that 13 and 15 bring in; 12 issues the products; 14 walks along the block's share
-// of the line and hands the pieces to the others.  One block an SM: 512 columns of TMEM (S0, S1, O0, O1).
+// that 13 and 15 bring in; 12 issues the products; 14 walks along the block's
+// share of the line and hands the pieces to the others.  One block an SM: it
+// needs all 512 columns of TMEM (S0, S1, O0, O1).
 //
-// The running maximum is only moved when a score exceeds it by more than 2^8
-// (the accumulator is then rescaled in TMEM); any fixed reference gives the
-// same quotient, and binary32 sums and 16-bit probabilities hold a factor of
-// 256.  The products of one thread execute in order, so a full S also means
-// that the previous O is done, and S may be written over the P that the
-// product before it reads.
+// With ref_i a row's reference, x_ij = s_ij scale log2(e) and p_ij =
+// 2^(x_ij - ref_i), a row's result is sum_j p_ij v_j / sum_j p_ij for any ref_i.
+// So the reference is only moved to the row's maximum when a score exceeds it
+// by more than 8 (the accumulator is then rescaled in TMEM): binary32 sums and
+// 16-bit probabilities hold a factor of 256.  The products of one thread execute
+// in order, so a full S also means that the previous O is done, and S may be
+// written over the P that the product before it reads.
+//
+// What bounds it, 16-bit caches: a row's 128 scores a tile cost its thread the
+// loads from TMEM, a maximum, the exponentials (4 clocks a warp each on an SMSP),
+// the sum, the rounding and the stores, about as long as the tensor core takes
+// for the other tile of rows; under the power limit the clock is what gives.
+// 4096 new tokens at the end of 32768 cached, 32 heads over 8 kv heads of 128:
+// 1332 to 1423 us, 1450 to 1540 TFLOP/s with the clock (a library product at its
+// best: 1861); tensor pipe 58 % busy in a short call (1024 over 8192: 102 us).
+// Half a row a thread, 16 softmax warps: 1590 us against 1389.  Exponentials
+// taken a block of 16 late: the same.
+// 8-bit caches, 5 x 2048 new tokens with windows of 4096: 706 to 721 us, 700 to
+// 715 TFLOP/s.  Of 717, widening costs 86, the scales' loads and products, a
+// column's for each of a row's scores, 92, and the tiles at a range's ends, with
+// one slot less for tiles, 130.  Rows held in the products'
+// own layout, which loads a quarter of the scales: 797.
 #include <cuda.h>
 
 #include <type_traits>

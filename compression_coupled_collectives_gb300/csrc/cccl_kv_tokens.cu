@@ -15,10 +15,9 @@
 // What bounds it: the loads.  32 tokens over 32 x 4096 cached (8 kv heads of
 // 128, groups of 4, 16-bit): 88 us, 6.1 TB/s, DRAM 77 % busy under the profiler;
 // INT8, 16 x 16384: 106 us, 5.4 TB/s, DRAM 68 % and half of the issue slots
-// taken, by the codes' way to fp16.  Three blocks an SM with 70 KB of copies in
-// flight each did better than two with longer rings or four with spills.  Short
-// calls are bound by the launch, the first page lookups and the joining: one
-// token over 517: 7.3 us.
+// taken, by the codes' way to fp16.  Three blocks an SM, each with 64 KB of
+// rings; four spill (INT8: 299 us against 264).  Short calls are bound by the
+// launch, the first page lookups and the joining: one token over 517: 7.1 us.
 //
 // Both products are taken transposed, S' = K Q' and O' = V' P', so that tokens
 // and channels fill the instruction's 16 and the rows its 8: a tile with the
@@ -473,13 +472,14 @@ __device__ __forceinline__ float load_cluster(uint32_t a) {
 }
 constexpr int kCluster = 8;  // at most
 
-// cluster: 1, or how many blocks share every item of their cluster's share
-// (then whole_items): each takes that part of the item's tiles, and they put
-// the parts together through each other's shared memory, in the blocks' order.
-template <class S>
+// how: whether items are left whole; with CLUSTERS (whole, then) the number of
+// blocks that share every item of their cluster's share: each takes that part of
+// its tiles, and they put the parts together through each other's shared memory,
+// in the blocks' order.  (Kernels of their own: as one with the others they cost
+// those 2 %.)
+template <class S, bool CLUSTERS>
 __global__ void __launch_bounds__(kThreads, S::kBlocksPerSm)
-    attend_tokens_kernel(const __grid_constant__ KvArgs a, const __grid_constant__ AttnArgs t, int whole_items,
-                         int cluster) {
+    attend_tokens_kernel(const __grid_constant__ KvArgs a, const __grid_constant__ AttnArgs t, int how) {
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ uint32_t prefix[kMaxBatch + 1];
     __shared__ float stats[2][kWarps][S::kRows];
@@ -488,7 +488,8 @@ __global__ void __launch_bounds__(kThreads, S::kBlocksPerSm)
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
     build_prefix<S::kRows, S::kTile>(a, t, prefix);
-    const uint32_t rank = cluster > 1 ? cluster_rank() : 0;
+    const int whole_items = CLUSTERS ? 1 : how, cluster = CLUSTERS ? how : 1;
+    const uint32_t rank = CLUSTERS ? cluster_rank() : 0;
     Walk w = make_walk(prefix[a.batch], blockIdx.x / cluster, gridDim.x / cluster, whole_items);
     const PartLayout parts = part_layout(a, (int)gridDim.x, S::kRows);
     if (!whole_items && w.x >= w.x1 && threadIdx.x == 0) parts.cuts[w.share].last = -1;
@@ -500,8 +501,8 @@ __global__ void __launch_bounds__(kThreads, S::kBlocksPerSm)
             parts.cuts[w.share] = cut_of<S::kRows, S::kTile>(p, w.line, w.share);
         const bool full = p.count == p.range.n;
         const int which = p.from > 0 ? 0 : 1;
-        const int32_t from = p.from + (int32_t)rank * p.count / cluster;
-        const int32_t count = p.from + (int32_t)(rank + 1) * p.count / cluster - from;
+        const int32_t from = CLUSTERS ? p.from + (int32_t)rank * p.count / cluster : p.from;
+        const int32_t count = CLUSTERS ? p.from + (int32_t)(rank + 1) * p.count / cluster - from : p.count;
         const int32_t live = live_rows<S::kRows>(t, p);
         int32_t first[S::NR][2], last[S::NR][2], all_from = 0, all_to = 0x7FFFFFFF;
 #pragma unroll
@@ -610,7 +611,7 @@ __global__ void __launch_bounds__(kThreads, S::kBlocksPerSm)
                 v[6] += f * hi.z;
                 v[7] += f * hi.w;
             }
-            if (cluster > 1) {
+            if constexpr (CLUSTERS) {
                 float4* dst = reinterpret_cast<float4*>(smem + S::kMerge) + (row * (S::DP + 4) + d) / 4;
                 dst[0] = make_float4(v[0], v[1], v[2], v[3]);
                 dst[1] = make_float4(v[4], v[5], v[6], v[7]);
@@ -632,7 +633,7 @@ __global__ void __launch_bounds__(kThreads, S::kBlocksPerSm)
             }
             if (store_row_part<typename S::T>(t, p, S::kRows, row, d, v, m, sum)) atomicOr(&odd_rows, 1u << row);
         }
-        if (cluster > 1) {
+        if constexpr (CLUSTERS) {
             __syncwarp();
             cluster_sync();
             // this block finishes rows rank, rank + cluster, ...: a warp each
@@ -692,7 +693,11 @@ cudaError_t launch_tokens(const KvArgs& a, const AttnArgs& t, int max_new, int m
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     e = once.run(dev, [] {
-        return cudaFuncSetAttribute(attend_tokens_kernel<S>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+        const cudaError_t e = cudaFuncSetAttribute(attend_tokens_kernel<S, false>,
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+        if (e != cudaSuccess) return e;
+        return cudaFuncSetAttribute(attend_tokens_kernel<S, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    S::kSmem);
     });
     if (e != cudaSuccess) return e;
     // Cutting items costs a second kernel, about 3.5 us; not cutting them costs up
@@ -702,13 +707,13 @@ cudaError_t launch_tokens(const KvArgs& a, const AttnArgs& t, int max_new, int m
     const bool whole = max_len <= (items >= S::kShares ? 8 : 4) * S::kTile;
     // Few items: each is shared by a cluster of 4 or 8 blocks, which join their
     // parts through shared memory.  Without, with (us; 8 kv heads of 128, 16-bit,
-    // tiles of 64 tokens): one token over 120: 6.4, 6.7 (not taken); 250: 8.0, 6.9;
-    // 517: 9.8, 7.3; 2048: 12.0, 9.5; 4096: 15.9, 12.8.  Two: 250: 8.4, 7.6; 1024:
-    // 10.5, 9.5; 2048: 12.5, 10.7; 4096: 15.2, 15.8 (not taken).  Four: 1024: 11.3,
+    // tiles of 64 tokens): one token over 120: 6.4, 6.7 (not taken); 250: 8.0, 6.5;
+    // 517: 9.8, 7.1; 2048: 12.0, 9.2; 4096: 15.9, 12.4.  Two: 250: 8.4, 7.3; 1024:
+    // 10.5, 9.1; 2048: 12.5, 10.3; 4096: 15.2, 15.8 (not taken).  Four: 1024: 11.3,
     // 11.8 (not taken).  Blocks a cluster, 4 and 8: one over 250: 7.0, 7.5; two
     // over 517: 9.0, 9.8; one over 2048: 12.8, 10.1.  A share does the items that
     // begin in it, and lengths differ: with one share an item some do two (two
-    // tokens over 2048: 14.1 against 10.7), with up to four few do.
+    // tokens over 2048: 14.1 against 11.2), with up to four few do.
     const int64_t tiled = items * (((int64_t)t.group.d * max_new + S::kRows - 1) / S::kRows);
     const bool alone = tiled * kCluster * 2 <= kSms;
     if (tiled * kCluster * 2 <= S::kShares && max_len > 2 * S::kTile && max_len <= (alone ? 64 : 32) * S::kTile) {
@@ -726,10 +731,10 @@ cudaError_t launch_tokens(const KvArgs& a, const AttnArgs& t, int max_new, int m
         at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
         cfg.attrs = at;
         cfg.numAttrs = 1;
-        return cudaLaunchKernelEx(&cfg, attend_tokens_kernel<S>, a, t, 1, cluster);
+        return cudaLaunchKernelEx(&cfg, attend_tokens_kernel<S, true>, a, t, cluster);
     }
     const int shares = shares_for(a, t, max_new, max_len, S::kRows, S::kTile, S::kShares);
-    attend_tokens_kernel<S><<<shares, kThreads, S::kSmem, s>>>(a, t, whole ? 1 : 0, 1);
+    attend_tokens_kernel<S, false><<<shares, kThreads, S::kSmem, s>>>(a, t, whole ? 1 : 0);
     e = cudaGetLastError();
     if (e != cudaSuccess || whole) return e;
     return launch_join(join_rows_kernel<typename S::T, S::FMT, S::kRows>, a, t, shares, S::kRows / kJoinFew,
