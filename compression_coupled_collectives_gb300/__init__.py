@@ -3,8 +3,10 @@ buffers and the fused compressed reduce, on one GB300 GPU.
 
 Every function here marshals arguments for the C ABI of ``include/cccl.h``
 (same names) and calls it; all compute runs in the library's sm_103a kernels.
-torch supplies device memory and streams only.  There is no fallback: importing
-this package raises ImportError when ``libcccl.so`` has not been built.
+What works on a paged key/value cache (``include/cccl_kv.h``) is in ``kv`` and
+reachable from here too: ``kv_write``, ``kv_read``, ``kv_attention``.  torch
+supplies device memory and streams only.  There is no fallback: importing this
+package raises ImportError when ``libcccl.so`` has not been built.
 """
 
 from __future__ import annotations
