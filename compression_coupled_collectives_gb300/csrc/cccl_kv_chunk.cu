@@ -12,7 +12,9 @@
 // rows of Q and write the result); 8-11 bring K and V in, or widen 8-bit codes
 // that 13 and 15 bring in; 12 issues the products; 14 walks along the block's
 // share of the line and hands the pieces to the others.  One block an SM: it
-// needs all 512 columns of TMEM (S0, S1, O0, O1).
+// needs all 512 columns of TMEM (S0, S1, O0, O1).  Where there are few items a
+// cluster's blocks share each and join their parts before they end (through
+// the workspace, which stays in the L2: shared memory is full of tiles).
 //
 // With ref_i a row's reference, x_ij = s_ij scale log2(e) and p_ij =
 // 2^(x_ij - ref_i), a row's result is sum_j p_ij v_j / sum_j p_ij for any ref_i.
@@ -255,6 +257,30 @@ __device__ __forceinline__ void walk_role(const KvArgs& a, const AttnArgs& t, Sh
         if (!more) break;
     }
     if (!w.whole && lane == 0) part_layout(a, gridDim.x, kRows).cuts[w.share] = cut;
+}
+// The walking warp where `cluster` blocks share an item: one piece, this block's
+// part of item blockIdx.x / cluster (count 0: none; items of fewer tiles than
+// blocks leave some without).  prefix counts items.
+__device__ __forceinline__ int parts_of(const Piece& p, int cluster) { return min(cluster, p.range.n); }
+__device__ __forceinline__ void share_role(const KvArgs& a, const AttnArgs& t, Shared* sh, int cluster) {
+    const uint32_t items = sh->prefix[a.batch];
+    Walk w = make_walk(items, blockIdx.x / cluster, items, 1);
+    Piece p{};
+    if (next_piece<kRows, 0>(a, t, sh->prefix, w, p)) p.range = tile_range<kRows, kTokens>(t, p.seq, p.rt);
+    const int rank = (int)cluster_rank(), n = parts_of(p, cluster);
+    p.from = p.count = 0;
+    if (rank < n) {
+        p.from = (int32_t)((int64_t)rank * p.range.n / n);
+        p.count = (int32_t)((int64_t)(rank + 1) * p.range.n / n) - p.from;
+    }
+    if ((threadIdx.x & 31) == 0) {
+        sh->ring[0] = p;
+        mbar_arrive(&sh->piece_full[0]);
+        if (p.count > 0) {
+            sh->ring[1].count = 0;
+            mbar_arrive(&sh->piece_full[1]);
+        }
+    }
 }
 // The other warps: piece n.  Its count is 0 after the last one; false: leave.
 __device__ __forceinline__ bool take_piece(const Waiter& wait, uint32_t n, Piece* to) {
@@ -884,11 +910,68 @@ __device__ __forceinline__ void softmax_role(const KvArgs& a, const AttnArgs& t,
     }
 }
 
-template <class T, int FMT>
+// Warps 0 to 7, after the cluster's PARTS blocks have left their parts of item
+// ring[0] in the workspace: this block joins 256 / PARTS of the rows, 32 rows and
+// 16 channels a warp at a time, in the parts' order.
+template <class T, int FMT, int PARTS>
+__device__ __forceinline__ void join_item(const KvArgs& a, const AttnArgs& t, Shared* sh) {
+    const Piece p = sh->ring[0];
+    const int n = parts_of(p, PARTS);
+    if (n < 2) return;  // no item, or its only block wrote the result
+    const int rank = (int)cluster_rank(), share0 = (int)blockIdx.x - rank;
+    constexpr int kJoinRows = kRows / PARTS;
+    const int row0 = rank * kJoinRows, live = live_rows<kRows>(t, p);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const PartLayout parts = part_layout(a, gridDim.x, kRows);
+    uint32_t* odd_rows = sh->prefix;  // no longer needed: 32 rows an entry
+    if (threadIdx.x < kRows / 32) odd_rows[threadIdx.x] = 0;
+    asm volatile("bar.sync 1, 256;" ::: "memory");
+#pragma unroll 1
+    for (int u = warp; u < kJoinRows / 32 * (a.dim / 16); u += 8) {
+        const int band = u % (kJoinRows / 32), d = 16 * (u / (kJoinRows / 32)), row = row0 + 32 * band + lane;
+        if (row >= live) continue;
+        float part_m[PARTS], part_sum[PARTS], x[PARTS][16];
+#pragma unroll
+        for (int k = 0; k < PARTS; ++k) {  // of fewer parts the last again, with no weight
+            const int part = min(k, n - 1);
+            const float* st = parts.stats(share0 + part, part == 0);
+            const float* src = parts.acc(share0 + part, part == 0) + (size_t)d * kRows + row;
+            part_m[k] = __ldcg(st + row);
+            part_sum[k] = __ldcg(st + kRows + row);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) x[k][e] = __ldcg(src + e * kRows);
+        }
+        float m = -INFINITY;
+#pragma unroll
+        for (int k = 0; k < PARTS; ++k) m = fmaxf(m, part_m[k]);
+        const float base = m == -INFINITY ? 0.f : m;
+        float sum = 0.f, v[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) v[e] = 0.f;
+#pragma unroll
+        for (int k = 0; k < PARTS; ++k) {
+            const float f = k < n ? exp2f(part_m[k] - base) : 0.f;
+            sum += f * part_sum[k];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) v[e] += f * x[k][e];
+        }
+        bool odd = store_row_part<T>(t, p, kRows, row, d, v, m, sum);
+        odd |= store_row_part<T>(t, p, kRows, row, d + 8, v + 8, m, sum);
+        if (odd) atomicOr(&odd_rows[band], 1u << lane);
+    }
+    asm volatile("bar.sync 1, 256;" ::: "memory");
+    for (int r = warp; r < kJoinRows; r += 8)
+        if (odd_rows[r / 32] >> (r % 32) & 1) fix_row<T, FMT>(a, t, p, kRows, row0 + r);
+}
+
+// how: whether items are left whole (0: they are cut at shares' ends); with
+// CLUSTERS how many blocks, a cluster, share each item.  (Kernels of their own:
+// as one with the others they cost those 1 %.)
+template <class T, int FMT, bool CLUSTERS>
 __global__ void __launch_bounds__(kThreads, 1)
     attend_chunk_kernel(const __grid_constant__ KvArgs a, const __grid_constant__ AttnArgs t,
                         const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map, int32_t box,
-                        int whole_items) {
+                        int how) {
     constexpr int kN = kSlots<FMT>;
     extern __shared__ uint8_t raw[];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -928,7 +1011,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         sh->stop = 0;
         fence_mbar_init();
     }
-    build_prefix<kRows, kTokens>(a, t, sh->prefix);
+    int cluster = 1;
+    if constexpr (CLUSTERS) {
+        build_prefix<kRows, 0>(a, t, sh->prefix);
+        // (more items than the call's bounds allow: every block for itself)
+        if (sh->prefix[a.batch] <= gridDim.x / how) cluster = how;
+        __syncthreads();
+    }
+    if (cluster == 1) build_prefix<kRows, kTokens>(a, t, sh->prefix);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -937,6 +1027,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp < 8) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
         softmax_role<T, FMT>(a, t, sh, base + (warp / 4) * tile_bytes, raw_codes + raw_bytes);
+        if (CLUSTERS && cluster > 1) {
+            __syncwarp();
+            cluster_sync();
+            if (cluster == 2)
+                join_item<T, FMT, 2>(a, t, sh);
+            else
+                join_item<T, FMT, 4>(a, t, sh);
+        }
     } else if (warp < 12) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLoaderRegs));
         if constexpr (FMT == kKv16Bit)
@@ -956,10 +1054,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             fetch_role<FMT, 2, kRawSlots>(a, t, sh, fetch, (warp - 13) / 2, raw_codes, kTokens * a.dim, sh->raw_full,
                                           sh->raw_free);
         } else if (warp == 14) {
-            walk_role(a, t, sh, make_walk(sh->prefix[a.batch], blockIdx.x, gridDim.x, whole_items));
+            if (CLUSTERS && cluster > 1)
+                share_role(a, t, sh, cluster);
+            else
+                walk_role(a, t, sh, make_walk(sh->prefix[a.batch], blockIdx.x, gridDim.x, CLUSTERS ? 1 : how));
         }
     }
     __syncwarp();
+    if (CLUSTERS && cluster > 1 && warp >= 8) cluster_sync();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -1030,7 +1132,11 @@ cudaError_t launch_one(const KvArgs& a, const AttnArgs& t, int max_new, int max_
         const cudaError_t set = cudaFuncSetAttribute(join_columns_kernel<T, FMT, kRows>,
                                                      cudaFuncAttributeMaxDynamicSharedMemorySize, join_bytes(128));
         if (set != cudaSuccess) return set;
-        return cudaFuncSetAttribute(attend_chunk_kernel<T, FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        const cudaError_t both = cudaFuncSetAttribute(attend_chunk_kernel<T, FMT, true>,
+                                                      cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                      (int)shared_bytes<FMT>(128));
+        if (both != cudaSuccess) return both;
+        return cudaFuncSetAttribute(attend_chunk_kernel<T, FMT, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     (int)shared_bytes<FMT>(128));
     });
     if (e != cudaSuccess) return e;
@@ -1043,8 +1149,21 @@ cudaError_t launch_one(const KvArgs& a, const AttnArgs& t, int max_new, int max_
     // of up to 97 tokens over 1500: 32.6 us whole, 37.3 cut; three of 700 over
     // 2500: 49.9, 63.9; two of 256 over 4096: 63.9, 45.4.
     const bool whole = max_len <= 20 * kTokens;
+    // Few items: each is shared by a cluster of 2 or 4 blocks, which join their
+    // parts before they end.  At most 128 blocks: more clusters than can be
+    // resident at once run one after the other (16 of 8 blocks do).  Without, with
+    // (us, 16-bit): 128 new tokens (16 items, 4 blocks) over 256: 14.1, 15.7 (not
+    // taken); 512: 17.1, 16.5; 1024: 24.1, 18.2; 4096: 39.0, 28.2; 8192: 48.0, 41.3;
+    // 16384: 58.0, 65.9 (not taken).  512 new (64 items, 2 blocks) over 512: 18.1,
+    // 20.3 (not taken); 1024: 25.1, 24.5; 2048: 37.4, 31.2; 4096: 50.6, 43.1.
+    // INT8: 128 over 1024: 34.0, 23.1; 2 x 256 over 2048: 52.2, 40.3.
+    const int64_t tiled = (int64_t)a.batch * a.kv_heads * (((int64_t)t.group.d * max_new + kRows - 1) / kRows);
+    const int cluster = 4 * tiled <= 128 ? 4 : 2 * tiled <= 128 ? 2 : 1;
+    if (cluster > 1 && max_len > (cluster == 4 ? 3 : 7) * kTokens && max_len <= 16 * cluster * kTokens)
+        return launch_clusters(attend_chunk_kernel<T, FMT, true>, (int)tiled * cluster, cluster, kThreads,
+                               shared_bytes<FMT>(a.dim), s, a, t, k_map, v_map, box, cluster);
     const int shares = shares_for(a, t, max_new, max_len, kRows, kTokens, kShares);
-    attend_chunk_kernel<T, FMT>
+    attend_chunk_kernel<T, FMT, false>
         <<<shares, kThreads, shared_bytes<FMT>(a.dim), s>>>(a, t, k_map, v_map, box, whole ? 1 : 0);
     e = cudaGetLastError();
     if (e != cudaSuccess || whole) return e;

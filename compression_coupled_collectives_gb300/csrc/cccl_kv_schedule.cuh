@@ -27,7 +27,8 @@ struct TileRange {
     int32_t first, last;  // visible tokens of any row: first .. last - 1
     int32_t lo, n;        // tiles lo .. lo + n - 1 (n >= 1)
 };
-// (A call's rows are below 2^31: n_tokens * q_heads is.)
+// (A call's rows are below 2^31: n_tokens * q_heads is.)  TOKENS of 0 counts
+// every item as one tile.
 template <int ROWS, int TOKENS>
 __device__ __forceinline__ TileRange tile_range(const AttnArgs& t, const Sequence& s, int32_t rt) {
     const uint32_t rows = (uint32_t)s.n * t.group.d, r0 = (uint32_t)rt * ROWS;
@@ -38,6 +39,9 @@ __device__ __forceinline__ TileRange tile_range(const AttnArgs& t, const Sequenc
     visible_range(t, s.len, base + (int32_t)div_by(t.group, min(r0 + ROWS, rows) - 1), ignore, r.last);
     if (r.first >= r.last) {
         r.first = r.last = r.lo = 0;
+        r.n = 1;
+    } else if constexpr (TOKENS == 0) {
+        r.lo = 0;
         r.n = 1;
     } else {
         r.lo = r.first / TOKENS;
@@ -460,6 +464,32 @@ __global__ void __launch_bounds__(kJoinManyThreads) join_columns_kernel(const __
         if (store_row_part<T>(t, p, ROWS, row0 + r, d, y, sh.top[r], sh.total[r])) atomicOr(&sh.odd_rows, 1u << r);
     }
     join_end<T, FMT, ROWS>(a, t, sh, p);
+}
+
+// Clusters of blocks.
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+template <class... Params, class... Args>
+cudaError_t launch_clusters(void (*kernel)(Params...), int blocks, int cluster, int threads, size_t shared,
+                            cudaStream_t s, Args... args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)blocks);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = shared;
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = (unsigned)cluster;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 // Shares that a call can need, at most `most`: the tiles of a batch whose

@@ -443,15 +443,7 @@ __device__ __forceinline__ void step(uint32_t stage, int32_t base, const uint32_
     values<S>(stage, hi, lo, st.acc);
 }
 
-// Blocks of a cluster.
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
+// Shared memory of a cluster's blocks.
 __device__ __forceinline__ uint32_t in_block(uint32_t addr, uint32_t rank) {
     uint32_t r;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
@@ -720,18 +712,8 @@ cudaError_t launch_tokens(const KvArgs& a, const AttnArgs& t, int max_new, int m
         const int cluster = max_len <= 8 * S::kTile ? kCluster / 2 : kCluster;
         const bool equal = a.batch == 1 && tiled == items;
         const int64_t clusters = equal ? items : std::min<int64_t>(4 * tiled, S::kShares / cluster);
-        cudaLaunchConfig_t cfg{};
-        cfg.gridDim = dim3((unsigned)(clusters * cluster));
-        cfg.blockDim = dim3(kThreads);
-        cfg.dynamicSmemBytes = S::kSmem;
-        cfg.stream = s;
-        cudaLaunchAttribute at[1];
-        at[0].id = cudaLaunchAttributeClusterDimension;
-        at[0].val.clusterDim.x = cluster;
-        at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-        cfg.attrs = at;
-        cfg.numAttrs = 1;
-        return cudaLaunchKernelEx(&cfg, attend_tokens_kernel<S, true>, a, t, cluster);
+        return launch_clusters(attend_tokens_kernel<S, true>, (int)clusters * cluster, cluster, kThreads, S::kSmem, s,
+                               a, t, cluster);
     }
     const int shares = shares_for(a, t, max_new, max_len, S::kRows, S::kTile, S::kShares);
     attend_tokens_kernel<S, false><<<shares, kThreads, S::kSmem, s>>>(a, t, whole ? 1 : 0);

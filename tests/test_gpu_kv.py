@@ -312,6 +312,32 @@ def test_large_values_do_not_overflow_on_the_way(cc, new, over):
     assert (out.float() / big.float() - 1).abs().max() <= 2.0 ** -8
 
 
+@pytest.mark.parametrize("over", [{}, dict(max_new=32, max_len=600), dict(max_len=4000), dict(max_len=8000)])
+@pytest.mark.parametrize("window", [0, 300])
+@pytest.mark.parametrize("fmt", ["16bit", "int8", "e4m3"])
+def test_few_items_shared_by_blocks(cc, fmt, window, over):
+    """Sequences without new tokens, of fewer tiles than an item has blocks, and more rows than the program said."""
+    c = Case([900, 40, 0, 513, 130], [200, 33, 0, 64, 1], heads=2, group=4, dim=112, page=16, fmt=fmt, seed=60,
+             fill=float("nan"))
+    cache, batch = c.objects(cc, **over)
+    out, lse = cc.kv_attention(cache, batch, c.q, window=window)
+    check(c, out, lse, window=window)
+
+
+@pytest.mark.parametrize("new", [1, 9, 64, 300])
+def test_values_that_are_not_finite_in_shared_items(cc, new):
+    c = Case([700], [new], heads=2, group=2, dim=64, page=16, seed=61)
+    for p, head, value in ((5, 0, math.inf), (390, 0, math.inf), (390, 1, math.nan)):
+        c.v[(int(c.table[0, p // 16]), p % 16)][head, 7] = value
+    cache, batch = c.objects(cc)
+    out, _ = cc.kv_attention(cache, batch, c.q)
+    assert (out[:, :2, 7] == math.inf).all() and torch.isnan(out[:, 2:, 7]).all()
+    keep = torch.arange(64, device="cuda") != 7
+    c.v.nan_to_num_(0.0, 0.0, 0.0)
+    ref, _, tol, _ = c.attention()
+    assert ((out.double() - ref).abs() <= tol)[..., keep].all()
+
+
 def test_strided_queries_outputs_and_guards(cc):
     """q and out as slices of wider tensors; nothing around the output changes."""
     for new in (1, 50):
