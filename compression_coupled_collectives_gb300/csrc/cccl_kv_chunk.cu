@@ -13,8 +13,7 @@
 // that 13 and 15 bring in; 12 issues the products; 14 walks along the block's
 // share of the line and hands the pieces to the others.  One block an SM: it
 // needs all 512 columns of TMEM (S0, S1, O0, O1).  Where there are few items a
-// cluster's blocks share each and join their parts before they end (through
-// the workspace, which stays in the L2: shared memory is full of tiles).
+// cluster's blocks share each and join their parts through shared memory.
 //
 // With ref_i a row's reference, x_ij = s_ij scale log2(e) and p_ij =
 // 2^(x_ij - ref_i), a row's result is sum_j p_ij v_j / sum_j p_ij for any ref_i.
@@ -708,7 +707,7 @@ __device__ __forceinline__ uint32_t bits_below(int32_t n) {
 
 template <class T, int FMT>
 __device__ __forceinline__ void softmax_role(const KvArgs& a, const AttnArgs& t, Shared* sh, uint32_t q_tile,
-                                             uint32_t stages) {
+                                             uint32_t stages, float* joint) {
     const int i = threadIdx.x / 128, row = threadIdx.x % 128, warp = row >> 5, lane = row & 31;
     const int me = threadIdx.x >> 5;
     const Waiter wait{sh, a.ws};
@@ -751,6 +750,10 @@ __device__ __forceinline__ void softmax_role(const KvArgs& a, const AttnArgs& t,
             const RowPlace at = row_place(t, cur, kRows, tile_row);
             const PartLayout parts = part_layout(a, gridDim.x, kRows);
             const int which = cur.from > 0 ? 0 : 1;
+            float* const acc = joint != nullptr ? joint : parts.acc(blockIdx.x, which);
+            float* const stats = joint != nullptr ? joint + kRows * a.dim : parts.stats(blockIdx.x, which);
+            // a joint part takes the tiles' place: when both row tiles' products are done
+            if (joint != nullptr && live_rows<kRows>(t, cur) > kTileRows && !wait(&sh->o_full[1], 0)) return;
             const bool none = last <= first;
             const float inv = none ? 0.f : 1.f / l;
             bool odd = false;
@@ -772,7 +775,7 @@ __device__ __forceinline__ void softmax_role(const KvArgs& a, const AttnArgs& t,
                     store_rows<kStageRows<FMT>>(stage, y, is_row ? to + 2 * c : nullptr, 2 * (a.dim - c));
                 }
             } else {
-                float* dst = parts.acc(blockIdx.x, which) + tile_row;
+                float* dst = acc + tile_row;
 #pragma unroll 1
                 for (int c = 0; c < a.dim; c += 16) {
                     uint32_t o[16];
@@ -792,8 +795,8 @@ __device__ __forceinline__ void softmax_role(const KvArgs& a, const AttnArgs& t,
                     fix_row<T, FMT>(a, t, cur, kRows, i * kTileRows + 32 * warp + __ffs(todo) - 1);
                 }
             } else if (is_row) {
-                parts.stats(blockIdx.x, which)[tile_row] = m;
-                parts.stats(blockIdx.x, which)[kRows + tile_row] = l;
+                stats[tile_row] = m;
+                stats[kRows + tile_row] = l;
             }
             tc_fence_before();
         }
@@ -911,18 +914,16 @@ __device__ __forceinline__ void softmax_role(const KvArgs& a, const AttnArgs& t,
 }
 
 // Warps 0 to 7, after the cluster's PARTS blocks have left their parts of item
-// ring[0] in the workspace: this block joins 256 / PARTS of the rows, 32 rows and
-// 16 channels a warp at a time, in the parts' order.
+// ring[0] at `joint` of their shared memory: this block joins 256 / PARTS of the
+// rows, 32 rows and 16 channels a warp at a time, in the parts' order.
 template <class T, int FMT, int PARTS>
-__device__ __forceinline__ void join_item(const KvArgs& a, const AttnArgs& t, Shared* sh) {
+__device__ __forceinline__ void join_item(const KvArgs& a, const AttnArgs& t, Shared* sh, uint32_t joint) {
     const Piece p = sh->ring[0];
     const int n = parts_of(p, PARTS);
     if (n < 2) return;  // no item, or its only block wrote the result
-    const int rank = (int)cluster_rank(), share0 = (int)blockIdx.x - rank;
     constexpr int kJoinRows = kRows / PARTS;
-    const int row0 = rank * kJoinRows, live = live_rows<kRows>(t, p);
+    const int row0 = (int)cluster_rank() * kJoinRows, live = live_rows<kRows>(t, p);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const PartLayout parts = part_layout(a, gridDim.x, kRows);
     uint32_t* odd_rows = sh->prefix;  // no longer needed: 32 rows an entry
     if (threadIdx.x < kRows / 32) odd_rows[threadIdx.x] = 0;
     asm volatile("bar.sync 1, 256;" ::: "memory");
@@ -934,12 +935,11 @@ __device__ __forceinline__ void join_item(const KvArgs& a, const AttnArgs& t, Sh
 #pragma unroll
         for (int k = 0; k < PARTS; ++k) {  // of fewer parts the last again, with no weight
             const int part = min(k, n - 1);
-            const float* st = parts.stats(share0 + part, part == 0);
-            const float* src = parts.acc(share0 + part, part == 0) + (size_t)d * kRows + row;
-            part_m[k] = __ldcg(st + row);
-            part_sum[k] = __ldcg(st + kRows + row);
+            const uint32_t from = in_block(joint + 4 * row, part);
+            part_m[k] = load_cluster(from + 4 * kRows * a.dim);
+            part_sum[k] = load_cluster(from + 4 * kRows * (a.dim + 1));
 #pragma unroll
-            for (int e = 0; e < 16; ++e) x[k][e] = __ldcg(src + e * kRows);
+            for (int e = 0; e < 16; ++e) x[k][e] = load_cluster(from + 4 * kRows * (d + e));
         }
         float m = -INFINITY;
 #pragma unroll
@@ -1026,14 +1026,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     const Fetch fetch{&k_map, &v_map, box};
     if (warp < 8) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
-        softmax_role<T, FMT>(a, t, sh, base + (warp / 4) * tile_bytes, raw_codes + raw_bytes);
+        // 256 rows of sums and two statistics: less than Q and the slots, at every dim
+        float* const joint = reinterpret_cast<float*>(raw + (base - smem_addr(raw)));
+        softmax_role<T, FMT>(a, t, sh, base + (warp / 4) * tile_bytes, raw_codes + raw_bytes,
+                             CLUSTERS && cluster > 1 ? joint : nullptr);
         if (CLUSTERS && cluster > 1) {
             __syncwarp();
             cluster_sync();
             if (cluster == 2)
-                join_item<T, FMT, 2>(a, t, sh);
+                join_item<T, FMT, 2>(a, t, sh, base);
             else
-                join_item<T, FMT, 4>(a, t, sh);
+                join_item<T, FMT, 4>(a, t, sh, base);
         }
     } else if (warp < 12) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLoaderRegs));
@@ -1061,7 +1064,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     }
     __syncwarp();
-    if (CLUSTERS && cluster > 1 && warp >= 8) cluster_sync();
+    if (CLUSTERS && cluster > 1) {
+        if (warp >= 8) cluster_sync();
+        cluster_sync();  // nobody's shared memory is given up before all have read it
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -1075,6 +1081,8 @@ constexpr size_t shared_bytes(int dim) {
            (FMT == kKv16Bit ? 0 : (size_t)kRawSlots * kTokens * dim) + kStageBytes<FMT> + sizeof(Shared);
 }
 
+static_assert(1024 * (128 + 2) <= (2 + kSlots<kKvInt8>) * 2 * kHalfBytes && 1024 * (64 + 2) <= (2 + kSlots<kKvInt8>) * kHalfBytes,
+              "a joint part takes the place of Q and the slots");
 static_assert(shared_bytes<kKv16Bit>(128) <= 232448 && shared_bytes<kKvInt8>(128) <= 232448, "227 KB a block");
 
 using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
@@ -1149,14 +1157,14 @@ cudaError_t launch_one(const KvArgs& a, const AttnArgs& t, int max_new, int max_
     // of up to 97 tokens over 1500: 32.6 us whole, 37.3 cut; three of 700 over
     // 2500: 49.9, 63.9; two of 256 over 4096: 63.9, 45.4.
     const bool whole = max_len <= 20 * kTokens;
-    // Few items: each is shared by a cluster of 2 or 4 blocks, which join their
-    // parts before they end.  At most 128 blocks: more clusters than can be
-    // resident at once run one after the other (16 of 8 blocks do).  Without, with
-    // (us, 16-bit): 128 new tokens (16 items, 4 blocks) over 256: 14.1, 15.7 (not
-    // taken); 512: 17.1, 16.5; 1024: 24.1, 18.2; 4096: 39.0, 28.2; 8192: 48.0, 41.3;
-    // 16384: 58.0, 65.9 (not taken).  512 new (64 items, 2 blocks) over 512: 18.1,
-    // 20.3 (not taken); 1024: 25.1, 24.5; 2048: 37.4, 31.2; 4096: 50.6, 43.1.
-    // INT8: 128 over 1024: 34.0, 23.1; 2 x 256 over 2048: 52.2, 40.3.
+    // Few items: each is shared by a cluster of 2 or 4 blocks.  At most 128 blocks:
+    // clusters that cannot be resident together run one after the other (16 of 8
+    // blocks do).  Without, with (us, 16-bit): 128 new tokens (16 items, 4 blocks)
+    // over 256: 14.1, 15.7 (not taken); 512: 17.1, 15.5; 1024: 24.1, 17.1; 4096:
+    // 39.0, 26.5; 8192: 48.0, 40.0; 16384: 58.0, 65.9 (not taken).  512 new (64
+    // items, 2 blocks) over 512: 18.1, 20.3 (not taken); 1024: 25.1, 21.2; 2048:
+    // 37.4, 27.5; 4096: 50.6, 39.7.  INT8: 128 over 1024: 34.0, 22.5; 2 x 256 over
+    // 2048: 52.2, 36.4.
     const int64_t tiled = (int64_t)a.batch * a.kv_heads * (((int64_t)t.group.d * max_new + kRows - 1) / kRows);
     const int cluster = 4 * tiled <= 128 ? 4 : 2 * tiled <= 128 ? 2 : 1;
     if (cluster > 1 && max_len > (cluster == 4 ? 3 : 7) * kTokens && max_len <= 16 * cluster * kTokens)

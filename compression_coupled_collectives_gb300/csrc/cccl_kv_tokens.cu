@@ -443,25 +443,6 @@ __device__ __forceinline__ void step(uint32_t stage, int32_t base, const uint32_
     values<S>(stage, hi, lo, st.acc);
 }
 
-// Shared memory of a cluster's blocks.
-__device__ __forceinline__ uint32_t in_block(uint32_t addr, uint32_t rank) {
-    uint32_t r;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
-    return r;
-}
-__device__ __forceinline__ float4 load_cluster4(uint32_t a) {
-    float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "r"(a)
-                 : "memory");
-    return v;
-}
-__device__ __forceinline__ float load_cluster(uint32_t a) {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
-    return v;
-}
 constexpr int kCluster = 8;  // at most
 
 // how: whether items are left whole; with CLUSTERS (whole, then) the number of
