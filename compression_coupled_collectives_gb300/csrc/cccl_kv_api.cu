@@ -60,7 +60,8 @@ bool fill(const cccl_kv_cache* c, const cccl_kv_batch* b, void* d_ws, size_t ws_
     if (c->format != CCCL_KV_16BIT) {
         const int64_t ss[3] = {c->scale_page_stride, c->scale_token_stride, c->scale_head_stride};
         if (!aligned(c->k_scale, 4) || !aligned(c->v_scale, 4) || !extent(n, ss, 3, 1, &scales)) return false;
-        if (!device_range(c->k_scale, 4 * (size_t)scales) || !device_range(c->v_scale, 4 * (size_t)scales)) return false;
+        if (!device_range(c->k_scale, 4 * (size_t)scales) || !device_range(c->v_scale, 4 * (size_t)scales))
+            return false;
     }
     if (!device_range(c->k, (size_t)(values * elem)) || !device_range(c->v, (size_t)(values * elem)) ||
         !device_range(d_ws, need) || !device_range(b->page_table, 4 * (size_t)entries) ||

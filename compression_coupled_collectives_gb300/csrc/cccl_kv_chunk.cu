@@ -35,8 +35,8 @@
 // 8-bit caches, 5 x 2048 new tokens with windows of 4096: 706 to 721 us, 700 to
 // 715 TFLOP/s.  Of 717, widening costs 86, the scales' loads and products, a
 // column's for each of a row's scores, 92, and the tiles at a range's ends, with
-// one slot less for tiles, 130.  Rows held in the products'
-// own layout, which loads a quarter of the scales: 797.
+// one slot less for tiles, 130.  Rows held in the products' own layout, which
+// loads a quarter of the scales: 797.
 #include <cuda.h>
 
 #include <type_traits>
@@ -295,9 +295,9 @@ __device__ __forceinline__ bool take_piece(const Waiter& wait, uint32_t n, Piece
 // ---------------------------------------------------------------- K and V
 // Tiles come through a ring, K and V in turn.  A tile that every row of the
 // item's range covers is brought by TMA, a page (or 128 tokens) a box, each warp
-// issuing the boxes that begin in its rows; one that the range cuts, or pages that TMA's
-// boxes do not fit (`box` is 0), by 16-byte copies that put zeros where the
-// range ends, so that no product meets what nobody wrote.
+// issuing the boxes that begin in its rows; one that the range cuts, or pages
+// that TMA's boxes do not fit (`box` is 0), by 16-byte copies that put zeros where
+// the range ends, so that no product meets what nobody wrote.
 struct Fetch {
     const CUtensorMap *k, *v;
     int32_t box;  // tokens of a TMA box; 0: none
@@ -365,7 +365,8 @@ __device__ __forceinline__ void fetch_role(const KvArgs& a, const AttnArgs& t, S
     auto leave = [&]() {
         copy_wait<0>();
         if (f.box > 0)
-            for (uint32_t k = entry > SLOTS ? entry - SLOTS : 0; k < entry; ++k) mbar_wait(&full[k % SLOTS], (k / SLOTS) & 1);
+            for (uint32_t k = entry > SLOTS ? entry - SLOTS : 0; k < entry; ++k)
+                mbar_wait(&full[k % SLOTS], (k / SLOTS) & 1);
     };
     auto hand_over = [&](uint32_t upto) {  // this warp's copies of entries below `upto` are done
         if (handed >= upto) return;
@@ -525,7 +526,8 @@ __device__ __forceinline__ void mma_role(const KvArgs& a, const AttnArgs& t, Sha
     const Waiter wait{sh, a.ws};
     const uint32_t tmem = sh->tmem;
     // a negative scale: Q enters with its sign changed, the softmax takes the scale's size
-    const uint32_t qk = instruction(M::kHalf, kTokens, false) | (t.scale < 0.f ? 1u << 13 : 0u), pv = instruction(M::kHalf, a.dim > 64 ? 128 : 64, true);
+    const uint32_t qk = instruction(M::kHalf, kTokens, false) | (t.scale < 0.f ? 1u << 13 : 0u);
+    const uint32_t pv = instruction(M::kHalf, a.dim > 64 ? 128 : 64, true);
     const int steps = a.dim / 16;
     const uint32_t q_bytes = slot_bytes;
     uint32_t entry = 0;
@@ -540,7 +542,8 @@ __device__ __forceinline__ void mma_role(const KvArgs& a, const AttnArgs& t, Sha
 #pragma unroll
             for (int ks = 0; ks < 8; ++ks) {
                 constexpr uint32_t kHalf = kHalfBytes >> 4;
-                if (ks < steps) mma_ss(d, qd + (ks >> 2) * kHalf + (ks & 3) * 2, kd + (ks >> 2) * kHalf + (ks & 3) * 2, qk, ks > 0);
+                const uint32_t at = (ks >> 2) * kHalf + (ks & 3) * 2;
+                if (ks < steps) mma_ss(d, qd + at, kd + at, qk, ks > 0);
             }
             tc_commit(&sh->s_full[i]);
         }
@@ -1081,7 +1084,8 @@ constexpr size_t shared_bytes(int dim) {
            (FMT == kKv16Bit ? 0 : (size_t)kRawSlots * kTokens * dim) + kStageBytes<FMT> + sizeof(Shared);
 }
 
-static_assert(1024 * (128 + 2) <= (2 + kSlots<kKvInt8>) * 2 * kHalfBytes && 1024 * (64 + 2) <= (2 + kSlots<kKvInt8>) * kHalfBytes,
+static_assert(1024 * (128 + 2) <= (2 + kSlots<kKvInt8>) * 2 * kHalfBytes &&
+                  1024 * (64 + 2) <= (2 + kSlots<kKvInt8>) * kHalfBytes,
               "a joint part takes the place of Q and the slots");
 static_assert(shared_bytes<kKv16Bit>(128) <= 232448 && shared_bytes<kKvInt8>(128) <= 232448, "227 KB a block");
 

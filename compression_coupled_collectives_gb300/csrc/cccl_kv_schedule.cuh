@@ -10,7 +10,8 @@
 // the GPU evenly, and one sequence's long context is shared by many blocks.
 // An item that a share's end cuts leaves partial results (an unnormalised
 // accumulator, its maximum and its sum for each row) that a second kernel
-// joins, in the order of the line, so that results do not vary.
+// joins, in the order of the line, so that results do not vary.  Few items are
+// instead shared by a cluster of blocks each, which joins their parts itself.
 //
 // The lengths are in device memory, so every block works the division out
 // itself (a few loads a sequence).
@@ -393,7 +394,8 @@ __global__ void __launch_bounds__(kJoinFewThreads) join_rows_kernel(const __grid
 #pragma unroll 4
     for (int i = stride; i < n; i += 4) {
         if (mine) {
-            const float4 x = *reinterpret_cast<const float4*>(parts.acc(first + i, i == 0) + (size_t)row * a.dim + 4 * lane);
+            const float* src = parts.acc(first + i, i == 0) + (size_t)row * a.dim + 4 * lane;
+            const float4 x = *reinterpret_cast<const float4*>(src);
             const float f = sh.weight[r][i];
             v.x += f * x.x;
             v.y += f * x.y;
@@ -514,7 +516,8 @@ cudaError_t launch_clusters(void (*kernel)(Params...), int blocks, int cluster, 
 // Shares that a call can need, at most `most`: the tiles of a batch whose
 // sequences keep to the program's expectations.
 inline int shares_for(const KvArgs& a, const AttnArgs& t, int max_new, int max_len, int rows, int tokens, int most) {
-    const double row_tiles = ((double)max_new * t.group.d + rows - 1) / rows, tiles = ((double)max_len + 2 * tokens - 1) / tokens;
+    const double row_tiles = ((double)max_new * t.group.d + rows - 1) / rows;
+    const double tiles = ((double)max_len + 2 * tokens - 1) / tokens;
     const double all = (double)a.batch * a.kv_heads * row_tiles * tiles;
     return all < most ? (int)all : most;
 }

@@ -74,7 +74,8 @@ typedef struct {
  * whose position is negative (n above kv_lens[b]) is in no page: a write
  * skips it, a read gives zeros, and in attention its position hides every key
  * from it.  kv_lens counts the new tokens, so one batch serves a write and
- * the attention after it. */
+ * the attention after it.  The arrays must not change while a call runs: its
+ * blocks read them more than once and rely on seeing the same. */
 typedef struct {
     const int32_t *page_table; /* device, [batch][table_stride], 4-byte aligned */
     const int32_t *cu_tokens;  /* device, [batch + 1], 4-byte aligned */
