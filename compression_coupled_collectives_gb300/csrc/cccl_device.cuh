@@ -112,7 +112,13 @@ constexpr uint64_t kValueMask = (1ull << 62) - 1;
 // Bounded waits: every spin gives up after kWaitLimitNs of GPU time (read
 // from %globaltimer), records kStatusTimeout and returns; nothing waits
 // forever.
-constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s
+#ifndef CCCL_WAIT_LIMIT_NS
+#define CCCL_WAIT_LIMIT_NS 2000000000ull  // 2 s; a build that tests giving up sets 0: at the first look
+#endif
+constexpr uint64_t kWaitLimitNs = CCCL_WAIT_LIMIT_NS;
+// The same for a block that leaves and waits for what it has itself in flight
+// (copies to its shared memory, products): microseconds unless something is broken.
+constexpr uint64_t kDrainLimitNs = 50000000ull;  // 50 ms
 
 __host__ __device__ constexpr uint64_t pad16(uint64_t x) { return (x + 15) & ~uint64_t(15); }
 __host__ __device__ constexpr uint64_t data_start(uint64_t n_chunks) { return kStreamHeaderBytes + pad16(8 * n_chunks); }
@@ -219,11 +225,12 @@ __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
     return ok != 0;
 }
 
-// Bounded wait for phase `parity` of `bar`; false if kWaitLimitNs ran out.
+// Bounded wait for phase `parity` of `bar`; false if limit_ns ran out.
 // Each try suspends the warp in hardware (up to kSuspendHintNs) until the
 // phase completes, so a waiting warp costs no issue slots.
 constexpr uint32_t kSuspendHintNs = 100000;
-__device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity) {
+__device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, uint64_t limit_ns = kWaitLimitNs) {
+    if (kWaitLimitNs == 0 && limit_ns == 0) return mbar_test(bar, parity);
     const uint32_t a = smem_addr(bar);
     uint64_t t0 = 0;
     for (uint32_t it = 0;; ++it) {
@@ -237,7 +244,7 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity) {
         const uint64_t now = globaltimer_ns();
         if (it == 0)
             t0 = now;
-        else if (now - t0 > kWaitLimitNs)
+        else if (now - t0 > limit_ns)
             return false;
     }
 }

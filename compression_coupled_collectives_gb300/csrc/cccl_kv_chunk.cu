@@ -236,26 +236,29 @@ struct Waiter {
     }
 };
 
-// The walking warp: pieces to the ring, one without tiles at the end; then, for
-// the joining kernel, whether an item is cut at this share's start.
+// The walking warp: pieces to the ring, one without tiles at the end; and, for
+// the joining kernel, whether an item is cut at this share's start (said before
+// anything is waited for: that kernel runs even if this one gives up).
 __device__ __forceinline__ void walk_role(const KvArgs& a, const AttnArgs& t, Shared* sh, Walk w) {
     const Waiter wait{sh, a.ws};
     const int lane = threadIdx.x & 31;
-    Cut cut{0, 0, 0, -1, {}};
     Piece p{};
     for (uint32_t n = 0;; ++n) {
         const uint32_t s = n % kRing, use = n / kRing;
         const bool more = next_piece<kRows, kTokens>(a, t, sh->prefix, w, p);
-        if (n == 0 && more && !w.whole) cut = cut_of<kRows, kTokens>(p, w.line, w.share);
         if (use > 0 && !wait(&sh->piece_free[s], (use - 1) & 1)) return;
         if (lane == 0) {
             sh->ring[s] = p;
             if (!more) sh->ring[s].count = 0;
             mbar_arrive(&sh->piece_full[s]);
         }
-        if (!more) break;
+        if (n == 0 && !w.whole) {
+            Cut cut{0, 0, 0, -1, {}};
+            if (more) cut = cut_of<kRows, kTokens>(p, w.line, w.share);
+            if (lane == 0) part_layout(a, gridDim.x, kRows).cuts[w.share] = cut;
+        }
+        if (!more) return;
     }
-    if (!w.whole && lane == 0) part_layout(a, gridDim.x, kRows).cuts[w.share] = cut;
 }
 // The walking warp where `cluster` blocks share an item: one piece, this block's
 // part of item blockIdx.x / cluster (count 0: none; items of fewer tiles than
@@ -361,13 +364,6 @@ __device__ __forceinline__ void fetch_role(const KvArgs& a, const AttnArgs& t, S
     const int first_row = warp * span + (boxes > 0 ? lane % boxes : 0) * f.box;
     const uint32_t expect = (uint32_t)boxes * (uint32_t)f.box * (slot_bytes / kTokens);
     uint32_t entry = 0, handed = 0;
-    // leaving early: no copy of this warp may still be in flight when the block ends
-    auto leave = [&]() {
-        copy_wait<0>();
-        if (f.box > 0)
-            for (uint32_t k = entry > SLOTS ? entry - SLOTS : 0; k < entry; ++k)
-                mbar_wait(&full[k % SLOTS], (k / SLOTS) & 1);
-    };
     auto hand_over = [&](uint32_t upto) {  // this warp's copies of entries below `upto` are done
         if (handed >= upto) return;
         if (kWide) fence_proxy_async_smem();
@@ -400,7 +396,7 @@ __device__ __forceinline__ void fetch_role(const KvArgs& a, const AttnArgs& t, S
                     // about to wait: hand over what has been brought so far
                     copy_wait<0>();
                     hand_over(entry);
-                    if (!wait(&free_[s], (use - 1) & 1)) return leave();
+                    if (!wait(&free_[s], (use - 1) & 1)) goto leave;
                 }
                 if (tma) {
                     copy_wait<0>();
@@ -431,9 +427,13 @@ __device__ __forceinline__ void fetch_role(const KvArgs& a, const AttnArgs& t, S
             }
         }
     }
+leave:
+    // early or not: no copy of this warp may still be in flight when the block ends
     copy_wait<0>();
     hand_over(entry);
-    if (*reinterpret_cast<volatile uint32_t*>(&sh->stop) != 0) leave();
+    if (f.box > 0)
+        for (uint32_t k = entry > SLOTS ? entry - SLOTS : 0; k < entry; ++k)
+            if (!mbar_wait(&full[k % SLOTS], (k / SLOTS) & 1, kDrainLimitNs)) break;
 }
 
 // 8-bit caches: codes to fp16, four warps of 32 rows each.  A lane takes 16
@@ -520,8 +520,9 @@ __device__ __forceinline__ void widen_role(const KvArgs& a, const AttnArgs& t, S
 }
 
 // ---------------------------------------------------------------- products
+// Returns whether this lane is the one that issued them.
 template <class M, int SLOTS>
-__device__ __forceinline__ void mma_role(const KvArgs& a, const AttnArgs& t, Shared* sh, uint32_t q_base,
+__device__ __forceinline__ bool mma_role(const KvArgs& a, const AttnArgs& t, Shared* sh, uint32_t q_base,
                                          uint32_t slots, uint32_t slot_bytes) {
     const Waiter wait{sh, a.ws};
     const uint32_t tmem = sh->tmem;
@@ -567,9 +568,9 @@ __device__ __forceinline__ void mma_role(const KvArgs& a, const AttnArgs& t, Sha
         const int tiles = live_rows<kRows>(t, p) > kTileRows ? 2 : 1;
         const int32_t count = p.count;
         // K of the first tile
-        if (!wait(&sh->kv_full[entry % SLOTS], (entry / SLOTS) & 1)) return;
+        if (!wait(&sh->kv_full[entry % SLOTS], (entry / SLOTS) & 1)) return leader != 0;
         for (int i = 0; i < tiles; ++i) {
-            if (!wait(&sh->q_full[i], q_phase[i])) return;
+            if (!wait(&sh->q_full[i], q_phase[i])) return leader != 0;
             q_phase[i] ^= 1;
             tc_fence_after();
             product_qk(i, entry % SLOTS);
@@ -579,14 +580,14 @@ __device__ __forceinline__ void mma_role(const KvArgs& a, const AttnArgs& t, Sha
         for (int32_t j = 0; j < count; ++j) {
             const uint32_t v_entry = entry, k_entry = entry + 1;
             const bool more = j + 1 < count;
-            if (!wait(&sh->kv_full[v_entry % SLOTS], (v_entry / SLOTS) & 1)) return;
+            if (!wait(&sh->kv_full[v_entry % SLOTS], (v_entry / SLOTS) & 1)) return leader != 0;
             for (int i = 0; i < tiles; ++i) {
-                if (!wait(&sh->p_full[i], p_phase[i])) return;
+                if (!wait(&sh->p_full[i], p_phase[i])) return leader != 0;
                 p_phase[i] ^= 1;
                 tc_fence_after();
                 product_pv(i, v_entry % SLOTS, j > 0);
                 if (more) {
-                    if (i == 0 && !wait(&sh->kv_full[k_entry % SLOTS], (k_entry / SLOTS) & 1)) return;
+                    if (i == 0 && !wait(&sh->kv_full[k_entry % SLOTS], (k_entry / SLOTS) & 1)) return leader != 0;
                     product_qk(i, k_entry % SLOTS);
                 } else {
                     commit(&sh->o_full[i]);
@@ -597,6 +598,7 @@ __device__ __forceinline__ void mma_role(const KvArgs& a, const AttnArgs& t, Sha
             entry += more ? 2 : 1;
         }
     }
+    return leader != 0;
 }
 
 // ---------------------------------------------------------------- softmax
@@ -1033,6 +1035,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         float* const joint = reinterpret_cast<float*>(raw + (base - smem_addr(raw)));
         softmax_role<T, FMT>(a, t, sh, base + (warp / 4) * tile_bytes, raw_codes + raw_bytes,
                              CLUSTERS && cluster > 1 ? joint : nullptr);
+        copy_wait<0>();  // of Q, where the role gave up
         if (CLUSTERS && cluster > 1) {
             __syncwarp();
             cluster_sync();
@@ -1050,12 +1053,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLoaderRegs));
         if (warp == 12) {
-            mma_role<Operand<T, FMT>, kN>(a, t, sh, base, slots, tile_bytes);
+            const bool issued = mma_role<Operand<T, FMT>, kN>(a, t, sh, base, slots, tile_bytes);
             __syncwarp();
-            if (threadIdx.x == 12 * 32) {  // every product is done before TMEM goes
-                tc_commit(&sh->drained);
-                wait_long(sh, a.ws, &sh->drained, 0);
-            }
+            // every product is done before TMEM goes (the thread that issued them says so)
+            if (issued) tc_commit(&sh->drained);
+            mbar_wait(&sh->drained, 0, kDrainLimitNs);
         } else if (warp != 14 && FMT != kKv16Bit) {  // 13 and 15
             fetch_role<FMT, 2, kRawSlots>(a, t, sh, fetch, (warp - 13) / 2, raw_codes, kTokens * a.dim, sh->raw_full,
                                           sh->raw_free);
