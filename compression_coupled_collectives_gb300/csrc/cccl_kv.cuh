@@ -126,21 +126,6 @@ __device__ __forceinline__ uint32_t round_pair(float lo, float hi) {
     return (uint32_t)T::round(lo) | ((uint32_t)T::round(hi) << 16);
 }
 
-// The binary32 value of an 8-bit code (NaN for E4M3's two NaN codes).
-template <int FMT>
-__device__ __forceinline__ float code_value(uint8_t c) {
-    if (FMT == kKvInt8) return (float)(int8_t)c;
-    __nv_fp8_e4m3 e;
-    e.__x = c;
-    return (float)e;
-}
-// Value i of a stored vector, without its scale.
-template <class T, int FMT>
-__device__ __forceinline__ float stored_value(const uint8_t* vec, int i) {
-    if (FMT == kKv16Bit) return T::load(reinterpret_cast<const uint16_t*>(vec)[i]);
-    return code_value<FMT>(vec[i]);
-}
-
 __device__ __forceinline__ float warp_sum(float x) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, o);
@@ -231,63 +216,133 @@ template <int N>
 __device__ __forceinline__ void copy_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
+// 4 stored values (8 or 4 bytes) as binary32, without their scale.
+template <int FMT>
+__device__ __forceinline__ uint2 load_stored4(const uint8_t* p) {
+    if (FMT == kKv16Bit) return *reinterpret_cast<const uint2*>(p);
+    return make_uint2(*reinterpret_cast<const uint32_t*>(p), 0);
+}
+template <class T, int FMT>
+__device__ __forceinline__ float4 stored4_values(uint2 x) {
+    if (FMT == kKv16Bit)
+        return make_float4(T::load((uint16_t)(x.x & 0xFFFFu)), T::load((uint16_t)(x.x >> 16)),
+                           T::load((uint16_t)(x.y & 0xFFFFu)), T::load((uint16_t)(x.y >> 16)));
+    uint32_t lo, hi;
+    expand4_in_order<FMT>(x.x, lo, hi);
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&lo));
+    const float2 g = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+    return make_float4(f.x, f.y, g.x, g.y);
+}
 // One row of attention by one warp, straight from the definition: a pass for
-// the maximum, one for the sum of the exponentials, one for the values with
-// their normalised weights (so that no sum passes the values' own size),
-// visible keys only, IEEE arithmetic throughout (a NaN or an infinity among the visible values goes where the
-// formula takes it, one in a hidden place goes nowhere).  The tensor-core
-// kernels compute hidden places as products with zero, which is not the same
-// when such a place holds a NaN or an infinity; they send the rows whose sums
-// come out non-finite through here.
-// Lane l holds values l, l + 32, l + 64, l + 96 of the head.
+// the maximum and the sum of the exponentials, one for the values with their
+// normalised weights (so that no sum passes the values' own size), visible keys
+// only, IEEE arithmetic throughout (a NaN or an infinity among the visible
+// values goes where the formula takes it, one in a hidden place goes nowhere).
+// The tensor-core kernels compute hidden places as products with zero, which is
+// not the same when such a place holds a NaN or an infinity; they send the rows
+// whose sums come out non-finite through here, where nothing waits for them.
+// 32 keys at a time: every lane looks one up and owns its score.  A key's
+// channels lie across the warp, 4 a lane; the loads of 4 keys are in flight.
+// (Registers are few here: the kernels' own count must not grow by this.)
 template <class T, int FMT>
 __device__ __noinline__ void attend_row(const KvArgs& a, const AttnArgs& t, int b, int32_t len, int64_t row,
                                         int32_t pos, int head) {
+    constexpr uint32_t kAll = 0xFFFFFFFFu;
+    constexpr int kFlight = 4;
     const int lane = threadIdx.x & 31;
     const int kv_head = (int)div_by(t.group, (uint32_t)head);
-    const uint16_t* q = reinterpret_cast<const uint16_t*>(t.q + row * t.q_token + (int64_t)head * t.q_head);
-    float qv[4], acc[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) qv[i] = lane + 32 * i < a.dim ? T::load(q[lane + 32 * i]) : 0.f;
+    const bool inside = 4 * lane < a.dim;
+    const uint32_t column = (FMT == kKv16Bit ? 8 : 4) * lane;
+    float4 q = make_float4(0.f, 0.f, 0.f, 0.f), acc = q;
+    if (inside)
+        q = stored4_values<T, kKv16Bit>(load_stored4<kKv16Bit>(t.q + row * t.q_token + (int64_t)head * t.q_head + 8 * lane));
     int32_t first, last;
     visible_range(t, len, pos, first, last);
-    float m = -INFINITY, sum = 0.f;
-    for (int pass = 0; pass < 3; ++pass) {
-        for (int32_t j = first; j < last; ++j) {
-            int64_t at, scale_at;
-            const bool there = slot_of(a, b, (uint32_t)j, at, scale_at);
-            float s = 0.f, kscale = 1.f, vscale = 1.f;
-            if (there) {
-                const uint8_t* kv = a.k + at + (int64_t)kv_head * a.head_stride;
+    float m = -INFINITY, sum = 0.f;  // of this lane's keys; then of all
+#pragma unroll 1
+    for (int pass = 0; pass < 2; ++pass) {
+#pragma unroll 1
+        for (int32_t base = first; base < last; base += 32) {
+            const bool seen = lane < last - base;
+            int64_t at = 0, scale_at = 0;
+            const bool there = seen && slot_of(a, b, (uint32_t)(base + lane), at, scale_at);
+            at += (int64_t)kv_head * a.head_stride;
+            float kscale = 1.f, vscale = 1.f, s = 0.f;
+            if (FMT != kKv16Bit && there) {
+                kscale = a.k_scale[scale_at + (int64_t)kv_head * a.s_head];
+                vscale = a.v_scale[scale_at + (int64_t)kv_head * a.s_head];
+            }
+            const uint32_t real = __ballot_sync(kAll, there);
+#pragma unroll 1
+            for (int i = 0; i < 32; i += kFlight) {
+                uint2 x[kFlight];
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (lane + 32 * i < a.dim) s += qv[i] * stored_value<T, FMT>(kv, lane + 32 * i);
-                if (FMT != kKv16Bit) {
-                    kscale = a.k_scale[scale_at + (int64_t)kv_head * a.s_head];
-                    vscale = a.v_scale[scale_at + (int64_t)kv_head * a.s_head];
+                for (int k = 0; k < kFlight; ++k) {
+                    const int64_t from = __shfl_sync(kAll, at, i + k);
+                    x[k] = make_uint2(0, 0);
+                    if (inside && (real >> (i + k) & 1u) != 0) x[k] = load_stored4<FMT>(a.k + from + column);
+                }
+#pragma unroll
+                for (int k = 0; k < kFlight; ++k) {
+                    const float4 y = stored4_values<T, FMT>(x[k]);
+                    float dot = q.x * y.x;
+                    dot += q.y * y.y;
+                    dot += q.z * y.z;
+                    dot += q.w * y.w;
+                    dot = warp_sum(dot);
+                    if (lane == i + k && there) s = dot;  // (else 0, also where the query is infinite)
                 }
             }
-            s = warp_sum(s) * kscale * t.scale;
+            s *= kscale * t.scale;
             if (pass == 0) {
-                m = (s > m || s != s) ? s : m;  // keeps a NaN: no later s compares above it
-                if (m != m) break;
-            } else if (pass == 1) {
-                sum += expf(s - m);
-            } else {
-                const float p = expf(s - m) / sum;
-                if (there) {
-                    const uint8_t* vv = a.v + at + (int64_t)kv_head * a.head_stride;
+                if (seen) {
+                    const float to = (s > m || s != s) ? s : m;  // keeps a NaN: no later s compares above it
+                    const float from = to == -INFINITY ? 0.f : to;
+                    sum = sum * expf(m - from) + expf(s - from);
+                    m = to;
+                }
+                continue;
+            }
+            const float p = seen ? expf(s - m) / sum : 0.f;
+#pragma unroll 1
+            for (int i = 0; i < 32; i += kFlight) {
+                uint2 x[kFlight];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (lane + 32 * i < a.dim) acc[i] += p * (stored_value<T, FMT>(vv, lane + 32 * i) * vscale);
+                for (int k = 0; k < kFlight; ++k) {
+                    const int64_t from = __shfl_sync(kAll, at, i + k);
+                    x[k] = make_uint2(0, 0);
+                    if (inside && (real >> (i + k) & 1u) != 0) x[k] = load_stored4<FMT>(a.v + from + column);
+                }
+#pragma unroll
+                for (int k = 0; k < kFlight; ++k) {
+                    const float weight = __shfl_sync(kAll, p, i + k), scale = __shfl_sync(kAll, vscale, i + k);
+                    if ((real >> (i + k) & 1u) != 0) {
+                        const float4 y = stored4_values<T, FMT>(x[k]);
+                        acc.x += weight * (y.x * scale);
+                        acc.y += weight * (y.y * scale);
+                        acc.z += weight * (y.z * scale);
+                        acc.w += weight * (y.w * scale);
+                    }
                 }
             }
         }
-    }
-    uint16_t* out = reinterpret_cast<uint16_t*>(t.out + row * t.o_token + (int64_t)head * t.o_head);
+        if (pass == 0) {  // all lanes' keys together
+            const float own = m;
+            const bool odd = __any_sync(kAll, own != own) != 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        if (lane + 32 * i < a.dim) out[lane + 32 * i] = T::round(acc[i]);
+            for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, o));
+            sum = warp_sum(sum * expf(own - (m == -INFINITY ? 0.f : m)));
+            // scores of -infinity alone are 0 / 0, as in the formula
+            if (odd || sum != sum || (m == -INFINITY && last > first)) {  // no weight is a number
+                m = sum = __uint_as_float(0x7FC00000u);
+                acc = make_float4(m, m, m, m);
+                break;
+            }
+        }
+    }
+    if (inside)
+        *reinterpret_cast<uint2*>(t.out + row * t.o_token + (int64_t)head * t.o_head + 8 * lane) =
+            make_uint2(round_pair<T>(acc.x, acc.y), round_pair<T>(acc.z, acc.w));
     if (t.lse != nullptr && lane == 0) t.lse[row * t.q_heads + head] = last > first ? m + logf(sum) : -INFINITY;
 }
 

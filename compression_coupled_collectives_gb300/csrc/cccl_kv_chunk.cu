@@ -85,6 +85,7 @@ struct Shared {
     uint64_t drained;
     uint32_t tmem;
     uint32_t stop;  // a bounded wait ran out: every role leaves
+    uint32_t odd;   // a row that the block wrote came out non-finite
     uint32_t prefix[kMaxBatch + 1];
     // One warp walks along the line and hands the pieces on; every other warp
     // takes a copy (softmax warps keep two, this piece and the next, here rather
@@ -795,10 +796,7 @@ __device__ __forceinline__ void softmax_role(const KvArgs& a, const AttnArgs& t,
             if (full) {
                 if (is_row && t.lse != nullptr)
                     t.lse[at.token * t.q_heads + at.head] = none ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
-                for (uint32_t todo = __ballot_sync(0xFFFFFFFFu, odd && is_row); todo != 0; todo &= todo - 1) {
-                    __syncwarp();
-                    fix_row<T, FMT>(a, t, cur, kRows, i * kTileRows + 32 * warp + __ffs(todo) - 1);
-                }
+                if (odd && is_row) *reinterpret_cast<volatile uint32_t*>(&sh->odd) = 1;
             } else if (is_row) {
                 stats[tile_row] = m;
                 stats[kRows + tile_row] = l;
@@ -929,9 +927,6 @@ __device__ __forceinline__ void join_item(const KvArgs& a, const AttnArgs& t, Sh
     constexpr int kJoinRows = kRows / PARTS;
     const int row0 = (int)cluster_rank() * kJoinRows, live = live_rows<kRows>(t, p);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    uint32_t* odd_rows = sh->prefix;  // no longer needed: 32 rows an entry
-    if (threadIdx.x < kRows / 32) odd_rows[threadIdx.x] = 0;
-    asm volatile("bar.sync 1, 256;" ::: "memory");
 #pragma unroll 1
     for (int u = warp; u < kJoinRows / 32 * (a.dim / 16); u += 8) {
         const int band = u % (kJoinRows / 32), d = 16 * (u / (kJoinRows / 32)), row = row0 + 32 * band + lane;
@@ -962,11 +957,43 @@ __device__ __forceinline__ void join_item(const KvArgs& a, const AttnArgs& t, Sh
         }
         bool odd = store_row_part<T>(t, p, kRows, row, d, v, m, sum);
         odd |= store_row_part<T>(t, p, kRows, row, d + 8, v + 8, m, sum);
-        if (odd) atomicOr(&odd_rows[band], 1u << lane);
+        if (odd) *reinterpret_cast<volatile uint32_t*>(&sh->odd) = 1;
     }
-    asm volatile("bar.sync 1, 256;" ::: "memory");
-    for (int r = warp; r < kJoinRows; r += 8)
-        if (odd_rows[r / 32] >> (r % 32) & 1) fix_row<T, FMT>(a, t, p, kRows, row0 + r);
+}
+
+// The same warps, when their part in the pipeline is over and some row came out
+// non-finite: the rows that the block wrote are looked through and those worked out
+// again.  (Not between two pieces: a row's keys are gone through by one warp, and
+// no bounded wait may span that.)  Rows from + warp, + 8 and so on, below `to`.
+template <class T, int FMT>
+__device__ __forceinline__ void repair_rows(const KvArgs& a, const AttnArgs& t, const Piece& p, int from, int to) {
+    constexpr uint32_t kExponent = T::kHalf ? 0x7C00u : 0x7F80u;
+    const int lane = threadIdx.x & 31, end = min(to, live_rows<kRows>(t, p));
+    for (int row = from + (threadIdx.x >> 5); row < end; row += 8) {
+        const RowPlace at = row_place(t, p, kRows, row);
+        const uint16_t* out =
+            reinterpret_cast<const uint16_t*>(t.out + at.token * t.o_token + (int64_t)at.head * t.o_head);
+        bool odd = false;
+        for (int d = lane; d < a.dim; d += 32) odd |= (out[d] & kExponent) == kExponent;
+        if (__any_sync(0xFFFFFFFFu, odd)) fix_row<T, FMT>(a, t, p, kRows, row);
+    }
+}
+// cluster: the blocks that share an item, or 1.
+template <class T, int FMT>
+__device__ __noinline__ void repair_role(const KvArgs& a, const AttnArgs& t, Shared* sh, int whole, int cluster) {
+    Piece p;
+    if (cluster > 1) {
+        p = sh->ring[0];
+        const int rank = (int)cluster_rank(), rows = kRows / cluster;
+        if (parts_of(p, cluster) > 1)
+            repair_rows<T, FMT>(a, t, p, rank * rows, (rank + 1) * rows);
+        else if (p.count > 0)
+            repair_rows<T, FMT>(a, t, p, 0, kRows);
+        return;
+    }
+    Walk w = make_walk(sh->prefix[a.batch], blockIdx.x, gridDim.x, whole);
+    while (next_piece<kRows, kTokens>(a, t, sh->prefix, w, p))
+        if (p.count == p.range.n) repair_rows<T, FMT>(a, t, p, 0, kRows);  // cut items: where they are joined
 }
 
 // how: whether items are left whole (0: they are cut at shares' ends); with
@@ -1013,7 +1040,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&sh->piece_free[i], FMT == kKv16Bit ? 13 : 15);  // the warps that take pieces
         }
         mbar_init(&sh->drained, 1);
-        sh->stop = 0;
+        sh->stop = sh->odd = 0;
         fence_mbar_init();
     }
     int cluster = 1;
@@ -1036,14 +1063,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         softmax_role<T, FMT>(a, t, sh, base + (warp / 4) * tile_bytes, raw_codes + raw_bytes,
                              CLUSTERS && cluster > 1 ? joint : nullptr);
         copy_wait<0>();  // of Q, where the role gave up
+        __syncwarp();
         if (CLUSTERS && cluster > 1) {
-            __syncwarp();
             cluster_sync();
             if (cluster == 2)
                 join_item<T, FMT, 2>(a, t, sh, base);
             else
                 join_item<T, FMT, 4>(a, t, sh, base);
+            __syncwarp();
         }
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+        if (sh->odd != 0 && sh->stop == 0) repair_role<T, FMT>(a, t, sh, CLUSTERS ? 1 : how, cluster);
     } else if (warp < 12) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLoaderRegs));
         if constexpr (FMT == kKv16Bit)
