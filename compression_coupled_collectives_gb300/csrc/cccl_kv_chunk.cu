@@ -17,9 +17,9 @@
 //
 // With ref_i a row's reference, x_ij = s_ij scale log2(e) and p_ij =
 // 2^(x_ij - ref_i), a row's result is sum_j p_ij v_j / sum_j p_ij for any ref_i.
-// So the reference is only moved to the row's maximum when a score exceeds it
-// by more than 8 (the accumulator is then rescaled in TMEM): binary32 sums and
-// 16-bit probabilities hold a factor of 256.  The products of one thread execute
+// So the reference is only moved when a score exceeds it by more than some slack
+// (the accumulator is then rescaled in TMEM): binary32 sums and 16-bit
+// probabilities hold that factor (kSlack, kLower).  The products of one thread execute
 // in order, so a full S also means that the previous O is done, and S may be
 // written over the P that the product before it reads.
 //
@@ -61,7 +61,17 @@ constexpr int kLoaderWarps = 4;
 constexpr int kMostSlots = 4, kRawSlots = 3;
 template <int FMT>
 constexpr int kSlots = FMT == kKv16Bit ? 4 : 3;
-constexpr float kSlack = 8.f;    // base 2
+// How far (base 2) a row's reference lies below its maximum when it is set, and
+// how far the maximum may then rise before it is set again.  fp16 holds 2^-24 to
+// 2^16: with 9 (8 where the value's scale adds up to 1) and 6 a probability is off
+// by 2^-34 (2^-33) of the largest at most, apart from its rounding to 11 bits.
+// Setting it again costs, a lower reference saves bits: with a slack of 4, 6 and 8
+// 5 x 2048 windowed INT8 chunks took 760, 750 and 745 us, 2048 fp16 tokens over
+// 16384 379, 368 and 368.  bf16 has binary32's range.  Operand M:
+template <class M>
+constexpr float kSlack = M::kHalf ? 6.f : 8.f;
+template <class M, int FMT>
+constexpr float kLower = !M::kHalf ? 0.f : FMT == kKv16Bit ? 9.f : 8.f;
 // Halves of result rows (128 bytes) that a softmax warp has on their way out at
 // a time
 template <int FMT>
@@ -714,6 +724,7 @@ __device__ __forceinline__ uint32_t bits_below(int32_t n) {
 template <class T, int FMT>
 __device__ __forceinline__ void softmax_role(const KvArgs& a, const AttnArgs& t, Shared* sh, uint32_t q_tile,
                                              uint32_t stages, float* joint) {
+    using M = Operand<T, FMT>;
     const int i = threadIdx.x / 128, row = threadIdx.x % 128, warp = row >> 5, lane = row & 31;
     const int me = threadIdx.x >> 5;
     const Waiter wait{sh, a.ws};
@@ -862,9 +873,10 @@ __device__ __forceinline__ void softmax_role(const KvArgs& a, const AttnArgs& t,
                 const uint4 v = *reinterpret_cast<const uint4*>(sh->v_top[scale_slot]);
                 top += scale_exponent(max(max(v.x, v.y), max(v.z, v.w)));
             }
+            top -= kLower<M, FMT>;
             if (j == 0) {
                 m = top;
-            } else if (__any_sync(0xFFFFFFFFu, top > m + kSlack)) {
+            } else if (__any_sync(0xFFFFFFFFu, top > m + kSlack<M>)) {
                 const float to = fmaxf(m, top);
                 const float f = to == -INFINITY ? 1.f : exp2_fast(m - to);
                 m = to;
@@ -901,8 +913,8 @@ __device__ __forceinline__ void softmax_role(const KvArgs& a, const AttnArgs& t,
                         x = mul2(x, f[k]);
                         y = mul2(y, f[k + 1]);
                     }
-                    pr[i0 / 2] = pack<Operand<T, FMT>>(x.x, x.y);
-                    pr[i0 / 2 + 1] = pack<Operand<T, FMT>>(y.x, y.y);
+                    pr[i0 / 2] = pack<M>(x.x, x.y);
+                    pr[i0 / 2 + 1] = pack<M>(y.x, y.y);
                 }
                 if (c % 64 == 32) tc_store32(at_s + (c / 64) * 32, pr + (c / 64) * 32);
             }

@@ -28,7 +28,8 @@
 //
 // Precision: products of 16-bit values are exact and summed in binary32.  A
 // probability enters the second product as the sum of two 16-bit values (high
-// part and remainder), so nothing is rounded before the result.  8-bit codes
+// part and remainder): 16 bits of it with bf16, 22 with fp16 (see kLower), far
+// more than the result keeps.  8-bit codes
 // are exact in fp16; the key's scale multiplies the score and the value's scale
 // the probability, both in binary32.
 #include <algorithm>
@@ -110,6 +111,11 @@ struct Shape {
     using M = typename std::conditional<FMT_ == kKv16Bit, T_, HfType>::type;  // the products' operands
     static constexpr int FMT = FMT_, DP = DP_, NR = NR_;
     static constexpr int kRows = 8 * NR;
+    // The reference lies this much (base 2) below the row's maximum.  fp16 ends at
+    // 2^-24: the largest probability is made 2^14 (times a value's scale, at most
+    // 2^15), so that those down to 2^-28 of it keep 22 bits in their two parts and
+    // none is off by more than 2^-39 of it.  bf16 has binary32's range.
+    static constexpr float kLower = M::kHalf ? 14.f : 0.f;
     static constexpr int kElem = FMT == kKv16Bit ? 2 : 1;
     static constexpr int kRowBytes = DP * kElem;                      // 64, 128 or 256
     static constexpr int kTokens = kRowBytes == 256 ? 16 : 32;        // tokens of a warp's stage
@@ -404,7 +410,7 @@ __device__ __forceinline__ void step(uint32_t stage, int32_t base, const uint32_
             m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 4));
             m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 8));
             m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 16));
-            m = fmaxf(st.m[nr][i], m + extra);
+            m = fmaxf(st.m[nr][i], m + extra - S::kLower);
             moved |= m != st.m[nr][i];
             const float from = m == -INFINITY ? 0.f : m;  // nothing seen so far: every term is 0
             keep[nr][i] = exp2_fast(st.m[nr][i] - from);

@@ -135,9 +135,12 @@ cccl_status cccl_kv_read(const cccl_kv_cache *h_cache, const cccl_kv_batch *h_ba
  * Scores, maxima, sums and accumulators are binary32; 16-bit operands enter
  * the tensor cores as they are, 8-bit codes exactly (their scales are applied
  * in binary32), queries for 8-bit caches exactly down to 2^-29 of a row's
- * largest value.  Calls with few rows a kv head round nothing else before the
- * result; others round each probability once to 16 bits.  The same call gives
- * the same bits.  d_out may not overlap d_q or the cache.
+ * largest value.  A probability meets the values with 16 bits or more in calls
+ * with few rows a kv head, rounded once to 16-bit floating point in others;
+ * over fp16 and 8-bit caches that is fp16, whose smallest step is off by up to
+ * 2^-39 (few rows) or 2^-33 (others) of the row's largest probability times the
+ * largest value scale.  The same call gives the same bits.  d_out may not
+ * overlap d_q or the cache.
  * Returns INVALID_ARG, CUDA or OK. */
 cccl_status cccl_kv_attention(const cccl_kv_cache *h_cache, const cccl_kv_batch *h_batch, const void *d_q, int q_heads,
                               int64_t q_token_stride, int64_t q_head_stride, float scale, int causal, int64_t window,
