@@ -188,16 +188,18 @@ __device__ __forceinline__ uint32_t scaled_pair(uint32_t w, float power) {
     const __half2 h = __floats2half2_rn(T::load((uint16_t)(w & 0xFFFFu)) * power, T::load((uint16_t)(w >> 16)) * power);
     return *reinterpret_cast<const uint32_t*>(&h);
 }
-// Probabilities times the value's scale: the running maximum of a row's scores
-// is taken with the exponent of the largest value scale of the same tokens, so
-// that exp2(s - reference) * scale stays in fp16's range whatever the scales'
-// size.  The quotient does not depend on the reference.  Limited so that the
-// sum of exp2(s - reference) stays in binary32's range: scales below 2^-100
-// may lose what lies below 2^-124, scales above 2^60 can overflow fp16 (such
-// rows come out non-finite and are worked out by attend_row).
-__device__ __forceinline__ float scale_exponent(uint32_t largest_scale_bits) {
-    const int e = (int)(largest_scale_bits >> 23) - 127;
-    return (float)min(max(e, -100), 60);
+// Probabilities meet their value's scale before they go to fp16, so a row's
+// reference follows the largest of 2^s_j |scale_j| over the keys that it sees,
+// whatever other keys' scales are: the largest product is then near the top of
+// fp16's range.  The quotient does not depend on the reference.  This is
+// log2 |scale_j| but for 0.09 (the fraction's bits taken for its logarithm);
+// limited, so that the sum of 2^(s_j - reference) stays in binary32's range, to
+// -90 (smaller scales may lose bits, zeros do not matter) and 100 (products of
+// larger ones can overflow fp16: such rows come out non-finite and are worked out
+// by attend_row).  lower: taken off.
+__device__ __forceinline__ uint32_t scale_bits(float scale) { return __float_as_uint(scale) & 0x7FFFFFFFu; }
+__device__ __forceinline__ float scale_log2(uint32_t bits, float lower = 0.f) {
+    return fminf(fmaxf(fmaf((float)bits, 0x1p-23f, -127.f - lower), -90.f - lower), 100.f - lower);
 }
 
 __device__ __forceinline__ float exp2_fast(float x) {

@@ -63,15 +63,21 @@ template <int FMT>
 constexpr int kSlots = FMT == kKv16Bit ? 4 : 3;
 // How far (base 2) a row's reference lies below its maximum when it is set, and
 // how far the maximum may then rise before it is set again.  fp16 holds 2^-24 to
-// 2^16: with 9 (8 where the value's scale adds up to 1) and 6 a probability is off
-// by 2^-34 (2^-33) of the largest at most, apart from its rounding to 11 bits.
-// Setting it again costs, a lower reference saves bits: with a slack of 4, 6 and 8
-// 5 x 2048 windowed INT8 chunks took 760, 750 and 745 us, 2048 fp16 tokens over
-// 16384 379, 368 and 368.  bf16 has binary32's range.  Operand M:
+// 2^16: with 9 and 6 (and 0.09 for scale_log2) a probability is off by 2^-34 of the
+// largest at most, apart from its rounding to 11 bits; kSpread may take 4 bits.
+// Setting it again costs, a lower reference saves bits: with 7 and 8 5 x 2048
+// windowed INT8 chunks took 707 us for 710, 4096 E4M3 tokens over 32768 1893 for
+// 1908, 2048 fp16 tokens over 16384 357 for 364.  bf16 has binary32's range.
+// Operand M:
 template <class M>
 constexpr float kSlack = M::kHalf ? 6.f : 8.f;
-template <class M, int FMT>
-constexpr float kLower = !M::kHalf ? 0.f : FMT == kKv16Bit ? 9.f : 8.f;
+template <class M>
+constexpr float kLower = M::kHalf ? 9.f : 0.f;
+// 8-bit caches: where the value scales of 32 rows, and the largest of the tile's
+// four such groups, lie within a factor of 4 (a difference of scale_bits; zeros
+// do not count), the largest stands for all in a row's reference, which then lies
+// up to 4 too high.  Every tile the exact way: 1012 us for 723.
+constexpr uint32_t kSpread = 2u << 23;
 // Halves of result rows (128 bytes) that a softmax warp has on their way out at
 // a time
 template <int FMT>
@@ -104,7 +110,9 @@ struct Shared {
     uint64_t piece_full[kRing], piece_free[kRing];
     alignas(16) float k_scale[kScaleSlots][kTokens];
     alignas(16) float v_scale[kScaleSlots][kTokens];
-    alignas(16) uint32_t v_top[kScaleSlots][kLoaderWarps];  // the largest value scale of each warp's rows
+    // the largest value scale of each warp's rows (scale_bits), its lowest bit
+    // instead saying whether others of them lie far below
+    alignas(16) uint32_t v_top[kScaleSlots][kLoaderWarps];
 };
 
 // ---------------------------------------------------------------- tcgen05
@@ -142,19 +150,17 @@ __device__ __forceinline__ void tc_load16(uint32_t at, uint32_t* r) {
         : CCCL_R4(r, 0), CCCL_R4(r, 4), CCCL_R4(r, 8), CCCL_R4(r, 12)
         : "r"(at));
 }
+__device__ __forceinline__ void tc_load8(uint32_t at, uint32_t* r) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : CCCL_R4(r, 0), CCCL_R4(r, 4)
+                 : "r"(at));
+}
 __device__ __forceinline__ void tc_store32(uint32_t at, const uint32_t* r) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,"
         "%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::CCCL_W4(r, 0),
         CCCL_W4(r, 4), CCCL_W4(r, 8), CCCL_W4(r, 12), CCCL_W4(r, 16), CCCL_W4(r, 20), CCCL_W4(r, 24), CCCL_W4(r, 28),
         "r"(at)
-        : "memory");
-}
-__device__ __forceinline__ void tc_store16(uint32_t at, const uint32_t* r) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::CCCL_W4(
-            r, 0),
-        CCCL_W4(r, 4), CCCL_W4(r, 8), CCCL_W4(r, 12), "r"(at)
         : "memory");
 }
 #undef CCCL_R4
@@ -508,8 +514,9 @@ __device__ __forceinline__ void widen_role(const KvArgs& a, const AttnArgs& t, S
                 const uint32_t n = (entry / 2) % kScaleSlots;
                 sh->k_scale[n][32 * warp + lane] = scales.k;
                 sh->v_scale[n][32 * warp + lane] = scales.v;
-                const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(scales.v));
-                if (lane == 0) sh->v_top[n][warp] = top;
+                const uint32_t bits = scale_bits(scales.v), top = __reduce_max_sync(0xFFFFFFFFu, bits);
+                const bool far = __any_sync(0xFFFFFFFFu, bits != 0 && top - bits > kSpread);
+                if (lane == 0) sh->v_top[n][warp] = (top & ~1u) | (far ? 1u : 0u);
             }
             if (j + 1 < p.count) scales = row_scales(a, p, base + (j + 1) * kTokens);
 #pragma unroll 1
@@ -716,6 +723,12 @@ __device__ __forceinline__ void load_scales(uint32_t at, float2* f) {
                      : "r"(at + 8 * k));
 }
 
+// Whether a tile's value scales lie further apart than kSpread; v: its v_top.
+__device__ __forceinline__ bool scales_apart(const uint4& v) {
+    const uint32_t most = max(max(v.x, v.y), max(v.z, v.w));
+    return ((v.x | v.y | v.z | v.w) & 1u) != 0 || (v.x != 0 && most - v.x > kSpread) ||
+           (v.y != 0 && most - v.y > kSpread) || (v.z != 0 && most - v.z > kSpread) || (v.w != 0 && most - v.w > kSpread);
+}
 // n low bits set (0 for n <= 0, all for n >= 32)
 __device__ __forceinline__ uint32_t bits_below(int32_t n) {
     return n <= 0 ? 0u : (n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u);
@@ -869,25 +882,44 @@ __device__ __forceinline__ void softmax_role(const KvArgs& a, const AttnArgs& t,
                 top1 = max3(top1, __uint_as_float(s[c + 2]), __uint_as_float(s[c + 3]));
             }
             float top = fmaxf(top0, top1) * to_base2;
+            uint4 v{};
             if (FMT != kKv16Bit) {
-                const uint4 v = *reinterpret_cast<const uint4*>(sh->v_top[scale_slot]);
-                top += scale_exponent(max(max(v.x, v.y), max(v.z, v.w)));
+                v = *reinterpret_cast<const uint4*>(sh->v_top[scale_slot]);
+                top += scale_log2(max(max(v.x, v.y), max(v.z, v.w)));
             }
-            top -= kLower<M, FMT>;
+            const bool move = j == 0 || __any_sync(0xFFFFFFFFu, top > m + (kSlack<M> + kLower<M>));
+            // 8-bit caches: so far a bound of what the tile adds at most; what it is
+            // exactly is only looked for where the reference would follow it
+            if (FMT != kKv16Bit && move && scales_apart(v)) {
+                top = -INFINITY;
+#pragma unroll 1
+                for (int c = 0; c < kTokens; c += 8) {
+                    uint32_t o[8];  // S again: few registers
+                    tc_load8(at_s + c, o);
+                    tc_wait_load();
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const float x = __uint_as_float(o[k]) * sh->k_scale[scale_slot][c + k];
+                        const float y = fmaf(x, to_base2, scale_log2(scale_bits(sh->v_scale[scale_slot][c + k])));
+                        if (base + c + k >= first && base + c + k < last) top = fmaxf(top, y);
+                    }
+                }
+            }
             if (j == 0) {
-                m = top;
-            } else if (__any_sync(0xFFFFFFFFu, top > m + kSlack<M>)) {
-                const float to = fmaxf(m, top);
+                m = top - kLower<M>;
+            } else if (move) {
+                const float to = fmaxf(m, top - kLower<M>);
                 const float f = to == -INFINITY ? 1.f : exp2_fast(m - to);
                 m = to;
                 l *= f;
-                for (int c = 0; c < a.dim; c += 16) {
-                    uint32_t o[16];
-                    tc_load16(at_o + c, o);
+#pragma unroll 1
+                for (int c = 0; c < a.dim; c += 32) {  // (128 columns are its own at any dim)
+                    uint32_t o[32];
+                    tc_load32(at_o + c, o);
                     tc_wait_load();
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-                    tc_store16(at_o + c, o);
+                    for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                    tc_store32(at_o + c, o);
                 }
             }
             const float from = m == -INFINITY ? 0.f : -m;

@@ -361,9 +361,8 @@ __device__ __forceinline__ void step(uint32_t stage, int32_t base, const uint32_
     constexpr int MT = S::kTokens / 16;
     float s[MT][S::NR][4];
     scores<S>(stage, q, s);
-    float vscale[MT][2], extra = 0.f;
+    float vscale[MT][2], vlog[MT][2];
     if (S::FMT != kKv16Bit) {
-        uint32_t top = 0;
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -371,14 +370,13 @@ __device__ __forceinline__ void step(uint32_t stage, int32_t base, const uint32_
                 const uint32_t at = stage + 2 * S::kSide + 4 * (16 * mt + 8 * h + g);
                 const float ks = lds4(at);
                 vscale[mt][h] = lds4(at + 4 * S::kTokens);
-                top = max(top, __float_as_uint(vscale[mt][h]));
+                vlog[mt][h] = scale_log2(scale_bits(vscale[mt][h]), S::kLower);
 #pragma unroll
                 for (int nr = 0; nr < S::NR; ++nr) {
                     s[mt][nr][2 * h] *= ks;
                     s[mt][nr][2 * h + 1] *= ks;
                 }
             }
-        extra = scale_exponent(__reduce_max_sync(0xFFFFFFFFu, top));
     }
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
@@ -406,11 +404,14 @@ __device__ __forceinline__ void step(uint32_t stage, int32_t base, const uint32_
         for (int i = 0; i < 2; ++i) {
             float m = -INFINITY;
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) m = fmaxf(m, fmaxf(s[mt][nr][i], s[mt][nr][2 + i]));
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    m = fmaxf(m, s[mt][nr][2 * h + i] + (S::FMT != kKv16Bit ? vlog[mt][h] : 0.f));
             m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 4));
             m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 8));
             m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 16));
-            m = fmaxf(st.m[nr][i], m + extra - S::kLower);
+            m = fmaxf(st.m[nr][i], S::FMT != kKv16Bit ? m : m - S::kLower);
             moved |= m != st.m[nr][i];
             const float from = m == -INFINITY ? 0.f : m;  // nothing seen so far: every term is 0
             keep[nr][i] = exp2_fast(st.m[nr][i] - from);

@@ -138,9 +138,10 @@ cccl_status cccl_kv_read(const cccl_kv_cache *h_cache, const cccl_kv_batch *h_ba
  * largest value.  A probability meets the values with 16 bits or more in calls
  * with few rows a kv head, rounded once to 16-bit floating point in others;
  * over fp16 and 8-bit caches that is fp16, whose smallest step is off by up to
- * 2^-39 (few rows) or 2^-33 (others) of the row's largest probability times the
- * largest value scale.  The same call gives the same bits.  d_out may not
- * overlap d_q or the cache.
+ * 2^-39 (few rows), 2^-34 (others) or 2^-30 (others, 8-bit caches) of the row's
+ * largest probability (times its value's scale).  Value scales may have either
+ * sign; those smaller than 2^-90 may lose bits.  The same call gives the same
+ * bits.  d_out may not overlap d_q or the cache.
  * Returns INVALID_ARG, CUDA or OK. */
 cccl_status cccl_kv_attention(const cccl_kv_cache *h_cache, const cccl_kv_batch *h_batch, const void *d_q, int q_heads,
                               int64_t q_token_stride, int64_t q_head_stride, float scale, int causal, int64_t window,

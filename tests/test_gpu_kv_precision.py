@@ -58,12 +58,12 @@ def bounds(c, window=0):
       as the sum of two 16-bit values (bf16 2^-16, fp16 2^-22), others as one
       (2^-8, 2^-11); 8-bit caches and fp16 ones take fp16, whose smallest step adds
       2^-25 of a largest probability (times its value's scale) of 2^14 (few rows)
-      or 2^8 (others);
+      or 2^9 (others; over 8-bit caches 2^5);
     - the result's one rounding."""
     half = c.dtype == HF or c.fmt != "16bit"
     few = few_rows(c)
     p_unit = (2.0 ** -22 if half else 2.0 ** -16) if few else (2.0 ** -11 if half else 2.0 ** -8)
-    p_floor = (2.0 ** -39 if few else 2.0 ** -33) if half else 0.0
+    p_floor = (2.0 ** -39 if few else 2.0 ** -34 if c.fmt == "16bit" else 2.0 ** -30) if half else 0.0
     u, scale, G = UNIT[c.dtype], 1.0 / math.sqrt(c.dim), c.group
     out = torch.zeros(c.T, c.heads * G, c.dim, dtype=torch.float64, device=c.device)
     tol = torch.zeros_like(out)
@@ -140,3 +140,62 @@ def test_one_key_outweighs_the_rest(cc, dtype, fmt, length, new):
         for over in ({}, CUT, dict(max_len=2000)):
             cache, batch = c.objects(cc, **over)
             check(c, cc.kv_attention(cache, batch, c.q)[0])
+
+
+@pytest.mark.parametrize("new", [1, 2, 64])
+@pytest.mark.parametrize("dtype,fmt", [(BF, "int8"), (HF, "int8"), (BF, "e4m3"), (HF, "e4m3"), (HF, "16bit")])
+def test_one_value_far_larger_than_the_rest(cc, dtype, fmt, new):
+    """It has next to no weight, or only the last row sees it: the other values keep their bits."""
+    length = 700
+    small, large = (1.0, 2.0 ** 20) if dtype == BF else (2.0 ** -12, 2.0 ** 8)
+    for where in ("faint", "last"):
+        c = axis_case(length, new, dtype, fmt, seed=81)
+        for p in range(length):
+            put(c, "v", 0, p, small * (0.5 + torch.rand(2, 128, device="cuda")))
+        big = large * (0.5 + torch.rand(2, 128, device="cuda"))
+        if where == "faint":
+            put(c, "k", 0, 600, axis_key(-40))
+            put(c, "v", 0, 600, big)
+        elif new > 1:
+            put(c, "v", 0, length - 1, big)
+        for over in ({}, CUT):
+            cache, batch = c.objects(cc, **over)
+            out, _ = cc.kv_attention(cache, batch, c.q)
+            check(c, out)
+            if where == "last" and fmt != "16bit" and dtype == BF and new > 1:
+                # of any size: nothing of it reaches the other rows
+                scales = c.vs.clone()
+                for junk in (1e30, 3e38, math.inf, math.nan, -1e30):
+                    c.vs[int(c.table[0, (length - 1) // 16]), (length - 1) % 16] = junk
+                    got, _ = cc.kv_attention(cache, batch, c.q)
+                    c.vs.copy_(scales)
+                    check(c, got, rows=slice(0, new - 1))
+
+
+@pytest.mark.parametrize("new", [1, 64])
+@pytest.mark.parametrize("dtype,fmt", [(BF, "int8"), (HF, "int8"), (BF, "e4m3"), (BF, "16bit"), (HF, "16bit")])
+def test_values_of_many_sizes(cc, dtype, fmt, new):
+    """Every token's values have a size of their own, and (8-bit caches) a scale of either sign."""
+    c = axis_case(600, new, dtype, fmt, seed=82)
+    g = torch.Generator(device="cuda").manual_seed(83)
+    span = 12 if dtype == BF else 6
+    for p in range(600):
+        size = 2.0 ** float(torch.randint(-span, span + 1, (1,), generator=g, device="cuda"))
+        put(c, "v", 0, p, size * torch.randn(2, 128, generator=g, device="cuda"))
+        put(c, "k", 0, p, axis_key(0) + 2 * torch.randn(2, 128, generator=g, device="cuda"))
+    if fmt != "16bit":
+        c.vs[:, ::2] *= -1
+    for over in ({}, CUT):
+        cache, batch = c.objects(cc, **over)
+        check(c, cc.kv_attention(cache, batch, c.q)[0])
+
+
+@pytest.mark.parametrize("new", [1, 64])
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("power", [-85, 95])
+def test_value_scales_of_any_size(cc, fmt, power, new):
+    c = axis_case(500, new, BF, fmt, seed=84)
+    c.vs *= 2.0 ** power
+    for over in ({}, CUT):
+        cache, batch = c.objects(cc, **over)
+        check(c, cc.kv_attention(cache, batch, c.q)[0])
