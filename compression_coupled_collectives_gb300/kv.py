@@ -122,11 +122,14 @@ class KvBatch:
         batch = kv_lens.numel()
         if cu_tokens.numel() != batch + 1 or page_table.shape[0] != batch:
             raise ValueError("page_table has a row, kv_lens an entry and cu_tokens one more for each sequence")
+        width = page_table.shape[1]
+        row = page_table.stride(0) if batch > 1 else width
+        if row < width:
+            raise ValueError("page_table's rows overlap (an expanded table has to be copied: .contiguous())")
         self.page_table, self.cu_tokens, self.kv_lens = page_table, cu_tokens, kv_lens
         self.n_tokens, self.batch = int(n_tokens), batch
         self._c = _Batch(page_table.data_ptr(), cu_tokens.data_ptr(), kv_lens.data_ptr(),
-                         max(page_table.stride(0), page_table.shape[1]), self.n_tokens, batch, page_table.shape[1],
-                         int(max_new), int(max_len))
+                         row, self.n_tokens, batch, width, int(max_new), int(max_len))
         self._ref = ctypes.addressof(self._c)
 
 
