@@ -72,8 +72,8 @@ typedef struct {
  * cu_tokens[b + 1] - 1 of the packed tensors, and they are its last ones:
  * with n of them, row cu_tokens[b] + i is position kv_lens[b] - n + i.  A row
  * whose position is negative (n above kv_lens[b]) is in no page: a write
- * skips it, a read gives zeros, and in attention its position hides every key
- * from it.  kv_lens counts the new tokens, so one batch serves a write and
+ * skips it, a read gives zeros, and in causal attention it sees no key (without
+ * causal it sees all of them, whatever the window).  kv_lens counts the new tokens, so one batch serves a write and
  * the attention after it.  The arrays must not change while a call runs: its
  * blocks read them more than once and rely on seeing the same. */
 typedef struct {
