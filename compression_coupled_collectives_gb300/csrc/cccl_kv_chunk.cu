@@ -621,18 +621,17 @@ __device__ __forceinline__ bool mma_role(const KvArgs& a, const AttnArgs& t, Sha
 
 // ---------------------------------------------------------------- softmax
 // Rows 32 warp .. + 31 of row tile i of Q into shared memory, 16 lanes a row;
-// rows that do not exist are zeros, and all are when the scale is zero (every
-// score is then 0 times the products, so are zeros').  A row that goes as it is
-// comes by asynchronous copies, which the caller waits for; bf16 rows for 8-bit
-// caches pass through registers for their power of two, and what undoes that
-// of row 32 warp + lane is returned.  (Code that runs once an item is fetched
-// anew each time and waits behind the K and V copies in flight: it is kept
-// short, with few rounds to memory.)
+// rows that do not exist are zeros.  A row that goes as it is comes by
+// asynchronous copies, which the caller waits for; bf16 rows for 8-bit caches
+// pass through registers for their power of two, and what undoes that of row
+// 32 warp + lane is returned.  (Code that runs once an item is fetched anew each
+// time and waits behind the K and V copies in flight: it is kept short, with few
+// rounds to memory.)
 template <class T, int FMT>
 __device__ __forceinline__ float bring_rows(const KvArgs& a, const AttnArgs& t, const Piece& p, int i, int warp,
-                                            uint32_t q_tile, bool zero) {
+                                            uint32_t q_tile) {
     const int lane = threadIdx.x & 31, chunk = lane & 15;
-    const int row0 = i * kTileRows + 32 * warp, live = zero ? 0 : live_rows<kRows>(t, p) - row0;
+    const int row0 = i * kTileRows + 32 * warp, live = live_rows<kRows>(t, p) - row0;
     const RowPlace mine = row_place(t, p, kRows, row0 + lane);
     const int64_t from = mine.token * t.q_token + (int64_t)mine.head * t.q_head;
     const bool inside = 8 * chunk < a.dim;
@@ -743,8 +742,7 @@ __device__ __forceinline__ void softmax_role(const KvArgs& a, const AttnArgs& t,
     const Waiter wait{sh, a.ws};
     const uint32_t tmem = sh->tmem + ((uint32_t)(32 * warp) << 16), stage = stages + me * (128 * kStageRows<FMT>);
     const uint32_t at_s = tmem + kColS + 128 * i, at_o = tmem + kColO + 128 * i;
-    const bool zero = t.scale == 0.f;
-    const float scale_base2 = (zero ? 1.f : fabsf(t.scale)) * 1.4426950408889634f;
+    const float scale_base2 = fabsf(t.scale) * 1.4426950408889634f;  // not zero (see launch_kv_attention)
     uint32_t s_phase = 0, o_phase = 0, taken = 0, tile = 0;  // tile: this block's tiles of tokens, whoever's
     int slot = 1;                                 // of the piece at hand
     int32_t first = 0, last = 0;                  // what this row sees
@@ -768,7 +766,7 @@ __device__ __forceinline__ void softmax_role(const KvArgs& a, const AttnArgs& t,
         }
         ++taken;
         const bool more = next->count > 0;
-        if (more) to_base2 *= bring_rows<T, FMT>(a, t, *next, i, warp, q_tile, zero);
+        if (more) to_base2 *= bring_rows<T, FMT>(a, t, *next, i, warp, q_tile);
         if (!begin) {  // the end of the piece at hand
             const Piece& cur = sh->piece[me][slot];
             if (!wait(&sh->o_full[i], o_phase)) return;

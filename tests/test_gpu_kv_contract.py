@@ -46,3 +46,20 @@ def test_rows_before_position_zero(cc, new, fmt, window, over):
         check(c, out, lse, causal=causal, window=window)
         if window == 0:
             assert (lse[:new - 2] == -math.inf).all() == causal
+
+
+@pytest.mark.parametrize("fmt", ["16bit", "int8", "e4m3"])
+@pytest.mark.parametrize("new", [1, 40])
+def test_a_scale_of_zero_keeps_what_is_not_finite(cc, new, fmt):
+    """0 times a score is 0 where the score is finite (the result is a mean) and NaN elsewhere."""
+    c = Case([300, 60], [new, new], heads=2, group=4, dim=128, page=16, fmt=fmt, seed=91)
+    ref, ref_lse, tol, ltol = c.attention(scale=0.0)
+    for over in ({}, CUT):
+        q = c.q.clone()
+        q[0, 1, 5], q[-1, 6, 127], q[-1, 2, 0] = math.nan, math.inf, -math.inf
+        cache, batch = c.objects(cc, **over)
+        out, lse = cc.kv_attention(cache, batch, q, scale=0.0)
+        odd = ~torch.isfinite(q).all(-1)
+        assert out[odd].isnan().all() and lse[odd].isnan().all()
+        assert ((out.double() - ref).abs() <= tol)[~odd].all()
+        assert ((lse.double() - ref_lse).abs() <= ltol)[~odd].all()
