@@ -107,7 +107,9 @@ size_t cccl_kv_workspace_bytes(const cccl_kv_cache *h_cache, const cccl_kv_batch
  * code is x * inv rounded to the nearest integer, ties to even, or to the
  * nearest E4M3 value, limited to +-L.  A vector with a NaN or an infinity gets
  * a NaN as its scale, and reads back as NaN throughout.
- * Two rows of one call that name the same page and slot: one of them stays.
+ * Two rows of one call that name the same page and slot: what that slot holds
+ * afterwards is undefined (in 8-bit formats one row's codes may meet the other's
+ * scale); nothing else is affected.
  * Returns INVALID_ARG, CUDA or OK. */
 cccl_status cccl_kv_write(const cccl_kv_cache *h_cache, const cccl_kv_batch *h_batch, const void *d_k,
                           int64_t k_token_stride, int64_t k_head_stride, const void *d_v, int64_t v_token_stride,

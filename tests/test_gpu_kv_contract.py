@@ -63,3 +63,30 @@ def test_a_scale_of_zero_keeps_what_is_not_finite(cc, new, fmt):
         assert out[odd].isnan().all() and lse[odd].isnan().all()
         assert ((out.double() - ref).abs() <= tol)[~odd].all()
         assert ((lse.double() - ref_lse).abs() <= ltol)[~odd].all()
+
+
+@pytest.mark.parametrize("fmt", ["16bit", "int8", "e4m3"])
+def test_a_slot_named_twice_affects_no_other(cc, fmt):
+    """Two sequences end in the same page: their rows for its slots clash, all others are stored and read back."""
+    c = Case([40, 40], [40, 40], heads=2, group=1, dim=64, page=16, fmt=fmt, seed=92)
+    c.table[1, 2] = c.table[0, 2]  # positions 32 .. 39 of both
+    cache, batch = c.objects(cc)
+    before = c.k.clone()
+    cc.kv_write(cache, batch, c.k_new, c.v_new)
+    k, v = cc.kv_read(cache, batch)
+    clash = (torch.arange(80, device="cuda") % 40) >= 32
+    for got, new in ((k, c.k_new), (v, c.v_new)):
+        if fmt == "16bit":
+            assert torch.equal(got[~clash], new[~clash])
+        else:
+            # half a step of a code (E4M3: 2^-4 of a value), and the rounding to bf16
+            largest = new.double().abs().amax(-1, keepdim=True)
+            bound = largest / 254 if fmt == "int8" else new.double().abs() * 2.0 ** -4 + largest * 2.0 ** -18
+            err = (got.double() - new.double()).abs()
+            assert (err <= (bound + (new.double().abs() + bound) * 2.0 ** -8) * (1 + 2.0 ** -16))[~clash].all()
+        assert torch.equal(got[:40][32:], got[40:][32:])  # whatever it is, both read the same
+    used = torch.zeros(c.pages, 16, dtype=torch.bool, device="cuda")
+    for b in range(2):
+        for p in range(40):
+            used[int(c.table[b, p // 16]), p % 16] = True
+    assert torch.equal(c.k[~used].view(torch.uint8), before[~used].view(torch.uint8))
