@@ -90,3 +90,22 @@ def test_a_slot_named_twice_affects_no_other(cc, fmt):
         for p in range(40):
             used[int(c.table[b, p // 16]), p % 16] = True
     assert torch.equal(c.k[~used].view(torch.uint8), before[~used].view(torch.uint8))
+
+
+@pytest.mark.parametrize("new", [2, 40])
+def test_rows_of_no_sequence_keep_their_log_sums(cc, new):
+    """Rows before the first sequence's and after the last one's: neither result nor log-sum-exp is written."""
+    c = Case([100, 50], [new, new], heads=2, group=2, dim=64, page=16, seed=93)
+    ref, ref_lse, tol, ltol = c.attention()
+    q = torch.cat([c.q[:3], c.q, c.q[:4]])
+    out, lse = torch.full_like(q, 5.0), torch.full((q.shape[0], 4), 5.0, device="cuda")
+    cache, _ = c.objects(cc)
+    for over in (100, 1 << 20):
+        batch = cc.KvBatch(c.table, c.cu + 3, c.len_dev, n_tokens=q.shape[0], max_new=new, max_len=over)
+        ws = cc.empty_kv_workspace(cache, batch, 4)
+        cc.cccl_kv_attention(cache, batch, q, out, ws, lse=lse)
+        assert cc.cccl_get_result(ws)[1] == cc.CCCL_OK
+        assert ((out[3:-4].double() - ref).abs() <= tol).all()
+        assert ((lse[3:-4].double() - ref_lse).abs() <= ltol).all()
+        for t in (out, lse):
+            assert (t[:3] == 5.0).all() and (t[-4:] == 5.0).all()

@@ -199,3 +199,36 @@ def test_value_scales_of_any_size(cc, fmt, power, new):
     for over in ({}, CUT):
         cache, batch = c.objects(cc, **over)
         check(c, cc.kv_attention(cache, batch, c.q)[0])
+
+
+def opposed(dtype, fmt, new, device="cuda"):
+    """Few keys of like weight whose values nearly cancel: what a probability is rounded by shows in the result."""
+    lens = [2, 3, 4, 5, 6, 9, 12, 16] * 4
+    c = Case(lens, [min(new, n) for n in lens], heads=4, group=4, dim=16, page=16, dtype=dtype, fmt=fmt, seed=85, device=device)
+    g = torch.Generator(device=device).manual_seed(86)
+    for b, n in enumerate(lens):
+        # K and V of one size: 8-bit codes are the same for all but their signs
+        sign = torch.where(torch.arange(n) % 2 == 0, 1.0, -1.0)
+        for p in range(n):
+            k = torch.randint(0, 2, (4, 16), generator=g, device=device) * 1.0 - 0.5
+            put(c, "k", b, p, k)
+            put(c, "v", b, p, torch.full((4, 16), 1.0, device=device) * float(sign[p]))
+    c.q = (0.5 * torch.randn(c.q.shape, generator=g, device=device)).to(dtype)
+    return c
+
+
+@pytest.mark.parametrize("dtype,fmt", TYPES)
+def test_few_rows_keep_their_probabilities(cc, dtype, fmt):
+    c = opposed(dtype, fmt, 1)
+    assert few_rows(c)
+    for over in ({}, CUT):
+        cache, batch = c.objects(cc, **over)
+        check(c, cc.kv_attention(cache, batch, c.q)[0])
+
+
+@pytest.mark.parametrize("length,new", [(131077, 1), (70001, 150)])
+@pytest.mark.parametrize("dtype,fmt", TYPES)
+def test_long_contexts(cc, dtype, fmt, length, new):
+    c = Case([length], [new], heads=1, group=4, dim=64, page=16, dtype=dtype, fmt=fmt, seed=87)
+    cache, batch = c.objects(cc)
+    check(c, cc.kv_attention(cache, batch, c.q)[0])
