@@ -295,7 +295,7 @@ __device__ __noinline__ void attend_row(const KvArgs& a, const AttnArgs& t, int 
                     if (lane == i + k && there) s = dot;  // (else 0, also where the query is infinite)
                 }
             }
-            s *= kscale * t.scale;
+            s = s * kscale * t.scale;  // (in this order: the scales' product may leave binary32's range)
             if (pass == 0) {
                 if (seen) {
                     const float to = (s > m || s != s) ? s : m;  // keeps a NaN: no later s compares above it

@@ -109,3 +109,21 @@ def test_rows_of_no_sequence_keep_their_log_sums(cc, new):
         assert ((lse[3:-4].double() - ref_lse).abs() <= ltol).all()
         for t in (out, lse):
             assert (t[:3] == 5.0).all() and (t[-4:] == 5.0).all()
+
+
+@pytest.mark.parametrize("new", [1, 64])
+def test_rows_worked_out_again_apply_scales_in_order(cc, new):
+    """Key scales near binary32's limit and scores of zero: an infinite value leaves the other channels' mean alone."""
+    c = Case([300], [new], heads=1, group=2, dim=64, page=16, fmt="e4m3", seed=94)
+    c.q[:] = 0
+    c.ks[:] = 2.0 ** 127
+    ref, ref_lse, tol, ltol = c.attention(scale=4.0)
+    at = (int(c.table[0, 3]), 2)
+    c.v[at][0, 7] = 0x7F  # E4M3's NaN in one channel
+    for over in ({}, CUT):
+        cache, batch = c.objects(cc, **over)
+        out, lse = cc.kv_attention(cache, batch, c.q, scale=4.0)
+        assert out[..., 7].isnan().all()
+        keep = torch.arange(64, device="cuda") != 7
+        assert ((out.double() - ref).abs() <= tol)[..., keep].all()
+        assert ((lse.double() - ref_lse).abs() <= ltol).all()
