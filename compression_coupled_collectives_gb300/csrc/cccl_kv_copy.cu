@@ -28,10 +28,15 @@ struct TokenSlots {
     int64_t at[kMaxTokensPerBlock], scale_at[kMaxTokensPerBlock];
     int8_t state[kMaxTokensPerBlock];  // 0 no sequence's row, 1 in the cache, 2 not in the cache
 };
-// Warp 0, a token a lane.
+// Warp 0, a token a lane.  The first block's other warps meanwhile look at every
+// sequence, for what no row leads to (a length, rows in no order).
 __device__ __forceinline__ void find_slots(const KvArgs& a, int64_t t0, int count, TokenSlots& s) {
     const int lane = threadIdx.x & 31;
-    if (threadIdx.x >= 32) return;
+    if (threadIdx.x >= 32) {
+        if (blockIdx.x == 0)
+            for (int b = (int)threadIdx.x - 32; b < a.batch; b += kCopyThreads - 32) load_sequence(a, b);
+        return;
+    }
     // the last sequence that starts at or before t0: 32 candidates a step
     int lo = 0, hi = a.batch;  // starts at lo, or no sequence does
     while (hi - lo > 1) {

@@ -127,3 +127,36 @@ def test_rows_worked_out_again_apply_scales_in_order(cc, new):
         keep = torch.arange(64, device="cuda") != 7
         assert ((out.double() - ref).abs() <= tol)[..., keep].all()
         assert ((lse.double() - ref_lse).abs() <= ltol).all()
+
+
+@pytest.mark.parametrize("fmt", ["16bit", "int8"])
+@pytest.mark.parametrize("spoil", ["length", "negative length", "past the rows", "order"])
+def test_writes_and_reads_report_every_sequence(cc, fmt, spoil):
+    """Also one that no row leads to: the others' tokens are stored and read as ever."""
+    lens, new = [40, 50, 30, 20], [40, 0, 30, 20]
+    c = Case(lens, new, heads=2, group=1, dim=64, page=16, fmt=fmt, seed=95)
+    cache, batch = c.objects(cc)
+    cc.kv_write(cache, batch, c.k_new, c.v_new)
+    good = cc.kv_read(cache, batch)
+    cu, kv_lens = c.cu.clone(), c.len_dev.clone()
+    if spoil == "length":
+        kv_lens[1] = 100000
+    elif spoil == "negative length":
+        kv_lens[1] = -1
+    elif spoil == "past the rows":
+        cu[-1] += 7
+    else:
+        cu[1] = 45  # sequence 0 ends past sequence 1's end
+        cu[2] = 40
+    bad = cc.KvBatch(c.table, cu, kv_lens, n_tokens=c.T, max_new=40, max_len=50)
+    for write in (True, False):
+        ws = cc.empty_kv_workspace(cache, bad)
+        k, v = torch.zeros_like(c.k_new), torch.zeros_like(c.v_new)
+        if write:
+            cc.cccl_kv_write(cache, bad, c.k_new, c.v_new, ws)
+        else:
+            cc.cccl_kv_read(cache, bad, k, v, ws)
+        assert cc.cccl_get_result(ws)[1] == cc.CCCL_ERR_INVALID_ARG
+    if "length" in spoil:
+        for a, b in zip((k, v), good):
+            assert torch.equal(a, b)
