@@ -1,6 +1,4 @@
 // cccl_kv_attention.cu -- which attention kernel a call takes.
-#include <algorithm>
-
 #include "cccl_kv.cuh"
 #include "cccl_kv_launch.h"
 
@@ -18,19 +16,13 @@ static bool few_rows(int format, int group, int max_new) {
 }
 
 size_t kv_attention_scratch(int format, int dim, int group, int max_new) {
-    // (the larger of the two in the second case, where a scale may take either)
-    return few_rows(format, group, max_new) ? kv_tokens_scratch(dim)
-                                            : std::max(kv_chunk_scratch(dim), kv_tokens_scratch(dim));
+    return few_rows(format, group, max_new) ? kv_tokens_scratch(dim) : kv_chunk_scratch(dim);
 }
 
 cudaError_t launch_kv_attention(int dtype, int format, const KvArgs& a, const AttnArgs& t, int max_new, int max_len,
                                 cudaStream_t s) {
-    // A scale of zero: the chunk kernel applies the scale after it has hidden scores
-    // as -infinity, which zero would turn into NaN; the other one hides them last,
-    // takes any number of rows and needs no more workspace.
-    return few_rows(format, (int)t.group.d, max_new) || t.scale == 0.f
-               ? launch_kv_tokens(dtype, format, a, t, max_new, max_len, s)
-               : launch_kv_chunk(dtype, format, a, t, max_new, max_len, s);
+    return few_rows(format, (int)t.group.d, max_new) ? launch_kv_tokens(dtype, format, a, t, max_new, max_len, s)
+                                                     : launch_kv_chunk(dtype, format, a, t, max_new, max_len, s);
 }
 
 }  // namespace cccl

@@ -742,7 +742,11 @@ __device__ __forceinline__ void softmax_role(const KvArgs& a, const AttnArgs& t,
     const Waiter wait{sh, a.ws};
     const uint32_t tmem = sh->tmem + ((uint32_t)(32 * warp) << 16), stage = stages + me * (128 * kStageRows<FMT>);
     const uint32_t at_s = tmem + kColS + 128 * i, at_o = tmem + kColO + 128 * i;
-    const float scale_base2 = fabsf(t.scale) * 1.4426950408889634f;  // not zero (see launch_kv_attention)
+    const float scale_base2 = fabsf(t.scale) * 1.4426950408889634f;
+    // hidden scores are -infinity when the scale meets them: a scale of zero (or one
+    // that a row's power makes zero) is the smallest number instead, which leaves
+    // nothing of any finite score
+    const float least = __uint_as_float(1u);
     uint32_t s_phase = 0, o_phase = 0, taken = 0, tile = 0;  // tile: this block's tiles of tokens, whoever's
     int slot = 1;                                 // of the piece at hand
     int32_t first = 0, last = 0;                  // what this row sees
@@ -751,7 +755,7 @@ __device__ __forceinline__ void softmax_role(const KvArgs& a, const AttnArgs& t,
         // the next piece that has rows for this warpgroup.  Its rows of Q may
         // come now: the last S is done, so is every product with these.
         uint32_t skipped = 0;  // tiles of pieces without
-        float to_base2 = scale_base2;
+        float to_base2 = 1.f;
         Piece* const next = &sh->piece[me][slot ^ 1];
         for (;; ++taken) {
             Piece p;
@@ -766,7 +770,7 @@ __device__ __forceinline__ void softmax_role(const KvArgs& a, const AttnArgs& t,
         }
         ++taken;
         const bool more = next->count > 0;
-        if (more) to_base2 *= bring_rows<T, FMT>(a, t, *next, i, warp, q_tile);
+        if (more) to_base2 = fmaxf(scale_base2 * bring_rows<T, FMT>(a, t, *next, i, warp, q_tile), least);
         if (!begin) {  // the end of the piece at hand
             const Piece& cur = sh->piece[me][slot];
             if (!wait(&sh->o_full[i], o_phase)) return;

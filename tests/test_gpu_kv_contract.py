@@ -160,3 +160,19 @@ def test_writes_and_reads_report_every_sequence(cc, fmt, spoil):
     if "length" in spoil:
         for a, b in zip((k, v), good):
             assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("new", [1, 64])
+@pytest.mark.parametrize("fmt", ["16bit", "int8"])
+@pytest.mark.parametrize("scale", [1e-38, -1e-38, 1e-44, 1e30])
+def test_scales_of_any_size(cc, scale, fmt, new):
+    """Scales next to binary32's limits, with queries (and for the largest keys) of a size that suits."""
+    c = Case([300, 129], [new, new], heads=2, group=2, dim=64, page=16, fmt=fmt, seed=96)
+    if scale == 1e30:
+        c.q = (c.q.float() * 1e-30).to(c.dtype)
+    elif scale != 1e-44:
+        c.q = (c.q.float() * 1e36).to(c.dtype)
+    for over in ({}, CUT):
+        cache, batch = c.objects(cc, **over)
+        out, lse = cc.kv_attention(cache, batch, c.q, scale=scale)
+        check(c, out, lse, scale=scale)
