@@ -28,15 +28,20 @@
 // the sum, the rounding and the stores, about as long as the tensor core takes
 // for the other tile of rows; under the power limit the clock is what gives.
 // 4096 new tokens at the end of 32768 cached, 32 heads over 8 kv heads of 128:
-// 1332 to 1423 us, 1450 to 1540 TFLOP/s with the clock (a library product at its
-// best: 1861); tensor pipe 58 % busy in a short call (1024 over 8192: 102 us).
+// 1306 to 1339 us from a graph of a few calls, 1540 to 1580 TFLOP/s with the clock,
+// 1443 us in a loop, where the power limit holds it at 1430 (a library product:
+// 1931 and 1740); tensor pipe 59 % busy in a short call (1024 over 8192: 100 us).
 // Half a row a thread, 16 softmax warps: 1590 us against 1389.  Exponentials
 // taken a block of 16 late: the same.
-// 8-bit caches, 5 x 2048 new tokens with windows of 4096: 706 to 721 us, 700 to
-// 715 TFLOP/s.  Of 717, widening costs 86, the scales' loads and products, a
+// 8-bit caches, 5 x 2048 new tokens with windows of 4096: 702 to 711 us, 710 to
+// 720 TFLOP/s; the long chunk over E4M3 1896 to 1909 us, 1085.  Where it goes, by
+// leaving parts out, of 717: widening 86, the scales' loads and products, a
 // column's for each of a row's scores, 92, and the tiles at a range's ends, with
 // one slot less for tiles, 130.  Rows held in the products' own layout, which
 // loads a quarter of the scales: 797.
+// Moving a reference rescales the accumulator, 32 columns at a time in a loop that
+// is not unrolled: 16 columns, unrolled, took 763 us for 710 (INT8, above) and 1329
+// for 1315 (the long chunk), not unrolled 718 and 1344.
 #include <cuda.h>
 
 #include <type_traits>
@@ -76,7 +81,9 @@ constexpr float kLower = M::kHalf ? 9.f : 0.f;
 // 8-bit caches: where the value scales of 32 rows, and the largest of the tile's
 // four such groups, lie within a factor of 4 (a difference of scale_bits; zeros
 // do not count), the largest stands for all in a row's reference, which then lies
-// up to 4 too high.  Every tile the exact way: 1012 us for 723.
+// up to 4 too high; else it is looked for score by score (2048 new tokens over
+// 16384: 526 us alike, 535 apart).  That way for every tile whose reference moves:
+// 999 us for 703 (5 x 2048 windowed INT8 chunks).
 constexpr uint32_t kSpread = 2u << 23;
 // Halves of result rows (128 bytes) that a softmax warp has on their way out at
 // a time

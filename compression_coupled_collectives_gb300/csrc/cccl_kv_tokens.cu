@@ -13,11 +13,13 @@
 // shared memory (few, short items) or by a second kernel (any).
 //
 // What bounds it: the loads.  32 tokens over 32 x 4096 cached (8 kv heads of
-// 128, groups of 4, 16-bit): 88 us, 6.1 TB/s, DRAM 77 % busy under the profiler;
-// INT8, 16 x 16384: 106 us, 5.4 TB/s, DRAM 68 % and half of the issue slots
-// taken, by the codes' way to fp16.  Three blocks an SM, each with 64 KB of
-// rings; four spill (INT8: 299 us against 264).  Short calls are bound by the
-// launch, the first page lookups and the joining: one token over 517: 7.1 us.
+// 128, groups of 4, 16-bit): 88 to 93 us, 5.8 to 6.1 TB/s, DRAM 75 % busy under the
+// profiler; INT8, 16 x 16384: 106 to 112 us, 4.9 to 5.2 TB/s, DRAM 65 % and 56 % of
+// the issue slots taken, by the codes' way to fp16; one token over 131077 of E4M3, whose codes take fewer
+// instructions: 57 us under the profiler, DRAM 62 %, 44 % of the issue slots, and
+// 11 more for joining 57 parts.  Three blocks an SM, each with 64 KB of rings; four
+// spill (INT8: 299 us against 264).  Short calls are bound by the launch, the first
+// page lookups and the joining: one token over 517: 7.1 us.
 //
 // Both products are taken transposed, S' = K Q' and O' = V' P', so that tokens
 // and channels fill the instruction's 16 and the rows its 8: a tile with the

@@ -230,7 +230,7 @@ def kv_write(cache: KvCache, batch: KvBatch, k: torch.Tensor, v: torch.Tensor, s
 
 
 def kv_read(cache: KvCache, batch: KvBatch, stream=None) -> tuple[torch.Tensor, torch.Tensor]:
-    """Read and wait; returns k and v [n_tokens, kv_heads, head_dim]."""
+    """Read and wait; returns k and v [n_tokens, kv_heads, head_dim] (rows of no sequence: undefined)."""
     with torch.cuda.stream(stream):
         ws = empty_kv_workspace(cache, batch)
         shape = (batch.n_tokens, cache.kv_heads, cache.head_dim)
@@ -243,7 +243,8 @@ def kv_read(cache: KvCache, batch: KvBatch, stream=None) -> tuple[torch.Tensor, 
 
 def kv_attention(cache: KvCache, batch: KvBatch, q: torch.Tensor, *, scale: float | None = None, causal: bool = True,
                  window: int = 0, stream=None) -> tuple[torch.Tensor, torch.Tensor]:
-    """Attend and wait; returns the result [n_tokens, q_heads, head_dim] and each row's log-sum-exp."""
+    """Attend and wait; returns the result [n_tokens, q_heads, head_dim] and each row's log-sum-exp (rows of no
+    sequence: undefined)."""
     with torch.cuda.stream(stream):
         ws = empty_kv_workspace(cache, batch, q.shape[1])
         out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
