@@ -244,17 +244,17 @@ __device__ __forceinline__ float4 stored4_values(uint2 x) {
 // not the same when such a place holds a NaN or an infinity; they send the rows
 // whose sums come out non-finite through here, where nothing waits for them.
 // 32 keys at a time: every lane looks one up and owns its score.  A key's
-// channels lie across the warp, 4 a lane; the loads of 4 keys are in flight, and
+// channels lie across the warp, 4 a lane; the loads of 2 keys are in flight, and
 // waiting for them is most of its time: one NaN in one of 8 heads makes 4096 new
-// tokens over 32768 take 1.27 s for 1.3 ms, one token over 32768 17 ms for 0.07.
-// (Registers are few here: the kernels' own count must not grow by this.  8 and 16
-// lanes a key, 16 and 8 channels a lane, took 0.79 s and cost single tokens 0.5 to
-// 2.5 % through the joining kernel's registers.)
+// tokens over 32768 take 1.77 s for 1.3 ms, one token over 32768 21 ms for 0.07.
+// Registers are few here, since the kernels' own count must not grow by this: 4
+// keys in flight took 1.27 s, 16 and 8 lanes a key less still, but through the
+// joining kernels' spills single tokens 0.5 to 2.5 % more.
 template <class T, int FMT>
 __device__ __noinline__ void attend_row(const KvArgs& a, const AttnArgs& t, int b, int32_t len, int64_t row,
                                         int32_t pos, int head) {
     constexpr uint32_t kAll = 0xFFFFFFFFu;
-    constexpr int kFlight = 4;
+    constexpr int kFlight = 2;
     const int lane = threadIdx.x & 31;
     const int kv_head = (int)div_by(t.group, (uint32_t)head);
     const bool inside = 4 * lane < a.dim;

@@ -28,12 +28,12 @@
 // the sum, the rounding and the stores, about as long as the tensor core takes
 // for the other tile of rows; under the power limit the clock is what gives.
 // 4096 new tokens at the end of 32768 cached, 32 heads over 8 kv heads of 128:
-// 1306 to 1339 us from a graph of a few calls, 1540 to 1580 TFLOP/s with the clock,
+// 1302 to 1339 us from a graph of a few calls, 1540 to 1580 TFLOP/s with the clock,
 // 1443 us in a loop, where the power limit holds it at 1430 (a library product:
 // 1931 and 1740); tensor pipe 59 % busy in a short call (1024 over 8192: 100 us).
 // Half a row a thread, 16 softmax warps: 1590 us against 1389.  Exponentials
 // taken a block of 16 late: the same.
-// 8-bit caches, 5 x 2048 new tokens with windows of 4096: 702 to 711 us, 710 to
+// 8-bit caches, 5 x 2048 new tokens with windows of 4096: 702 to 712 us, 710 to
 // 720 TFLOP/s; the long chunk over E4M3 1896 to 1909 us, 1085.  Where it goes, by
 // leaving parts out, of 717: widening 86, the scales' loads and products, a
 // column's for each of a row's scores, 92, and the tiles at a range's ends, with
