@@ -261,7 +261,8 @@ __device__ __noinline__ void attend_row(const KvArgs& a, const AttnArgs& t, int 
     const uint32_t column = (FMT == kKv16Bit ? 8 : 4) * lane;
     float4 q = make_float4(0.f, 0.f, 0.f, 0.f), acc = q;
     if (inside)
-        q = stored4_values<T, kKv16Bit>(load_stored4<kKv16Bit>(t.q + row * t.q_token + (int64_t)head * t.q_head + 8 * lane));
+        q = stored4_values<T, kKv16Bit>(
+            load_stored4<kKv16Bit>(t.q + row * t.q_token + (int64_t)head * t.q_head + 8 * lane));
     int32_t first, last;
     visible_range(t, len, pos, first, last);
     float m = -INFINITY, sum = 0.f;  // of this lane's keys; then of all

@@ -732,8 +732,8 @@ __device__ __forceinline__ void load_scales(uint32_t at, float2* f) {
 // Whether a tile's value scales lie further apart than kSpread; v: its v_top.
 __device__ __forceinline__ bool scales_apart(const uint4& v) {
     const uint32_t most = max(max(v.x, v.y), max(v.z, v.w));
-    return ((v.x | v.y | v.z | v.w) & 1u) != 0 || (v.x != 0 && most - v.x > kSpread) ||
-           (v.y != 0 && most - v.y > kSpread) || (v.z != 0 && most - v.z > kSpread) || (v.w != 0 && most - v.w > kSpread);
+    auto low = [&](uint32_t x) { return x != 0 && most - x > kSpread; };
+    return ((v.x | v.y | v.z | v.w) & 1u) != 0 || low(v.x) || low(v.y) || low(v.z) || low(v.w);
 }
 // n low bits set (0 for n <= 0, all for n >= 32)
 __device__ __forceinline__ uint32_t bits_below(int32_t n) {
