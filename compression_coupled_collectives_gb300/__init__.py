@@ -4,9 +4,12 @@ buffers and the fused compressed reduce, on one GB300 GPU.
 Every function here marshals arguments for the C ABI of ``include/cccl.h``
 (same names) and calls it; all compute runs in the library's sm_103a kernels.
 What works on a paged key/value cache (``include/cccl_kv.h``) is in ``kv`` and
-reachable from here too: ``kv_write``, ``kv_read``, ``kv_attention``.  torch
-supplies device memory and streams only.  There is no fallback: importing this
-package raises ImportError when ``libcccl.so`` has not been built.
+reachable from here too: ``kv_write``, ``kv_read``, ``kv_attention``; a step
+with drafted tokens over it (``include/cccl_step.h``) is in ``step``:
+``step_plan``, ``step_write``, ``step_attention``, ``step_verify``,
+``step_keep``.  torch supplies device memory and streams only.  There is no
+fallback: importing this package raises ImportError when ``libcccl.so`` has not
+been built.
 """
 
 from __future__ import annotations
@@ -401,3 +404,6 @@ def reduce_typed(dtype: int, streams: Sequence[torch.Tensor], n_elems: int, op: 
 from .kv import (CCCL_KV_16BIT, CCCL_KV_E4M3, CCCL_KV_INT8, KV_MAX_BATCH, KV_MAX_DIM, KV_MAX_HEADS,  # noqa: E402
                  KvBatch, KvCache, cccl_kv_attention, cccl_kv_clear_status, cccl_kv_read, cccl_kv_workspace_bytes,
                  cccl_kv_write, empty_kv_workspace, kv_attention, kv_read, kv_write)
+from .step import (STEP_MAX_DRAFT, STEP_MAX_VOCAB, StepRotary, StepTables, cccl_step_attention,  # noqa: E402
+                   cccl_step_keep, cccl_step_plan, cccl_step_verify, cccl_step_write, empty_step_workspace,
+                   step_attention, step_keep, step_plan, step_verify, step_write)

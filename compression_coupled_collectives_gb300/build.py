@@ -14,7 +14,8 @@ ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libcccl.so")
 SOURCES = ["cccl_compress.cu", "cccl_decompress.cu", "cccl_reduce.cu", "cccl_api.cu",
            "cccl_kv_api.cu", "cccl_kv_copy.cu", "cccl_kv_attention.cu", "cccl_kv_tokens.cu",
-           "cccl_kv_chunk.cu"]
+           "cccl_kv_chunk.cu", "cccl_step_tokens.cu", "cccl_step_chunk.cu", "cccl_step_api.cu",
+           "cccl_step_plan.cu", "cccl_step_write.cu", "cccl_step_verify.cu", "cccl_step_keep.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
          "-I", os.path.join(ROOT, "include")]
@@ -29,7 +30,7 @@ def _nvcc() -> str:
 
 def _deps():
     files = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cu", ".cuh", ".h"))]
-    files += [os.path.join(ROOT, "include", f) for f in ("cccl.h", "cccl_kv.h")]
+    files += [os.path.join(ROOT, "include", f) for f in ("cccl.h", "cccl_kv.h", "cccl_step.h")]
     return files
 
 

@@ -61,6 +61,15 @@ struct AttnArgs {
     int32_t causal, q_heads;
     FastDiv group;  // query heads that share a kv head
 };
+// Attention of drafted tokens: token i of a sequence's n new ones sees what was
+// cached before them and those of them whose bit is set in its row of `mask`
+// (bit k in word k / 32; bits from 32 words on are clear).  The kernels are
+// written for either kind of arguments, Args.
+struct TreeArgs : AttnArgs {
+    const uint32_t* mask;
+    int64_t mask_stride;  // words from one row to the next
+    int32_t words;        // of a row
+};
 
 // Sequence b's rows and length, with everything that does not fit clamped
 // (and reported): 0 <= row, row + n <= n_tokens, 0 <= len <= table capacity.
@@ -101,12 +110,85 @@ __device__ __forceinline__ bool slot_of(const KvArgs& a, int b, uint32_t p, int6
     return page >= 0;
 }
 
-// The keys that a row at position `pos` of a sequence of `len` tokens sees:
-// first .. last - 1 (empty when last <= first).
-__device__ __forceinline__ void visible_range(const AttnArgs& t, int32_t len, int32_t pos, int32_t& first,
+// The keys that a row at position `pos` of a sequence sees: first .. last - 1
+// (none when last <= first).  row: its place in the packed tensors.
+__device__ __forceinline__ void visible_range(const AttnArgs& t, const Sequence& s, int64_t, int32_t pos, int32_t& first,
                                               int32_t& last) {
-    last = max(t.causal ? min(len, pos + 1) : len, 0);
+    last = max(t.causal ? min(s.len, pos + 1) : s.len, 0);
     first = t.window > 0 && pos >= t.window ? min(pos - t.window + 1, last) : 0;
+}
+// Drafted tokens: the tokens before the draft lie at positions below this.
+__device__ __forceinline__ int32_t before_draft(const Sequence& s) { return s.len - s.n; }
+__device__ __forceinline__ const uint32_t* draft_bits(const TreeArgs& t, int64_t row) {
+    return t.mask + row * t.mask_stride;
+}
+// Word w of a row's mask without the bits of tokens at negative positions and of
+// those from n on.
+__device__ __forceinline__ uint32_t draft_word(const uint32_t* bits, int32_t w, int32_t before, int32_t n) {
+    const int32_t lo = max(-before, 0) - 32 * w, hi = n - 32 * w;  // bits lo .. hi - 1
+    if (hi <= 0 || lo >= 32) return 0;
+    uint32_t x = bits[w];
+    if (lo > 0) x &= ~0u << lo;
+    if (hi < 32) x &= ~(~0u << hi);
+    return x;
+}
+// Here what lies between first and last is visible where it is not drafted or
+// its bit is set (drafted_seen).  A window leaves the last `window` of what the
+// row sees without it: tokens before the draft, then drafted ones by their place.
+// last is one past the last of them, so a row sees something exactly when
+// first < last.  (A tree of n tokens has few words: n / 32.)
+static __device__ __noinline__ int2 draft_range(const uint32_t* bits, int32_t words, int32_t before, int32_t n,
+                                                int32_t window) {
+    words = min(words, (n + 31) / 32);
+    int32_t highest = -1, count = 0;
+    for (int32_t w = 0; w < words; ++w) {
+        const uint32_t x = draft_word(bits, w, before, n);
+        count += __popc(x);
+        if (x != 0) highest = 32 * w + 31 - __clz(x);
+    }
+    const int32_t last = highest >= 0 ? before + highest + 1 : max(before, 0);
+    if (window <= 0) return make_int2(0, last);
+    if (count <= window) return make_int2((int32_t)max((int64_t)before + count - window, (int64_t)0), last);
+    // the window ends among the drafted tokens: skip the first count - window of them
+    int32_t skip = count - window;
+    for (int32_t w = 0; w < words; ++w) {
+        uint32_t x = draft_word(bits, w, before, n);
+        if (__popc(x) <= skip) {
+            skip -= __popc(x);
+            continue;
+        }
+        for (; skip > 0; --skip) x &= x - 1;
+        return make_int2(before + 32 * w + __ffs(x) - 1, last);
+    }
+    return make_int2(last, last);  // (not reached)
+}
+__device__ __forceinline__ void visible_range(const TreeArgs& t, const Sequence& s, int64_t row, int32_t, int32_t& first,
+                                              int32_t& last) {
+    const int2 r = draft_range(draft_bits(t, row), t.words, before_draft(s), s.n, t.window);
+    first = r.x;
+    last = r.y;
+}
+// Whether a row sees position j, which lies between its first and last.
+__device__ __forceinline__ bool drafted_seen(const AttnArgs&, const Sequence&, int64_t, int32_t) { return true; }
+__device__ __forceinline__ bool drafted_seen(const TreeArgs& t, const Sequence& s, int64_t row, int32_t j) {
+    const int32_t k = j - before_draft(s);
+    return k < 0 || (k < 32 * (int64_t)t.words && (draft_bits(t, row)[k >> 5] >> (k & 31) & 1u) != 0);
+}
+// The positions below which every one between a row's first and last is seen.
+__device__ __forceinline__ int32_t gapless_below(const AttnArgs&, const Sequence&, int32_t last) { return last; }
+__device__ __forceinline__ int32_t gapless_below(const TreeArgs&, const Sequence& s, int32_t last) {
+    return min(last, max(before_draft(s), 0));
+}
+// Bit i: whether a row sees position j + i, where that lies between its first and last.
+__device__ __forceinline__ uint32_t seen_32(const AttnArgs&, const Sequence&, int64_t, int32_t) { return ~0u; }
+__device__ __forceinline__ uint32_t seen_32(const TreeArgs& t, const Sequence& s, int64_t row, int32_t j) {
+    const int32_t k = j - before_draft(s);
+    if (k <= -32) return ~0u;
+    const uint32_t* bits = draft_bits(t, row);
+    const int32_t w = k >> 5;  // rounded down
+    const uint32_t x = w >= 0 && w < t.words ? bits[w] : 0u, y = w + 1 < t.words ? bits[w + 1] : 0u;
+    const uint32_t z = __funnelshift_r(x, y, (uint32_t)k & 31u);
+    return k < 0 ? z | ~(~0u << -k) : z;
 }
 
 // ---------------------------------------------------------------- values
@@ -250,8 +332,8 @@ __device__ __forceinline__ float4 stored4_values(uint2 x) {
 // Registers are few here, since the kernels' own count must not grow by this: 4
 // keys in flight took 1.27 s, 16 and 8 lanes a key less still, but through the
 // joining kernels' spills single tokens 0.5 to 2.5 % more.
-template <class T, int FMT>
-__device__ __noinline__ void attend_row(const KvArgs& a, const AttnArgs& t, int b, int32_t len, int64_t row,
+template <class T, int FMT, class Args>
+__device__ __noinline__ void attend_row(const KvArgs& a, const Args& t, int b, const Sequence& sequence, int64_t row,
                                         int32_t pos, int head) {
     constexpr uint32_t kAll = 0xFFFFFFFFu;
     constexpr int kFlight = 2;
@@ -264,13 +346,13 @@ __device__ __noinline__ void attend_row(const KvArgs& a, const AttnArgs& t, int 
         q = stored4_values<T, kKv16Bit>(
             load_stored4<kKv16Bit>(t.q + row * t.q_token + (int64_t)head * t.q_head + 8 * lane));
     int32_t first, last;
-    visible_range(t, len, pos, first, last);
+    visible_range(t, sequence, row, pos, first, last);
     float m = -INFINITY, sum = 0.f;  // of this lane's keys; then of all
 #pragma unroll 1
     for (int pass = 0; pass < 2; ++pass) {
 #pragma unroll 1
         for (int32_t base = first; base < last; base += 32) {
-            const bool seen = lane < last - base;
+            const bool seen = lane < last - base && drafted_seen(t, sequence, row, base + lane);
             int64_t at = 0, scale_at = 0;
             const bool there = seen && slot_of(a, b, (uint32_t)(base + lane), at, scale_at);
             at += (int64_t)kv_head * a.head_stride;

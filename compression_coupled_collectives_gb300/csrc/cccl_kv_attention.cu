@@ -25,4 +25,10 @@ cudaError_t launch_kv_attention(int dtype, int format, const KvArgs& a, const At
                                                      : launch_kv_chunk(dtype, format, a, t, max_new, max_len, s);
 }
 
+cudaError_t launch_step_attention(int dtype, int format, const KvArgs& a, const TreeArgs& t, int max_new, int max_len,
+                                  cudaStream_t s) {
+    return few_rows(format, (int)t.group.d, max_new) ? launch_step_tokens(dtype, format, a, t, max_new, max_len, s)
+                                                     : launch_step_chunk(dtype, format, a, t, max_new, max_len, s);
+}
+
 }  // namespace cccl

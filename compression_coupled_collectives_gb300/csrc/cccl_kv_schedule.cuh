@@ -28,16 +28,30 @@ struct TileRange {
     int32_t first, last;  // visible tokens of any row: first .. last - 1
     int32_t lo, n;        // tiles lo .. lo + n - 1 (n >= 1)
 };
-// (A call's rows are below 2^31: n_tokens * q_heads is.)  TOKENS of 0 counts
-// every item as one tile.
-template <int ROWS, int TOKENS>
-__device__ __forceinline__ TileRange tile_range(const AttnArgs& t, const Sequence& s, int32_t rt) {
+// What any row of tile rt may see.
+template <int ROWS>
+__device__ __forceinline__ void tile_visible(const AttnArgs& t, const Sequence& s, int32_t rt, int32_t& first,
+                                             int32_t& last) {
     const uint32_t rows = (uint32_t)s.n * t.group.d, r0 = (uint32_t)rt * ROWS;
     const int32_t base = s.len - s.n;
-    TileRange r;
     int32_t ignore;
-    visible_range(t, s.len, base + (int32_t)div_by(t.group, r0), r.first, ignore);
-    visible_range(t, s.len, base + (int32_t)div_by(t.group, min(r0 + ROWS, rows) - 1), ignore, r.last);
+    visible_range(t, s, 0, base + (int32_t)div_by(t.group, r0), first, ignore);
+    visible_range(t, s, 0, base + (int32_t)div_by(t.group, min(r0 + ROWS, rows) - 1), ignore, last);
+}
+// (Drafted tokens: whatever the masks say.  A row that sees none of them sees the
+// last `window` tokens before them.)
+template <int ROWS>
+__device__ __forceinline__ void tile_visible(const TreeArgs& t, const Sequence& s, int32_t, int32_t& first,
+                                             int32_t& last) {
+    first = t.window > 0 ? (int32_t)max((int64_t)before_draft(s) - t.window, (int64_t)0) : 0;
+    last = s.len;
+}
+// (A call's rows are below 2^31: n_tokens * q_heads is.)  TOKENS of 0 counts
+// every item as one tile.
+template <int ROWS, int TOKENS, class Args>
+__device__ __forceinline__ TileRange tile_range(const Args& t, const Sequence& s, int32_t rt) {
+    TileRange r;
+    tile_visible<ROWS>(t, s, rt, r.first, r.last);
     if (r.first >= r.last) {
         r.first = r.last = r.lo = 0;
         r.n = 1;
@@ -58,8 +72,8 @@ __device__ __forceinline__ int32_t row_tiles(const AttnArgs& t, const Sequence& 
 // Block-wide: prefix[b] = tiles before sequence b on the line, prefix[batch] =
 // all.  Ends with a barrier.  2^32 tiles would take hours: such lengths are
 // reported as invalid and the line is empty.
-template <int ROWS, int TOKENS>
-__device__ __forceinline__ void build_prefix(const KvArgs& a, const AttnArgs& t, uint32_t* prefix) {
+template <int ROWS, int TOKENS, class Args>
+__device__ __forceinline__ void build_prefix(const KvArgs& a, const Args& t, uint32_t* prefix) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
     // a thread a sequence; those of many row tiles are left to a warp each
     constexpr int32_t kFew = 4;
@@ -145,8 +159,8 @@ __device__ __forceinline__ Walk make_walk(uint32_t T, uint32_t share, uint32_t b
 // The next piece; false at the share's end.  p is the piece before, once there
 // was one.  (Items after the first are reached by stepping on; what finds the
 // first shares its code with that, since all of it runs cold.)
-template <int ROWS, int TOKENS>
-__device__ __forceinline__ bool next_piece(const KvArgs& a, const AttnArgs& t, const uint32_t* prefix, Walk& w,
+template <int ROWS, int TOKENS, class Args>
+__device__ __forceinline__ bool next_piece(const KvArgs& a, const Args& t, const uint32_t* prefix, Walk& w,
                                            Piece& p) {
     const int lane = threadIdx.x & 31;
     while (w.x < w.x1) {
@@ -281,12 +295,12 @@ __device__ __forceinline__ RowPlace row_place(const AttnArgs& t, const Piece& p,
 // Values d .. d + 7 of a finished row: v / sum, and with d = 0 its log-sum-exp
 // (m in base 2).  True when something is not finite, though the row sees keys:
 // the row is then worked out by fix_row.
-template <class T>
-__device__ __forceinline__ bool store_row_part(const AttnArgs& t, const Piece& p, int rows, int row, int d,
+template <class T, class Args>
+__device__ __forceinline__ bool store_row_part(const Args& t, const Piece& p, int rows, int row, int d,
                                                const float* v, float m, float sum) {
     const RowPlace at = row_place(t, p, rows, row);
     int32_t first, last;
-    visible_range(t, p.seq.len, at.pos, first, last);
+    visible_range(t, p.seq, at.token, at.pos, first, last);
     const bool none = last <= first;
     const float inv = none ? 0.f : 1.f / sum;
     float y[8];
@@ -304,10 +318,10 @@ __device__ __forceinline__ bool store_row_part(const AttnArgs& t, const Piece& p
     return odd;
 }
 // One warp: the row from the definition.
-template <class T, int FMT>
-__device__ __forceinline__ void fix_row(const KvArgs& a, const AttnArgs& t, const Piece& p, int rows, int row) {
+template <class T, int FMT, class Args>
+__device__ __forceinline__ void fix_row(const KvArgs& a, const Args& t, const Piece& p, int rows, int row) {
     const RowPlace at = row_place(t, p, rows, row);
-    attend_row<T, FMT>(a, t, p.b, p.seq.len, at.token, at.pos, at.head);
+    attend_row<T, FMT>(a, t, p.b, p.seq, at.token, at.pos, at.head);
 }
 
 // What the joining kernels of share blockIdx.x begin with: the cut, and for the
@@ -362,8 +376,8 @@ __device__ __forceinline__ bool join_begin(const KvArgs& a, const AttnArgs& t, c
     __syncthreads();
     return true;
 }
-template <class T, int FMT, int ROWS, int JOIN, int PARTS>
-__device__ __forceinline__ void join_end(const KvArgs& a, const AttnArgs& t, JoinShared<JOIN, PARTS>& sh,
+template <class T, int FMT, int ROWS, int JOIN, int PARTS, class Args>
+__device__ __forceinline__ void join_end(const KvArgs& a, const Args& t, JoinShared<JOIN, PARTS>& sh,
                                          const Piece& p) {
     __syncthreads();
     for (uint32_t odd = sh.odd_rows; odd != 0; odd &= odd - 1) {
@@ -377,9 +391,9 @@ __device__ __forceinline__ void join_end(const KvArgs& a, const AttnArgs& t, Joi
 // each taking every 4th part; a row's warps are added in their order.
 constexpr int kMaxShares = 456;
 constexpr int kJoinFew = 4, kJoinFewThreads = 512;
-template <class T, int FMT, int ROWS>
+template <class T, int FMT, int ROWS, class Args>
 __global__ void __launch_bounds__(kJoinFewThreads) join_rows_kernel(const __grid_constant__ KvArgs a,
-                                                                    const __grid_constant__ AttnArgs t, int shares) {
+                                                                    const __grid_constant__ Args t, int shares) {
     __shared__ JoinShared<kJoinFew, kMaxShares> sh;
     __shared__ float4 meet[4][kJoinFew][32];
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -427,9 +441,9 @@ __global__ void __launch_bounds__(kJoinFewThreads) join_rows_kernel(const __grid
 // Items of 256 rows, few parts: 32 rows a block, a row a lane, 16 columns a
 // warp; the rows go out through shared memory.
 constexpr int kJoinMany = 32, kJoinManyThreads = 256, kManyShares = 152;
-template <class T, int FMT, int ROWS>
+template <class T, int FMT, int ROWS, class Args>
 __global__ void __launch_bounds__(kJoinManyThreads) join_columns_kernel(const __grid_constant__ KvArgs a,
-                                                                        const __grid_constant__ AttnArgs t,
+                                                                        const __grid_constant__ Args t,
                                                                         int shares) {
     __shared__ JoinShared<kJoinMany, kManyShares> sh;
     extern __shared__ float tile[];  // [32][dim + 1]
@@ -524,8 +538,9 @@ inline int shares_for(const KvArgs& a, const AttnArgs& t, int max_new, int max_l
 
 // Launched so that its blocks may start while the kernel before it still runs;
 // they wait for its end before they read.
-inline cudaError_t launch_join(void (*kernel)(KvArgs, AttnArgs, int), const KvArgs& a, const AttnArgs& t, int shares,
-                               int blocks_y, int threads, size_t shared, cudaStream_t s) {
+template <class Args>
+cudaError_t launch_join(void (*kernel)(KvArgs, Args, int), const KvArgs& a, const Args& t, int shares, int blocks_y,
+                        int threads, size_t shared, cudaStream_t s) {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)shares, (unsigned)blocks_y);
     cfg.blockDim = dim3((unsigned)threads);

@@ -1,0 +1,373 @@
+// cccl_step_verify.cu -- which drafted tokens the target keeps, and the next one.
+//
+// A cluster of blocks a sequence.  Its first block's first warp goes through the
+// tree; what needs a whole row of probabilities is done by all blocks, each over
+// its part of the row: a pass adds up R = max(p - A q, 0) warp by warp, and for
+// the next token the warp in whose part the sum passes u S looks its values
+// through again.  The first block says what to do next (Order); the others follow,
+// so that all meet at the same barriers whatever is in memory.
+//
+// Most steps take one pass: sums before it are only needed for a second child's
+// chance where the draft gave probabilities.  So the time is one read of a row of
+// p (and q) a sequence, behind the chain of loads that leads to it (rows, tokens
+// and parents, probabilities of the tokens).
+//
+// Sums: a value is taken as an integer multiple of 2^-56 (a binary32 number has 24
+// bits, so those above 2^-33 lose nothing and 2^17 smaller ones lose 2^-39 in all),
+// and integer sums do not depend on their order: neither on how a row is divided
+// nor on the number of blocks.
+#include "cccl_kv_launch.h"
+#include "cccl_kv_schedule.cuh"
+#include "cccl_step.cuh"
+
+namespace cccl {
+
+namespace {
+
+constexpr int kThreads = 512, kWarps = kThreads / 32, kMostBlocks = 8;
+constexpr uint64_t kOne = 1ull << 53;  // A of 1
+
+// x limited to 0..1, what is not a number to 0, in multiples of 2^-56.
+__device__ __forceinline__ uint64_t fixed(float x) {
+    int32_t b = __float_as_int(x);
+    b = b > 0x7F800000 ? 0 : min(max(b, 0), 0x3F800000);
+    const uint32_t e = (uint32_t)b >> 23, m = ((uint32_t)b & 0x7FFFFFu) | 0x800000u;
+    return ((uint64_t)m << 33) >> min(127u - e, 63u);
+}
+__device__ __forceinline__ float limited(float x) { return x > 0.f ? fminf(x, 1.f) : 0.f; }
+// A (in multiples of 2^-53) times q
+__device__ __forceinline__ uint64_t times(uint64_t A, uint64_t q) {
+    return A == kOne ? q : (__umul64hi(A, q) << 11) | ((A * q) >> 53);
+}
+template <bool DRAFT>
+__device__ __forceinline__ uint64_t weight(float p, float q, uint64_t A) {
+    const uint64_t x = fixed(p);
+    if (!DRAFT || A == 0) return x;
+    const uint64_t y = times(A, fixed(q));
+    return x > y ? x - y : 0;
+}
+__device__ __forceinline__ uint64_t warp_sum64(uint64_t x) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, o);
+    return x;
+}
+
+struct Order {
+    int64_t row;       // of p and q; -1: the sequence has none
+    uint64_t A;
+    uint64_t u;        // of the next token, in multiples of 2^-56
+    int32_t last;      // the next token is drawn (else only the sum is wanted)
+    int32_t refused;   // how many tokens p is taken without
+};
+struct Shared {
+    Order order;                    // the first block's
+    uint64_t totals[kMostBlocks];   // of every block, in every block
+    uint64_t warps[kWarps];
+    int32_t refused[kMaxDraft];     // the first block's; then every block's copy
+    int32_t parent[kMaxDraft], token[kMaxDraft], kept[kMaxDraft];
+    float p[kMaxDraft], q[kMaxDraft], u[kMaxDraft];
+};
+
+// The first warp's way through the tree.
+struct Way {
+    int32_t at, next, kept;  // current token, the next to look at, how many are kept
+    uint64_t A;
+    double left;     // without q: S
+    int32_t refused;
+    bool known;      // the sum at A has been taken
+    uint64_t sum;
+};
+// On to the end (true) or to where a sum is needed.
+template <bool DRAFT>
+__device__ __forceinline__ bool advance(Shared& s, int32_t n, Way& w) {
+    const int lane = threadIdx.x & 31;
+    for (;;) {
+        // the next token whose parent is the current one
+        int32_t i = -1;
+        for (int32_t base = w.next & ~31; base < n && i < 0; base += 32) {
+            const int32_t k = base + lane;
+            const uint32_t mine = __ballot_sync(0xFFFFFFFFu, k >= w.next && k < n && s.parent[k] == w.at);
+            if (mine != 0) i = base + __ffs(mine) - 1;
+        }
+        if (i < 0) return true;
+        const int32_t x = s.token[i];
+        const float p = limited(s.p[i]), u = s.u[i];
+        bool keep, again = false;
+        if (DRAFT) {
+            const float q = limited(s.q[i]);
+            if (w.A == 0) {
+                keep = (double)u * (double)q < (double)p;  // the product is exact
+            } else {
+                if (!w.known) {
+                    w.next = i;
+                    return false;
+                }
+                keep = (double)u * ((double)w.sum * 0x1p-56) * (double)q < (double)weight<DRAFT>(p, q, w.A) * 0x1p-56;
+            }
+        } else {
+            for (int32_t k = lane; k < w.refused; k += 32) again |= s.refused[k] == x;
+            again = __any_sync(0xFFFFFFFFu, again) != 0;
+            keep = !again && (double)u * w.left < (double)p;
+        }
+        w.next = i + 1;
+        if (keep) {
+            if (lane == 0) s.kept[w.kept] = i;
+            ++w.kept;
+            w.at = i;
+            w.A = 0;
+            w.left = 1.0;
+            w.refused = 0;
+        } else if (DRAFT) {
+            w.A += w.A == 0 ? kOne : w.sum >> 3;
+        } else if (!again) {
+            if (lane == 0) s.refused[w.refused] = x;
+            ++w.refused;
+            w.left -= (double)p;
+        }
+        w.known = false;
+        __syncwarp();
+    }
+}
+
+// A warp's part of a row: values from .. to - 1.
+struct Part {
+    int32_t from, to;
+};
+__device__ __forceinline__ Part part_of(int32_t vocab, int blocks, int rank, int warp) {
+    const int32_t each = ((vocab + blocks * kWarps - 1) / (blocks * kWarps) + 127) & ~127;
+    const int64_t from = (int64_t)(rank * kWarps + warp) * each;
+    return Part{(int32_t)min(from, (int64_t)vocab), (int32_t)min(from + each, (int64_t)vocab)};
+}
+// Values at .. at + 3 (VEC; lanes side by side) or at, at + 32, at + 64, at + 96.
+template <bool VEC>
+__device__ __forceinline__ void load4(const float* row, int32_t at, int32_t to, float* x) {
+    if (VEC && at + 4 <= to) {
+        const float4 v = *reinterpret_cast<const float4*>(row + at);
+        x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+        return;
+    }
+    constexpr int kStep = VEC ? 1 : 32;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = at + i * kStep < to ? row[at + i * kStep] : 0.f;
+}
+
+constexpr int kFlight = 4;  // times 128 values a warp
+
+template <bool DRAFT, bool VEC>
+__device__ __forceinline__ uint64_t add_up(const float* p, const float* q, const Order& o, const Part& part) {
+    const int lane = threadIdx.x & 31;
+    uint64_t sum = 0;
+    for (int32_t base = part.from + (VEC ? 4 * lane : lane); base < part.to; base += 128 * kFlight) {
+        float x[kFlight][4], y[kFlight][4] = {};
+#pragma unroll
+        for (int k = 0; k < kFlight; ++k) {
+            load4<VEC>(p, base + 128 * k, part.to, x[k]);
+            if (DRAFT && o.A != 0) load4<VEC>(q, base + 128 * k, part.to, y[k]);
+        }
+#pragma unroll
+        for (int k = 0; k < kFlight; ++k)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sum += weight<DRAFT>(x[k][i], y[k][i], o.A);
+    }
+    return warp_sum64(sum);
+}
+
+// The first value of the part at which the running sum passes `goal` (it does so
+// within the part), by one warp: 512 values at a time, then 32 of those.
+template <bool DRAFT>
+__device__ __forceinline__ int32_t find(const float* p, const float* q, const Order& o, const int32_t* refused,
+                                        const Part& part, uint64_t goal) {
+    constexpr int kRows = 16;
+    const int lane = threadIdx.x & 31;
+    for (int32_t base = part.from; base < part.to; base += 32 * kRows) {
+        float x[kRows], y[kRows];
+#pragma unroll
+        for (int k = 0; k < kRows; ++k) {
+            const int32_t at = base + 32 * k + lane;
+            x[k] = at < part.to ? p[at] : 0.f;
+            y[k] = DRAFT && o.A != 0 && at < part.to ? q[at] : 0.f;
+        }
+        uint64_t w[kRows], all = 0;
+#pragma unroll
+        for (int k = 0; k < kRows; ++k) {
+            w[k] = weight<DRAFT>(x[k], y[k], o.A);
+            for (int32_t i = 0; i < o.refused && w[k] != 0; ++i)
+                if (refused[i] == base + 32 * k + lane) w[k] = 0;
+            all += w[k];
+        }
+        __syncwarp();
+        all = warp_sum64(all);
+        if (goal >= all) {
+            goal -= all;
+            continue;
+        }
+#pragma unroll
+        for (int k = 0; k < kRows; ++k) {
+            uint64_t upto = w[k];
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const uint64_t z = __shfl_up_sync(0xFFFFFFFFu, upto, d);
+                if (lane >= d) upto += z;
+            }
+            const uint32_t past = __ballot_sync(0xFFFFFFFFu, upto > goal);
+            if (past != 0) return base + 32 * k + __ffs(past) - 1;
+            goal -= __shfl_sync(0xFFFFFFFFu, upto, 31);
+        }
+    }
+    return part.from;  // (not reached: the part's sum is above the goal)
+}
+
+template <bool DRAFT, bool VEC>
+__global__ void __launch_bounds__(kThreads) verify_kernel(const __grid_constant__ VerifyArgs a, int blocks) {
+    __shared__ Shared s;
+    const int rank = (int)cluster_rank(), b = (int)blockIdx.x / blocks;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    int64_t row0 = 0;
+    int32_t rows = 0, n = 0;
+    Way w{0, 1, 1, 0, 1.0, 0, false, 0};
+    if (rank == 0) {
+        const int64_t lo = a.cu[b], hi = a.cu[b + 1];
+        row0 = min(max(lo, (int64_t)0), a.rows);
+        const int64_t end = min(max(hi, row0), a.rows);
+        rows = (int32_t)(end - row0);
+        n = min(rows, kMaxDraft);
+        if (threadIdx.x == 0 && (row0 != lo || end != hi || n < rows)) record_error(a.ws, kStatusInvalidArg);
+        for (int32_t i = threadIdx.x; i < n; i += kThreads) {
+            int32_t up = -1;
+            float p = 0.f, q = 0.f;
+            const int32_t x = a.tokens[row0 + i];
+            if (i > 0 && x >= 0 && x < a.vocab) {
+                up = a.parents != nullptr ? a.parents[row0 + i] : i - 1;
+                if (up < 0 || up >= i) up = -1;
+                if (up >= 0) {
+                    p = a.p[(row0 + up) * a.p_stride + x];
+                    if (DRAFT) q = a.q[(row0 + up) * a.q_stride + x];
+                }
+            }
+            s.parent[i] = up;
+            s.token[i] = x;
+            s.p[i] = p;
+            s.q[i] = q;
+            s.u[i] = a.uniform[row0 + i];
+        }
+        if (threadIdx.x == 0) s.kept[0] = 0;
+        __syncthreads();
+    }
+    for (;;) {
+        if (rank == 0 && warp == 0) {
+            Order o{-1, 0, 0, 1, 0};
+            if (n > 0) {
+                o.last = advance<DRAFT>(s, n, w) ? 1 : 0;
+                o.row = row0 + w.at;
+                o.A = w.A;
+                o.u = fixed(s.u[0]);
+                o.refused = DRAFT ? 0 : w.refused;
+            }
+            if (lane == 0) s.order = o;
+        }
+        __syncthreads();
+        cluster_sync();
+        Order o;
+        {
+            const uint32_t at = in_block(smem_addr(&s.order), 0);
+            uint32_t words[sizeof(Order) / 4];
+#pragma unroll
+            for (int i = 0; i < (int)(sizeof(Order) / 4); ++i) words[i] = __float_as_uint(load_cluster(at + 4 * i));
+            memcpy(&o, words, sizeof(Order));
+            if (rank != 0)
+                for (int32_t i = threadIdx.x; i < o.refused; i += kThreads)
+                    s.refused[i] = __float_as_int(load_cluster(in_block(smem_addr(&s.refused[i]), 0)));
+        }
+        __syncthreads();
+        if (o.row < 0) {  // no rows at all
+            if (rank == 0 && threadIdx.x == 0) {
+                a.n_kept[b] = 0;
+                a.next[b] = -1;
+            }
+            __syncwarp();
+            cluster_sync();  // the first block's order has been read
+            return;
+        }
+        const float* p = a.p + o.row * a.p_stride;
+        const float* q = DRAFT ? a.q + o.row * a.q_stride : nullptr;
+        const Part part = part_of(a.vocab, blocks, rank, warp);
+        uint64_t total = 0;
+        for (int turn = 0; turn < 2; ++turn) {
+            uint64_t sum = add_up<DRAFT, VEC>(p, q, o, part);
+            if (o.refused > 0) {
+                uint64_t off = 0;
+                for (int32_t k = lane; k < o.refused; k += 32)
+                    if (s.refused[k] >= part.from && s.refused[k] < part.to) off += fixed(p[s.refused[k]]);
+                __syncwarp();
+                sum -= warp_sum64(off);
+            }
+            if (lane == 0) s.warps[warp] = sum;
+            __syncthreads();
+            if (threadIdx.x < (uint32_t)blocks) {
+                uint64_t mine = 0;
+                for (int i = 0; i < kWarps; ++i) mine += s.warps[i];
+                const uint32_t to = in_block(smem_addr(&s.totals[rank]), threadIdx.x);
+                asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(to), "l"(mine) : "memory");
+            }
+            __syncwarp();
+            cluster_sync();
+            total = 0;
+            for (int i = 0; i < blocks; ++i) total += s.totals[i];
+            if (!o.last || total != 0) break;
+            // nothing is left of p: the next token comes from p itself
+            if (o.A == 0 && o.refused == 0) break;
+            o.A = 0;
+            o.refused = 0;
+            cluster_sync();  // everyone has the totals
+        }
+        if (!o.last) {
+            w.sum = total;
+            w.known = true;
+            continue;
+        }
+        if (total == 0) {
+            if (rank == 0 && threadIdx.x == 0) {
+                record_error(a.ws, kStatusInvalidArg);
+                a.next[b] = 0;
+            }
+        } else {
+            uint64_t goal = (__umul64hi(total, o.u) << 8) | ((total * o.u) >> 56);
+            if (goal >= total) goal = total - 1;
+            uint64_t before = 0;  // of the values before this warp's
+            for (int i = 0; i < rank; ++i) before += s.totals[i];
+            for (int i = 0; i < warp; ++i) before += s.warps[i];
+            if (before <= goal && goal - before < s.warps[warp]) {
+                const int32_t y = find<DRAFT>(p, q, o, s.refused, part, goal - before);
+                if (lane == 0) a.next[b] = y;
+            }
+        }
+        break;
+    }
+    if (rank == 0) {
+        for (int32_t i = threadIdx.x; i < rows; i += kThreads) a.path[row0 + i] = -1;
+        __syncthreads();
+        if (warp == 0) {  // the one that knows
+            for (int32_t i = lane; i < w.kept; i += 32) a.path[row0 + i] = s.kept[i];
+            if (lane == 0) a.n_kept[b] = w.kept;
+        }
+    }
+}
+
+template <bool DRAFT, bool VEC>
+cudaError_t launch_one(const VerifyArgs& a, cudaStream_t s) {
+    // a warp's part is at least 128 values; 8 blocks a sequence while that leaves them some
+    int blocks = kMostBlocks;
+    while (blocks > 1 && a.vocab <= blocks * kWarps * 64) blocks /= 2;
+    return launch_clusters(verify_kernel<DRAFT, VEC>, a.batch * blocks, blocks, kThreads, 0, s, a, blocks);
+}
+
+}  // namespace
+
+cudaError_t launch_step_verify(const VerifyArgs& a, cudaStream_t s) {
+    const bool wide = (reinterpret_cast<uintptr_t>(a.p) & 15) == 0 && a.p_stride % 4 == 0;
+    if (a.q == nullptr) return wide ? launch_one<false, true>(a, s) : launch_one<false, false>(a, s);
+    const bool both = wide && (reinterpret_cast<uintptr_t>(a.q) & 15) == 0 && a.q_stride % 4 == 0;
+    return both ? launch_one<true, true>(a, s) : launch_one<true, false>(a, s);
+}
+
+}  // namespace cccl
