@@ -71,6 +71,12 @@ def _numbers(t: torch.Tensor, dtype: torch.dtype, n: int | None, device: int, wh
     return t.data_ptr()
 
 
+def _stream_on(device: int, stream) -> int:
+    if device < 0:
+        raise ValueError("all tensors of a call are on one CUDA device")
+    return _current_stream(device) if stream is None else stream.cuda_stream
+
+
 def _here(cache: KvCache, *tensors: torch.Tensor | None) -> None:
     for t in tensors:
         if t is not None and t.get_device() != cache._device:
@@ -168,7 +174,7 @@ def cccl_step_plan(tables: StepTables, lens: torch.Tensor, new: torch.Tensor, ws
                None if mask is None else mask.data_ptr(), stride, rows, words, 0)
     status = _plan(tables._ref, _numbers(lens, i32, batch, dev, "lens"), _numbers(new, i32, batch, dev, "new"),
                    None if parents is None else _numbers(parents, i32, rows, dev, "parents"), ctypes.addressof(out),
-                   ws.data_ptr(), ws.nbytes, _current_stream(dev) if stream is None else stream.cuda_stream)
+                   ws.data_ptr(), ws.nbytes, _stream_on(dev, stream))
     if status:
         _check(status, "cccl_step_plan")
 
@@ -259,7 +265,7 @@ def cccl_step_verify(p: torch.Tensor, q: torch.Tensor | None, tokens: torch.Tens
                    _numbers(cu_tokens, i32, batch + 1, dev, "cu_tokens"), rows, batch, vocab)
     status = _verify(ctypes.addressof(draft), _numbers(path, i32, rows, dev, "path"),
                      _numbers(n_kept, i32, batch, dev, "n_kept"), _numbers(next_token, i32, batch, dev, "next_token"),
-                     ws.data_ptr(), ws.nbytes, _current_stream(dev) if stream is None else stream.cuda_stream)
+                     ws.data_ptr(), ws.nbytes, _stream_on(dev, stream))
     if status:
         _check(status, "cccl_step_verify")
 
