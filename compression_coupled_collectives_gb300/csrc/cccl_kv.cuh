@@ -168,6 +168,35 @@ __device__ __forceinline__ void visible_range(const TreeArgs& t, const Sequence&
     first = r.x;
     last = r.y;
 }
+// Where a row's keys are to be looked for: its range, or without a window's
+// need of it all of the sequence, so that nothing waits for the mask (which is
+// asked for, for the tiles that need it).
+__device__ __forceinline__ void search_range(const AttnArgs& t, const Sequence& s, int64_t row, int32_t pos,
+                                             int32_t& first, int32_t& last) {
+    visible_range(t, s, row, pos, first, last);
+}
+__device__ __forceinline__ void search_range(const TreeArgs& t, const Sequence& s, int64_t row, int32_t pos,
+                                             int32_t& first, int32_t& last) {
+    if (t.window > 0) {
+        visible_range(t, s, row, pos, first, last);
+        return;
+    }
+    first = 0;
+    last = s.len;
+    asm volatile("prefetch.global.L1 [%0];" ::"l"(draft_bits(t, row)));
+}
+// Whether a row whose weights add up to `sum` sees no key.
+__device__ __forceinline__ bool sees_none(const AttnArgs& t, const Sequence& s, int64_t row, int32_t pos, float) {
+    int32_t first, last;
+    visible_range(t, s, row, pos, first, last);
+    return last <= first;
+}
+__device__ __forceinline__ bool sees_none(const TreeArgs& t, const Sequence& s, int64_t row, int32_t pos, float sum) {
+    if (sum > 0.f) return false;
+    int32_t first, last;
+    visible_range(t, s, row, pos, first, last);
+    return last <= first;
+}
 // Whether a row sees position j, which lies between its first and last.
 __device__ __forceinline__ bool drafted_seen(const AttnArgs&, const Sequence&, int64_t, int32_t) { return true; }
 __device__ __forceinline__ bool drafted_seen(const TreeArgs& t, const Sequence& s, int64_t row, int32_t j) {

@@ -61,7 +61,11 @@ constexpr int kRows = 256, kTileRows = 128, kTokens = 128;
 constexpr int kThreads = 512;
 constexpr int kShares = 152;
 static_assert(kShares <= kManyShares, "the joining kernel has room for every share's part");
-constexpr int kScaleSlots = 3;   // tiles of tokens whose scales are kept
+constexpr int kMostScaleSlots = 4;
+// Tiles of tokens whose scales are kept: with rows in two tiles, and where the
+// tiles of tokens are shared (narrow, below).
+template <class Args>
+constexpr int kScaleSlots = std::is_same<Args, TreeArgs>::value ? 4 : 3;
 constexpr int kLoaderWarps = 4;
 // K and V tiles in shared memory, as 16-bit values; tiles of 8-bit codes on
 // their way there
@@ -89,10 +93,10 @@ constexpr float kLower = M::kHalf ? 9.f : 0.f;
 constexpr uint32_t kSpread = 2u << 23;
 // Halves of result rows (128 bytes) that a softmax warp has on their way out at
 // a time
-template <int FMT>
-constexpr int kStageRows = FMT == kKv16Bit ? 16 : 8;
-template <int FMT>
-constexpr int kStageBytes = 8 * 128 * kStageRows<FMT>;
+template <int FMT, class Args>
+constexpr int kStageRows = FMT == kKv16Bit ? 16 : (std::is_same<Args, TreeArgs>::value ? 4 : 8);
+template <int FMT, class Args>
+constexpr int kStageBytes = 8 * 128 * kStageRows<FMT, Args>;
 
 // Registers of a thread: the launch's 4 x 128 a warpgroup, divided anew (two
 // softmax warpgroups, two of the others).
@@ -105,9 +109,10 @@ constexpr int kRing = 4;  // pieces handed on and not yet taken by all
 
 struct Shared {
     uint64_t q_full[2], s_full[2], p_full[2], o_full[2];
-    uint64_t kv_full[kMostSlots], kv_free[kMostSlots], scale_full[kScaleSlots];
+    uint64_t kv_full[kMostSlots], kv_free[kMostSlots], scale_full[kMostScaleSlots];
     uint64_t raw_full[kRawSlots], raw_free[kRawSlots];
     uint64_t drained;
+    uint64_t half_full[2], half_read[2];  // narrow items: a warpgroup's statistics are there, it has read both accumulators
     uint32_t tmem;
     uint32_t stop;  // a bounded wait ran out: every role leaves
     uint32_t odd;   // a row that the block wrote came out non-finite
@@ -117,12 +122,20 @@ struct Shared {
     // than in registers, which hold a row of S).
     Piece ring[kRing], piece[8][2];
     uint64_t piece_full[kRing], piece_free[kRing];
-    alignas(16) float k_scale[kScaleSlots][kTokens];
-    alignas(16) float v_scale[kScaleSlots][kTokens];
+    alignas(16) float k_scale[kMostScaleSlots][kTokens];
+    alignas(16) float v_scale[kMostScaleSlots][kTokens];
     // the largest value scale of each warp's rows (scale_bits), its lowest bit
     // instead saying whether others of them lie far below
-    alignas(16) uint32_t v_top[kScaleSlots][kLoaderWarps];
+    alignas(16) uint32_t v_top[kMostScaleSlots][kLoaderWarps];
 };
+
+// Narrow items, behind Shared: the reference and the sum of each warpgroup's rows.
+struct Halves {
+    float m[2][kTileRows], l[2][kTileRows];
+};
+template <class Args>
+constexpr size_t kHalvesBytes = std::is_same<Args, TreeArgs>::value ? sizeof(Halves) : 0;
+__device__ __forceinline__ Halves& halves_of(Shared* sh) { return *reinterpret_cast<Halves*>(sh + 1); }
 
 // ---------------------------------------------------------------- tcgen05
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -507,8 +520,8 @@ __device__ __forceinline__ RowScales row_scales(const KvArgs& a, const Piece& p,
     }
     return r;
 }
-template <int FMT>
-__device__ __forceinline__ void widen_role(const KvArgs& a, const AttnArgs& t, Shared* sh, uint32_t raw,
+template <int FMT, class Args>
+__device__ __forceinline__ void widen_role(const KvArgs& a, const Args& t, Shared* sh, uint32_t raw,
                                            uint32_t raw_bytes, uint32_t slots, uint32_t slot_bytes) {
     constexpr int kN = kSlots<FMT>;
     const int warp = (threadIdx.x >> 5) - 8, lane = threadIdx.x & 31;
@@ -522,7 +535,8 @@ __device__ __forceinline__ void widen_role(const KvArgs& a, const AttnArgs& t, S
             {
                 // V of tile j - 1 has a slot, so K of tile j - 2 was freed, so both
                 // row tiles are done with the scales of tile j - 3: three slots do
-                const uint32_t n = (entry / 2) % kScaleSlots;
+                // (narrow items: K of j - 2 meets the queries when tile j - 4 is done)
+                const uint32_t n = (entry / 2) % kScaleSlots<Args>;
                 sh->k_scale[n][32 * warp + lane] = scales.k;
                 sh->v_scale[n][32 * warp + lane] = scales.v;
                 const uint32_t bits = scale_bits(scales.v), top = __reduce_max_sync(0xFFFFFFFFu, bits);
@@ -539,7 +553,7 @@ __device__ __forceinline__ void widen_role(const KvArgs& a, const AttnArgs& t, S
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
-                    if (side == 0) mbar_arrive(&sh->scale_full[(entry / 2) % kScaleSlots]);
+                    if (side == 0) mbar_arrive(&sh->scale_full[(entry / 2) % kScaleSlots<Args>]);
                     mbar_arrive(&sh->kv_full[s]);
                     mbar_arrive(&sh->raw_free[q]);
                 }
@@ -548,10 +562,27 @@ __device__ __forceinline__ void widen_role(const KvArgs& a, const AttnArgs& t, S
     }
 }
 
+// Items of drafted tokens that have no more than one tile of rows are narrow: one
+// tile's softmax alone leaves the tensor core waiting most of the time, so both
+// warpgroups take the same rows (each has them in its Q), the one the tiles of
+// tokens of even number, the other the odd ones, and they put their accumulators
+// together at the piece's end.  32 sequences of 4096 tokens, 16 drafted, groups of
+// 4: NARROW_NOTE.
+template <class Args>
+__device__ __forceinline__ bool narrow(const Args& t, const Piece& p) {
+    return std::is_same<Args, TreeArgs>::value && live_rows<kRows>(t, p) <= kTileRows;
+}
+// Tiles of tokens of warpgroup i.
+template <class Args>
+__device__ __forceinline__ int32_t own_tiles(const Args& t, const Piece& p, int i) {
+    if (narrow(t, p)) return (p.count - i + 1) / 2;
+    return live_rows<kRows>(t, p) > i * kTileRows ? p.count : 0;
+}
+
 // ---------------------------------------------------------------- products
 // Returns whether this lane is the one that issued them.
-template <class M, int SLOTS>
-__device__ __forceinline__ bool mma_role(const KvArgs& a, const AttnArgs& t, Shared* sh, uint32_t q_base,
+template <class M, int SLOTS, class Args>
+__device__ __forceinline__ bool mma_role(const KvArgs& a, const Args& t, Shared* sh, uint32_t q_base,
                                          uint32_t slots, uint32_t slot_bytes) {
     const Waiter wait{sh, a.ws};
     const uint32_t tmem = sh->tmem;
@@ -596,6 +627,38 @@ __device__ __forceinline__ bool mma_role(const KvArgs& a, const AttnArgs& t, Sha
     for (uint32_t n = 0; take_piece(wait, n, &p) && p.count > 0; ++n) {
         const int tiles = live_rows<kRows>(t, p) > kTileRows ? 2 : 1;
         const int32_t count = p.count;
+        if (narrow(t, p)) {
+            auto scores = [&](int32_t j) {  // of tile j, when its K is there
+                const uint32_t k = entry + 2 * (uint32_t)j;
+                if (!wait(&sh->kv_full[k % SLOTS], (k / SLOTS) & 1)) return false;
+                if (j < 2) {
+                    if (!wait(&sh->q_full[j], q_phase[j])) return false;
+                    q_phase[j] ^= 1;
+                }
+                tc_fence_after();
+                product_qk(j & 1, k % SLOTS);
+                commit(&sh->kv_free[k % SLOTS]);
+                return true;
+            };
+            for (int32_t j = 0; j < min(count, 2); ++j)
+                if (!scores(j)) return leader != 0;
+            for (int32_t j = 0; j < count; ++j) {
+                const int i = j & 1;
+                const uint32_t v = entry + 2 * (uint32_t)j + 1;
+                if (!wait(&sh->kv_full[v % SLOTS], (v / SLOTS) & 1)) return leader != 0;
+                if (!wait(&sh->p_full[i], p_phase[i])) return leader != 0;
+                p_phase[i] ^= 1;
+                tc_fence_after();
+                product_pv(i, v % SLOTS, j > 1);
+                commit(&sh->kv_free[v % SLOTS]);
+                if (j + 2 >= count)
+                    commit(&sh->o_full[i]);
+                else if (!scores(j + 2))
+                    return leader != 0;
+            }
+            entry += 2 * (uint32_t)count;
+            continue;
+        }
         // K of the first tile
         if (!wait(&sh->kv_full[entry % SLOTS], (entry / SLOTS) & 1)) return leader != 0;
         for (int i = 0; i < tiles; ++i) {
@@ -748,10 +811,11 @@ template <class T, int FMT, class Args>
 __device__ __forceinline__ void softmax_role(const KvArgs& a, const Args& t, Shared* sh, uint32_t q_tile,
                                              uint32_t stages, float* joint) {
     using M = Operand<T, FMT>;
+    constexpr bool kTree = std::is_same<Args, TreeArgs>::value;
     const int i = threadIdx.x / 128, row = threadIdx.x % 128, warp = row >> 5, lane = row & 31;
     const int me = threadIdx.x >> 5;
     const Waiter wait{sh, a.ws};
-    const uint32_t tmem = sh->tmem + ((uint32_t)(32 * warp) << 16), stage = stages + me * (128 * kStageRows<FMT>);
+    const uint32_t tmem = sh->tmem + ((uint32_t)(32 * warp) << 16), stage = stages + me * (128 * kStageRows<FMT, Args>);
     const uint32_t at_s = tmem + kColS + 128 * i, at_o = tmem + kColO + 128 * i;
     const float scale_base2 = fabsf(t.scale) * 1.4426950408889634f;
     // hidden scores are -infinity when the scale meets them: a scale of zero (or one
@@ -761,6 +825,7 @@ __device__ __forceinline__ void softmax_role(const KvArgs& a, const Args& t, Sha
     uint32_t s_phase = 0, o_phase = 0, taken = 0, tile = 0;  // tile: this block's tiles of tokens, whoever's
     int slot = 1;                                 // of the piece at hand
     int32_t first = 0, last = 0;                  // what this row sees
+    uint32_t halves = 0;                          // narrow pieces put together so far
     float m = -INFINITY, l = 0.f;
     for (bool begin = true;; begin = false) {
         // the next piece that has rows for this warpgroup.  Its rows of Q may
@@ -771,7 +836,7 @@ __device__ __forceinline__ void softmax_role(const KvArgs& a, const Args& t, Sha
         for (;; ++taken) {
             Piece p;
             if (!take_piece(wait, taken, &p)) return;
-            if (p.count > 0 && live_rows<kRows>(t, p) <= i * kTileRows) {
+            if (p.count > 0 && own_tiles(t, p, i) == 0) {
                 skipped += (uint32_t)p.count;
                 continue;
             }
@@ -781,14 +846,17 @@ __device__ __forceinline__ void softmax_role(const KvArgs& a, const Args& t, Sha
         }
         ++taken;
         const bool more = next->count > 0;
-        if (more) to_base2 = fmaxf(scale_base2 * bring_rows<T, FMT>(a, t, *next, i, warp, q_tile), least);
+        if (more)
+            to_base2 = fmaxf(scale_base2 * bring_rows<T, FMT>(a, t, *next, narrow(t, *next) ? 0 : i, warp, q_tile), least);
         if (!begin) {  // the end of the piece at hand
             const Piece& cur = sh->piece[me][slot];
             if (!wait(&sh->o_full[i], o_phase)) return;
             o_phase ^= 1;
             tc_fence_after();
             const bool full = cur.count == cur.range.n;
-            const int tile_row = i * kTileRows + row;
+            // narrow: the other warpgroup has the rest of these rows' tiles
+            const bool shared = narrow(t, cur) && cur.count > 1;
+            const int tile_row = (narrow(t, cur) ? 0 : i * kTileRows) + row;
             const bool is_row = tile_row < live_rows<kRows>(t, cur);
             const RowPlace at = row_place(t, cur, kRows, tile_row);
             const PartLayout parts = part_layout(a, gridDim.x, kRows);
@@ -797,17 +865,48 @@ __device__ __forceinline__ void softmax_role(const KvArgs& a, const Args& t, Sha
             float* const stats = joint != nullptr ? joint + kRows * a.dim : parts.stats(blockIdx.x, which);
             // a joint part takes the tiles' place: when both row tiles' products are done
             if (joint != nullptr && live_rows<kRows>(t, cur) > kTileRows && !wait(&sh->o_full[1], 0)) return;
-            const bool none = last <= first;
+            float mine = 1.f, theirs = 0.f;  // the accumulators' weights
+            if (kTree && shared) {
+                Halves& half = halves_of(sh);
+                half.m[i][row] = m;
+                half.l[i][row] = l;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh->half_full[i]);
+                if (!wait(&sh->half_full[i ^ 1], halves & 1)) return;
+                ++halves;
+                tc_fence_after();
+                const float other = half.m[i ^ 1][row], to = fmaxf(m, other);
+                const float base = to == -INFINITY ? 0.f : to;
+                mine = exp2_fast(m - base);
+                theirs = exp2_fast(other - base);
+                l = l * mine + half.l[i ^ 1][row] * theirs;
+                m = to;
+            }
+            // two warpgroups with the same rows take 64 columns of them in turn
+            const int from = kTree && shared ? 64 * i : 0, step = kTree && shared ? 128 : 64;
+            const bool none = kTree ? is_row && sees_none(t, cur.seq, at.token, at.pos, l) : last <= first;
             const float inv = none ? 0.f : 1.f / l;
             bool odd = false;
             if (full) {
                 uint8_t* const to = t.out + at.token * t.o_token + (int64_t)at.head * t.o_head;
 #pragma unroll 1
-                for (int c = 0; c < a.dim; c += 64) {
+                for (int c = from; c < a.dim; c += step) {
                     uint32_t o[64], y[32];
                     tc_load32(at_o + c, o);
                     tc_load32(at_o + c + 32, o + 32);
                     tc_wait_load();
+                    if (kTree && shared) {
+#pragma unroll
+                        for (int h = 0; h < 64; h += 16) {
+                            uint32_t x[16];
+                            tc_load16((i == 0 ? at_o + 128 : at_o - 128) + c + h, x);
+                            tc_wait_load();
+#pragma unroll
+                            for (int k = 0; k < 16; ++k)
+                                o[h + k] = __float_as_uint(__uint_as_float(o[h + k]) * mine +
+                                                           __uint_as_float(x[k]) * theirs);
+                        }
+                    }
 #pragma unroll
                     for (int k = 0; k < 64; k += 2) {
                         const float u = none ? 0.f : __uint_as_float(o[k]) * inv;
@@ -815,30 +914,45 @@ __device__ __forceinline__ void softmax_role(const KvArgs& a, const Args& t, Sha
                         odd |= c + k < a.dim && !(fabsf(u) <= 3.402823466e+38f && fabsf(v) <= 3.402823466e+38f);
                         y[k / 2] = pack<T>(u, v);
                     }
-                    store_rows<kStageRows<FMT>>(stage, y, is_row ? to + 2 * c : nullptr, 2 * (a.dim - c));
+                    store_rows<kStageRows<FMT, Args>>(stage, y, is_row ? to + 2 * c : nullptr, 2 * (a.dim - c));
                 }
             } else {
                 float* dst = acc + tile_row;
 #pragma unroll 1
-                for (int c = 0; c < a.dim; c += 16) {
+                for (int c = from; c < a.dim; c += 16) {
+                    if (kTree && shared && (c & 64) != from) continue;
                     uint32_t o[16];
                     tc_load16(at_o + c, o);
                     tc_wait_load();
+                    if (kTree && shared) {
+                        uint32_t x[16];
+                        tc_load16((i == 0 ? at_o + 128 : at_o - 128) + c, x);
+                        tc_wait_load();
+#pragma unroll
+                        for (int k = 0; k < 16; ++k)
+                            o[k] = __float_as_uint(__uint_as_float(o[k]) * mine + __uint_as_float(x[k]) * theirs);
+                    }
                     if (is_row) {
 #pragma unroll
                         for (int k = 0; k < 16; ++k) dst[(size_t)(c + k) * kRows] = __uint_as_float(o[k]);
                     }
                 }
             }
-            if (full) {
-                if (is_row && t.lse != nullptr)
-                    t.lse[at.token * t.q_heads + at.head] = none ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
-                if (odd && is_row) *reinterpret_cast<volatile uint32_t*>(&sh->odd) = 1;
-            } else if (is_row) {
-                stats[tile_row] = m;
-                stats[kRows + tile_row] = l;
+            if (!(kTree && shared && i != 0)) {
+                if (full) {
+                    if (is_row && t.lse != nullptr)
+                        t.lse[at.token * t.q_heads + at.head] = none ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+                } else if (is_row) {
+                    stats[tile_row] = m;
+                    stats[kRows + tile_row] = l;
+                }
             }
+            if (full && odd && is_row) *reinterpret_cast<volatile uint32_t*>(&sh->odd) = 1;
             tc_fence_before();
+            if (kTree && shared) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh->half_read[i]);
+            }
         }
         if (!more) return;
         copy_wait<0>();
@@ -849,19 +963,30 @@ __device__ __forceinline__ void softmax_role(const KvArgs& a, const Args& t, Sha
         tile += skipped;
         const Piece& cur = sh->piece[me][slot];
         first = last = 0;
-        const RowPlace own = row_place(t, cur, kRows, i * kTileRows + row);
-        if (i * kTileRows + row < live_rows<kRows>(t, cur))
-            visible_range(t, cur.seq, own.token, own.pos, first, last);
-        const int32_t count = cur.count;
+        const bool alone = kTree && narrow(t, cur);  // its rows are row tile 0's
+        const RowPlace own = row_place(t, cur, kRows, (alone ? 0 : i * kTileRows) + row);
+        const bool is_row = (alone ? 0 : i * kTileRows) + row < live_rows<kRows>(t, cur);
+        if (is_row) search_range(t, cur.seq, own.token, own.pos, first, last);
+        const int32_t count = cur.count, stride = alone ? 2 : 1;
         m = -INFINITY;
         l = 0.f;
         int32_t base = (cur.range.lo + cur.from) * kTokens;
-        for (int32_t j = 0; j < count; ++j, ++tile, base += kTokens) {
-            if (!wait(&sh->s_full[i], s_phase)) return;
-            s_phase ^= 1;
-            tc_fence_after();
-            const uint32_t scale_slot = tile % kScaleSlots;
-            if (FMT != kKv16Bit && !wait(&sh->scale_full[scale_slot], (tile / kScaleSlots) & 1)) return;
+        if (alone && i != 0) {
+            ++tile;
+            base += kTokens;
+        }
+        const bool idle = kTree && __any_sync(0xFFFFFFFFu, is_row) == 0;  // a warp without rows
+        // every place from here to there is seen by all of the warp's rows
+        const int32_t whole_from = kTree ? __reduce_max_sync(0xFFFFFFFFu, is_row ? first : 0) : 0;
+        const int32_t whole_to =
+            kTree ? __reduce_min_sync(0xFFFFFFFFu, is_row ? gapless_below(t, cur.seq, last) : 0x7FFFFFFF) : 0;
+        // one tile of tokens; false: a wait ran out.  MASKED: some places are hidden
+        // from some rows (drafted tokens: in code of its own, since as a branch that is
+        // hardly ever taken it cost every tile 10 %)
+        auto one_tile = [&](bool start, auto masked) -> bool {
+            constexpr bool kMasked = decltype(masked)::value;
+            const uint32_t scale_slot = tile % kScaleSlots<Args>;
+            if (FMT != kKv16Bit && !wait(&sh->scale_full[scale_slot], (tile / kScaleSlots<Args>) & 1)) return false;
             uint32_t s[kTokens];
 #pragma unroll
             for (int c = 0; c < kTokens; c += 32) tc_load32(at_s + c, s + c);
@@ -881,7 +1006,7 @@ __device__ __forceinline__ void softmax_role(const KvArgs& a, const Args& t, Sha
                     }
                 }
             }
-            if (base < first || base + kTokens > gapless_below(t, cur.seq, last)) {
+            if (kTree ? kMasked : base < first || base + kTokens > last) {
 #pragma unroll
                 for (int c = 0; c < kTokens; c += 32) {
                     uint32_t seen = bits_below(last - base - c) & ~bits_below(first - base - c);
@@ -902,7 +1027,7 @@ __device__ __forceinline__ void softmax_role(const KvArgs& a, const Args& t, Sha
                 v = *reinterpret_cast<const uint4*>(sh->v_top[scale_slot]);
                 top += scale_log2(max(max(v.x, v.y), max(v.z, v.w)));
             }
-            const bool move = j == 0 || __any_sync(0xFFFFFFFFu, top > m + (kSlack<M> + kLower<M>));
+            const bool move = start || __any_sync(0xFFFFFFFFu, top > m + (kSlack<M> + kLower<M>));
             // 8-bit caches: so far a bound of what the tile adds at most; what it is
             // exactly is only looked for where the reference would follow it
             if (FMT != kKv16Bit && move && scales_apart(v)) {
@@ -917,11 +1042,12 @@ __device__ __forceinline__ void softmax_role(const KvArgs& a, const Args& t, Sha
                         const float x = __uint_as_float(o[k]) * sh->k_scale[scale_slot][c + k];
                         const float y = fmaf(x, to_base2, scale_log2(scale_bits(sh->v_scale[scale_slot][c + k])));
                         const int32_t at = base + c + k;
-                        if (at >= first && at < last && drafted_seen(t, cur.seq, own.token, at)) top = fmaxf(top, y);
+                        if (at >= first && at < last && (!kMasked || drafted_seen(t, cur.seq, own.token, at)))
+                            top = fmaxf(top, y);
                     }
                 }
             }
-            if (j == 0) {
+            if (start) {
                 m = top - kLower<M>;
             } else if (move) {
                 const float to = fmaxf(m, top - kLower<M>);
@@ -969,10 +1095,33 @@ __device__ __forceinline__ void softmax_role(const KvArgs& a, const Args& t, Sha
             sum0 = add2(sum0, sum1);
             l += sum0.x + sum0.y;
             tc_wait_store();
+            return true;
+        };
+        int32_t j = alone ? i : 0;
+        bool start = true;
+        for (; j < count; j += stride, tile += stride, base += stride * kTokens, start = false) {
+            if (!wait(&sh->s_full[i], s_phase)) return;
+            s_phase ^= 1;
+            tc_fence_after();
+            if constexpr (kTree) {
+                if (!idle) {  // (what an idle warp's rows come to is nobody's)
+                    if (base >= whole_from && base + kTokens <= whole_to) {
+                        if (!one_tile(start, std::false_type{})) return;
+                    } else {
+                        if (!one_tile(start, std::true_type{})) return;
+                    }
+                }
+                // the other warpgroup may still be reading this one's accumulator of the piece before
+                if (start && halves > 0 && !wait(&sh->half_read[i ^ 1], (halves - 1) & 1)) return;
+            } else {
+                if (!one_tile(start, std::false_type{})) return;
+            }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh->p_full[i]);
         }
+        // on to the end of the piece's tiles, whoever's
+        if (alone) tile -= (uint32_t)(j - count);
     }
 }
 
@@ -1072,7 +1221,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tile_bytes = (a.dim > 64 ? 2 : 1) * kHalfBytes;
     const uint32_t raw_bytes = FMT == kKv16Bit ? 0 : kRawSlots * kTokens * a.dim;
     Shared* sh = reinterpret_cast<Shared*>(raw + (base - smem_addr(raw)) + (2 + kN) * tile_bytes + raw_bytes +
-                                           kStageBytes<FMT>);
+                                           kStageBytes<FMT, Args>);
     const int warp = threadIdx.x >> 5;
     if (warp == 0) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&sh->tmem))
@@ -1094,12 +1243,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&sh->raw_full[i], 2);
             mbar_init(&sh->raw_free[i], kLoaderWarps);
         }
-        for (int i = 0; i < kScaleSlots; ++i) mbar_init(&sh->scale_full[i], kLoaderWarps);
+        for (int i = 0; i < kMostScaleSlots; ++i) mbar_init(&sh->scale_full[i], kLoaderWarps);
         for (int i = 0; i < kRing; ++i) {
             mbar_init(&sh->piece_full[i], 1);
             mbar_init(&sh->piece_free[i], FMT == kKv16Bit ? 13 : 15);  // the warps that take pieces
         }
         mbar_init(&sh->drained, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sh->half_full[i], 4);
+            mbar_init(&sh->half_read[i], 4);
+        }
         sh->stop = sh->odd = 0;
         fence_mbar_init();
     }
@@ -1170,16 +1323,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(sh->tmem) : "memory");
 }
 
-template <int FMT>
+template <int FMT, class Args>
 constexpr size_t shared_bytes(int dim) {
     return 1024 + (size_t)(2 + kSlots<FMT>) * (dim > 64 ? 2 : 1) * kHalfBytes +
-           (FMT == kKv16Bit ? 0 : (size_t)kRawSlots * kTokens * dim) + kStageBytes<FMT> + sizeof(Shared);
+           (FMT == kKv16Bit ? 0 : (size_t)kRawSlots * kTokens * dim) + kStageBytes<FMT, Args> + sizeof(Shared) + kHalvesBytes<Args>;
 }
 
 static_assert(1024 * (128 + 2) <= (2 + kSlots<kKvInt8>) * 2 * kHalfBytes &&
                   1024 * (64 + 2) <= (2 + kSlots<kKvInt8>) * kHalfBytes,
               "a joint part takes the place of Q and the slots");
-static_assert(shared_bytes<kKv16Bit>(128) <= 232448 && shared_bytes<kKvInt8>(128) <= 232448, "227 KB a block");
+static_assert(shared_bytes<kKv16Bit, AttnArgs>(128) <= 232448 && shared_bytes<kKvInt8, AttnArgs>(128) <= 232448 &&
+                  shared_bytes<kKv16Bit, TreeArgs>(128) <= 232448 && shared_bytes<kKvInt8, TreeArgs>(128) <= 232448,
+              "227 KB a block");
 
 using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
                               const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
@@ -1238,10 +1393,10 @@ cudaError_t launch_one(const KvArgs& a, const Args& t, int max_new, int max_len,
         if (set != cudaSuccess) return set;
         const cudaError_t both = cudaFuncSetAttribute(attend_chunk_kernel<T, FMT, Args, true>,
                                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                      (int)shared_bytes<FMT>(128));
+                                                      (int)shared_bytes<FMT, Args>(128));
         if (both != cudaSuccess) return both;
         return cudaFuncSetAttribute(attend_chunk_kernel<T, FMT, Args, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    (int)shared_bytes<FMT>(128));
+                                    (int)shared_bytes<FMT, Args>(128));
     });
     if (e != cudaSuccess) return e;
     CUtensorMap k_map{}, v_map{};
@@ -1265,10 +1420,10 @@ cudaError_t launch_one(const KvArgs& a, const Args& t, int max_new, int max_len,
     const int cluster = 4 * tiled <= 128 ? 4 : 2 * tiled <= 128 ? 2 : 1;
     if (cluster > 1 && max_len > (cluster == 4 ? 3 : 7) * kTokens && max_len <= 16 * cluster * kTokens)
         return launch_clusters(attend_chunk_kernel<T, FMT, Args, true>, (int)tiled * cluster, cluster, kThreads,
-                               shared_bytes<FMT>(a.dim), s, a, t, k_map, v_map, box, cluster);
+                               shared_bytes<FMT, Args>(a.dim), s, a, t, k_map, v_map, box, cluster);
     const int shares = shares_for(a, t, max_new, max_len, kRows, kTokens, kShares);
     attend_chunk_kernel<T, FMT, Args, false>
-        <<<shares, kThreads, shared_bytes<FMT>(a.dim), s>>>(a, t, k_map, v_map, box, whole ? 1 : 0);
+        <<<shares, kThreads, shared_bytes<FMT, Args>(a.dim), s>>>(a, t, k_map, v_map, box, whole ? 1 : 0);
     e = cudaGetLastError();
     if (e != cudaSuccess || whole) return e;
     return launch_join(join_columns_kernel<T, FMT, kRows, Args>, a, t, shares, kRows / kJoinMany, kJoinManyThreads,

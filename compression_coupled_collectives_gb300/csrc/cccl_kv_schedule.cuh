@@ -299,9 +299,7 @@ template <class T, class Args>
 __device__ __forceinline__ bool store_row_part(const Args& t, const Piece& p, int rows, int row, int d,
                                                const float* v, float m, float sum) {
     const RowPlace at = row_place(t, p, rows, row);
-    int32_t first, last;
-    visible_range(t, p.seq, at.token, at.pos, first, last);
-    const bool none = last <= first;
+    const bool none = sees_none(t, p.seq, at.token, at.pos, sum);
     const float inv = none ? 0.f : 1.f / sum;
     float y[8];
     bool odd = false;

@@ -505,7 +505,7 @@ __global__ void __launch_bounds__(kThreads, S::kBlocksPerSm)
                 first[nr][i] = last[nr][i] = 0;
                 if (8 * nr + 2 * c + i < live) {
                     const RowPlace at = row_place(t, p, S::kRows, 8 * nr + 2 * c + i);
-                    visible_range(t, p.seq, at.token, at.pos, first[nr][i], last[nr][i]);
+                    search_range(t, p.seq, at.token, at.pos, first[nr][i], last[nr][i]);
                     all_from = max(all_from, first[nr][i]);
                     all_to = min(all_to, gapless_below(t, p.seq, last[nr][i]));
                 }
