@@ -136,6 +136,20 @@ bool device_range(const void* p, size_t bytes) {
     return a >= base && bytes <= size && a - base <= size - bytes;
 }
 
+bool DeviceRanges::ok(const void* p, size_t bytes) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+    if (size_ == 0 || a < base_ || a - base_ >= size_) {
+        const AddrRangeFn range = addr_range_fn();
+        CUdeviceptr base = 0;
+        size_t size = 0;
+        if (p == nullptr || range == nullptr || range(&base, &size, reinterpret_cast<CUdeviceptr>(p)) != CUDA_SUCCESS)
+            return false;
+        base_ = (uintptr_t)base;
+        size_ = size;
+    }
+    return a >= base_ && bytes <= size_ && a - base_ <= size_ - bytes;
+}
+
 }  // namespace cccl
 
 extern "C" {

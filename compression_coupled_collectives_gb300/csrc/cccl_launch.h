@@ -31,6 +31,16 @@ class PerDeviceOnce {
 
 // True if [p, p + bytes) lies inside one device (or managed) allocation.
 bool device_range(const void* p, size_t bytes);
+// The same for many pointers of one call: those that lie in the allocation of the
+// one before are not looked up again.
+class DeviceRanges {
+  public:
+    bool ok(const void* p, size_t bytes);
+
+  private:
+    uintptr_t base_ = 0;
+    size_t size_ = 0;
+};
 
 constexpr int kMaxRanks = 64;
 

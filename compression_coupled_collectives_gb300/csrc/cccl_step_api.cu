@@ -14,7 +14,6 @@
 #include "cccl_step.h"
 
 using cccl::aligned;
-using cccl::device_range;
 using cccl::empty;
 using cccl::extent;
 using cccl::fill;
@@ -23,19 +22,23 @@ using cccl::shapes_ok;
 
 namespace {
 
-// n numbers of `bytes` each, aligned to their size.
-bool numbers(const void* p, int64_t n, int bytes) {
-    return aligned(p, (uintptr_t)bytes) && device_range(p, (size_t)n * (size_t)bytes);
-}
-// rows of `inner` numbers, `stride` apart
-bool rows_ok(const void* p, int64_t rows, int64_t stride, int64_t inner, int bytes) {
-    const int64_t n[1] = {rows}, st[1] = {stride};
-    int64_t values = 0;
-    return extent(n, st, 1, inner, &values) && numbers(p, values, bytes);
-}
-bool workspace(void* d_ws, size_t ws_bytes) {
-    return aligned(d_ws, 16) && ws_bytes >= sizeof(cccl::WsHeader) && device_range(d_ws, sizeof(cccl::WsHeader));
-}
+// The pointers of one call.
+struct Pointers {
+    cccl::DeviceRanges ranges;
+    // n numbers of `bytes` each, aligned to their size
+    bool numbers(const void* p, int64_t n, int bytes) {
+        return aligned(p, (uintptr_t)bytes) && ranges.ok(p, (size_t)n * (size_t)bytes);
+    }
+    // rows of `inner` numbers, `stride` apart
+    bool rows(const void* p, int64_t rows, int64_t stride, int64_t inner, int bytes) {
+        const int64_t n[1] = {rows}, st[1] = {stride};
+        int64_t values = 0;
+        return extent(n, st, 1, inner, &values) && numbers(p, values, bytes);
+    }
+    bool workspace(void* d_ws, size_t ws_bytes) {
+        return aligned(d_ws, 16) && ws_bytes >= sizeof(cccl::WsHeader) && ranges.ok(d_ws, sizeof(cccl::WsHeader));
+    }
+};
 cccl_status status_of(cudaError_t e) { return e == cudaSuccess ? CCCL_OK : CCCL_ERR_CUDA; }
 
 }  // namespace
@@ -55,16 +58,17 @@ cccl_status cccl_step_plan(const cccl_step_tables* h_tables, const int32_t* d_le
                            : o->mask_words != 0)
         return CCCL_ERR_INVALID_ARG;
     if (t->batch == 0) return CCCL_OK;
-    if (!workspace(d_ws, ws_bytes) || !rows_ok(t->page_table, t->batch, t->table_stride, t->table_pages, 4) ||
-        !numbers(t->held, t->batch, 4) || !numbers(t->free_pages, t->free_capacity, 4) || !numbers(t->free_count, 1, 4) ||
-        !numbers(d_lens, t->batch, 4) || !numbers(d_new, t->batch, 4) ||
-        !numbers(o->cu_tokens, (int64_t)t->batch + 1, 4) || !numbers(o->kv_lens, t->batch, 4) ||
-        !numbers(o->held, t->batch, 4) || !numbers(o->free_count, 1, 4))
+    Pointers at;
+    if (!at.workspace(d_ws, ws_bytes) || !at.rows(t->page_table, t->batch, t->table_stride, t->table_pages, 4) ||
+        !at.numbers(t->held, t->batch, 4) || !at.numbers(t->free_pages, t->free_capacity, 4) || !at.numbers(t->free_count, 1, 4) ||
+        !at.numbers(d_lens, t->batch, 4) || !at.numbers(d_new, t->batch, 4) ||
+        !at.numbers(o->cu_tokens, (int64_t)t->batch + 1, 4) || !at.numbers(o->kv_lens, t->batch, 4) ||
+        !at.numbers(o->held, t->batch, 4) || !at.numbers(o->free_count, 1, 4))
         return CCCL_ERR_INVALID_ARG;
-    if (o->rows > 0 && ((d_parents != nullptr && !numbers(d_parents, o->rows, 4)) ||
-                        (o->slots != nullptr && !numbers(o->slots, o->rows, 8)) ||
-                        (o->positions != nullptr && !numbers(o->positions, o->rows, 4)) ||
-                        (o->mask != nullptr && !rows_ok(o->mask, o->rows, o->mask_stride, o->mask_words, 4))))
+    if (o->rows > 0 && ((d_parents != nullptr && !at.numbers(d_parents, o->rows, 4)) ||
+                        (o->slots != nullptr && !at.numbers(o->slots, o->rows, 8)) ||
+                        (o->positions != nullptr && !at.numbers(o->positions, o->rows, 4)) ||
+                        (o->mask != nullptr && !at.rows(o->mask, o->rows, o->mask_stride, o->mask_words, 4))))
         return CCCL_ERR_INVALID_ARG;
     cccl::PlanArgs a{};
     a.lens = d_lens;
@@ -133,8 +137,9 @@ cccl_status cccl_step_write(const cccl_kv_cache* h_cache, const cccl_kv_batch* h
         return CCCL_ERR_INVALID_ARG;
     if (empty(b)) return CCCL_OK;
     cccl::KvArgs a{};
-    if (!fill(c, b, d_ws, ws_bytes, sizeof(cccl::WsHeader), &a) || !numbers(r->turns, r->rot_dim / 2, 8) ||
-        (d_positions != nullptr && !numbers(d_positions, b->n_tokens, 4)) ||
+    Pointers at;
+    if (!fill(c, b, d_ws, ws_bytes, sizeof(cccl::WsHeader), &a) || !at.numbers(r->turns, r->rot_dim / 2, 8) ||
+        (d_positions != nullptr && !at.numbers(d_positions, b->n_tokens, 4)) ||
         !packed_ok(d_k, b->n_tokens, c->kv_heads, c->head_dim, k_token_stride, k_head_stride) ||
         !packed_ok(d_v, b->n_tokens, c->kv_heads, c->head_dim, v_token_stride, v_head_stride))
         return CCCL_ERR_INVALID_ARG;
@@ -172,11 +177,12 @@ cccl_status cccl_step_attention(const cccl_kv_cache* h_cache, const cccl_kv_batc
     if (empty(b)) return CCCL_OK;
     if (b->n_tokens > INT32_MAX / q_heads) return CCCL_ERR_INVALID_ARG;
     cccl::KvArgs a{};
+    Pointers at;
     if (!fill(c, b, d_ws, ws_bytes, cccl_kv_workspace_bytes(c, b, q_heads), &a) ||
         !packed_ok(d_q, b->n_tokens, q_heads, c->head_dim, q_token_stride, q_head_stride) ||
         !packed_ok(d_out, b->n_tokens, q_heads, c->head_dim, o_token_stride, o_head_stride) ||
-        !rows_ok(d_mask, b->n_tokens, mask_stride, mask_words, 4) ||
-        (d_lse != nullptr && !numbers(d_lse, b->n_tokens * q_heads, 4)))
+        !at.rows(d_mask, b->n_tokens, mask_stride, mask_words, 4) ||
+        (d_lse != nullptr && !at.numbers(d_lse, b->n_tokens * q_heads, 4)))
         return CCCL_ERR_INVALID_ARG;
     cccl::TreeArgs t{};
     t.q = static_cast<const uint8_t*>(d_q);
@@ -205,14 +211,15 @@ cccl_status cccl_step_verify(const cccl_step_draft* h_draft, int32_t* d_path, in
         d->vocab < 1 || d->vocab > CCCL_STEP_MAX_VOCAB)
         return CCCL_ERR_INVALID_ARG;
     if (d->batch == 0) return CCCL_OK;
-    if (!workspace(d_ws, ws_bytes) || !numbers(d->cu_tokens, (int64_t)d->batch + 1, 4) ||
-        !numbers(d_n_kept, d->batch, 4) || !numbers(d_next, d->batch, 4))
+    Pointers at;
+    if (!at.workspace(d_ws, ws_bytes) || !at.numbers(d->cu_tokens, (int64_t)d->batch + 1, 4) ||
+        !at.numbers(d_n_kept, d->batch, 4) || !at.numbers(d_next, d->batch, 4))
         return CCCL_ERR_INVALID_ARG;
     if (d->rows > 0 &&
-        (d->p_stride < d->vocab || !rows_ok(d->p, d->rows, d->p_stride, d->vocab, 4) || !numbers(d->tokens, d->rows, 4) ||
-         !numbers(d->uniform, d->rows, 4) || !numbers(d_path, d->rows, 4) ||
-         (d->parents != nullptr && !numbers(d->parents, d->rows, 4)) ||
-         (d->q != nullptr && (d->q_stride < d->vocab || !rows_ok(d->q, d->rows, d->q_stride, d->vocab, 4)))))
+        (d->p_stride < d->vocab || !at.rows(d->p, d->rows, d->p_stride, d->vocab, 4) || !at.numbers(d->tokens, d->rows, 4) ||
+         !at.numbers(d->uniform, d->rows, 4) || !at.numbers(d_path, d->rows, 4) ||
+         (d->parents != nullptr && !at.numbers(d->parents, d->rows, 4)) ||
+         (d->q != nullptr && (d->q_stride < d->vocab || !at.rows(d->q, d->rows, d->q_stride, d->vocab, 4)))))
         return CCCL_ERR_INVALID_ARG;
     cccl::VerifyArgs a{};
     a.p = d->p;
@@ -240,9 +247,10 @@ cccl_status cccl_step_keep(const cccl_kv_cache* h_cache, const cccl_kv_batch* h_
     if (!shapes_ok(c, b)) return CCCL_ERR_INVALID_ARG;
     if (b->batch == 0) return CCCL_OK;
     cccl::KvArgs a{};
-    if (!fill(c, b, d_ws, ws_bytes, sizeof(cccl::WsHeader), &a) || !numbers(d_n_kept, b->batch, 4) ||
-        (d_lens != nullptr && (!numbers(d_lens, b->batch, 4) || d_lens == b->kv_lens)) ||
-        (b->n_tokens > 0 && !numbers(d_path, b->n_tokens, 4)))
+    Pointers at;
+    if (!fill(c, b, d_ws, ws_bytes, sizeof(cccl::WsHeader), &a) || !at.numbers(d_n_kept, b->batch, 4) ||
+        (d_lens != nullptr && (!at.numbers(d_lens, b->batch, 4) || d_lens == b->kv_lens)) ||
+        (b->n_tokens > 0 && !at.numbers(d_path, b->n_tokens, 4)))
         return CCCL_ERR_INVALID_ARG;
     const cccl::KeepArgs x{d_path, d_n_kept, d_lens};
     return status_of(cccl::launch_step_keep(c->format, a, x, reinterpret_cast<cudaStream_t>(stream)));

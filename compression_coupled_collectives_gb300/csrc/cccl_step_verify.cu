@@ -24,7 +24,8 @@ namespace cccl {
 
 namespace {
 
-constexpr int kThreads = 512, kWarps = kThreads / 32, kMostBlocks = 8;
+constexpr int kThreads = 256, kWarps = kThreads / 32, kMostBlocks = 8;
+constexpr int kBlocksPerSm = 4;
 constexpr uint64_t kOne = 1ull << 53;  // A of 1
 
 // x limited to 0..1, what is not a number to 0, in multiples of 2^-56.
@@ -218,7 +219,7 @@ __device__ __forceinline__ int32_t find(const float* p, const float* q, const Or
 }
 
 template <bool DRAFT, bool VEC>
-__global__ void __launch_bounds__(kThreads) verify_kernel(const __grid_constant__ VerifyArgs a, int blocks) {
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm) verify_kernel(const __grid_constant__ VerifyArgs a, int blocks) {
     __shared__ Shared s;
     const int rank = (int)cluster_rank(), b = (int)blockIdx.x / blocks;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;

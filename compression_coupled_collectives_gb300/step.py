@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+import struct
 
 import torch
 
@@ -19,6 +20,7 @@ from . import _check, _lib
 from .kv import KvBatch, KvCache, _current_stream, _finish, _hand_over, _packed, _raw_stream, empty_kv_workspace
 
 STEP_MAX_DRAFT, STEP_MAX_VOCAB = 1024, 1 << 20
+_int32 = torch.int32
 
 _i32, _i64, _vp, _sz, _int = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int
 
@@ -61,14 +63,25 @@ _plan, _write, _attention = _lib.cccl_step_plan, _lib.cccl_step_write, _lib.cccl
 _verify, _keep = _lib.cccl_step_verify, _lib.cccl_step_keep
 
 
+# a call's host structures as bytes, which take less time to fill than ctypes' fields (their layouts are tested alike)
+_pack_out = struct.Struct("@7P2q2i").pack
+_pack_draft = struct.Struct("@2P2q4Pq2i").pack
+
+
 def _numbers(t: torch.Tensor, dtype: torch.dtype, n: int | None, device: int, what: str) -> int:
     """The address of a contiguous [n] tensor on the call's device."""
+    if t.dtype is dtype and t.numel() == n and t.is_contiguous() and t.get_device() == device:
+        return t.data_ptr()
     if t.dtype is not dtype or t.dim() != 1 or (n is not None and t.shape[0] != n) or \
             (t.shape[0] > 1 and t.stride(0) != 1):
         raise TypeError("%s: expected a contiguous %s of %s numbers" % (what, dtype, "some" if n is None else n))
     if t.get_device() != device:
         raise ValueError("%s is on another device" % what)
     return t.data_ptr()
+
+
+def _maybe(t: torch.Tensor | None, dtype: torch.dtype, n: int, device: int, what: str) -> int:
+    return 0 if t is None else _numbers(t, dtype, n, device, what)
 
 
 def _stream_on(device: int, stream) -> int:
@@ -156,7 +169,7 @@ def cccl_step_plan(tables: StepTables, lens: torch.Tensor, new: torch.Tensor, ws
     ``held`` and ``free_count`` receive the tables' new counts (default: in
     place).  ``parents`` [rows]: the trees; without, chains.  ``rows``: the rows
     of the packed tensors, where none of these says it."""
-    dev, batch, i32 = tables._device, tables.batch, torch.int32
+    dev, batch, i32 = tables._device, tables.batch, _int32
     held = tables.held if held is None else held
     free_count = tables.free_count if free_count is None else free_count
     if rows is None:
@@ -167,26 +180,24 @@ def cccl_step_plan(tables: StepTables, lens: torch.Tensor, new: torch.Tensor, ws
         else:
             raise ValueError("rows: how many rows the packed tensors have")
     words, stride = (0, 0) if mask is None else _mask_of(mask, rows, dev)
-    out = _Out(_numbers(cu_tokens, i32, batch + 1, dev, "cu_tokens"), _numbers(kv_lens, i32, batch, dev, "kv_lens"),
-               _numbers(held, i32, batch, dev, "held"), _numbers(free_count, i32, 1, dev, "free_count"),
-               None if slots is None else _numbers(slots, torch.int64, rows, dev, "slots"),
-               None if positions is None else _numbers(positions, i32, rows, dev, "positions"),
-               None if mask is None else mask.data_ptr(), stride, rows, words, 0)
+    out = _pack_out(_numbers(cu_tokens, i32, batch + 1, dev, "cu_tokens"), _numbers(kv_lens, i32, batch, dev, "kv_lens"),
+                    _numbers(held, i32, batch, dev, "held"), _numbers(free_count, i32, 1, dev, "free_count"),
+                    _maybe(slots, torch.int64, rows, dev, "slots"), _maybe(positions, i32, rows, dev, "positions"),
+                    0 if mask is None else mask.data_ptr(), stride, rows, words, 0)
     status = _plan(tables._ref, _numbers(lens, i32, batch, dev, "lens"), _numbers(new, i32, batch, dev, "new"),
-                   None if parents is None else _numbers(parents, i32, rows, dev, "parents"), ctypes.addressof(out),
-                   ws.data_ptr(), ws.nbytes, _stream_on(dev, stream))
+                   _maybe(parents, i32, rows, dev, "parents"), out, ws.data_ptr(), ws.nbytes, _stream_on(dev, stream))
     if status:
         _check(status, "cccl_step_plan")
 
 
 def _mask_of(mask: torch.Tensor, rows: int, device: int) -> tuple[int, int]:
     """Words of a mask's rows and the stride between them."""
-    if mask.dtype is not torch.int32 or mask.dim() != 2 or mask.shape[0] != rows or mask.shape[1] < 1 or \
-            mask.stride(1) != 1:
+    shape, stride = mask.shape, mask.stride()
+    if mask.dtype is not _int32 or len(shape) != 2 or shape[0] != rows or shape[1] < 1 or stride[1] != 1:
         raise TypeError("mask: expected int32 [rows, words], contiguous in its last axis")
     if mask.get_device() != device:
         raise ValueError("mask is on another device")
-    return mask.shape[1], mask.stride(0) if rows > 1 else mask.shape[1]
+    return shape[1], stride[0] if rows > 1 else shape[1]
 
 
 def cccl_step_write(cache: KvCache, batch: KvBatch, rotary: StepRotary, q: torch.Tensor | None, k: torch.Tensor,
@@ -239,10 +250,11 @@ def cccl_step_attention(cache: KvCache, batch: KvBatch, q: torch.Tensor, mask: t
 
 def _probabilities(x: torch.Tensor, rows: int, vocab: int, what: str) -> int:
     """The stride between rows."""
-    if x.dtype is not torch.float32 or x.dim() != 2 or x.shape[0] != rows or x.shape[1] != vocab or \
-            (vocab > 1 and x.stride(1) != 1):
+    shape, stride = x.shape, x.stride()
+    if x.dtype is not torch.float32 or len(shape) != 2 or shape[0] != rows or shape[1] != vocab or \
+            (vocab > 1 and stride[1] != 1):
         raise TypeError("%s: expected float32 [rows, vocab], contiguous in its last axis" % what)
-    return x.stride(0) if rows > 1 else vocab
+    return stride[0] if rows > 1 else vocab
 
 
 def cccl_step_verify(p: torch.Tensor, q: torch.Tensor | None, tokens: torch.Tensor, parents: torch.Tensor | None,
@@ -253,19 +265,18 @@ def cccl_step_verify(p: torch.Tensor, q: torch.Tensor | None, tokens: torch.Tens
     random numbers ``uniform`` [rows] (float32, 0 <= u < 1), into ``path``
     [rows], ``n_kept`` and ``next_token`` [batch] (int32)."""
     rows, vocab = p.shape
-    dev, batch, i32 = p.get_device(), n_kept.shape[0], torch.int32
+    dev, batch, i32 = p.get_device(), n_kept.numel(), _int32
     p_stride = _probabilities(p, rows, vocab, "p")
     q_stride = 0 if q is None else _probabilities(q, rows, vocab, "q")
     if q is not None and q.get_device() != dev:
         raise ValueError("q is on another device")
-    draft = _Draft(p.data_ptr(), None if q is None else q.data_ptr(), p_stride, q_stride,
-                   _numbers(tokens, i32, rows, dev, "tokens"),
-                   None if parents is None else _numbers(parents, i32, rows, dev, "parents"),
-                   _numbers(uniform, torch.float32, rows, dev, "uniform"),
-                   _numbers(cu_tokens, i32, batch + 1, dev, "cu_tokens"), rows, batch, vocab)
-    status = _verify(ctypes.addressof(draft), _numbers(path, i32, rows, dev, "path"),
-                     _numbers(n_kept, i32, batch, dev, "n_kept"), _numbers(next_token, i32, batch, dev, "next_token"),
-                     ws.data_ptr(), ws.nbytes, _stream_on(dev, stream))
+    draft = _pack_draft(p.data_ptr(), 0 if q is None else q.data_ptr(), p_stride, q_stride,
+                        _numbers(tokens, i32, rows, dev, "tokens"), _maybe(parents, i32, rows, dev, "parents"),
+                        _numbers(uniform, torch.float32, rows, dev, "uniform"),
+                        _numbers(cu_tokens, i32, batch + 1, dev, "cu_tokens"), rows, batch, vocab)
+    status = _verify(draft, _numbers(path, i32, rows, dev, "path"), _numbers(n_kept, i32, batch, dev, "n_kept"),
+                     _numbers(next_token, i32, batch, dev, "next_token"), ws.data_ptr(), ws.nbytes,
+                     _stream_on(dev, stream))
     if status:
         _check(status, "cccl_step_verify")
 
@@ -274,7 +285,7 @@ def cccl_step_keep(cache: KvCache, batch: KvBatch, path: torch.Tensor, n_kept: t
                    lens: torch.Tensor | None, ws: torch.Tensor, stream=None) -> None:
     """Enqueue moving of the kept tokens' keys and values together; ``lens``
     [batch] (or None) receives the lengths without the others."""
-    dev, i32 = cache._device, torch.int32
+    dev, i32 = cache._device, _int32
     status = _keep(cache._ref, batch._ref, _numbers(path, i32, batch.n_tokens, dev, "path"),
                    _numbers(n_kept, i32, batch.batch, dev, "n_kept"),
                    None if lens is None else _numbers(lens, i32, batch.batch, dev, "lens"), ws.data_ptr(), ws.nbytes,

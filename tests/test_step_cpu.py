@@ -63,6 +63,14 @@ def test_structures_match_the_header(tmp_path):
     assert got == want
 
 
+def test_packed_structures_are_the_declared_ones(cc):
+    from compression_coupled_collectives_gb300 import step
+
+    for pack, cls in ((step._pack_out, step._Out), (step._pack_draft, step._Draft)):
+        values = list(range(1, len(cls._fields_) + 1))
+        assert pack(*values) == bytes(cls(*values))
+
+
 @pytest.mark.parametrize("rot,base,factor,length,few,many", [
     (128, 1e4, 1.0, 0, 1, 32), (64, 5e5, 8.0, 8192, 1, 4), (16, 1e6, 4.0, 0, 1, 32), (96, 1e4, 16.0, 4096, 1, 32),
     (48, 0.5, 1.0, 0, 1, 32)])
