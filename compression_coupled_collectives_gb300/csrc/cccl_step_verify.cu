@@ -26,26 +26,46 @@ namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32, kMostBlocks = 8;
 constexpr int kBlocksPerSm = 4;
-constexpr uint64_t kOne = 1ull << 53;  // A of 1
+// Values are gone through 512 at a time.  kSteps: of the longest part (2^20 values
+// in 64 parts, or 2^12 or less in 8).
+constexpr int kFlight = 4, kStep = 128 * kFlight, kSteps = (1 << 20) / (kMostBlocks * kWarps) / kStep;
+constexpr uint64_t kOne = 1ull << 53;    // A of 1
+constexpr uint64_t kWhole = 1ull << 56;  // a sum of 1
 
-// x limited to 0..1, what is not a number to 0, in multiples of 2^-56.
+// x limited to 0..1, what is not a number to 0 (as __saturatef has it), and the
+// same in multiples of 2^-56, cut off: 2^(e - 127) m / 2^23 2^56 with e the
+// exponent's and m the fraction's bits (subnormals fall off).
+__device__ __forceinline__ float limited(float x) { return __saturatef(x); }
 __device__ __forceinline__ uint64_t fixed(float x) {
-    int32_t b = __float_as_int(x);
-    b = b > 0x7F800000 ? 0 : min(max(b, 0), 0x3F800000);
-    const uint32_t e = (uint32_t)b >> 23, m = ((uint32_t)b & 0x7FFFFFu) | 0x800000u;
+    const uint32_t b = __float_as_uint(limited(x)), e = b >> 23, m = (b & 0x7FFFFFu) | 0x800000u;
     return ((uint64_t)m << 33) >> min(127u - e, 63u);
 }
-__device__ __forceinline__ float limited(float x) { return x > 0.f ? fminf(x, 1.f) : 0.f; }
-// A (in multiples of 2^-53) times q
-__device__ __forceinline__ uint64_t times(uint64_t A, uint64_t q) {
-    return A == kOne ? q : (__umul64hi(A, q) << 11) | ((A * q) >> 53);
+// a b < c 2^56 for factors of up to 64 bits and c below 2^64
+__device__ __forceinline__ bool product_below(uint64_t a, uint64_t b, uint64_t c) {
+    const uint64_t hi = __umul64hi(a, b), lo = a * b;
+    return hi < c >> 8 || (hi == c >> 8 && lo < c << 56);
 }
-template <bool DRAFT>
+// u q < p, exactly (u q = h + e)
+__device__ __forceinline__ bool product_below(float u, float q, float p) {
+    const float h = u * q, e = fmaf(u, q, -h);
+    return h < p || (h == p && e < 0.f);
+}
+// A (in multiples of 2^-53, up to one for every token) times q, at most 2^60:
+// that is 16, and p is at most 1
+__device__ __forceinline__ uint64_t times(uint64_t A, uint64_t q) {
+    const uint64_t hi = __umul64hi(A, q);
+    return hi >= 1ull << 49 ? 1ull << 60 : (hi << 11) | ((A * q) >> 53);
+}
+// R of one value.  Most rows are taken as they are (A = 0) or without one q (A =
+// 1); code for those alone saves a third of the instructions.
+enum Mode { kPlain, kLessOne, kLessA };
+template <Mode MODE>
 __device__ __forceinline__ uint64_t weight(float p, float q, uint64_t A) {
     const uint64_t x = fixed(p);
-    if (!DRAFT || A == 0) return x;
-    const uint64_t y = times(A, fixed(q));
-    return x > y ? x - y : 0;
+    if (MODE == kPlain) return x;
+    const uint64_t y = fixed(q);
+    const int64_t d = (int64_t)(x - (MODE == kLessOne ? y : times(A, y)));
+    return (uint64_t)(d & ~(d >> 63));
 }
 __device__ __forceinline__ uint64_t warp_sum64(uint64_t x) {
 #pragma unroll
@@ -53,7 +73,7 @@ __device__ __forceinline__ uint64_t warp_sum64(uint64_t x) {
     return x;
 }
 
-struct Order {
+struct alignas(16) Order {
     int64_t row;       // of p and q; -1: the sequence has none
     uint64_t A;
     uint64_t u;        // of the next token, in multiples of 2^-56
@@ -64,6 +84,7 @@ struct Shared {
     Order order;                    // the first block's
     uint64_t totals[kMostBlocks];   // of every block, in every block
     uint64_t warps[kWarps];
+    uint64_t upto[kWarps][kSteps];  // of each warp's part, after every step
     int32_t refused[kMaxDraft];     // the first block's; then every block's copy
     int32_t parent[kMaxDraft], token[kMaxDraft], kept[kMaxDraft];
     float p[kMaxDraft], q[kMaxDraft], u[kMaxDraft];
@@ -73,7 +94,7 @@ struct Shared {
 struct Way {
     int32_t at, next, kept;  // current token, the next to look at, how many are kept
     uint64_t A;
-    double left;     // without q: S
+    uint64_t left;   // without q: S, in multiples of 2^-56
     int32_t refused;
     bool known;      // the sum at A has been taken
     uint64_t sum;
@@ -97,18 +118,18 @@ __device__ __forceinline__ bool advance(Shared& s, int32_t n, Way& w) {
         if (DRAFT) {
             const float q = limited(s.q[i]);
             if (w.A == 0) {
-                keep = (double)u * (double)q < (double)p;  // the product is exact
+                keep = product_below(u, q, p);
             } else {
                 if (!w.known) {
                     w.next = i;
                     return false;
                 }
-                keep = (double)u * ((double)w.sum * 0x1p-56) * (double)q < (double)weight<DRAFT>(p, q, w.A) * 0x1p-56;
+                keep = (double)u * ((double)w.sum * 0x1p-56) * (double)q < (double)weight<kLessA>(p, q, w.A) * 0x1p-56;
             }
         } else {
             for (int32_t k = lane; k < w.refused; k += 32) again |= s.refused[k] == x;
             again = __any_sync(0xFFFFFFFFu, again) != 0;
-            keep = !again && (double)u * w.left < (double)p;
+            keep = !again && product_below(fixed(u), w.left, fixed(p));
         }
         w.next = i + 1;
         if (keep) {
@@ -116,14 +137,14 @@ __device__ __forceinline__ bool advance(Shared& s, int32_t n, Way& w) {
             ++w.kept;
             w.at = i;
             w.A = 0;
-            w.left = 1.0;
+            w.left = kWhole;
             w.refused = 0;
         } else if (DRAFT) {
             w.A += w.A == 0 ? kOne : w.sum >> 3;
         } else if (!again) {
             if (lane == 0) s.refused[w.refused] = x;
             ++w.refused;
-            w.left -= (double)p;
+            w.left -= min(w.left, fixed(p));
         }
         w.known = false;
         __syncwarp();
@@ -152,68 +173,100 @@ __device__ __forceinline__ void load4(const float* row, int32_t at, int32_t to, 
     for (int i = 0; i < 4; ++i) x[i] = at + i * kStep < to ? row[at + i * kStep] : 0.f;
 }
 
-constexpr int kFlight = 4;  // times 128 values a warp
-
-template <bool DRAFT, bool VEC>
-__device__ __forceinline__ uint64_t add_up(const float* p, const float* q, const Order& o, const Part& part) {
+// The part's sum, and after every step the sum so far.  A load follows the use of
+// what it replaces, so that most of a step's loads are always on their way.
+template <Mode MODE, bool VEC>
+__device__ __forceinline__ uint64_t add_up(const float* p, const float* q, const Order& o, const Part& part,
+                                           uint64_t* upto) {
     const int lane = threadIdx.x & 31;
+    constexpr bool both = MODE != kPlain;
+    float x[kFlight][4], y[kFlight][4] = {};
+    int32_t at = part.from + (VEC ? 4 * lane : lane);
+#pragma unroll
+    for (int k = 0; k < kFlight; ++k) {
+        load4<VEC>(p, at + 128 * k, part.to, x[k]);
+        if (both) load4<VEC>(q, at + 128 * k, part.to, y[k]);
+    }
     uint64_t sum = 0;
-    for (int32_t base = part.from + (VEC ? 4 * lane : lane); base < part.to; base += 128 * kFlight) {
-        float x[kFlight][4], y[kFlight][4] = {};
+    int step = 0;
+    for (int32_t base = part.from; base < part.to; base += kStep, ++step) {
+        at += kStep;
 #pragma unroll
         for (int k = 0; k < kFlight; ++k) {
-            load4<VEC>(p, base + 128 * k, part.to, x[k]);
-            if (DRAFT && o.A != 0) load4<VEC>(q, base + 128 * k, part.to, y[k]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sum += weight<MODE>(x[k][i], y[k][i], o.A);
+            load4<VEC>(p, at + 128 * k, part.to, x[k]);
+            if (both) load4<VEC>(q, at + 128 * k, part.to, y[k]);
         }
-#pragma unroll
-        for (int k = 0; k < kFlight; ++k)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) sum += weight<DRAFT>(x[k][i], y[k][i], o.A);
+        const uint64_t all = warp_sum64(sum);
+        if (lane == 0) upto[step] = all;
     }
-    return warp_sum64(sum);
+    __syncwarp();
+    return step > 0 ? upto[step - 1] : 0;
 }
 
 // The first value of the part at which the running sum passes `goal` (it does so
-// within the part), by one warp: 512 values at a time, then 32 of those.
-template <bool DRAFT>
+// within the part), by one warp: 16 values in a row a lane, from the step on whose
+// sum passes it (upto counts refused tokens too: an earlier step may hold it, never
+// a later one, so with refused tokens the search begins at the front).
+template <Mode MODE, bool VEC>
 __device__ __forceinline__ int32_t find(const float* p, const float* q, const Order& o, const int32_t* refused,
-                                        const Part& part, uint64_t goal) {
-    constexpr int kRows = 16;
+                                        const Part& part, uint64_t goal, const uint64_t* upto) {
+    constexpr int kEach = 16;
+    static_assert(32 * kEach == kStep, "");
     const int lane = threadIdx.x & 31;
-    for (int32_t base = part.from; base < part.to; base += 32 * kRows) {
-        float x[kRows], y[kRows];
+    int step = 0;
+    if (o.refused == 0) {
+        const int steps = (part.to - part.from + kStep - 1) / kStep;
+        const uint32_t below = __ballot_sync(0xFFFFFFFFu, lane < steps && upto[min(lane, kSteps - 1)] <= goal);
+        step = __popc(below);
+        if (step > 0) goal -= upto[step - 1];
+    }
+    for (int32_t base = part.from + step * kStep; base < part.to; base += kStep) {
+        const int32_t at = base + kEach * lane;
+        float x[kEach], y[kEach] = {};
+        if constexpr (VEC) {
 #pragma unroll
-        for (int k = 0; k < kRows; ++k) {
-            const int32_t at = base + 32 * k + lane;
-            x[k] = at < part.to ? p[at] : 0.f;
-            y[k] = DRAFT && o.A != 0 && at < part.to ? q[at] : 0.f;
-        }
-        uint64_t w[kRows], all = 0;
+            for (int k = 0; k < kEach; k += 4) {
+                load4<true>(p, at + k, part.to, x + k);
+                if (MODE != kPlain) load4<true>(q, at + k, part.to, y + k);
+            }
+        } else {
 #pragma unroll
-        for (int k = 0; k < kRows; ++k) {
-            w[k] = weight<DRAFT>(x[k], y[k], o.A);
-            for (int32_t i = 0; i < o.refused && w[k] != 0; ++i)
-                if (refused[i] == base + 32 * k + lane) w[k] = 0;
-            all += w[k];
+            for (int k = 0; k < kEach; ++k) {
+                x[k] = at + k < part.to ? p[at + k] : 0.f;
+                if (MODE != kPlain) y[k] = at + k < part.to ? q[at + k] : 0.f;
+            }
         }
-        __syncwarp();
-        all = warp_sum64(all);
-        if (goal >= all) {
-            goal -= all;
+        for (int32_t i = 0; i < o.refused; ++i) {
+            const int32_t k0 = refused[i] - at;
+#pragma unroll
+            for (int k = 0; k < kEach; ++k) x[k] = k == k0 ? 0.f : x[k];
+        }
+        uint64_t all = 0;
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) all += weight<MODE>(x[k], y[k], o.A);
+        uint64_t run_to = all;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const uint64_t z = __shfl_up_sync(0xFFFFFFFFu, run_to, d);
+            if (lane >= d) run_to += z;
+        }
+        const uint32_t past = __ballot_sync(0xFFFFFFFFu, run_to > goal);
+        if (past == 0) {
+            goal -= __shfl_sync(0xFFFFFFFFu, run_to, 31);
             continue;
         }
+        // the lane's first value at which its own sum passes what is left
+        const uint64_t left = goal - (run_to - all);
+        int32_t mine = kEach;
+        uint64_t run = 0;
 #pragma unroll
-        for (int k = 0; k < kRows; ++k) {
-            uint64_t upto = w[k];
-#pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const uint64_t z = __shfl_up_sync(0xFFFFFFFFu, upto, d);
-                if (lane >= d) upto += z;
-            }
-            const uint32_t past = __ballot_sync(0xFFFFFFFFu, upto > goal);
-            if (past != 0) return base + 32 * k + __ffs(past) - 1;
-            goal -= __shfl_sync(0xFFFFFFFFu, upto, 31);
+        for (int k = 0; k < kEach; ++k) {
+            run += weight<MODE>(x[k], y[k], o.A);
+            if (run > left && mine == kEach) mine = k;
         }
+        return __shfl_sync(0xFFFFFFFFu, at + mine, __ffs(past) - 1);
     }
     return part.from;  // (not reached: the part's sum is above the goal)
 }
@@ -225,7 +278,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) verify_kernel(const __
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int64_t row0 = 0;
     int32_t rows = 0, n = 0;
-    Way w{0, 1, 1, 0, 1.0, 0, false, 0};
+    Way w{0, 1, 1, 0, kWhole, 0, false, 0};
     if (rank == 0) {
         const int64_t lo = a.cu[b], hi = a.cu[b + 1];
         row0 = min(max(lo, (int64_t)0), a.rows);
@@ -271,10 +324,9 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) verify_kernel(const __
         Order o;
         {
             const uint32_t at = in_block(smem_addr(&s.order), 0);
-            uint32_t words[sizeof(Order) / 4];
-#pragma unroll
-            for (int i = 0; i < (int)(sizeof(Order) / 4); ++i) words[i] = __float_as_uint(load_cluster(at + 4 * i));
-            memcpy(&o, words, sizeof(Order));
+            const float4 lo = load_cluster4(at), hi = load_cluster4(at + 16);
+            memcpy(&o, &lo, 16);
+            memcpy(reinterpret_cast<char*>(&o) + 16, &hi, 16);
             if (rank != 0)
                 for (int32_t i = threadIdx.x; i < o.refused; i += kThreads)
                     s.refused[i] = __float_as_int(load_cluster(in_block(smem_addr(&s.refused[i]), 0)));
@@ -294,7 +346,10 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) verify_kernel(const __
         const Part part = part_of(a.vocab, blocks, rank, warp);
         uint64_t total = 0;
         for (int turn = 0; turn < 2; ++turn) {
-            uint64_t sum = add_up<DRAFT, VEC>(p, q, o, part);
+            const Mode mode = !DRAFT || o.A == 0 ? kPlain : (o.A == kOne ? kLessOne : kLessA);
+            uint64_t sum = mode == kPlain     ? add_up<kPlain, VEC>(p, q, o, part, s.upto[warp])
+                           : mode == kLessOne ? add_up<kLessOne, VEC>(p, q, o, part, s.upto[warp])
+                                              : add_up<kLessA, VEC>(p, q, o, part, s.upto[warp]);
             if (o.refused > 0) {
                 uint64_t off = 0;
                 for (int32_t k = lane; k < o.refused; k += 32)
@@ -338,7 +393,11 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) verify_kernel(const __
             for (int i = 0; i < rank; ++i) before += s.totals[i];
             for (int i = 0; i < warp; ++i) before += s.warps[i];
             if (before <= goal && goal - before < s.warps[warp]) {
-                const int32_t y = find<DRAFT>(p, q, o, s.refused, part, goal - before);
+                const uint64_t left = goal - before;
+                const int32_t y =
+                    !DRAFT || o.A == 0 ? find<kPlain, VEC>(p, q, o, s.refused, part, left, s.upto[warp])
+                    : o.A == kOne      ? find<kLessOne, VEC>(p, q, o, s.refused, part, left, s.upto[warp])
+                                       : find<kLessA, VEC>(p, q, o, s.refused, part, left, s.upto[warp]);
                 if (lane == 0) a.next[b] = y;
             }
         }

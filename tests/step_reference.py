@@ -129,7 +129,7 @@ def verify(p, q, tokens, parents, uniform, cu, most=1024):
             n_kept.append(0)
             following.append(-1)
             continue
-        at, A, refused, left, kept = 0, 0, [], 1.0, [0]
+        at, A, refused, left, kept = 0, 0, [], scale, [0]
 
         def weights(row, A, refused):
             out = [fixed(x) for x in p[row]]
@@ -146,7 +146,7 @@ def verify(p, q, tokens, parents, uniform, cu, most=1024):
             u = uniform[lo + i]
             px = _limited(p[lo + at][x])
             if q is None:
-                keep = x not in refused and u * left < px
+                keep = x not in refused and fixed(u) * left < fixed(px) * scale
             elif A == 0:
                 keep = u * _limited(q[lo + at][x]) < px
             else:
@@ -154,12 +154,12 @@ def verify(p, q, tokens, parents, uniform, cu, most=1024):
                 S = sum(w)
                 keep = u * (S / scale) * _limited(q[lo + at][x]) < w[x] / scale
             if keep:
-                at, A, refused, left = i, 0, [], 1.0
+                at, A, refused, left = i, 0, [], scale
                 kept.append(i)
             elif q is None:
                 if x not in refused:
                     refused.append(x)
-                    left -= px
+                    left = max(0, left - fixed(px))
             else:
                 A += 1 << 53 if A == 0 else S >> 3
         w = weights(lo + at, A, refused)

@@ -399,6 +399,24 @@ def test_verify_refuses_many_children(cc):
             d.check(cc)
 
 
+def test_verify_refuses_hundreds(cc):
+    """A draft that insists on what the target never says: A grows by one with every child."""
+    n, vocab = 600, 40
+    d = Draft([n], vocab, seed=2)
+    d.parents = [-1] + [0] * (n - 1)
+    d.tokens = [5] * n
+    d.p[0] = 1.0 / (vocab - 1)
+    d.p[0, 5] = 0
+    d.q[0] = 0
+    d.q[0, 5] = 1.0
+    d.cuda()
+    assert d.check(cc) == [1]
+    d.q[0] = 1e-6  # and now and then something else
+    d.q[0, 5] = 0.5
+    d.cuda()
+    d.check(cc)
+
+
 def test_verify_at_the_ends_of_the_random_numbers(cc):
     d = Draft([4, 4, 4], 700, seed=8)
     for u in (0.0, 1.0 - 2.0 ** -24, 1.0, 2.0, -1.0, float("nan")):
