@@ -44,6 +44,7 @@ inline bool shapes_ok(const cccl_kv_cache* c, const cccl_kv_batch* b) {
 
 // The remaining checks of a cache and batch, and the kernels' form of them.
 inline bool fill(const cccl_kv_cache* c, const cccl_kv_batch* b, void* d_ws, size_t ws_bytes, size_t need, KvArgs* a) {
+    DeviceRanges at;
     const int64_t elem = c->format == CCCL_KV_16BIT ? 2 : 1;
     const int64_t n[3] = {c->pages, c->page_tokens, c->kv_heads};
     const int64_t st[3] = {c->page_stride, c->token_stride, c->head_stride};
@@ -59,12 +60,12 @@ inline bool fill(const cccl_kv_cache* c, const cccl_kv_batch* b, void* d_ws, siz
     if (c->format != CCCL_KV_16BIT) {
         const int64_t ss[3] = {c->scale_page_stride, c->scale_token_stride, c->scale_head_stride};
         if (!aligned(c->k_scale, 4) || !aligned(c->v_scale, 4) || !extent(n, ss, 3, 1, &scales)) return false;
-        if (!device_range(c->k_scale, 4 * (size_t)scales) || !device_range(c->v_scale, 4 * (size_t)scales))
+        if (!at.ok(c->k_scale, 4 * (size_t)scales) || !at.ok(c->v_scale, 4 * (size_t)scales))
             return false;
     }
-    if (!device_range(c->k, (size_t)(values * elem)) || !device_range(c->v, (size_t)(values * elem)) ||
-        !device_range(d_ws, need) || !device_range(b->page_table, 4 * (size_t)entries) ||
-        !device_range(b->cu_tokens, 4 * ((size_t)b->batch + 1)) || !device_range(b->kv_lens, 4 * (size_t)b->batch))
+    if (!at.ok(c->k, (size_t)(values * elem)) || !at.ok(c->v, (size_t)(values * elem)) ||
+        !at.ok(d_ws, need) || !at.ok(b->page_table, 4 * (size_t)entries) ||
+        !at.ok(b->cu_tokens, 4 * ((size_t)b->batch + 1)) || !at.ok(b->kv_lens, 4 * (size_t)b->batch))
         return false;
     a->k = static_cast<uint8_t*>(c->k);
     a->v = static_cast<uint8_t*>(c->v);

@@ -628,33 +628,40 @@ __device__ __forceinline__ bool mma_role(const KvArgs& a, const Args& t, Shared*
         const int tiles = live_rows<kRows>(t, p) > kTileRows ? 2 : 1;
         const int32_t count = p.count;
         if (narrow(t, p)) {
-            auto scores = [&](int32_t j) {  // of tile j, when its K is there
-                const uint32_t k = entry + 2 * (uint32_t)j;
-                if (!wait(&sh->kv_full[k % SLOTS], (k / SLOTS) & 1)) return false;
-                if (j < 2) {
-                    if (!wait(&sh->q_full[j], q_phase[j])) return false;
-                    q_phase[j] ^= 1;
+            // whichever is ready first: scores of tile qk (K there; P of the tile before
+            // in its place in TMEM read, by a product issued before), values of tile pv
+            int32_t qk = 0, pv = 0;
+            uint64_t since = 0;
+            auto ready = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xFFFFFFFFu, mbar_test(bar, parity)) != 0; };
+            while (pv < count) {
+                const uint32_t k = entry + 2 * (uint32_t)qk, v = entry + 2 * (uint32_t)pv + 1;
+                const int i = pv & 1;
+                if (qk < count && qk < pv + 2 && ready(&sh->kv_full[k % SLOTS], (k / SLOTS) & 1) &&
+                    (qk > 1 || ready(&sh->q_full[qk], q_phase[qk & 1]))) {
+                    if (qk < 2) q_phase[qk] ^= 1;
+                    tc_fence_after();
+                    product_qk(qk & 1, k % SLOTS);
+                    commit(&sh->kv_free[k % SLOTS]);
+                    ++qk;
+                } else if (pv < qk && ready(&sh->kv_full[v % SLOTS], (v / SLOTS) & 1) &&
+                           ready(&sh->p_full[i], p_phase[i])) {
+                    p_phase[i] ^= 1;
+                    tc_fence_after();
+                    product_pv(i, v % SLOTS, pv > 1);
+                    commit(&sh->kv_free[v % SLOTS]);
+                    if (pv + 2 >= count) commit(&sh->o_full[i]);
+                    ++pv;
+                } else {  // bounded, as every wait
+                    const uint64_t now = globaltimer_ns();
+                    if (since == 0) since = now;
+                    if (__any_sync(0xFFFFFFFFu, kWaitLimitNs == 0 || now - since > kWaitLimitNs) != 0) {
+                        record_error(a.ws, kStatusTimeout);
+                        *reinterpret_cast<volatile uint32_t*>(&sh->stop) = 1;
+                        return leader != 0;
+                    }
+                    continue;
                 }
-                tc_fence_after();
-                product_qk(j & 1, k % SLOTS);
-                commit(&sh->kv_free[k % SLOTS]);
-                return true;
-            };
-            for (int32_t j = 0; j < min(count, 2); ++j)
-                if (!scores(j)) return leader != 0;
-            for (int32_t j = 0; j < count; ++j) {
-                const int i = j & 1;
-                const uint32_t v = entry + 2 * (uint32_t)j + 1;
-                if (!wait(&sh->kv_full[v % SLOTS], (v / SLOTS) & 1)) return leader != 0;
-                if (!wait(&sh->p_full[i], p_phase[i])) return leader != 0;
-                p_phase[i] ^= 1;
-                tc_fence_after();
-                product_pv(i, v % SLOTS, j > 1);
-                commit(&sh->kv_free[v % SLOTS]);
-                if (j + 2 >= count)
-                    commit(&sh->o_full[i]);
-                else if (!scores(j + 2))
-                    return leader != 0;
+                since = 0;
             }
             entry += 2 * (uint32_t)count;
             continue;

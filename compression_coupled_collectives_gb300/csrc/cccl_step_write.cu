@@ -3,7 +3,7 @@
 //
 // Bound by HBM: queries are read and written, keys and values read and stored.
 // The angles' sines and cosines are worked out once a token and shared by its
-// heads: a block brings up to 16 tokens and fills a table in shared memory first.
+// heads: a block brings up to 8 tokens and fills a table in shared memory first.
 //
 // Angles: a pair turns by turns / 2^64 of a full turn a position, so position p
 // stands at p * turns modulo 2^64 of one: whole turns fall out of the 64-bit
@@ -15,6 +15,8 @@
 // pieces of 8.  Interleaved pairs lie in one piece; with pairs half the rotary
 // part apart a lane takes piece j and the one rot_dim / 16 pieces on, so that it
 // holds both of every pair.
+#include <algorithm>
+
 #include "cccl_kv_copy.cuh"
 #include "cccl_kv_launch.h"
 #include "cccl_step.cuh"
@@ -23,11 +25,16 @@ namespace cccl {
 
 namespace {
 
+// Tokens of a block: up to 8, so that a large call has two blocks' worth for every
+// place on an SM, and one's search and angles run beside another's loads: 12572
+// tokens of 32 + 2 x 8 heads of 128 in 59.6 us at 16, 53.4 at 8, 53.7 at 4, 54.4 at 2.
+constexpr int kTokens = 8;
+
 // cos and sin of pairs 8 j + 2 i and + 1 of a block's tokens: a piece's 8 pairs
 // are 4 entries, those of a vector's lanes side by side (no bank met twice).
 template <int G>
 struct Angles {
-    float4 of[kMaxTokensPerBlock][4][G];
+    float4 of[kTokens][4][G];
 };
 template <int G>
 __device__ __forceinline__ void fill_angles(const RotaryArgs& r, const TokenSlots& slots, int64_t t0, int count,
@@ -185,7 +192,7 @@ __global__ void __launch_bounds__(kCopyThreads)
 
 template <class T, int FMT>
 cudaError_t launch_one(const KvArgs& a, const KvPacked& x, const RotaryArgs& r, bool interleaved, cudaStream_t s) {
-    const int tpb = tokens_per_block(a.n_tokens);
+    const int tpb = std::min(tokens_per_block(a.n_tokens), kTokens);
     const FastDiv heads = fast_div((uint32_t)a.kv_heads), q_heads = fast_div((uint32_t)(r.q_heads > 0 ? r.q_heads : 1));
     const dim3 grid((unsigned)((a.n_tokens + tpb - 1) / tpb));
     if (a.dim <= 64) {

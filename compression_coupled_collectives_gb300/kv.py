@@ -151,7 +151,7 @@ def _packed(x: torch.Tensor, cache: KvCache, n_tokens: int, heads: int, what: st
     """Token and head stride of a packed [n_tokens, heads, head_dim] tensor."""
     if x.dtype is not cache.dtype:
         raise TypeError("%s: expected %s, got %s" % (what, cache.dtype, x.dtype))
-    if tuple(x.shape) == (n_tokens, heads, cache.head_dim):
+    if x.shape == (n_tokens, heads, cache.head_dim):
         token, head, inner = x.stride()
         if inner == 1:
             return token, head
