@@ -567,7 +567,11 @@ __device__ __forceinline__ void widen_role(const KvArgs& a, const Args& t, Share
 // warpgroups take the same rows (each has them in its Q), the one the tiles of
 // tokens of even number, the other the odd ones, and they put their accumulators
 // together at the piece's end.  32 sequences of 4096 tokens, 16 drafted, groups of
-// 4: NARROW_NOTE.
+// 4: 128.9 us without, 110.6 with; 16 of 20480 in INT8: 419, 329.  Then the copies
+// bound it: without products and softmax the first takes 61 us of 71 at 2560 tokens;
+// in INT8, of 332: without widening 227, without the softmax 248, with copies alone
+// 194.  Items of 128 rows alone, one Q and four slots for tiles (or three, and five
+// for codes): 306 (301), but 33 drafted then take 590 for 398.
 template <class Args>
 __device__ __forceinline__ bool narrow(const Args& t, const Piece& p) {
     return std::is_same<Args, TreeArgs>::value && live_rows<kRows>(t, p) <= kTileRows;
@@ -1428,7 +1432,13 @@ cudaError_t launch_one(const KvArgs& a, const Args& t, int max_new, int max_len,
     if (cluster > 1 && max_len > (cluster == 4 ? 3 : 7) * kTokens && max_len <= 16 * cluster * kTokens)
         return launch_clusters(attend_chunk_kernel<T, FMT, Args, true>, (int)tiled * cluster, cluster, kThreads,
                                shared_bytes<FMT, Args>(a.dim), s, a, t, k_map, v_map, box, cluster);
-    const int shares = shares_for(a, t, max_new, max_len, kRows, kTokens, kShares);
+    int shares = shares_for(a, t, max_new, max_len, kRows, kTokens, kShares);
+    // One tree with several row tiles a head: with as many shares for each item its
+    // row tiles are walked in step, and all but the first find their tokens in the L2
+    // (61 drafted over 131077, groups of 8: 152 shares 232 us, 144 shares SHARES_US).
+    if (std::is_same<Args, TreeArgs>::value && a.batch == 1 && tiled > a.kv_heads && shares == kShares &&
+        8 * tiled <= kShares)
+        shares = (int)(kShares / tiled * tiled);
     attend_chunk_kernel<T, FMT, Args, false>
         <<<shares, kThreads, shared_bytes<FMT, Args>(a.dim), s>>>(a, t, k_map, v_map, box, whole ? 1 : 0);
     e = cudaGetLastError();
