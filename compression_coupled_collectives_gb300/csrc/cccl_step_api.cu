@@ -39,7 +39,11 @@ struct Pointers {
         return aligned(d_ws, 16) && ws_bytes >= sizeof(cccl::WsHeader) && ranges.ok(d_ws, sizeof(cccl::WsHeader));
     }
 };
-cccl_status status_of(cudaError_t e) { return e == cudaSuccess ? CCCL_OK : CCCL_ERR_CUDA; }
+cccl_status status_of(cudaError_t e) {
+    if (e == cudaSuccess) return CCCL_OK;
+    cudaGetLastError();  // a refused launch is not the next call's error
+    return CCCL_ERR_CUDA;
+}
 
 }  // namespace
 

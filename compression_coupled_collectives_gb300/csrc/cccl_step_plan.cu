@@ -116,6 +116,7 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const __grid_constant__ 
         const int64_t most = min((int64_t)a.table_pages * a.page_tokens.d, (int64_t)0x7FFF0000);
         bool bad = len < 0 || held < 0 || held > a.table_pages || fresh < 0 || fresh > a.rows || len + fresh > most;
         if (a.mask != nullptr && fresh > 32 * a.words) bad = true;
+        if (a.parents != nullptr && fresh > kMaxDraft) bad = true;  // (a walk up a chain takes as many loads)
         if (bad) {
             wrong = 1;
             fresh = 0;

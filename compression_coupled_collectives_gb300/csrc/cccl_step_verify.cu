@@ -317,7 +317,10 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) verify_kernel(const __
                 o.u = fixed(s.u[0]);
                 o.refused = DRAFT ? 0 : w.refused;
             }
-            if (lane == 0) s.order = o;
+            if (lane == 0) {
+                s.order = o;
+                a.next[b] = n > 0 ? 0 : -1;  // (some token also where a row's sum leaves 64 bits)
+            }
         }
         __syncthreads();
         cluster_sync();
@@ -333,10 +336,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) verify_kernel(const __
         }
         __syncthreads();
         if (o.row < 0) {  // no rows at all
-            if (rank == 0 && threadIdx.x == 0) {
-                a.n_kept[b] = 0;
-                a.next[b] = -1;
-            }
+            if (rank == 0 && threadIdx.x == 0) a.n_kept[b] = 0;
             __syncwarp();
             cluster_sync();  // the first block's order has been read
             return;
@@ -382,10 +382,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) verify_kernel(const __
             continue;
         }
         if (total == 0) {
-            if (rank == 0 && threadIdx.x == 0) {
-                record_error(a.ws, kStatusInvalidArg);
-                a.next[b] = 0;
-            }
+            if (rank == 0 && threadIdx.x == 0) record_error(a.ws, kStatusInvalidArg);
         } else {
             uint64_t goal = (__umul64hi(total, o.u) << 8) | ((total * o.u) >> 56);
             if (goal >= total) goal = total - 1;

@@ -90,10 +90,15 @@ def _stream_on(device: int, stream) -> int:
     return _current_stream(device) if stream is None else stream.cuda_stream
 
 
-def _here(cache: KvCache, *tensors: torch.Tensor | None) -> None:
-    for t in tensors:
-        if t is not None and t.get_device() != cache._device:
-            raise ValueError("all tensors of a call are on the cache's device")
+def _strides(x: torch.Tensor, cache: KvCache, shape: tuple, what: str) -> tuple:
+    """Token, head and value stride of a packed tensor of that shape, on the cache's device."""
+    if x.get_device() != cache._device:
+        raise ValueError("%s: all tensors of a call are on the cache's device" % what)
+    if x.dtype is cache.dtype and x.shape == shape:
+        s = x.stride()
+        if s[2] == 1:
+            return s
+    return *_packed(x, cache, shape[0], shape[1], what), 1  # (says what is wrong)
 
 
 def empty_step_workspace(device=None) -> torch.Tensor:
@@ -154,6 +159,7 @@ class StepRotary:
             raise ValueError("magnitude is a finite number")
         self.turns, self.rot_dim, self.interleaved = host.to(device or "cuda"), int(rot_dim), bool(interleaved)
         self.magnitude = float(magnitude)
+        self._device = self.turns.get_device()
         self._c = _Rotary(self.turns.data_ptr(), self.magnitude, self.rot_dim, 1 if interleaved else 0, 0)
         self._ref = ctypes.addressof(self._c)
 
@@ -207,21 +213,24 @@ def cccl_step_write(cache: KvCache, batch: KvBatch, rotary: StepRotary, q: torch
     (the same tensor or another; both None: no queries) and of ``k``
     [n_tokens, kv_heads, head_dim], and storing of ``k`` and ``v`` in the cache.
     ``positions`` [n_tokens]: where rows stand (default: their places)."""
-    n = batch.n_tokens
+    n, dev = batch.n_tokens, cache._device
     if (q is None) != (q_out is None):
         raise ValueError("q and q_out go together")
-    _here(cache, q, q_out, k, v, ws, rotary.turns)
-    heads = qt = qh = ot = oh = 0
+    if ws.get_device() != dev or rotary._device != dev:
+        raise ValueError("all tensors of a call are on the cache's device")
+    shape = (n, cache.kv_heads, cache.head_dim)
+    kt, kh, _ = _strides(k, cache, shape, "k")
+    vt, vh, _ = _strides(v, cache, shape, "v")
+    heads = qt = qh = ot = oh = q_at = out_at = 0
     if q is not None:
         heads = q.shape[1]
-        qt, qh = _packed(q, cache, n, heads, "q")
-        ot, oh = _packed(q_out, cache, n, heads, "q_out")
-    kt, kh = _packed(k, cache, n, cache.kv_heads, "k")
-    vt, vh = _packed(v, cache, n, cache.kv_heads, "v")
-    status = _write(cache._ref, batch._ref, rotary._ref,
-                    None if positions is None else _numbers(positions, torch.int32, n, cache._device, "positions"),
-                    None if q is None else q.data_ptr(), heads, qt, qh, None if q is None else q_out.data_ptr(), ot, oh,
-                    k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, ws.data_ptr(), ws.nbytes, _raw_stream(cache, stream))
+        shape = (n, heads, cache.head_dim)
+        qt, qh, _ = _strides(q, cache, shape, "q")
+        ot, oh, _ = _strides(q_out, cache, shape, "q_out")
+        q_at, out_at = q.data_ptr(), q_out.data_ptr()
+    status = _write(cache._ref, batch._ref, rotary._ref, _maybe(positions, _int32, n, dev, "positions"), q_at, heads, qt, qh,
+                    out_at, ot, oh, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, ws.data_ptr(), ws.nbytes,
+                    _raw_stream(cache, stream))
     if status:
         _check(status, "cccl_step_write")
 
@@ -234,11 +243,13 @@ def cccl_step_attention(cache: KvCache, batch: KvBatch, q: torch.Tensor, mask: t
     are set in ``mask`` [n_tokens, words] (int32), into ``out`` (same shape);
     ``lse`` (float32 [n_tokens, q_heads], contiguous) receives the log of each
     row's sum.  ``scale`` defaults to head_dim ** -0.5."""
-    heads = q.shape[1]
-    qt, qh = _packed(q, cache, batch.n_tokens, heads, "q")
-    ot, oh = _packed(out, cache, batch.n_tokens, heads, "out")
-    words, stride = _mask_of(mask, batch.n_tokens, cache._device)
-    _here(cache, q, out, lse, ws)
+    heads, dev = q.shape[1], cache._device
+    shape = (batch.n_tokens, heads, cache.head_dim)
+    qt, qh, _ = _strides(q, cache, shape, "q")
+    ot, oh, _ = _strides(out, cache, shape, "out")
+    words, stride = _mask_of(mask, batch.n_tokens, dev)
+    if ws.get_device() != dev or (lse is not None and lse.get_device() != dev):
+        raise ValueError("all tensors of a call are on the cache's device")
     if lse is not None and (lse.dtype != torch.float32 or lse.shape != q.shape[:2] or not lse.is_contiguous()):
         raise ValueError("lse: expected a contiguous float32 [n_tokens, q_heads]")
     status = _attention(cache._ref, batch._ref, q.data_ptr(), heads, qt, qh, cache._scale if scale is None else scale,

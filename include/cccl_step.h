@@ -87,8 +87,9 @@ typedef struct {
  * earlier is reported and taken as none.  Rows behind the last sequence's stay
  * as they are.
  * When the lengths, counts or pages do not fit (a negative number, more rows
- * than `rows`, more pages than a table row or free_pages has, a tree of more
- * than 32 * mask_words tokens) nothing is given to anyone: cu_tokens is all 0,
+ * than `rows`, more pages than a table row or free_pages has, with mask a
+ * sequence of more than 32 * mask_words tokens, with d_parents one of more than
+ * CCCL_STEP_MAX_DRAFT) nothing is given to anyone: cu_tokens is all 0,
  * kv_lens, held and free_count are what came in, the rest is untouched, and
  * CCCL_ERR_INVALID_ARG (too few free pages: CCCL_ERR_CAPACITY) is reported on
  * the device.  Outputs may not overlap inputs other than as said above.
@@ -194,7 +195,7 @@ typedef struct {
  * Probabilities enter sums as multiples of 2^-56, cut off below; sums are exact
  * after that, so results depend on nothing but the inputs.  Values that are not
  * numbers or negative count as 0, values above 1 as 1; where a row adds up to
- * more than 2 the next token is any.  A token outside 0..vocab - 1, or whose
+ * more than 2 the next token is any (and may be reported).  A token outside 0..vocab - 1, or whose
  * parent is not earlier, is passed over; a tree's tokens from
  * CCCL_STEP_MAX_DRAFT on are passed over and reported.
  * d_path [rows]: rows cu_tokens[b] + k, k < n_kept[b], the number of the k-th

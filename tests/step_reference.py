@@ -72,7 +72,7 @@ def plan(lens, new, held, table, free, count, page, parents, rows, width, words)
     for b in range(B):
         if lens[b] < 0 or new[b] < 0 or not 0 <= held[b] <= width or lens[b] + new[b] > width * page:
             return "invalid"
-        if words and new[b] > 32 * words:
+        if (words and new[b] > 32 * words) or (parents is not None and new[b] > 1024):
             return "invalid"
     if sum(new) > rows or not 0 <= count <= len(free):
         return "invalid"

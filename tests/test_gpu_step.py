@@ -142,9 +142,10 @@ def test_plan_twice_in_place_goes_on_from_there(cc):
         assert got[k] == second[k], k
 
 
-@pytest.mark.parametrize("what", ["lens", "new", "held", "held_high", "count", "count_high", "table", "rows", "words", "free"])
+@pytest.mark.parametrize("what", ["lens", "new", "held", "held_high", "count", "count_high", "table", "rows", "words", "free", "tree"])
 def test_plan_gives_nothing_where_something_does_not_fit(cc, what):
-    p = Plan(cc, [10, 20, 30], [5, 40, 1], 16, words=2, spare=0 if what == "free" else 4, seed=3, over=0.0)
+    p = Plan(cc, [10, 20, 30], [5, 40, 1] if what != "tree" else [5, 1025, 1], 16, words=2 if what != "tree" else None,
+             spare=0 if what == "free" else 4, seed=3, over=0.0)
     status = cc.CCCL_ERR_INVALID_ARG
     if what == "lens":
         p.lens[1] = -1
@@ -165,7 +166,7 @@ def test_plan_gives_nothing_where_something_does_not_fit(cc, what):
         p.parents.pop()
     elif what == "words":
         p.words = 1
-    else:
+    elif what == "free":
         p.count -= 1
         status = cc.CCCL_ERR_CAPACITY
     p.dev()
@@ -415,6 +416,20 @@ def test_verify_refuses_hundreds(cc):
     d.q[0, 5] = 0.5
     d.cuda()
     d.check(cc)
+
+
+def test_verify_of_rows_that_are_no_probabilities(cc):
+    """Sums that leave 64 bits: some token of the vocabulary, and the call after it is right."""
+    for vocab in (1 << 20, 5000):
+        p = torch.ones(4, vocab, device="cuda")
+        cu = ints([0, 1, 4])
+        for q in (None, torch.zeros_like(p)):
+            path, kept, following = (torch.full((n,), -3, dtype=torch.int32, device="cuda") for n in (4, 2, 2))
+            cc.cccl_step_verify(p, q, ints([0, 1, 2, 3]), None, torch.full((4,), 0.9, device="cuda"), cu, path, kept,
+                                following, cc.empty_step_workspace())
+            assert kept.tolist() == [1, 3]
+            assert all(0 <= y < vocab for y in following.tolist())
+    Draft([5, 3], 700, seed=1).check(cc)
 
 
 def test_verify_at_the_ends_of_the_random_numbers(cc):

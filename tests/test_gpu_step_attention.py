@@ -64,7 +64,8 @@ def test_trees(cc, shape, dtype, fmt):
     lens, new, heads, group, dim, page = SHAPES[shape]
     c = TreeCase(lens, new, heads=heads, group=group, dim=dim, page=page, dtype=dtype, fmt=fmt, seed=shape,
                  layout=["thd", "htd", "kv"][shape % 3], fill=float("nan"), mask_pad=shape % 2)
-    for over in ({}, CUT, dict(max_new=500)):  # (the last: the kernel for many rows, whatever their number)
+    # (the last two: the kernel for many rows, whatever their number, and the one for few)
+    for over in ({}, CUT, dict(max_new=500), dict(max_new=1, max_len=1)):
         check(c, *attend(cc, c, over))
 
 
@@ -225,3 +226,11 @@ def test_reported_errors(cc):
             attend(cc, c)
         c.len_dev.copy_(kept)
     check(c, *attend(cc, c))
+
+
+@pytest.mark.parametrize("fmt", ["16bit", "int8"])
+def test_long_contexts(cc, fmt):
+    """One tree of several row tiles a head, with as many blocks for each; few rows over many tiles."""
+    for lens, new, heads, group in (([20011], [61], 2, 8), ([9000], [3], 1, 4), ([12345, 700], [33, 33], 2, 4)):
+        c = TreeCase(lens, new, heads=heads, group=group, dim=128, page=64, fmt=fmt, seed=len(lens))
+        check(c, *attend(cc, c))
