@@ -571,7 +571,9 @@ __device__ __forceinline__ void widen_role(const KvArgs& a, const Args& t, Share
 // bound it: without products and softmax the first takes 61 us of 71 at 2560 tokens;
 // in INT8, of 332: without widening 227, without the softmax 248, with copies alone
 // 194.  Items of 128 rows alone, one Q and four slots for tiles (or three, and five
-// for codes): 306 (301), but 33 drafted then take 590 for 398.
+// for codes): 306 (301), but 33 drafted then take 590 for 398.  Two slots for tiles
+// and five for codes: 365.  Boxes asked for from the L2 a tile ahead of their copies:
+// 251 for 229 (16 x 20480, 16-bit).
 template <class Args>
 __device__ __forceinline__ bool narrow(const Args& t, const Piece& p) {
     return std::is_same<Args, TreeArgs>::value && live_rows<kRows>(t, p) <= kTileRows;
@@ -1435,7 +1437,7 @@ cudaError_t launch_one(const KvArgs& a, const Args& t, int max_new, int max_len,
     int shares = shares_for(a, t, max_new, max_len, kRows, kTokens, kShares);
     // One tree with several row tiles a head: with as many shares for each item its
     // row tiles are walked in step, and all but the first find their tokens in the L2
-    // (61 drafted over 131077, groups of 8: 152 shares 232 us, 144 shares SHARES_US).
+    // (61 drafted over 131077, groups of 8: 152 shares 232 us, 144 shares 213).
     if (std::is_same<Args, TreeArgs>::value && a.batch == 1 && tiled > a.kv_heads && shares == kShares &&
         8 * tiled <= kShares)
         shares = (int)(kShares / tiled * tiled);

