@@ -3,7 +3,7 @@
 //
 // Bound by HBM: queries are read and written, keys and values read and stored:
 // 12572 tokens of 32 + 2 x 8 heads of 128 in 53.4 us, 5.8 TB/s, 0.85 of the measured
-// copy; 95 tokens in 3.6.
+// copy; 91 tokens in 3.6.
 // The angles' sines and cosines are worked out once a token and shared by its
 // heads: a block brings up to 8 tokens and fills a table in shared memory first.
 //
