@@ -709,6 +709,65 @@ def test_calls_on_another_stream(cc):
         [91 + int(verdict[1][0]), 51 + int(verdict[1][1])]
 
 
+def test_places_past_32_bits(cc):
+    """Rows of probabilities and pages of a cache whose offsets do not fit 32 bits."""
+    rows, vocab = 2052, 1 << 20
+    p = torch.zeros(rows, vocab, device="cuda")
+    p[2049, 77], p[2050, 900000], p[2051, vocab - 1] = 1.0, 1.0, 1.0
+    tokens = ints([0] * 2050 + [77, 900000])
+    cu = ints([2049, 2052])
+    path, kept, following = cc.step_verify(p, None, tokens, None, torch.full((rows,), 0.5, device="cuda"), cu)
+    assert kept.tolist() == [3] and following.tolist() == [vocab - 1] and path.tolist()[2049:] == [0, 1, 2]
+    del p
+
+    def pool(dtype):  # three pages, 2^31 values from one to the next
+        whole = torch.empty(2 * (1 << 31) + 16 * 2 * 64, dtype=dtype, device="cuda")
+        return whole.as_strided((3, 16, 2, 64), (1 << 31, 128, 64, 1))
+
+    small = ref.TreeCase([40], [9], heads=2, group=2, dim=64, seed=3, spare=0)
+    k, v = pool(BF), pool(BF)
+    for far, near in ((k, small.k), (v, small.v)):
+        far.copy_(near)
+    rotary = cc.StepRotary(64)
+    cache, batch = small.objects(cc)
+    far = cc.KvCache(k, v)
+    path, kept = ints([0, 4, 7, 8] + [-1] * 5), ints([4])
+    for c in (cache, far):
+        small.got = (cc.step_write(c, batch, rotary, small.q, small.k_new, small.v_new),
+                     *cc.step_attention(c, batch, small.q, small.mask), cc.step_keep(c, batch, path, kept))
+        if c is cache:
+            want = small.got
+    for a, b in zip(want, small.got):
+        assert same_bits(a, b)
+    assert same_bits(k, small.k) and same_bits(v, small.v)
+
+
+def test_calls_at_the_same_time(cc):
+    """Two streams, each with its own workspace and outputs, over one cache."""
+    c = ref.TreeCase([500, 60, 900], [40, 9, 40], heads=2, group=4, dim=128, seed=6)
+    cache, batch = c.objects(cc)
+    d = Draft([40, 9, 40], 5000, seed=2)
+    args = (d.dp, d.dq, ints(d.tokens), ints(d.parents), d.u.cuda(), ints(d.cu))
+    want, _ = cc.step_attention(cache, batch, c.q, c.mask)
+    verdict = cc.step_verify(*args)
+    torch.cuda.synchronize()
+    runs = []
+    for _ in range(2):
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            runs.append((s, torch.empty_like(c.q), cc.empty_kv_workspace(cache, batch, 8),
+                         [torch.empty_like(x) for x in verdict], cc.empty_step_workspace()))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for s, out, ws, outs, ws2 in runs:
+            cc.cccl_step_attention(cache, batch, c.q, c.mask, out, ws, stream=s)
+            cc.cccl_step_verify(*args, *outs, ws2, stream=s)
+    torch.cuda.synchronize()
+    for _, out, ws, outs, ws2 in runs:
+        assert same_bits(out, want) and all(same_bits(a, b) for a, b in zip(outs, verdict))
+        assert cc.cccl_get_result(ws)[1] == 0 and cc.cccl_get_result(ws2)[1] == 0
+
+
 def test_guard_bands(cc):
     """Nothing is written past the outputs: each lies in a larger allocation that keeps its pattern."""
     def band(n, dtype):
