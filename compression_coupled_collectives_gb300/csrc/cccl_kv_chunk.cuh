@@ -840,28 +840,34 @@ __device__ __forceinline__ void softmax_role(const KvArgs& a, const Args& t, Sha
     int32_t first = 0, last = 0;                  // what this row sees
     uint32_t halves = 0;                          // narrow pieces put together so far
     float m = -INFINITY, l = 0.f;
-    for (bool begin = true;; begin = false) {
+    uint32_t skipped = 0;  // tiles of pieces without rows for this warpgroup, since the one at hand
+    for (bool open = false;;) {  // open: a piece is at hand
         // the next piece that has rows for this warpgroup.  Its rows of Q may
         // come now: the last S is done, so is every product with these.
-        uint32_t skipped = 0;  // tiles of pieces without
         float to_base2 = 1.f;
+        bool found = true;
         Piece* const next = &sh->piece[me][slot ^ 1];
-        for (;; ++taken) {
+        for (;;) {
             Piece p;
             if (!take_piece(wait, taken, &p)) return;
+            ++taken;
             if (p.count > 0 && own_tiles(t, p, i) == 0) {
                 skipped += (uint32_t)p.count;
-                continue;
+                // A shared piece is put together first: the other warpgroup, which waits
+                // for that, has taken one piece more and no others, so that a run of
+                // these would end where the ring is full.
+                found = !(kTree && open);
+                if (found) continue;
+            } else {
+                if (lane == 0) *next = p;
+                __syncwarp();
             }
-            if (lane == 0) *next = p;
-            __syncwarp();
             break;
         }
-        ++taken;
-        const bool more = next->count > 0;
+        const bool more = found && next->count > 0;
         if (more)
             to_base2 = fmaxf(scale_base2 * bring_rows<T, FMT>(a, t, *next, narrow(t, *next) ? 0 : i, warp, q_tile), least);
-        if (!begin) {  // the end of the piece at hand
+        if (open) {  // the end of the piece at hand
             const Piece& cur = sh->piece[me][slot];
             if (!wait(&sh->o_full[i], o_phase)) return;
             o_phase ^= 1;
@@ -967,6 +973,8 @@ __device__ __forceinline__ void softmax_role(const KvArgs& a, const Args& t, Sha
                 if (lane == 0) mbar_arrive(&sh->half_read[i]);
             }
         }
+        open = false;
+        if (kTree && !found) continue;
         if (!more) return;
         copy_wait<0>();
         fence_proxy_async_smem();
@@ -974,6 +982,8 @@ __device__ __forceinline__ void softmax_role(const KvArgs& a, const Args& t, Sha
         if (lane == 0) mbar_arrive(&sh->q_full[i]);
         slot ^= 1;
         tile += skipped;
+        skipped = 0;
+        open = true;
         const Piece& cur = sh->piece[me][slot];
         first = last = 0;
         const bool alone = kTree && narrow(t, cur);  // its rows are row tile 0's
