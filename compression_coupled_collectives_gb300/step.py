@@ -176,6 +176,8 @@ def cccl_step_plan(tables: StepTables, lens: torch.Tensor, new: torch.Tensor, ws
     place).  ``parents`` [rows]: the trees; without, chains.  ``rows``: the rows
     of the packed tensors, where none of these says it."""
     dev, batch, i32 = tables._device, tables.batch, _int32
+    if ws.get_device() != dev:
+        raise ValueError("ws is on another device")
     held = tables.held if held is None else held
     free_count = tables.free_count if free_count is None else free_count
     if rows is None:
@@ -281,6 +283,8 @@ def cccl_step_verify(p: torch.Tensor, q: torch.Tensor | None, tokens: torch.Tens
     q_stride = 0 if q is None else _probabilities(q, rows, vocab, "q")
     if q is not None and q.get_device() != dev:
         raise ValueError("q is on another device")
+    if ws.get_device() != dev:
+        raise ValueError("ws is on another device")
     draft = _pack_draft(p.data_ptr(), 0 if q is None else q.data_ptr(), p_stride, q_stride,
                         _numbers(tokens, i32, rows, dev, "tokens"), _maybe(parents, i32, rows, dev, "parents"),
                         _numbers(uniform, torch.float32, rows, dev, "uniform"),
@@ -297,6 +301,8 @@ def cccl_step_keep(cache: KvCache, batch: KvBatch, path: torch.Tensor, n_kept: t
     """Enqueue moving of the kept tokens' keys and values together; ``lens``
     [batch] (or None) receives the lengths without the others."""
     dev, i32 = cache._device, _int32
+    if ws.get_device() != dev:
+        raise ValueError("all tensors of a call are on the cache's device")
     status = _keep(cache._ref, batch._ref, _numbers(path, i32, batch.n_tokens, dev, "path"),
                    _numbers(n_kept, i32, batch.batch, dev, "n_kept"),
                    None if lens is None else _numbers(lens, i32, batch.batch, dev, "lens"), ws.data_ptr(), ws.nbytes,
