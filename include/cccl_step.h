@@ -213,8 +213,9 @@ cccl_status cccl_step_verify(const cccl_step_draft *h_draft, int32_t *d_path, in
  * in the cache changes.  d_lens [batch] (NULL: not wanted) gets the length
  * without the others: kv_lens[b] - n + n_kept[b] (0 where that is negative).
  * A path's entries k have to lie in k .. n - 1; others are not moved, and
- * reported, as is a count outside 0..n (clamped).  d_lens may not be the
- * batch's kv_lens (the call is one of several, for as many layers).
+ * reported, as is a count outside 0..n (clamped).  d_lens may not overlap the
+ * batch's arrays, d_path or d_n_kept, which the call's blocks read while it is
+ * written (and which further calls need, one a layer): refused.
  * d_ws: 16 bytes.  Returns INVALID_ARG, CUDA or OK. */
 cccl_status cccl_step_keep(const cccl_kv_cache *h_cache, const cccl_kv_batch *h_batch, const int32_t *d_path,
                            const int32_t *d_n_kept, int32_t *d_lens, void *d_ws, size_t ws_bytes, cccl_stream_t stream);
