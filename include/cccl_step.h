@@ -211,7 +211,9 @@ cccl_status cccl_step_verify(const cccl_step_draft *h_draft, int32_t *d_path, in
  * the cache holds (codes and scales as they are) at the place of sequence b's
  * new token d_path[cu_tokens[b] + k] goes to the place of its k-th; nothing else
  * in the cache changes.  d_lens [batch] (NULL: not wanted) gets the length
- * without the others: kv_lens[b] - n + n_kept[b] (0 where that is negative).
+ * without the others: kv_lens[b] - n + n_kept[b] (0 where that is negative),
+ * also where n_tokens is 0: other than in the calls above only batch 0 makes
+ * this one a no-op, since every sequence has a length.
  * A path's entries k have to lie in k .. n - 1; others are not moved, and
  * reported, as is a count outside 0..n (clamped).  d_lens may not overlap the
  * batch's arrays, d_path or d_n_kept, which the call's blocks read while it is

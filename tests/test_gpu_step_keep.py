@@ -45,3 +45,20 @@ def test_lengths_over_what_the_call_reads_are_refused(cc):
             assert pool[at:at + 3].tolist() == [41, 41, 41]
             pool.copy_(before)
     assert cc.cccl_get_result(ws)[1] == cc.CCCL_OK
+
+
+def test_a_batch_without_rows_has_lengths_all_the_same(cc):
+    """n_tokens 0: nothing moves, every length is written; counts that do not fit are reported; batch 0 is a no-op."""
+    c = Case([60, 0, 9], [0, 0, 0], heads=2, dim=64, page=16, seed=4)
+    cache, batch = c.objects(cc)
+    start = [c.k.clone(), c.v.clone()]
+    path = ints([])
+    assert cc.step_keep(cache, batch, path, ints([0, 0, 0])).tolist() == [60, 0, 9]
+    ws, lens = cc.empty_step_workspace(), ints([-1, -1, -1])
+    cc.cccl_step_keep(cache, batch, path, ints([0, 1, 0]), lens, ws)
+    assert cc.cccl_get_result(ws)[1] == cc.CCCL_ERR_INVALID_ARG and lens.tolist() == [60, 0, 9]
+    none = cc.KvBatch(c.table[:0], ints([0]), ints([]), n_tokens=0, max_new=1, max_len=1)
+    ws = cc.empty_step_workspace()
+    cc.cccl_step_keep(cache, none, path, ints([]), ints([]), ws)
+    assert cc.cccl_get_result(ws)[1] == cc.CCCL_OK
+    assert torch.equal(c.k, start[0]) and torch.equal(c.v, start[1])
