@@ -188,6 +188,8 @@ def cccl_step_plan(tables: StepTables, lens: torch.Tensor, new: torch.Tensor, ws
         else:
             raise ValueError("rows: how many rows the packed tensors have")
     words, stride = (0, 0) if mask is None else _mask_of(mask, rows, dev)
+    if rows == 0:  # an empty tensor has no address: no mask
+        words = 0
     out = _pack_out(_numbers(cu_tokens, i32, batch + 1, dev, "cu_tokens"), _numbers(kv_lens, i32, batch, dev, "kv_lens"),
                     _numbers(held, i32, batch, dev, "held"), _numbers(free_count, i32, 1, dev, "free_count"),
                     _maybe(slots, torch.int64, rows, dev, "slots"), _maybe(positions, i32, rows, dev, "positions"),
