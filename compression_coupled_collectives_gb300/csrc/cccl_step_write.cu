@@ -9,9 +9,11 @@
 //
 // Angles: a pair turns by turns / 2^64 of a full turn a position, so position p
 // stands at p * turns modulo 2^64 of one: whole turns fall out of the 64-bit
-// product exactly, at any position, and what is left is held to 2^-64 of a turn
-// (times p for the frequency's own rounding).  Its top 32 bits, as a number of
-// half turns in -1..1, go to sincospi, which takes nothing off a large argument.
+// product exactly, at any position, and nothing else is rounded there.  Its top 32
+// bits, as a number of half turns in -1..1, go to sincospi, which takes nothing off
+// a large argument.  The table itself, where it comes from binary64, is off by up
+// to 2^-55.5 of a turn a position (bases of 10^4 and 5 10^5): 2^-36 radians at
+// position 2^17.
 //
 // A vector (token, head, Q, K or V) belongs to G lanes of 16 values each, two
 // pieces of 8.  Interleaved pairs lie in one piece; with pairs half the rotary
