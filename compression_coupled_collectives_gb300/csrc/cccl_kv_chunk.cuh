@@ -1446,10 +1446,15 @@ cudaError_t launch_one(const KvArgs& a, const Args& t, int max_new, int max_len,
                                shared_bytes<FMT, Args>(a.dim), s, a, t, k_map, v_map, box, cluster);
     int shares = shares_for(a, t, max_new, max_len, kRows, kTokens, kShares);
     // One tree with several row tiles a head: with as many shares for each item its
-    // row tiles are walked in step, and all but the first find their tokens in the L2
-    // (61 drafted over 131077, groups of 8: 152 shares 232 us, 144 shares 213).
+    // row tiles are walked in step, and all but the first find their tokens in the L2.
+    // Not where that leaves more than a tenth of the SMs without a share.  152 shares,
+    // and so many an item, over 131072 tokens in 16 bits, groups of 8 (us): 8 heads of 2
+    // row tiles (144) 223, 206; 9 of 2 (144) 247, 232; 7 of 2 (140) 200, 190; 5 of 3
+    // (150) 213, 191; 2 of 9 (144) 247, 225; 4 of 4 (144) 206, 202; 1 of 10 (150) 147,
+    // 143; 1 of 13 (143) 177, 178; 1 of 17 (136, not taken) 217, 227.  Over 32768: 89,
+    // 80; 94, 87; 80, 76; 83, 75; 92, 81; 80, 77; 67, 63; 74, 70; 84, 82.
     if (std::is_same<Args, TreeArgs>::value && a.batch == 1 && tiled > a.kv_heads && shares == kShares &&
-        8 * tiled <= kShares)
+        8 * tiled <= kShares && 10 * (kShares % tiled) <= kShares)
         shares = (int)(kShares / tiled * tiled);
     attend_chunk_kernel<T, FMT, Args, false>
         <<<shares, kThreads, shared_bytes<FMT, Args>(a.dim), s>>>(a, t, k_map, v_map, box, whole ? 1 : 0);

@@ -45,3 +45,15 @@ def test_runs_of_pieces(cc, case, fmt):
         assert ((lse.double() - ref_lse).abs() <= ltol).all()
         for again in outs[1:]:
             assert torch.equal(again[0], out) and torch.equal(again[1], lse)
+
+
+@pytest.mark.parametrize("fmt", ["16bit", "e4m3"])
+@pytest.mark.parametrize("heads,tiles", [(2, 7), (1, 13), (1, 17), (5, 4)])
+def test_one_tree_of_many_row_tiles(cc, heads, tiles, fmt):
+    """As many shares for each of its items, or (17: too many SMs would be idle; 20: too few for each) an even cut."""
+    new = 32 * tiles - 5  # groups of 8: rows of 256
+    c = TreeCase([9001], [new], heads=heads, group=8, dim=64, fmt=fmt, seed=tiles)
+    ref, ref_lse, tol, ltol = c.attention()
+    cache, batch = c.objects(cc)
+    out, lse = cc.step_attention(cache, batch, c.q, c.mask)
+    assert ((out.double() - ref).abs() <= tol).all() and ((lse.double() - ref_lse).abs() <= ltol).all()
