@@ -69,6 +69,7 @@ struct TreeArgs : AttnArgs {
     const uint32_t* mask;
     int64_t mask_stride;  // words from one row to the next
     int32_t words;        // of a row
+    int32_t narrow_rows;  // items of so many rows at most are shared by two warpgroups (many rows)
 };
 
 // Sequence b's rows and length, with everything that does not fit clamped

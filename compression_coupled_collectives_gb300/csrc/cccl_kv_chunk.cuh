@@ -566,28 +566,40 @@ __device__ __forceinline__ void widen_role(const KvArgs& a, const Args& t, Share
 // tile's softmax alone leaves the tensor core waiting most of the time, so both
 // warpgroups take the same rows (each has them in its Q), the one the tiles of
 // tokens of even number, the other the odd ones, and they put their accumulators
-// together at the piece's end.  32 sequences of 4096 tokens, 16 drafted, groups of
-// 4: 128.9 us without, 110.6 with; 16 of 20480 in INT8: 419, 329.  Then the copies
-// bound it: without products and softmax the first takes 61 us of 71 at 2560 tokens;
-// in INT8, of 332: without widening 227, without the softmax 248, with copies alone
-// 194.  Items of 128 rows alone, one Q and four slots for tiles (or three, and five
-// for codes): 306 (301), but 33 drafted then take 590 for 398.  Two slots for tiles
-// and five for codes: 365.  Boxes asked for from the L2 a tile ahead of their copies:
-// 251 for 229 (16 x 20480, 16-bit).
-template <class Args>
+// together at the piece's end.  Without and with, 40 to 128 rows (us): 16-bit caches,
+// 32 sequences of 2560 77.5 to 78.8, 72.7 to 75.2; 32 of up to 4096 95 to 101, 89 to
+// 95; 16 of 20480 234 to 241, 231 to 237.  E4M3, 32 of up to 2560 123 to 129, 114;
+// 40 of up to 5000 243 to 252, 235 to 246; 16 of 20480 325, 317 (128 rows: 325, 339).
+// INT8 the same where items stay whole or clusters share them (122 to 128, 116; one
+// of 1024 21.5 to 23.1, 19.6 to 20.9), but not where they are cut: 12 of 8192 133 to
+// 136, 139 to 142; 40 of up to 5000 232 to 242, 242 to 251; 16 of 20480 313 to 316,
+// 327 to 334 (two of 65536 at 128 rows: 157, 154); hence not there (launch_one).
+// Then the copies bound it: without products and softmax 32 of 2560 take 61 us of 71;
+// 16 of 20480 in INT8, of 332: without widening 227, without the softmax 248, with
+// copies alone 194.  Items of 128 rows alone, one Q and four slots for tiles (or three,
+// and five for codes): 306 (301), but 33 drafted then take 590 for 398.  Two slots for
+// tiles and five for codes: 365.  Boxes asked for from the L2 a tile ahead of their
+// copies: 251 for 229 (16 x 20480, 16-bit).
+// ASKED: whether the call says so, else always (constants where they can be: a number
+// read instead cost 16-bit caches 0.3 to 1 %).
+template <bool ASKED, class Args>
 __device__ __forceinline__ bool narrow(const Args& t, const Piece& p) {
-    return std::is_same<Args, TreeArgs>::value && live_rows<kRows>(t, p) <= kTileRows;
+    if constexpr (std::is_same<Args, TreeArgs>::value)
+        return live_rows<kRows>(t, p) <= (ASKED ? t.narrow_rows : kTileRows);
+    return false;
 }
+template <int FMT, bool CLUSTERS>
+constexpr bool kNarrowAsked = FMT == kKvInt8 && !CLUSTERS;
 // Tiles of tokens of warpgroup i.
-template <class Args>
+template <bool ASKED, class Args>
 __device__ __forceinline__ int32_t own_tiles(const Args& t, const Piece& p, int i) {
-    if (narrow(t, p)) return (p.count - i + 1) / 2;
+    if (narrow<ASKED>(t, p)) return (p.count - i + 1) / 2;
     return live_rows<kRows>(t, p) > i * kTileRows ? p.count : 0;
 }
 
 // ---------------------------------------------------------------- products
 // Returns whether this lane is the one that issued them.
-template <class M, int SLOTS, class Args>
+template <class M, int SLOTS, bool ASKED, class Args>
 __device__ __forceinline__ bool mma_role(const KvArgs& a, const Args& t, Shared* sh, uint32_t q_base,
                                          uint32_t slots, uint32_t slot_bytes) {
     const Waiter wait{sh, a.ws};
@@ -633,7 +645,7 @@ __device__ __forceinline__ bool mma_role(const KvArgs& a, const Args& t, Shared*
     for (uint32_t n = 0; take_piece(wait, n, &p) && p.count > 0; ++n) {
         const int tiles = live_rows<kRows>(t, p) > kTileRows ? 2 : 1;
         const int32_t count = p.count;
-        if (narrow(t, p)) {
+        if (narrow<ASKED>(t, p)) {
             // whichever is ready first: scores of tile qk (K there; P of the tile before
             // in its place in TMEM read, by a product issued before), values of tile pv
             int32_t qk = 0, pv = 0;
@@ -820,7 +832,7 @@ __device__ __forceinline__ uint32_t bits_below(int32_t n) {
     return n <= 0 ? 0u : (n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u);
 }
 
-template <class T, int FMT, class Args>
+template <class T, int FMT, bool ASKED, class Args>
 __device__ __forceinline__ void softmax_role(const KvArgs& a, const Args& t, Shared* sh, uint32_t q_tile,
                                              uint32_t stages, float* joint) {
     using M = Operand<T, FMT>;
@@ -851,7 +863,7 @@ __device__ __forceinline__ void softmax_role(const KvArgs& a, const Args& t, Sha
             Piece p;
             if (!take_piece(wait, taken, &p)) return;
             ++taken;
-            if (p.count > 0 && own_tiles(t, p, i) == 0) {
+            if (p.count > 0 && own_tiles<ASKED>(t, p, i) == 0) {
                 skipped += (uint32_t)p.count;
                 // A shared piece is put together first: the other warpgroup, which waits
                 // for that, has taken one piece more and no others, so that a run of
@@ -866,7 +878,7 @@ __device__ __forceinline__ void softmax_role(const KvArgs& a, const Args& t, Sha
         }
         const bool more = found && next->count > 0;
         if (more)
-            to_base2 = fmaxf(scale_base2 * bring_rows<T, FMT>(a, t, *next, narrow(t, *next) ? 0 : i, warp, q_tile), least);
+            to_base2 = fmaxf(scale_base2 * bring_rows<T, FMT>(a, t, *next, narrow<ASKED>(t, *next) ? 0 : i, warp, q_tile), least);
         if (open) {  // the end of the piece at hand
             const Piece& cur = sh->piece[me][slot];
             if (!wait(&sh->o_full[i], o_phase)) return;
@@ -874,8 +886,8 @@ __device__ __forceinline__ void softmax_role(const KvArgs& a, const Args& t, Sha
             tc_fence_after();
             const bool full = cur.count == cur.range.n;
             // narrow: the other warpgroup has the rest of these rows' tiles
-            const bool shared = narrow(t, cur) && cur.count > 1;
-            const int tile_row = (narrow(t, cur) ? 0 : i * kTileRows) + row;
+            const bool shared = narrow<ASKED>(t, cur) && cur.count > 1;
+            const int tile_row = (narrow<ASKED>(t, cur) ? 0 : i * kTileRows) + row;
             const bool is_row = tile_row < live_rows<kRows>(t, cur);
             const RowPlace at = row_place(t, cur, kRows, tile_row);
             const PartLayout parts = part_layout(a, gridDim.x, kRows);
@@ -986,7 +998,7 @@ __device__ __forceinline__ void softmax_role(const KvArgs& a, const Args& t, Sha
         open = true;
         const Piece& cur = sh->piece[me][slot];
         first = last = 0;
-        const bool alone = kTree && narrow(t, cur);  // its rows are row tile 0's
+        const bool alone = kTree && narrow<ASKED>(t, cur);  // its rows are row tile 0's
         const RowPlace own = row_place(t, cur, kRows, (alone ? 0 : i * kTileRows) + row);
         const bool is_row = (alone ? 0 : i * kTileRows) + row < live_rows<kRows>(t, cur);
         if (is_row) search_range(t, cur.seq, own.token, own.pos, first, last);
@@ -1296,7 +1308,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
         // 256 rows of sums and two statistics: less than Q and the slots, at every dim
         float* const joint = reinterpret_cast<float*>(raw + (base - smem_addr(raw)));
-        softmax_role<T, FMT>(a, t, sh, base + (warp / 4) * tile_bytes, raw_codes + raw_bytes,
+        softmax_role<T, FMT, kNarrowAsked<FMT, CLUSTERS>>(a, t, sh, base + (warp / 4) * tile_bytes, raw_codes + raw_bytes,
                              CLUSTERS && cluster > 1 ? joint : nullptr);
         copy_wait<0>();  // of Q, where the role gave up
         __syncwarp();
@@ -1319,7 +1331,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLoaderRegs));
         if (warp == 12) {
-            const bool issued = mma_role<Operand<T, FMT>, kN>(a, t, sh, base, slots, tile_bytes);
+            const bool issued = mma_role<Operand<T, FMT>, kN, kNarrowAsked<FMT, CLUSTERS>>(a, t, sh, base, slots, tile_bytes);
             __syncwarp();
             // every product is done before TMEM goes (the thread that issued them says so)
             if (issued) tc_commit(&sh->drained);
@@ -1405,7 +1417,7 @@ int32_t box_tokens(uint32_t page_tokens) {
 constexpr int join_bytes(int dim) { return (int)sizeof(float) * kJoinMany * (dim + 1); }
 
 template <class T, int FMT, class Args>
-cudaError_t launch_one(const KvArgs& a, const Args& t, int max_new, int max_len, cudaStream_t s) {
+cudaError_t launch_one(const KvArgs& a, Args t, int max_new, int max_len, cudaStream_t s) {
     static PerDeviceOnce once;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -1441,7 +1453,10 @@ cudaError_t launch_one(const KvArgs& a, const Args& t, int max_new, int max_len,
     // 2048: 52.2, 36.4.
     const int64_t tiled = (int64_t)a.batch * a.kv_heads * (((int64_t)t.group.d * max_new + kRows - 1) / kRows);
     const int cluster = 4 * tiled <= 128 ? 4 : 2 * tiled <= 128 ? 2 : 1;
-    if (cluster > 1 && max_len > (cluster == 4 ? 3 : 7) * kTokens && max_len <= 16 * cluster * kTokens)
+    const bool clusters = cluster > 1 && max_len > (cluster == 4 ? 3 : 7) * kTokens && max_len <= 16 * cluster * kTokens;
+    if constexpr (std::is_same<Args, TreeArgs>::value)
+        t.narrow_rows = kNarrowAsked<FMT, false> && !whole ? 0 : kTileRows;
+    if (clusters)
         return launch_clusters(attend_chunk_kernel<T, FMT, Args, true>, (int)tiled * cluster, cluster, kThreads,
                                shared_bytes<FMT, Args>(a.dim), s, a, t, k_map, v_map, box, cluster);
     int shares = shares_for(a, t, max_new, max_len, kRows, kTokens, kShares);

@@ -25,7 +25,7 @@ CASES = {
     "ragged": (*_ragged(1, 256, 50, 300, 16), 4, 4, 0),
     "ragged_heads": (*_ragged(2, 64, 50, 200, 16), 12, 4, 0),
     "one_of_two_tiles": (([200] + [100] * 15) * 48, [12] * 768, 2, 4, 0),
-    "one_of_many_tiles": (([900] + [60] * 31) * 24, ([9] + [11] * 31) * 24, 4, 8, 0),
+    "one_of_many_tiles": (([520] + [60] * 31) * 24, ([9] + [11] * 31) * 24, 2, 4, 0),
     "wide_among_them": (*_ragged(3, 300, 40, 260, 40), 4, 4, 0),
     "window": (*_ragged(4, 200, 300, 1500, 20), 4, 3, 64),
     "sorted": (sorted(_ragged(5, 400, 30, 400, 16)[0], reverse=True), [16] * 400, 2, 6, 0),
