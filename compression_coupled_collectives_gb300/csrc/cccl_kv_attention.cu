@@ -11,6 +11,14 @@ namespace cccl {
 // of up to 4096 tokens, 8 kv heads of 128, in us (token kernel, chunk kernel):
 //   16-bit cache  20 rows 85, 98;  32 rows 100, 93;  64 rows 158, 93
 //   INT8 cache    32 rows 111, 152;  64 rows 175, 153
+// Drafted trees go by the same rule, since one workspace serves both kinds of call.
+// Their chunk kernel is the faster one from fewer rows on (token kernel, chunk kernel):
+//   16-bit, 32 of up to 4096   16 rows 80, 86;  20 rows 87, 85;  24 rows 96, 83
+//   16-bit, 4 of up to 2000    8 rows 15.9, 17.4;  16 rows 23.3, 17.5;  24 rows 25.9, 17.7
+//   16-bit, one of 517         16 rows 10.6, 14.6;  24 rows 12.1, 14.3
+//   INT8, 32 of up to 4096     32 rows 127, 181;  48 rows 149, 179;  64 rows 195, 187
+//   INT8, 8 of up to 20480     28 rows 135, 144;  32 rows 154, 150;  40 rows 185, 151
+//   INT8, one of 517           32 rows 15.5, 19.9
 static bool few_rows(int format, int group, int max_new) {
     return (int64_t)group * max_new <= (format == kKv16Bit ? 24 : 32);
 }

@@ -650,7 +650,9 @@ __device__ __forceinline__ bool mma_role(const KvArgs& a, const Args& t, Shared*
             // in its place in TMEM read, by a product issued before), values of tile pv
             int32_t qk = 0, pv = 0;
             uint64_t since = 0;
-            auto ready = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xFFFFFFFFu, mbar_test(bar, parity)) != 0; };
+            auto ready = [&](uint64_t* bar, uint32_t parity) {
+                return __all_sync(0xFFFFFFFFu, mbar_test(bar, parity)) != 0;
+            };
             while (pv < count) {
                 const uint32_t k = entry + 2 * (uint32_t)qk, v = entry + 2 * (uint32_t)pv + 1;
                 const int i = pv & 1;
@@ -878,7 +880,8 @@ __device__ __forceinline__ void softmax_role(const KvArgs& a, const Args& t, Sha
         }
         const bool more = found && next->count > 0;
         if (more)
-            to_base2 = fmaxf(scale_base2 * bring_rows<T, FMT>(a, t, *next, narrow<ASKED>(t, *next) ? 0 : i, warp, q_tile), least);
+            to_base2 = fmaxf(
+                scale_base2 * bring_rows<T, FMT>(a, t, *next, narrow<ASKED>(t, *next) ? 0 : i, warp, q_tile), least);
         if (open) {  // the end of the piece at hand
             const Piece& cur = sh->piece[me][slot];
             if (!wait(&sh->o_full[i], o_phase)) return;
@@ -1331,7 +1334,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLoaderRegs));
         if (warp == 12) {
-            const bool issued = mma_role<Operand<T, FMT>, kN, kNarrowAsked<FMT, CLUSTERS>>(a, t, sh, base, slots, tile_bytes);
+            const bool issued =
+                mma_role<Operand<T, FMT>, kN, kNarrowAsked<FMT, CLUSTERS>>(a, t, sh, base, slots, tile_bytes);
             __syncwarp();
             // every product is done before TMEM goes (the thread that issued them says so)
             if (issued) tc_commit(&sh->drained);
@@ -1361,7 +1365,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <int FMT, class Args>
 constexpr size_t shared_bytes(int dim) {
     return 1024 + (size_t)(2 + kSlots<FMT>) * (dim > 64 ? 2 : 1) * kHalfBytes +
-           (FMT == kKv16Bit ? 0 : (size_t)kRawSlots * kTokens * dim) + kStageBytes<FMT, Args> + sizeof(Shared) + kHalvesBytes<Args>;
+           (FMT == kKv16Bit ? 0 : (size_t)kRawSlots * kTokens * dim) + kStageBytes<FMT, Args> + sizeof(Shared) +
+           kHalvesBytes<Args>;
 }
 
 static_assert(1024 * (128 + 2) <= (2 + kSlots<kKvInt8>) * 2 * kHalfBytes &&

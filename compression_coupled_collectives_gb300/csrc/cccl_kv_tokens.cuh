@@ -359,9 +359,10 @@ struct Running {
 // One stage: scores, the softmax's step, values.  base: the stage's first
 // token.  to_base2: the factor of each row's products.
 template <class S>
-__device__ __forceinline__ void step(const typename S::Args& t, const Piece& p, uint32_t stage, int32_t base, const uint32_t (*q)[S::DP / 16][2],
-                                     const int32_t (*first)[2], const int32_t (*last)[2], bool whole_stage,
-                                     const float (*to_base2)[2], Running<S>& st) {
+__device__ __forceinline__ void step(const typename S::Args& t, const Piece& p, uint32_t stage, int32_t base,
+                                     const uint32_t (*q)[S::DP / 16][2], const int32_t (*first)[2],
+                                     const int32_t (*last)[2], bool whole_stage, const float (*to_base2)[2],
+                                     Running<S>& st) {
     const int lane = threadIdx.x & 31, g = lane >> 2;
     constexpr int MT = S::kTokens / 16;
     float s[MT][S::NR][4];
@@ -720,8 +721,8 @@ cudaError_t launch_tokens(const KvArgs& a, const typename S::Args& t, int max_ne
     attend_tokens_kernel<S, false><<<shares, kThreads, S::kSmem, s>>>(a, t, whole ? 1 : 0);
     e = cudaGetLastError();
     if (e != cudaSuccess || whole) return e;
-    return launch_join(join_rows_kernel<typename S::T, S::FMT, S::kRows, typename S::Args>, a, t, shares, S::kRows / kJoinFew,
-                       kJoinFewThreads, 0, s);
+    return launch_join(join_rows_kernel<typename S::T, S::FMT, S::kRows, typename S::Args>, a, t, shares,
+                       S::kRows / kJoinFew, kJoinFewThreads, 0, s);
 }
 
 template <class T, int FMT, int DP, class Args>

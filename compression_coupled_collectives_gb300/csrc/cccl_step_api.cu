@@ -69,7 +69,8 @@ cccl_status cccl_step_plan(const cccl_step_tables* h_tables, const int32_t* d_le
     if (t->batch == 0) return CCCL_OK;
     Pointers at;
     if (!at.workspace(d_ws, ws_bytes) || !at.rows(t->page_table, t->batch, t->table_stride, t->table_pages, 4) ||
-        !at.numbers(t->held, t->batch, 4) || !at.numbers(t->free_pages, t->free_capacity, 4) || !at.numbers(t->free_count, 1, 4) ||
+        !at.numbers(t->held, t->batch, 4) || !at.numbers(t->free_pages, t->free_capacity, 4) ||
+        !at.numbers(t->free_count, 1, 4) ||
         !at.numbers(d_lens, t->batch, 4) || !at.numbers(d_new, t->batch, 4) ||
         !at.numbers(o->cu_tokens, (int64_t)t->batch + 1, 4) || !at.numbers(o->kv_lens, t->batch, 4) ||
         !at.numbers(o->held, t->batch, 4) || !at.numbers(o->free_count, 1, 4))

@@ -157,7 +157,10 @@ cccl_status cccl_step_write(const cccl_kv_cache *h_cache, const cccl_kv_batch *h
  * `window` (those cached before the draft first, then drafted ones by their
  * number): with masks of ancestors, the window of its own path.
  * Workspace: cccl_kv_workspace_bytes(h_cache, h_batch, q_heads).  Rounding,
- * empty rows, hidden places and overlaps as in cccl_kv_attention.
+ * empty rows, hidden places and overlaps as in cccl_kv_attention: so the size of
+ * the program's trees (max_new, times the query heads that share a kv head: up to
+ * 24 such rows, 32 over an 8-bit cache, are few) says whether probabilities meet
+ * the values with 16 bits or more or are rounded once to 16-bit floating point.
  * Returns INVALID_ARG, CUDA or OK. */
 cccl_status cccl_step_attention(const cccl_kv_cache *h_cache, const cccl_kv_batch *h_batch, const void *d_q, int q_heads,
                                 int64_t q_token_stride, int64_t q_head_stride, float scale, const uint32_t *d_mask,
@@ -195,12 +198,14 @@ typedef struct {
  * At the end the next token is drawn from R at the last c by the root's random
  * number u: the first y with R(0) + .. + R(y) > u sum R (from p_c itself where
  * R is 0 throughout).
- * Probabilities enter sums as multiples of 2^-56, cut off below; sums are exact
- * after that, so results depend on nothing but the inputs.  Values that are not
- * numbers or negative count as 0, values above 1 as 1; where a row adds up to
- * more than 2 the next token is any (and may be reported).  A token outside 0..vocab - 1, or whose
- * parent is not earlier, is passed over; a tree's tokens from
- * CCCL_STEP_MAX_DRAFT on are passed over and reported.
+ * Probabilities enter sums as multiples of 2^-56, cut off below, and sums of those
+ * are exact.  A is held in multiples of 2^-53 and A q_c(y) in multiples of 2^-56,
+ * both cut off below; u q_c(x) < p_c(x) is decided exactly, u S q_c(x) < R(x) at
+ * A > 0 in binary64.  So results depend on nothing but the inputs.  Values that
+ * are not numbers or negative count as 0, values above 1 as 1; where a row adds
+ * up to more than 2 the next token is any (and may be reported).  A token outside
+ * 0..vocab - 1, or whose parent is not earlier, is passed over; a tree's tokens
+ * from CCCL_STEP_MAX_DRAFT on are passed over and reported.
  * d_path [rows]: rows cu_tokens[b] + k, k < n_kept[b], the number of the k-th
  * kept token (the root's 0 first), -1 in the others of the sequence.
  * d_next [batch]: the next token.  A sequence without rows has 0 kept and -1
