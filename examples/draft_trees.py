@@ -10,7 +10,8 @@ host, which only reads which tokens were kept.
     python examples/draft_trees.py [--users 4] [--tokens 48] [--nodes 13] [--temperature 0.7]
 
 Prints how many tokens a step kept; with --temperature 0 the answers are the ones
-that the model gives token by token."""
+that the model gives token by token, but where two of its bf16 scores are as good as
+equal: products of another number of rows may round them the other way."""
 
 from __future__ import annotations
 
