@@ -9,6 +9,9 @@
 // page is looked up in the table where the sequence held it before, else among
 // the free ones, so that nobody waits for the table's new entries.  64 trees of up to
 // 33 tokens: 5.9 us, of which an empty launch is half; 32 prompts, 63588 rows: 7.2.
+// A row of a tree walks to its root, a load a level, so deep ones take long: a chain
+// of 64 given as parents 7.1 us, of 256 27.5, of 1024 287, eight of those 2270 (the
+// same chains as none given: 4.7).
 #include "cccl_kv_launch.h"
 #include "cccl_kv_schedule.cuh"
 #include "cccl_step.cuh"
@@ -68,7 +71,7 @@ __device__ __forceinline__ void trees(const PlanArgs& a, const Sums& s, uint32_t
 
 // Slots, and positions where no tree gives them: 32 ROWS rows a warp at a time, one
 // search, then a step or two, ROWS rows' loads in flight.  (32 prompts, 63588 rows:
-// 8.7 us with one, 6.8 with four; 64 trees, 1378 rows: 5.8 and 7.0.)
+// 8.7 us with one, 7.2 with four; 64 trees, 1378 rows: 5.9 and 7.0.)
 template <int ROWS>
 __device__ __forceinline__ void places(const PlanArgs& a, const Sums& s, uint32_t rows, int64_t count, bool walk, int me,
                                        int all) {

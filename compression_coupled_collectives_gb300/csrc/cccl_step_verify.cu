@@ -10,9 +10,11 @@
 // Most steps take one pass: sums before it are only needed for a second child's
 // chance where the draft gave probabilities.  So the time is one read of a row of
 // p (and q) a sequence, behind the chain of loads that leads to it (rows, tokens
-// and parents, probabilities of the tokens): one sequence takes 7.4 us (128000
+// and parents, probabilities of the tokens): one sequence takes 7.4 to 8.9 us (128000
 // values, with q), every further one 0.16, its 1 MB at 6.2 TB/s.  64 chains of 4
-// drafted: 19.5 us (floor 9.7); 16 trees of up to 33, 50257 values, no q: 8.8.  On
+// drafted: 19.6 us (45 MB: q only where a child was refused; floor 6.7); 16 trees of
+// up to 33, 50257 values, no q: 9.0.  A second refused child and each one after it
+// takes a pass and two barriers more, 9 to 10 us (16 sequences: 12).  On
 // the way there, of 33.1: four blocks of 256 threads an SM instead of two of 512
 // 30.6; a search of 16 values a lane, tests in whole numbers 25.4; loads a step
 // ahead of their use, the search from the step that holds it 23.4; code for each
