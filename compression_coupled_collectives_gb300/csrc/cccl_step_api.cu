@@ -39,10 +39,11 @@ struct Pointers {
         return aligned(d_ws, 16) && ws_bytes >= sizeof(cccl::WsHeader) && ranges.ok(d_ws, sizeof(cccl::WsHeader));
     }
 };
-// whether n and m 4-byte numbers have none in common
-bool apart(const int32_t* a, int64_t n, const int32_t* b, int64_t m) {
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return x + 4 * (uintptr_t)n <= y || y + 4 * (uintptr_t)m <= x;
+// whether n numbers have none in common with `rows` rows of m, `stride` (>= m) apart
+bool apart(const int32_t* a, int64_t n, const int32_t* b, int64_t m, int64_t rows = 1, int64_t stride = 1) {
+    const int64_t at = ((int64_t)reinterpret_cast<uintptr_t>(a) - (int64_t)reinterpret_cast<uintptr_t>(b)) / 4;
+    const int64_t row = at < m ? 0 : (at - m) / stride + 1;  // the first that ends behind `at`
+    return m == 0 || row >= rows || row * stride >= at + n;
 }
 cccl_status status_of(cudaError_t e) {
     if (e == cudaSuccess) return CCCL_OK;
@@ -263,7 +264,7 @@ cccl_status cccl_step_keep(const cccl_kv_cache* h_cache, const cccl_kv_batch* h_
          (!at.numbers(d_lens, b->batch, 4) || !apart(d_lens, b->batch, b->kv_lens, b->batch) ||
           !apart(d_lens, b->batch, b->cu_tokens, (int64_t)b->batch + 1) ||
           !apart(d_lens, b->batch, d_n_kept, b->batch) || !apart(d_lens, b->batch, d_path, b->n_tokens) ||
-          !apart(d_lens, b->batch, b->page_table, (int64_t)(b->batch - 1) * b->table_stride + b->table_pages))) ||
+          !apart(d_lens, b->batch, b->page_table, b->table_pages, b->batch, b->table_stride))) ||
         (b->n_tokens > 0 && !at.numbers(d_path, b->n_tokens, 4)))
         return CCCL_ERR_INVALID_ARG;
     const cccl::KeepArgs x{d_path, d_n_kept, d_lens};

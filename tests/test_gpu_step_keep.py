@@ -62,3 +62,21 @@ def test_a_batch_without_rows_has_lengths_all_the_same(cc):
     cc.cccl_step_keep(cache, none, path, ints([]), ints([]), ws)
     assert cc.cccl_get_result(ws)[1] == cc.CCCL_OK
     assert torch.equal(c.k, start[0]) and torch.equal(c.v, start[1])
+
+
+def test_lengths_beside_the_tables_rows_are_taken(cc):
+    """In the gap between two rows of a table that is a slice, up to their very ends, and no further."""
+    c = Case([60, 40], [20, 20], heads=2, dim=64, page=16, seed=4)
+    cache, _ = c.objects(cc)
+    pool = torch.zeros(2, 8, dtype=torch.int32, device="cuda")
+    table = pool[:, 1:5]
+    table.copy_(c.table)
+    batch = cc.KvBatch(table, c.cu, c.len_dev, n_tokens=40, max_new=20, max_len=60)
+    path, kept, ws, flat = ints([0] * 40), ints([1, 1]), cc.empty_step_workspace(), pool.view(-1)
+    for at in (5, 6, 7, 13):
+        cc.cccl_step_keep(cache, batch, path, kept, flat[at:at + 2], ws)
+        assert flat[at:at + 2].tolist() == [41, 21]
+    for at in (0, 1, 4, 8, 9, 12):
+        with pytest.raises(cc.CcclError):
+            cc.cccl_step_keep(cache, batch, path, kept, flat[at:at + 2], ws)
+    assert torch.equal(table, c.table) and cc.cccl_get_result(ws)[1] == cc.CCCL_OK
